@@ -1,0 +1,1216 @@
+// Low-rank adapters of many requests beside a shared projection (include/mok_ops.h,
+// mok_lora_fwd and mok_lora_bwd).
+//
+//   u_t = scale_a xa_t A_a^T     y_t  = x_t W    + u_t B_a          (a = ids[t])
+//   v_t = scale_a dY_t B_a^T     dX_t = dY_t W^T + v_t A_a
+//   dA_a = sum_t v_t^T xa_t      dB_a = sum_t u_t^T dY_t            (t with ids[t] = a)
+//
+// Two kernels serve both directions, because A [n][r][K] and B [n][r][N] have one form:
+//
+//   shrink_kernel   the r values of every row (u or v): 128 rows against the A (or B) rows of
+//                   the distinct adapters among them, side by side in one MMA; each row keeps
+//                   the columns of its own adapter.
+//   proj_kernel     the shared projection, whose K loop simply goes on after W: one step per
+//                   distinct adapter of the row tile, [hi(u) | lo(u)] against that adapter's
+//                   B (or A) rows, into the same TMEM accumulator. The MMA's lane mask
+//                   (disable-output-lane) confines a step to the rows of its adapter. So rows
+//                   of different requests share a tile in any order, with no sorting and no
+//                   padding, the projection is one pass, and an adapter with an inf or NaN
+//                   cannot reach another request's rows.
+//
+// The weight gradients sum over the rows of one adapter, found by wgrad's row lists:
+// bucket_kernel lists each adapter's rows in ascending order, wgrad_kernel gathers them.
+//
+// u and v are kept as hi = bf16(u), lo = bf16(u - hi): the tensor cores take bf16, and the
+// pair carries 16 significant bits, so the low-rank path adds no visible rounding to the
+// bf16 inputs and results. Per 32 ranks a row holds 128 bytes: 32 hi, then 32 lo values.
+//
+// Every mbarrier wait is bounded (kTimeoutNs); on expiry the kernel sets the status word,
+// lets its copies and MMAs in flight finish, and returns.
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "mok_internal.h"
+#include "mok_ops.h"
+#include "mok_ptx.cuh"
+
+namespace mok {
+namespace {
+
+constexpr int BM = 128;                 // rows of a tile (TMEM lanes)
+constexpr int BK = 64;                  // contraction elements per pipeline stage
+constexpr int A_BYTES = BM * BK * 2;    // 16 KB: 128 rows x 128 bytes
+constexpr int kThreads = 192;           // producer warp, MMA warp, four epilogue warps
+constexpr int kMaxStages = 8;
+constexpr int kStagingBox = 4096;       // 32 rows x 128 bytes, one epilogue store
+constexpr int kBarBytes = 256;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr size_t kMaxSmem = 227 * 1024;
+
+// A distinct adapter of a row tile: its id and the lanes (rows) that do NOT use it.
+struct Slot {
+  int32_t id;
+  uint32_t off[4];
+  int32_t pad[3];
+};
+
+__device__ __forceinline__ void flag_timeout(uint32_t* status) {
+  if (status != nullptr) atomicOr(status, kErrTimeout);
+}
+// mbar_wait with the deadline taken only when the first try fails
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, globaltimer_ns() + kTimeoutNs);
+}
+
+// tcgen05.mma (kind::f16) that leaves the accumulator rows (TMEM lanes) of `off` untouched:
+// bit i of word j stands for lane 32 j + i.
+__device__ __forceinline__ void umma_bf16_rows(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc, const uint4 off,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(
+          tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(off.x), "r"(off.y), "r"(off.z),
+      "r"(off.w)
+      : "memory");
+}
+// 3-D tiled load: c0 innermost (elements), then c1, c2.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+// 16 consecutive TMEM columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// fp32 loads from the shared memory of CTA `rank` of the cluster (p: this CTA's address).
+__device__ __forceinline__ float ld_rank(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_rank(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_rank4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(mapa_rank(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// hi and lo of two neighbours. lo is 0 where hi is not finite: an inf stays an inf.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  const float ha = __low2float(h), hb = __high2float(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_bf16(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f);
+}
+
+// ------------------------------------------------------------------ barriers of a CTA
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  volatile int abort;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier area");
+
+__device__ __forceinline__ void init_bars(Bars* b) {
+  for (int s = 0; s < kMaxStages; ++s) {
+    mbar_init(&b->full[s], 1);
+    mbar_init(&b->empty[s], 1);
+  }
+  for (int a = 0; a < 2; ++a) {
+    mbar_init(&b->acc_full[a], 1);
+    mbar_init(&b->acc_empty[a], 128);
+  }
+  mbar_init(&b->drain, 1);
+  b->abort = 0;
+  fence_mbar_init();
+}
+
+// The ring of pipeline stages as one role (producer or MMA lane) walks it.
+struct Ring {
+  int stages;
+  int stage = 0;
+  uint32_t phase = 0;
+  uint32_t used = 0;     // stages filled so far (producer)
+  __device__ explicit Ring(int n) : stages(n) {}
+  __device__ void next() {
+    ++used;
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Producer: waits until the stage is free and announces the bytes that will land in it.
+__device__ __forceinline__ bool open_stage(Bars* b, const Ring& r, uint32_t bytes,
+                                           uint32_t* status) {
+  if (b->abort) return false;
+  if (!wait_bar(&b->empty[r.stage], r.phase ^ 1)) {   // passes at once in the first round
+    flag_timeout(status);
+    b->abort = 1;
+    return false;
+  }
+  mbar_arrive_expect_tx(&b->full[r.stage], bytes);
+  return true;
+}
+__device__ __forceinline__ bool await_stage(Bars* b, const Ring& r, uint32_t* status) {
+  if (b->abort || !wait_bar(&b->full[r.stage], r.phase)) {
+    if (!b->abort) flag_timeout(status);
+    b->abort = 1;
+    return false;
+  }
+  tc_fence_after();
+  return true;
+}
+// After an abort: every copy that was issued has landed (bounded), so that the shared memory
+// may go away.
+__device__ void drain_copies(Bars* b, const Ring& r) {
+  for (uint32_t s = 0; s < (uint32_t)r.stages && s < r.used; ++s) {
+    const uint32_t last = (r.used - 1 - s) / r.stages;   // last round that filled stage s
+    wait_bar(&b->full[s], last & 1);
+  }
+}
+__device__ void drain_mmas(Bars* b) {
+  umma_commit(&b->drain);
+  wait_bar(&b->drain, 0);
+}
+
+// ------------------------------------------------------------------ distinct adapters
+// The distinct adapters among the 128 rows of a tile in order of first use, from 128
+// threads (et = 0 .. 127, one row each). Called by the whole CTA (it synchronises).
+struct TileSlots {
+  int32_t id[BM];        // adapter of each row, -1: none
+  int32_t slot[BM];      // slot of each row's adapter, -1: none
+  int32_t slot_id[BM];   // adapter of each slot
+  uint32_t off[BM][4];   // rows outside each slot
+  int32_t warp_count[4];
+  int32_t count;
+};
+
+__device__ void find_slots(TileSlots& s, int et, const int32_t* ids, int n, int T, int row0) {
+  int id = -1;
+  if (et >= 0) {
+    id = row0 + et < T ? ids[row0 + et] : -1;
+    if (id < 0 || id >= n) id = -1;
+    s.id[et] = id;
+  }
+  __syncthreads();
+  uint32_t eq[4] = {0, 0, 0, 0};
+  int first = -1;
+  bool leads = false;
+  if (et >= 0 && id >= 0) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int4* v = reinterpret_cast<const int4*>(&s.id[32 * w]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int4 x = v[j];
+        eq[w] |= (uint32_t)(x.x == id) << (4 * j) | (uint32_t)(x.y == id) << (4 * j + 1) |
+                 (uint32_t)(x.z == id) << (4 * j + 2) | (uint32_t)(x.w == id) << (4 * j + 3);
+      }
+    }
+#pragma unroll
+    for (int w = 3; w >= 0; --w)
+      if (eq[w]) first = 32 * w + __ffs(eq[w]) - 1;
+    leads = first == et;
+  }
+  const unsigned lead = __ballot_sync(0xffffffffu, leads);
+  if (et >= 0 && (et & 31) == 0) s.warp_count[et >> 5] = __popc(lead);
+  __syncthreads();
+  if (et >= 0 && leads) {
+    int pos = __popc(lead & ((1u << (et & 31)) - 1));
+    for (int w = 0; w < (et >> 5); ++w) pos += s.warp_count[w];
+    s.slot_id[pos] = id;
+    s.slot[et] = pos;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s.off[pos][w] = ~eq[w];
+  }
+  if (et == 0) s.count = s.warp_count[0] + s.warp_count[1] + s.warp_count[2] + s.warp_count[3];
+  __syncthreads();
+  int mine = -1;
+  if (et >= 0 && id >= 0) mine = s.slot[first];
+  __syncthreads();
+  if (et >= 0) s.slot[et] = mine;
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ shrink
+// u = scale (x A_a^T), as hi | lo. One cluster of `split` CTAs per row tile (and per `cy`-th
+// chunk of its adapters): each CTA takes a share of the contraction, the partial sums meet
+// through distributed shared memory in rank order. A chunk is at most p.cols accumulator
+// columns: cols / rp adapters side by side, each rp columns wide.
+struct ShrinkParams {
+  int T, n, r, rp, nb;
+  int kiters, split, cy, cols, stages, stage_bytes;
+  const int32_t* ids;
+  const float* scale;
+  uint8_t* uq;        // [T][nb] blocks of 128 bytes
+  int32_t* n_slots;   // [row tiles]
+  Slot* slots;        // [row tiles][128]
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shrink_kernel(const __grid_constant__ CUtensorMap xmap,
+                  const __grid_constant__ CUtensorMap amap, const ShrinkParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) TileSlots ts;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);   // [128][rp + 1]
+  const int rs = p.rp + 1;
+  Bars* bars = reinterpret_cast<Bars*>(red + ((BM * rs + 3) & ~3));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int et = (int)threadIdx.x - 64;
+  const int q = (int)(blockIdx.x % p.split);
+  const int c0 = (int)(blockIdx.x / p.split) % p.cy;
+  const int m = (int)(blockIdx.x / p.split) / p.cy;
+  const int row0 = m * BM;
+
+  if (threadIdx.x == 0) {
+    init_bars(bars);
+    tma_prefetch_desc(&xmap);
+    tma_prefetch_desc(&amap);
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem, p.cols);
+  tc_fence_before();
+  find_slots(ts, et, p.ids, p.n, p.T, row0);
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const int count = ts.count, per = p.cols / p.rp;
+
+  if (c0 == 0 && q == 0 && et >= 0) {
+    if (et == 0) p.n_slots[m] = count;
+    if (et < count) {
+      Slot s;
+      s.id = ts.slot_id[et];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) s.off[w] = ts.off[et][w];
+      s.pad[0] = s.pad[1] = s.pad[2] = 0;
+      p.slots[(size_t)m * BM + et] = s;
+    }
+  }
+
+  const int kb0 = (int)((long long)p.kiters * q / p.split);
+  const int kb1 = (int)((long long)p.kiters * (q + 1) / p.split);
+  Ring ring(p.stages);
+  uint32_t parity = 0;
+  for (int c = c0; c * per < count; c += p.cy, parity ^= 1) {   // the same chunks in every rank
+    const int s0 = c * per, ns = min(per, count - s0);
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+          if (!open_stage(bars, ring, A_BYTES + ns * p.rp * 128, p.status)) break;
+          uint8_t* sa = smem + ring.stage * p.stage_bytes;
+          uint64_t* bar = &bars->full[ring.stage];
+          tma_load_2d(sa, &xmap, bar, kb * BK, row0);
+          for (int j = 0; j < ns; ++j)   // rp rows of 128 bytes per adapter (zeros past rank r)
+            tma_load_3d(sa + A_BYTES + j * p.rp * 128, &amap, bar, kb * BK, 0, ts.slot_id[s0 + j]);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0) {
+        const uint32_t idesc = idesc_bf16(BM, ns * p.rp, false, false);
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+          ok = await_stage(bars, ring, p.status);
+          if (!ok) break;
+          const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem, umma_desc_sw128(sa + kk * 32, 16, 1024),
+                      umma_desc_sw128(sa + A_BYTES + kk * 32, 16, 1024), idesc,
+                      (kb > kb0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->empty[ring.stage]);
+        }
+        if (ok) umma_commit(&bars->acc_full[0]);
+      }
+      __syncwarp();
+    } else {
+      bool ok = !bars->abort && wait_bar(&bars->acc_full[0], parity);
+      if (!ok) {
+        if (!bars->abort) flag_timeout(p.status);
+        bars->abort = 1;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      // rows of this warp's TMEM lanes, adapter by adapter
+      const int quarter = warp & 3, row = quarter * 32 + lane;
+      const int sl = ts.slot[row];
+      unsigned todo = ok ? __ballot_sync(0xffffffffu, sl >= s0 && sl < s0 + ns) : 0u;
+      while (todo) {
+        const int cur = __shfl_sync(0xffffffffu, sl, __ffs(todo) - 1);
+        todo &= ~__ballot_sync(0xffffffffu, sl == cur);
+        for (int i0 = 0; i0 < p.rp; i0 += 16) {
+          float v[16];
+          tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (cur - s0) * p.rp + i0, v);
+          if (sl == cur) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) red[row * rs + i0 + i] = v[i];
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+    }
+    cluster_sync_all();
+    if (et >= 0) {
+      const int rows = BM / p.split, half = p.rp / 2;
+      for (int it = et; it < rows * half; it += 128) {
+        const int row = q * rows + it / half, i = 2 * (it % half);
+        const int sl = ts.slot[row];
+        if (sl < s0 || sl >= s0 + ns) continue;
+        float a = 0.f, b = 0.f;
+        for (int k = 0; k < p.split; ++k) {
+          a += ld_rank(&red[row * rs + i], k);
+          b += ld_rank(&red[row * rs + i + 1], k);
+        }
+        const float f = p.scale[ts.id[row]];
+        uint32_t hi, lo;
+        // ranks r .. rp - 1 are padding: 0 also where a row with an inf met A's zero fill
+        split_pair(i < p.r ? f * a : 0.f, i + 1 < p.r ? f * b : 0.f, hi, lo);
+        uint8_t* dst = p.uq + ((size_t)(row0 + row) * p.nb + i / 32) * 128 + (i % 32) * 2;
+        *reinterpret_cast<uint32_t*>(dst) = hi;
+        *reinterpret_cast<uint32_t*>(dst + 64) = lo;
+      }
+    }
+    cluster_sync_all();   // the partial sums may be overwritten, the accumulator reused
+    tc_fence_after();
+  }
+  if (bars->abort) {
+    if (threadIdx.x == 0) drain_copies(bars, ring);
+    if (threadIdx.x == 32) drain_mmas(bars);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.cols);
+  }
+}
+
+// ------------------------------------------------------------------ projection
+// out tile [128][NT] = X W (TRANS: X W^T) + the adapters' steps. split == 1: persistent, one
+// CTA per tile at a time, two accumulators so that a tile's epilogue overlaps the next
+// tile's MMAs, results staged in shared memory and stored by TMA. split > 1 (too few tiles
+// for the SMs): a cluster of `split` CTAs shares one tile's contraction, W's and the
+// adapters' steps alike, and the partial sums meet in rank order through distributed shared
+// memory.
+struct ProjParams {
+  int T, out_cols, n;
+  int kiters;               // steps over W (0: the adapters' part alone)
+  int NT, n_tiles, m_tiles, split, stages, stage_bytes;
+  int rp, nb, rb;           // padded rank, 32-rank blocks, ranks per adapter step
+  int out_bf16;
+  const int32_t* ids;
+  const int32_t* n_slots;   // null: no adapters' part
+  const Slot* slots;
+  void* out;
+  uint32_t* status;
+};
+
+template <bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1)
+    proj_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                const __grid_constant__ CUtensorMap umap, const __grid_constant__ CUtensorMap emap,
+                const __grid_constant__ CUtensorMap omap, const ProjParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* staging = smem + p.stages * p.stage_bytes;
+  // split > 1: no staging boxes; the partial tile reuses the pipeline stages
+  Bars* bars = reinterpret_cast<Bars*>(staging + (p.split == 1 ? 8 * kStagingBox : 0));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = (int)(blockIdx.x % p.split);
+  const int tiles = p.m_tiles * p.n_tiles;
+  const int t0 = (int)(blockIdx.x / p.split), tstep = (int)(gridDim.x / p.split);
+  const int kb0 = (int)((long long)p.kiters * q / p.split);
+  const int kb1 = (int)((long long)p.kiters * (q + 1) / p.split);
+  const uint32_t tmem_cols = p.NT <= 64 ? 128 : p.NT <= 128 ? 256 : 512;   // two accumulators
+
+  if (threadIdx.x == 0) {
+    init_bars(bars);
+    tma_prefetch_desc(&xmap);
+    tma_prefetch_desc(&wmap);
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem, tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp == 0 && lane == 0) {
+    Ring ring(p.stages);
+    bool ok = true;
+    for (int tile = t0; ok && tile < tiles; tile += tstep) {
+      const int row0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * p.NT;
+      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+        ok = open_stage(bars, ring, A_BYTES + p.NT * 128, p.status);
+        if (!ok) break;
+        uint8_t* sa = smem + ring.stage * p.stage_bytes;
+        uint64_t* bar = &bars->full[ring.stage];
+        tma_load_2d(sa, &xmap, bar, kb * BK, row0);
+        if (TRANS) {   // NT rows of W, contraction along the row (K-major)
+          tma_load_2d(sa + A_BYTES, &wmap, bar, kb * BK, n0);
+        } else {       // 64 rows of W, 64-column chunks (MN-major)
+          for (int j = 0; j < p.NT / 64; ++j)
+            tma_load_2d(sa + A_BYTES + j * 64 * 128, &wmap, bar, n0 + j * 64, kb * BK);
+        }
+      }
+      if (!ok || p.n_slots == nullptr) continue;
+      const int ns = p.n_slots[row0 / BM];
+      const Slot* sl = p.slots + (size_t)(row0 / BM) * BM;
+      for (int s = q; ok && s < ns; s += p.split) {
+        const int id = sl[s].id;
+        for (int b = 0; b < p.nb; ++b, ring.next()) {
+          ok = open_stage(bars, ring, A_BYTES + p.NT * p.rb * 2, p.status);
+          if (!ok) break;
+          uint8_t* sa = smem + ring.stage * p.stage_bytes;
+          uint64_t* bar = &bars->full[ring.stage];
+          tma_load_2d(sa, &umap, bar, b * 64, row0);
+          for (int j = 0; j < p.NT / 64; ++j)   // rb ranks x 64 columns (zeros past rank r)
+            tma_load_3d(sa + A_BYTES + j * p.rb * 128, &emap, bar, n0 + j * 64, b * 32, id);
+        }
+      }
+    }
+    if (bars->abort) drain_copies(bars, ring);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(BM, p.NT, false, !TRANS);
+    const uint32_t idesc_e = idesc_bf16(BM, p.NT, false, true);
+    Ring ring(p.stages);
+    bool ok = true;
+    int local = 0;
+    for (int tile = t0; ok && tile < tiles; tile += tstep, ++local) {
+      const int acc = local & 1;
+      if (!wait_bar(&bars->acc_empty[acc], ((local >> 1) & 1) ^ 1)) {
+        flag_timeout(p.status);
+        bars->abort = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + acc * (tmem_cols / 2);
+      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+        ok = await_stage(bars, ring, p.status);
+        if (!ok) break;
+        const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(d, umma_desc_sw128(sa + kk * 32, 16, 1024),
+                    TRANS ? umma_desc_sw128(sa + A_BYTES + kk * 32, 16, 1024)
+                          : umma_desc_sw128(sa + A_BYTES + kk * 2048, 64 * 128, 1024),
+                    idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+        umma_commit(&bars->empty[ring.stage]);
+      }
+      if (ok && p.n_slots != nullptr) {
+        const int m = tile / p.n_tiles, ns = p.n_slots[m];
+        const Slot* sl = p.slots + (size_t)m * BM;
+        for (int s = q; ok && s < ns; s += p.split) {
+          const uint4 off = make_uint4(sl[s].off[0], sl[s].off[1], sl[s].off[2], sl[s].off[3]);
+          for (int b = 0; b < p.nb; ++b, ring.next()) {
+            ok = await_stage(bars, ring, p.status);
+            if (!ok) break;
+            const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+            for (int kk = 0; kk < p.rb / 16; ++kk) {   // hi and lo of 16 ranks, same rows of B
+              const uint64_t bd = umma_desc_sw128(sa + A_BYTES + kk * 2048, p.rb * 128, 1024);
+              // without W a row's first step starts its sum (each row is in one slot only)
+              umma_bf16_rows(d, umma_desc_sw128(sa + kk * 32, 16, 1024), bd, idesc_e, off,
+                             (p.kiters > 0 || b > 0 || kk > 0) ? 1u : 0u);
+              umma_bf16_rows(d, umma_desc_sw128(sa + 64 + kk * 32, 16, 1024), bd, idesc_e, off, 1u);
+            }
+            umma_commit(&bars->empty[ring.stage]);
+          }
+        }
+      }
+      if (ok) umma_commit(&bars->acc_full[acc]);
+    }
+    if (bars->abort) drain_mmas(bars);
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    uint8_t* box = staging + quarter * 2 * kStagingBox;
+    int local = 0, stored = 0;
+    for (int tile = t0; tile < tiles; tile += tstep, ++local) {
+      const int acc = local & 1;
+      const int row0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * p.NT;
+      bool ok = !bars->abort && wait_bar(&bars->acc_full[acc], (local >> 1) & 1);
+      if (!ok) {
+        if (!bars->abort) flag_timeout(p.status);
+        bars->abort = 1;
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * (tmem_cols / 2) + ((uint32_t)(quarter * 32) << 16);
+      const bool rows_here = row0 + quarter * 32 < p.T;
+      bool zero = false;   // adapters' part alone: rows without an adapter were never written
+      if (p.kiters == 0) {
+        const int id = row0 + row < p.T ? p.ids[row0 + row] : -1;
+        zero = id < 0 || id >= p.n;
+      }
+      if (p.split > 1) {
+        float* red = reinterpret_cast<float*>(smem) + row * (p.NT + 4);
+        for (int c = 0; rows_here && c < p.NT; c += 32) {
+          float v[32];
+          tmem_ld32(d + c, v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(red + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+        continue;
+      }
+      const int step = p.out_bf16 ? 64 : 32;   // columns of a 128-byte box row
+      for (int c = 0; rows_here && c < p.NT && n0 + c < p.out_cols; c += step, ++stored) {
+        uint8_t* dst = box + (stored & 1) * kStagingBox;
+        float v[32];
+        if (stored >= 2) {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
+        for (int h = 0; h < step / 32; ++h) {
+          tmem_ld32(d + c + 32 * h, v);
+          if (zero) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+          if (p.out_bf16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(dst + lane * 128 + (((4 * h + j) ^ (lane & 7)) * 16)) =
+                  make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                             pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                             pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(dst + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&omap, dst, n0 + c, row0 + quarter * 32);
+          bulk_commit();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->acc_empty[acc]);
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+
+  if (p.split > 1) {   // one tile per cluster
+    cluster_sync_all();
+    if (warp >= 2) {
+      const int et = (int)threadIdx.x - 64, tile = t0;
+      const int row0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * p.NT;
+      const int rows = min(BM, p.T - row0), groups = p.NT / 4;
+      const float* red = reinterpret_cast<const float*>(smem);
+      for (int it = q * 128 + et; it < rows * groups; it += 128 * p.split) {
+        const int r = it / groups, c = it % groups * 4;
+        if (n0 + c >= p.out_cols) continue;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < p.split; ++k) {
+          const float4 v = ld_rank4(red + r * (p.NT + 4) + c, k);
+          a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        }
+        const size_t at = (size_t)(row0 + r) * p.out_cols + n0 + c;
+        if (p.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+              make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = a;
+      }
+    }
+    cluster_sync_all();   // no rank leaves while another reads its partial tile
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------ row lists
+// One CTA per adapter: its rows in ascending order at rows[off[a] .. off[a] + cnt[a]), where
+// off[a] counts the rows of lower adapters. Each CTA reads all ids, so that no CTA waits for
+// another.
+constexpr int kBucketThreads = 1024;
+
+__global__ void __launch_bounds__(kBucketThreads)
+    bucket_kernel(int T, const int32_t* __restrict__ ids, int32_t* __restrict__ off,
+                  int32_t* __restrict__ cnt, int32_t* __restrict__ rows) {
+  __shared__ int s_less[32], s_eq[32];
+  const int a = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int less = 0;
+  for (int t = tid; t < T; t += kBucketThreads) {
+    const int id = ids[t];
+    less += id >= 0 && id < a;
+  }
+  less = __reduce_add_sync(0xffffffffu, less);
+  if (lane == 0) s_less[warp] = less;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < 32; ++w) base += s_less[w];
+  const int start = base;
+  for (int t0 = 0; t0 < T; t0 += kBucketThreads) {
+    const int t = t0 + tid;
+    const bool mine = t < T && ids[t] == a;
+    const unsigned b = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) s_eq[warp] = __popc(b);
+    __syncthreads();
+    int pos = base, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int c = s_eq[w];
+      if (w < warp) pos += c;
+      all += c;
+    }
+    if (mine) rows[pos + __popc(b & ((1u << lane) - 1))] = t;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    off[a] = start;
+    cnt[a] = base - start;
+  }
+}
+
+// ------------------------------------------------------------------ weight gradients
+// out[a] [r][C] = sum over adapter a's rows t of uq[t]^T g[t]: CTA = (adapter, 128 columns,
+// share of the rows); the shares of one block of columns are the ranks of a cluster, whose
+// partial sums meet in rank order through distributed shared memory. A pass over g: memory
+// bound, so the products run on warp-level MMAs (mma.sync m16n8k16), whose operands come
+// straight from the gathered rows: 64 rows per stage, cp.async, rows past the end zero-filled
+// (both operands, so that a stale value cannot meet a zero). MT = padded rank / 16.
+constexpr int kWgCols = 128;
+constexpr int kWgRows = 64;
+constexpr int kWgStages = 3;
+constexpr int kWgThreads = 128;
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p))
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct WgradParams {
+  int C, r, n, ctiles, split, out_bf16;
+  const int32_t* off;
+  const int32_t* cnt;
+  const int32_t* rows;
+  const uint8_t* uq;             // [T][nb] blocks of 128 bytes
+  const __nv_bfloat16* g;        // [T][C]
+  void* out;                     // [n][r][C]
+};
+
+template <int MT>
+__global__ void __launch_bounds__(kWgThreads) wgrad_kernel(const WgradParams p) {
+  constexpr int NB = (MT + 1) / 2;                 // 32-rank blocks of a row of uq
+  constexpr int G_BYTES = kWgRows * kWgCols * 2;
+  constexpr int U_ROW = NB * 128;
+  constexpr int STAGE = G_BYTES + kWgRows * U_ROW;
+  constexpr int RS = kWgCols + 4;                  // floats per row of the partial sums
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int q = (int)(blockIdx.x % p.split);
+  const int ct = (int)(blockIdx.x / p.split) % p.ctiles;
+  const int a = (int)(blockIdx.x / p.split) / p.ctiles;
+  const int c0 = ct * kWgCols;
+  const int cnt = p.cnt[a];
+  const int32_t* rows = p.rows + p.off[a];
+  const int blocks = (cnt + kWgRows - 1) / kWgRows;
+  const int b0 = (int)((long long)blocks * q / p.split);
+  const int b1 = (int)((long long)blocks * (q + 1) / p.split);
+
+  auto fetch = [&](int b) {
+    uint8_t* sg = smem + (b - b0) % kWgStages * STAGE;
+    uint8_t* su = sg + G_BYTES;
+#pragma unroll
+    for (int i = 0; i < kWgRows * 16 / kWgThreads; ++i) {
+      const int e = tid + i * kWgThreads, rr = e >> 4, ch = e & 15;
+      const int at = b * kWgRows + rr;
+      const bool on = at < cnt && c0 + ch * 8 < p.C;
+      const __nv_bfloat16* src = on ? p.g + (size_t)rows[at] * p.C + c0 + ch * 8 : p.g;
+      cp_async16(sg + rr * 256 + ((ch ^ (rr & 7)) * 16), src, on);
+    }
+#pragma unroll
+    for (int i = 0; i < kWgRows * NB * 8 / kWgThreads; ++i) {
+      const int e = tid + i * kWgThreads, rr = e / (NB * 8), ch = e % (NB * 8);
+      const int at = b * kWgRows + rr;
+      const bool on = at < cnt;
+      const uint8_t* src = on ? p.uq + (size_t)rows[at] * U_ROW + ch * 16 : p.uq;
+      cp_async16(su + rr * U_ROW + ((ch ^ (rr & 7)) * 16), src, on);
+    }
+  };
+
+  float acc[MT][4][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
+
+#pragma unroll
+  for (int s = 0; s < kWgStages - 1; ++s) {
+    if (b0 + s < b1) fetch(b0 + s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  for (int b = b0; b < b1; ++b) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kWgStages - 2) : "memory");
+    __syncthreads();   // stage b is in; every warp is done with the stage that is refilled next
+    if (b + kWgStages - 1 < b1) fetch(b + kWgStages - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint8_t* sg = smem + (b - b0) % kWgStages * STAGE;
+    const uint8_t* su = sg + G_BYTES;
+#pragma unroll
+    for (int k0 = 0; k0 < kWgRows; k0 += 16) {
+      uint32_t bf[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rr = k0 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        const int ch = warp * 4 + h * 2 + (lane >> 4);
+        ldsm4_t(bf + 4 * h, sg + rr * 256 + ((ch ^ (rr & 7)) * 16));
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int rr = k0 + (lane >> 4) * 8 + (lane & 7);
+        const int ch = (mt >> 1) * 8 + (mt & 1) * 2 + ((lane >> 3) & 1);
+        uint32_t hi[4], lo[4];
+        ldsm4_t(hi, su + rr * U_ROW + ((ch ^ (rr & 7)) * 16));
+        ldsm4_t(lo, su + rr * U_ROW + (((ch + 4) ^ (rr & 7)) * 16));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma16816(acc[mt][j], hi, bf[2 * j], bf[2 * j + 1]);
+          mma16816(acc[mt][j], lo, bf[2 * j], bf[2 * j + 1]);
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+
+  float* red = reinterpret_cast<float*>(smem);   // [16 MT][RS], over the stages
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int rr = mt * 16 + (lane >> 2), cc = warp * 32 + j * 8 + (lane & 3) * 2;
+      red[rr * RS + cc] = acc[mt][j][0];
+      red[rr * RS + cc + 1] = acc[mt][j][1];
+      red[(rr + 8) * RS + cc] = acc[mt][j][2];
+      red[(rr + 8) * RS + cc + 1] = acc[mt][j][3];
+    }
+  cluster_sync_all();
+  for (int it = q * kWgThreads + tid; it < p.r * (kWgCols / 4); it += kWgThreads * p.split) {
+    const int rr = it / (kWgCols / 4), cc = it % (kWgCols / 4) * 4;
+    if (c0 + cc >= p.C) continue;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < p.split; ++k) {
+      const float4 v = ld_rank4(red + rr * RS + cc, k);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    const size_t at = ((size_t)a * p.r + rr) * p.C + c0 + cc;
+    if (p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = s;
+  }
+  cluster_sync_all();
+}
+
+// ------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> fn{nullptr};
+  EncodeTiledFn f = fn.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+          cudaSuccess || q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiledFn>(p);
+  fn.store(f, std::memory_order_release);
+  return f;
+}
+
+// Map of a dense row-major tensor [d2][d1][d0] (d2 = 0: a matrix) with boxes of 128 bytes x
+// box1 rows, 128-byte swizzle; loads outside read zeros, stores outside are dropped.
+bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t d0, uint64_t d1, uint64_t d2,
+              int box1) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || !base) return false;
+  const uint64_t es = bf16 ? 2 : 4;
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {d0 * es, d0 * d1 * es};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box1, 1};
+  cuuint32_t step[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+             d2 ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int padded_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+
+// Parts of `saved`: the slots of each row tile, then u. The backward's workspace holds the
+// same for v, then the row lists.
+struct SavedParts {
+  size_t n_slots, slots, uq, total;
+};
+SavedParts saved_parts(const mok_lora_dims& d) {
+  const size_t mt = (size_t)(d.T + BM - 1) / BM, nb = (padded_rank(d.r) + 31) / 32;
+  SavedParts s;
+  s.n_slots = 0;
+  s.slots = align_up(mt * 4, 256);
+  s.uq = s.slots + align_up(mt * BM * sizeof(Slot), 256);
+  s.total = s.uq + align_up((size_t)d.T * nb * 128, 256);
+  return s;
+}
+struct WorkParts {
+  SavedParts v;
+  size_t off, cnt, rows, total;
+};
+WorkParts work_parts(const mok_lora_dims& d) {
+  WorkParts w;
+  w.v = saved_parts(d);
+  w.off = w.v.total;
+  w.cnt = w.off + align_up((size_t)d.n * 4, 256);
+  w.rows = w.cnt + align_up((size_t)d.n * 4, 256);
+  w.total = w.rows + align_up((size_t)d.T * 4, 256);
+  return w;
+}
+
+// SM count of the current device, and its kernels' shared-memory limits raised (once each).
+int device_sms() {
+  static std::atomic<int> sms[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && sms[dev].load(std::memory_order_acquire)) return sms[dev].load();
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  const void* fns[] = {(const void*)shrink_kernel, (const void*)proj_kernel<false>,
+                       (const void*)proj_kernel<true>, (const void*)wgrad_kernel<1>,
+                       (const void*)wgrad_kernel<2>, (const void*)wgrad_kernel<4>,
+                       (const void*)wgrad_kernel<8>};
+  for (const void* f : fns) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, f) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kMaxSmem - a.sharedSizeBytes)) != cudaSuccess)
+      return 0;
+  }
+  if (dev < 64) sms[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int grid, int threads, size_t smem, int cluster,
+                   cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The r values of every row: in [T][C] against w [n][r][C].
+mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void* w,
+                      const float* scale, const int32_t* ids, char* saved, uint32_t* status,
+                      int sms, cudaStream_t s) {
+  const SavedParts sp = saved_parts(d);
+  const int mt = (d.T + BM - 1) / BM;
+  ShrinkParams p = {};
+  p.T = d.T;
+  p.n = d.n;
+  p.r = d.r;
+  p.rp = padded_rank(d.r);
+  p.nb = (p.rp + 31) / 32;
+  p.kiters = (C + BK - 1) / BK;
+  p.cols = std::max(64, p.rp);
+  // CTAs: two per SM if there is work for them; a rank takes at least four steps
+  p.split = 1;
+  while (p.split < 8 && 2 * p.split * 4 <= p.kiters && mt * p.split < 2 * sms) p.split *= 2;
+  const int most = std::min(std::min(d.n, d.T), BM);   // distinct adapters of a tile
+  const int chunks = (most * p.rp + p.cols - 1) / p.cols;
+  p.cy = std::max(1, std::min(chunks, 2 * sms / (mt * p.split)));
+  p.stage_bytes = A_BYTES + p.cols * 128;
+  p.stages = 4;
+  p.ids = ids;
+  p.scale = scale;
+  p.uq = reinterpret_cast<uint8_t*>(saved + sp.uq);
+  p.n_slots = reinterpret_cast<int32_t*>(saved + sp.n_slots);
+  p.slots = reinterpret_cast<Slot*>(saved + sp.slots);
+  p.status = status;
+  CUtensorMap xm, am;
+  if (!make_map(&xm, in, true, C, d.T, 0, BM) || !make_map(&am, w, true, C, d.r, d.n, p.rp))
+    return MOK_ERR_CUDA;
+  const size_t smem = (size_t)p.stages * p.stage_bytes + align_up((size_t)BM * (p.rp + 1) * 4, 16) +
+                      kBarBytes + 1024;
+  return launch(shrink_kernel, mt * p.cy * p.split, kThreads, smem, p.split, s, xm, am, p) ==
+                 cudaSuccess
+             ? MOK_OK
+             : MOK_ERR_CUDA;
+}
+
+// out [T][cols] = in [T][C] W (trans: W^T) + the low-rank part. W == null: that part alone;
+// parts == null: no such part.
+mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const void* in,
+                    const void* W, const char* parts, const void* expand, const int32_t* ids,
+                    void* out, mok_out_dtype type, uint32_t* status, int sms, cudaStream_t s) {
+  const SavedParts sp = saved_parts(d);
+  ProjParams p = {};
+  p.T = d.T;
+  p.out_cols = cols;
+  p.n = d.n;
+  p.kiters = W ? (C + BK - 1) / BK : 0;
+  p.m_tiles = (d.T + BM - 1) / BM;
+  p.rp = padded_rank(d.r);
+  p.nb = (p.rp + 31) / 32;
+  p.rb = std::min(p.rp, 32);
+  p.out_bf16 = type == MOK_OUT_BF16;
+  // Tile width and contraction split: the pair with the least estimated time, waves x
+  // (steps x time of a step + fixed cost), in SM clocks. A step of NT columns takes the
+  // tensor core about 2.2 clocks per column, and never less than its loads need.
+  double best = 0;
+  for (int nt : {256, 192, 128, 64}) {
+    for (int split = 1; split <= 8; split *= 2) {
+      if (split > 1 && (p.kiters < 4 * split || nt > 128)) continue;
+      const double n_tiles = (cols + nt - 1) / nt, tiles = n_tiles * p.m_tiles;
+      const double waves = std::ceil(tiles * split / sms);
+      const double step = std::max(2.2 * nt, 250.0);
+      const double t = waves * (std::ceil((double)p.kiters / split) * step) +
+                       (split > 1 ? 3000.0 : 1500.0);
+      if (best == 0 || t < best) {
+        best = t;
+        p.NT = nt;
+        p.split = split;
+      }
+    }
+  }
+  p.n_tiles = (cols + p.NT - 1) / p.NT;
+  p.stage_bytes = A_BYTES + p.NT * 128;
+  p.stages = std::min(kMaxStages, (int)((kMaxSmem - 1024 - kBarBytes - 8 * kStagingBox) / p.stage_bytes));
+  if (parts) {
+    p.n_slots = reinterpret_cast<const int32_t*>(parts + sp.n_slots);
+    p.slots = reinterpret_cast<const Slot*>(parts + sp.slots);
+  }
+  p.ids = ids;
+  p.out = out;
+  p.status = status;
+  CUtensorMap xm, wm, um, em, om;
+  bool ok = make_map(&om, out, p.out_bf16, cols, d.T, 0, 32);
+  if (W) {
+    ok = ok && make_map(&xm, in, true, C, d.T, 0, BM);
+    ok = ok && (trans ? make_map(&wm, W, true, C, cols, 0, p.NT) : make_map(&wm, W, true, cols, C, 0, BK));
+  } else {
+    xm = wm = om;   // not read
+  }
+  if (parts) {
+    ok = ok && make_map(&um, parts + sp.uq, true, (uint64_t)p.nb * 64, d.T, 0, BM);
+    ok = ok && make_map(&em, expand, true, cols, d.r, d.n, p.rb);
+  } else {
+    um = em = om;
+  }
+  if (!ok) return MOK_ERR_CUDA;
+  const int tiles = p.m_tiles * p.n_tiles;
+  const size_t smem = (size_t)p.stages * p.stage_bytes + (p.split == 1 ? 8 * kStagingBox : 0) +
+                      kBarBytes + 1024;
+  const int grid = p.split == 1 ? std::min(tiles, sms) : tiles * p.split;
+  const cudaError_t e =
+      trans ? launch(proj_kernel<true>, grid, kThreads, smem, p.split, s, xm, wm, um, em, om, p)
+            : launch(proj_kernel<false>, grid, kThreads, smem, p.split, s, xm, wm, um, em, om, p);
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+mok_status run_wgrad(const mok_lora_dims& d, int C, const char* uq, const void* g, char* ws,
+                     const WorkParts& wp, void* out, mok_out_dtype type, int sms, cudaStream_t s) {
+  WgradParams p = {};
+  p.C = C;
+  p.r = d.r;
+  p.n = d.n;
+  p.ctiles = (C + kWgCols - 1) / kWgCols;
+  p.out_bf16 = type == MOK_OUT_BF16;
+  p.off = reinterpret_cast<const int32_t*>(ws + wp.off);
+  p.cnt = reinterpret_cast<const int32_t*>(ws + wp.cnt);
+  p.rows = reinterpret_cast<const int32_t*>(ws + wp.rows);
+  p.uq = reinterpret_cast<const uint8_t*>(uq);
+  p.g = static_cast<const __nv_bfloat16*>(g);
+  p.out = out;
+  // row shares: enough CTAs to keep the SMs' loads in flight, and at least two stages each
+  p.split = 1;
+  const long long base = (long long)d.n * p.ctiles;
+  while (p.split < 8 && base * p.split < 6LL * sms && d.T / p.split > 2 * kWgRows) p.split *= 2;
+  const int mt = padded_rank(d.r) / 16, nb = (mt + 1) / 2;
+  const size_t stages = (size_t)kWgStages * kWgRows * (kWgCols * 2 + nb * 128);
+  const size_t red = (size_t)mt * 16 * (kWgCols + 4) * 4;
+  const size_t smem = std::max(stages, red);
+  const long long grid = base * p.split;
+  if (grid > 0x7fffffff) return MOK_ERR_UNSUPPORTED;
+  cudaError_t e;
+  switch (mt) {
+    case 1: e = launch(wgrad_kernel<1>, (int)grid, kWgThreads, smem, p.split, s, p); break;
+    case 2: e = launch(wgrad_kernel<2>, (int)grid, kWgThreads, smem, p.split, s, p); break;
+    case 4: e = launch(wgrad_kernel<4>, (int)grid, kWgThreads, smem, p.split, s, p); break;
+    default: e = launch(wgrad_kernel<8>, (int)grid, kWgThreads, smem, p.split, s, p); break;
+  }
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+bool ok_dims(const mok_lora_dims* d) {
+  return d && d->T >= 0 && d->T <= (1 << 24) && d->K >= 8 && d->N >= 8 && d->K % 8 == 0 &&
+         d->N % 8 == 0 && d->K <= (1 << 20) && d->N <= (1 << 20) && d->n >= 1 &&
+         d->n <= (1 << 20) && d->r >= 1 && d->r <= 128;
+}
+bool ok_ptr(const void* p, uintptr_t align) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0;
+}
+bool ok_weights(const mok_lora_weights* w) {
+  return w && ok_ptr(w->W, 16) && ok_ptr(w->A, 16) && ok_ptr(w->B, 16) && ok_ptr(w->scale, 4);
+}
+bool ok_type(mok_out_dtype t) { return t == MOK_OUT_BF16 || t == MOK_OUT_F32; }
+
+}  // namespace
+}  // namespace mok
+
+extern "C" mok_status mok_lora_get_sizes(const mok_lora_dims* dims, mok_lora_sizes* out) {
+  using namespace mok;
+  if (!ok_dims(dims) || !out) return MOK_ERR_INVALID_ARG;
+  out->saved_bytes = saved_parts(*dims).total;
+  out->workspace_bytes = work_parts(*dims).total;
+  return MOK_OK;
+}
+
+extern "C" mok_status mok_lora_fwd(const mok_lora_dims* dims, const mok_lora_weights* w,
+                                   const void* x, const void* x_ad, const int32_t* ids, void* y,
+                                   mok_out_dtype out, void* saved, uint32_t* status,
+                                   void* stream) {
+  using namespace mok;
+  if (!ok_dims(dims) || !ok_weights(w) || !ok_type(out)) return MOK_ERR_INVALID_ARG;
+  if (dims->T == 0) return MOK_OK;
+  if (!ok_ptr(x, 16) || (x_ad && !ok_ptr(x_ad, 16)) || !ok_ptr(ids, 4) || !ok_ptr(y, 16) ||
+      (status && !ok_ptr(status, 4)))
+    return MOK_ERR_INVALID_ARG;
+  if (!ok_ptr(saved, 256)) return MOK_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms <= 0) return MOK_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* sv = static_cast<char*>(saved);
+  mok_status st = run_shrink(*dims, dims->K, x_ad ? x_ad : x, w->A, w->scale, ids, sv, status, sms, s);
+  if (st != MOK_OK) return st;
+  return run_proj(*dims, dims->K, dims->N, false, x, w->W, sv, w->B, ids, y, out, status, sms, s);
+}
+
+extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_weights* w,
+                                   const void* x, const void* x_ad, const int32_t* ids,
+                                   const void* saved, const void* dY, void* dX, void* dXa,
+                                   void* dA, void* dB, mok_out_dtype out, void* workspace,
+                                   uint32_t* status, void* stream) {
+  using namespace mok;
+  if (!ok_dims(dims) || !ok_weights(w) || !ok_type(out)) return MOK_ERR_INVALID_ARG;
+  if (!ok_ptr(dA, 16) || !ok_ptr(dB, 16)) return MOK_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dims->T == 0) {
+    const size_t es = out == MOK_OUT_BF16 ? 2 : 4, nr = (size_t)dims->n * dims->r;
+    if (cudaMemsetAsync(dA, 0, nr * dims->K * es, s) != cudaSuccess ||
+        cudaMemsetAsync(dB, 0, nr * dims->N * es, s) != cudaSuccess)
+      return MOK_ERR_CUDA;
+    return MOK_OK;
+  }
+  if (!ok_ptr(x, 16) || !ok_ptr(ids, 4) || !ok_ptr(dY, 16) || !ok_ptr(dX, 16) ||
+      (status && !ok_ptr(status, 4)))
+    return MOK_ERR_INVALID_ARG;
+  if (x_ad ? (!ok_ptr(x_ad, 16) || !ok_ptr(dXa, 16)) : dXa != nullptr) return MOK_ERR_INVALID_ARG;
+  if (!ok_ptr(saved, 256) || !ok_ptr(workspace, 256)) return MOK_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms <= 0) return MOK_ERR_CUDA;
+  const mok_lora_dims& d = *dims;
+  const char* sv = static_cast<const char*>(saved);
+  char* ws = static_cast<char*>(workspace);
+  const WorkParts wp = work_parts(d);
+  mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, status, sms, s);
+  if (st != MOK_OK) return st;
+  st = run_proj(d, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, sms, s);
+  if (st != MOK_OK) return st;
+  if (x_ad) {
+    st = run_proj(d, d.N, d.K, true, nullptr, nullptr, ws, w->A, ids, dXa, out, status, sms, s);
+    if (st != MOK_OK) return st;
+  }
+  bucket_kernel<<<d.n, kBucketThreads, 0, s>>>(d.T, ids, reinterpret_cast<int32_t*>(ws + wp.off),
+                                               reinterpret_cast<int32_t*>(ws + wp.cnt),
+                                               reinterpret_cast<int32_t*>(ws + wp.rows));
+  if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+  st = run_wgrad(d, d.K, ws + wp.v.uq, x_ad ? x_ad : x, ws, wp, dA, out, sms, s);
+  if (st != MOK_OK) return st;
+  return run_wgrad(d, d.N, sv + saved_parts(d).uq, dY, ws, wp, dB, out, sms, s);
+}
+
+extern "C" mok_status mok_lora_get_status(uint32_t* status, void* stream) {
+  using namespace mok;
+  if (!ok_ptr(status, 4)) return MOK_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t bits = 0;
+  if (cudaMemcpyAsync(&bits, status, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaMemsetAsync(status, 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    return MOK_ERR_CUDA;
+  return (bits & kErrTimeout) ? MOK_ERR_TIMEOUT : MOK_OK;
+}

@@ -37,6 +37,16 @@ def _dev(t, name: str, dtype: torch.dtype, numel: int, optional: bool = False):
     return t.data_ptr()
 
 
+_RESULT_CODES = {torch.bfloat16: mok.MOK_OUT_BF16, torch.float32: mok.MOK_OUT_F32}
+
+
+def _result_code(dtype, name: str) -> int:
+    """The ABI's code of a tensor type that may be bf16 or fp32."""
+    if dtype not in _RESULT_CODES:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+    return _RESULT_CODES[dtype]
+
+
 class MoELayer:
     """One MoE SwiGLU layer of fixed dims on one CUDA device."""
 

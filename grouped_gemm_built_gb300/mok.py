@@ -1,4 +1,4 @@
-"""ctypes binding of libmok (the C ABI in include/mok.h), with the same names.
+"""ctypes binding of libmok (the C ABI in include/mok.h and mok_ops.h), with the same names.
 
 Argument marshalling only: every step of the layer runs in the library's CUDA kernels.
 Pointers are passed as Python ints (e.g. ``tensor.data_ptr()``), streams as the raw
@@ -39,6 +39,10 @@ MOK_SMPAIRS_OFF = 2
 MOK_FWD_MEGAKERNEL = 0
 MOK_FWD_LAUNCHES = 1
 MOK_FWD_AUTO = 2
+MOK_SCORE_SOFTMAX = 0
+MOK_SCORE_SIGMOID = 1
+MOK_GROUP_MAX = 0
+MOK_GROUP_TOP2 = 1
 
 
 class MokDims(ctypes.Structure):
@@ -67,6 +71,24 @@ class MokSizes(ctypes.Structure):
                 ("saved_bytes", c_size_t), ("mx_weight_bytes", c_size_t),
                 ("padded_rows_max", c_int), ("macrobatches", c_int), ("ring_slots", c_int),
                 ("macrobatch_tokens", c_int)]
+
+
+class MokRouting(ctypes.Structure):
+    _fields_ = [("E", c_int), ("k", c_int), ("score", c_int), ("groups", c_int),
+                ("top_groups", c_int), ("group_score", c_int), ("renormalize", c_int),
+                ("scale", ctypes.c_float)]
+
+
+class MokLoraDims(ctypes.Structure):
+    _fields_ = [(n, c_int) for n in ("T", "K", "N", "n", "r")]
+
+
+class MokLoraWeights(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("W", "A", "B", "scale")]
+
+
+class MokLoraSizes(ctypes.Structure):
+    _fields_ = [("saved_bytes", c_size_t), ("workspace_bytes", c_size_t)]
 
 
 class MokError(RuntimeError):
@@ -106,6 +128,19 @@ def _declare(L):
         "mok_quantize_weights_mxfp8": (c_int, [c_void_p, _P(MokWeights), c_void_p, c_void_p]),
         "mok_get_status": (c_int, [c_void_p, _P(MokSched), c_void_p]),
         "mok_plan_noalloc": (c_int, [c_void_p, _P(MokSched), c_void_p]),
+        "mok_route": (c_int, [_P(MokRouting), c_int, c_void_p, c_int, c_void_p, c_void_p,
+                              c_void_p, c_void_p]),
+        "mok_route_bwd": (c_int, [_P(MokRouting), c_int, c_void_p, c_int, c_void_p, c_void_p,
+                                  c_void_p, c_int, c_void_p]),
+        "mok_dropout": (c_int, [c_void_p, c_void_p, c_void_p, c_size_t, ctypes.c_float,
+                                ctypes.c_uint64, ctypes.c_uint64, c_int, c_void_p]),
+        "mok_lora_get_sizes": (c_int, [_P(MokLoraDims), _P(MokLoraSizes)]),
+        "mok_lora_fwd": (c_int, [_P(MokLoraDims), _P(MokLoraWeights), c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+        "mok_lora_bwd": (c_int, [_P(MokLoraDims), _P(MokLoraWeights), c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+        "mok_lora_get_status": (c_int, [c_void_p, c_void_p]),
         "mok_profile_enable": (c_int, [c_void_p, c_int]),
         "mok_profile_report": (c_int, [c_void_p, c_char_p, c_size_t, _P(c_int)]),
     }
@@ -245,6 +280,45 @@ def mok_get_status(ctx, sched: MokSched, stream) -> int:
 def mok_plan_noalloc(ctx, sched: MokSched, stream) -> None:
     """Schedule from caller-supplied routing, with no workspace (see include/mok.h)."""
     _check(lib().mok_plan_noalloc(ctx, ctypes.byref(sched), _v(stream)), "mok_plan_noalloc")
+
+
+def mok_route(rule: MokRouting, T, logits, logits_type, bias, topk_idx, gates, stream) -> None:
+    _check(lib().mok_route(ctypes.byref(rule), T, logits, logits_type, bias, topk_idx, gates,
+                           stream), "mok_route")
+
+
+def mok_route_bwd(rule: MokRouting, T, logits, logits_type, topk_idx, dgates, dlogits,
+                  dlogits_type, stream) -> None:
+    _check(lib().mok_route_bwd(ctypes.byref(rule), T, logits, logits_type, topk_idx, dgates,
+                               dlogits, dlogits_type, stream), "mok_route_bwd")
+
+
+def mok_dropout(x, add, y, n, p, seed, offset, dtype, stream) -> None:
+    _check(lib().mok_dropout(x, add, y, n, p, seed & (2**64 - 1), offset & (2**64 - 1), dtype,
+                             stream), "mok_dropout")
+
+
+def mok_lora_get_sizes(dims: MokLoraDims) -> MokLoraSizes:
+    s = MokLoraSizes()
+    _check(lib().mok_lora_get_sizes(ctypes.byref(dims), ctypes.byref(s)), "mok_lora_get_sizes")
+    return s
+
+
+def mok_lora_fwd(dims: MokLoraDims, w: MokLoraWeights, x, x_ad, ids, y, out, saved, status,
+                 stream) -> None:
+    _check(lib().mok_lora_fwd(ctypes.byref(dims), ctypes.byref(w), x, x_ad, ids, y, out, saved,
+                              status, stream), "mok_lora_fwd")
+
+
+def mok_lora_bwd(dims: MokLoraDims, w: MokLoraWeights, x, x_ad, ids, saved, dY, dX, dXa, dA, dB,
+                 out, workspace, status, stream) -> None:
+    _check(lib().mok_lora_bwd(ctypes.byref(dims), ctypes.byref(w), x, x_ad, ids, saved, dY, dX,
+                              dXa, dA, dB, out, workspace, status, stream), "mok_lora_bwd")
+
+
+def mok_lora_get_status(status, stream) -> int:
+    """Synchronises the stream; returns the status (0 = ok) and clears it."""
+    return lib().mok_lora_get_status(status, stream)
 
 
 def mok_profile_enable(ctx, enable: bool) -> None:

@@ -1,0 +1,72 @@
+"""Routing to experts on torch tensors (``mok_route`` and ``mok_route_bwd`` in
+include/mok_ops.h): softmax or sigmoid scores, a balance bias that steers the choice only,
+expert groups, top-k, and the gradient of the gates with respect to the logits.
+
+The results feed a layer without a router of its own (``MoELayer(router=False)``):
+``plan(topk_idx=idx, gates=gates)``, then ``backward`` gives the ``dgates`` that
+``Routing.backward`` takes.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import mok
+from .layer import _dev, _result_code
+
+
+class Routing:
+    """A routing rule over E experts; see ``mok_routing`` for what each field means."""
+
+    SCORES = {"softmax": mok.MOK_SCORE_SOFTMAX, "sigmoid": mok.MOK_SCORE_SIGMOID}
+    GROUP_SCORES = {"max": mok.MOK_GROUP_MAX, "top2": mok.MOK_GROUP_TOP2}
+
+    def __init__(self, E: int, k: int, score: str = "softmax", groups: int = 1,
+                 top_groups: int = 1, group_score: str = "max", renormalize: bool = True,
+                 scale: float = 1.0):
+        if score not in self.SCORES:
+            raise ValueError(f"score must be one of {sorted(self.SCORES)}, got {score!r}")
+        if group_score not in self.GROUP_SCORES:
+            raise ValueError(f"group_score must be one of {sorted(self.GROUP_SCORES)}, "
+                             f"got {group_score!r}")
+        self.E, self.k = E, k
+        self.rule = mok.MokRouting(E=E, k=k, score=self.SCORES[score], groups=groups,
+                                   top_groups=top_groups,
+                                   group_score=self.GROUP_SCORES[group_score],
+                                   renormalize=1 if renormalize else 0, scale=scale)
+        mok.mok_route(self.rule, 0, None, mok.MOK_OUT_F32, None, None, None, None)  # checks it
+
+    def _logits(self, logits):
+        dt = logits.dtype if isinstance(logits, torch.Tensor) else None
+        code = _result_code(dt, "logits")
+        if logits.dim() != 2 or logits.shape[1] != self.E:
+            raise ValueError(f"logits must be [T, {self.E}], got {tuple(logits.shape)}")
+        return _dev(logits, "logits", dt, logits.numel()), code, logits.shape[0]
+
+    def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None):
+        """(topk_idx [T,k] int32, gates [T,k] fp32) from logits [T,E] bf16 or fp32 and the
+        selection bias [E] fp32."""
+        pl, code, T = self._logits(logits)
+        pb = _dev(bias, "bias", torch.float32, self.E, optional=True)
+        idx = torch.empty((T, self.k), dtype=torch.int32, device=logits.device)
+        gates = torch.empty((T, self.k), dtype=torch.float32, device=logits.device)
+        with torch.cuda.device(logits.device):
+            mok.mok_route(self.rule, T, pl, code, pb, idx.data_ptr(), gates.data_ptr(),
+                          torch.cuda.current_stream().cuda_stream)
+        return idx, gates
+
+    def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, dgates: torch.Tensor,
+                 dtype: Optional[torch.dtype] = None):
+        """dlogits [T,E] (``dtype``, the logits' type by default) from dgates [T,k] fp32, at
+        the choice that ``forward`` made from these logits."""
+        pl, code, T = self._logits(logits)
+        dtype = dtype or logits.dtype
+        dcode = _result_code(dtype, "dlogits")
+        pi = _dev(topk_idx, "topk_idx", torch.int32, T * self.k)
+        pd = _dev(dgates, "dgates", torch.float32, T * self.k)
+        out = torch.empty((T, self.E), dtype=dtype, device=logits.device)
+        with torch.cuda.device(logits.device):
+            mok.mok_route_bwd(self.rule, T, pl, code, pi, pd, out.data_ptr(), dcode,
+                              torch.cuda.current_stream().cuda_stream)
+        return out
