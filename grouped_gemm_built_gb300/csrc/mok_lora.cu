@@ -1038,8 +1038,8 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
       const double n_tiles = (cols + nt - 1) / nt, tiles = n_tiles * p.m_tiles;
       const double waves = std::ceil(tiles * split / sms);
       const double step = std::max(2.2 * nt, 250.0);
-      const double t = waves * (std::ceil((double)p.kiters / split) * step) +
-                       (split > 1 ? 3000.0 : 1500.0);
+      const double t = waves * (std::ceil((double)p.kiters / split) * step +
+                                (split > 1 ? 6000.0 : 1500.0));
       if (best == 0 || t < best) {
         best = t;
         p.NT = nt;
