@@ -2,15 +2,16 @@
 // scores, a bias that steers the choice only, expert groups, top-k, gates renormalised or
 // not; and the gradient of the gates with respect to the logits.
 //
-// One warp per token. Lane l holds the logits of experts l, l + 32, ...: coalesced loads,
-// every step of the choice a register loop plus a warp reduction, nothing shared between
-// warps. Comparisons run on 32-bit keys with the order of the fp32 scores, so a maximum over
-// the warp is one integer reduction instruction and a second one finds the lowest id that
-// has it. Bound by latency for few tokens and by instruction issue for many (the T E logits
-// are read once, a few microseconds' worth of HBM).
+// One warp per token; lane l holds the NV consecutive logits l NV .. l NV + NV - 1 (16-byte
+// loads), so lower lanes hold lower ids and the lowest id among equal scores is the lowest
+// lane of a ballot. Scores are compared through 32-bit keys in the order of the fp32 values:
+// the maximum over the warp is one integer reduction instruction per chosen expert. A group
+// of experts is a run of lanes, its score a lane-local pass and a few shuffles. Bound by
+// latency for few tokens and by instruction issue for many (the T E logits are read once).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,11 +54,112 @@ __device__ __forceinline__ float warp_max(float v) {   // no NaN among the value
 struct Rule {
   int T, E, k, groups, per, top_groups;
   bool sigmoid, top2, renorm;
+  bool vec;          // rows of logits (and gradients) allow vector accesses
+  int lanes_shift;   // log2 of the lanes per group, -1: groups do not fall on such runs
   float scale;
 };
 
 // 1 - sigmoid(l) is sigmoid(-l): no cancellation near 1
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+
+// The NV consecutive elements from e0 of a row of E; `fill` past its end. vec: e0 NV-aligned,
+// E a multiple of NV, addresses aligned for the widest access that divides NV elements.
+template <int NV, typename T>
+__device__ __forceinline__ void load_row(const T* row, int e0, int E, bool vec, float fill,
+                                         float* v) {
+  constexpr int bytes = NV * (int)sizeof(T);
+  if constexpr (bytes % 4 == 0) {
+    if (vec) {
+      if (e0 < E) {
+        uint32_t w[bytes / 4];
+        if constexpr (bytes % 16 == 0) {
+#pragma unroll
+          for (int i = 0; i < bytes / 16; ++i) {
+            const uint4 q = reinterpret_cast<const uint4*>(row + e0)[i];
+            w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+          }
+        } else if constexpr (bytes % 8 == 0) {
+#pragma unroll
+          for (int i = 0; i < bytes / 8; ++i) {
+            const uint2 q = reinterpret_cast<const uint2*>(row + e0)[i];
+            w[2 * i] = q.x; w[2 * i + 1] = q.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < bytes / 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(row + e0)[i];
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+          else v[i] = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = fill;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = e0 + i < E ? load(row + e0 + i) : fill;
+}
+template <int NV, typename T>
+__device__ __forceinline__ void store_row(T* row, int e0, int E, bool vec, const float* v) {
+  constexpr int bytes = NV * (int)sizeof(T);
+  if constexpr (bytes % 4 == 0) {
+    if (vec) {
+      if (e0 >= E) return;
+      uint32_t w[bytes / 4];
+#pragma unroll
+      for (int i = 0; i < bytes / 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          w[i] = __float_as_uint(v[i]);
+        } else {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+      if constexpr (bytes % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < bytes / 16; ++i)
+          reinterpret_cast<uint4*>(row + e0)[i] =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      } else if constexpr (bytes % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < bytes / 8; ++i)
+          reinterpret_cast<uint2*>(row + e0)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < bytes / 4; ++i) reinterpret_cast<uint32_t*>(row + e0)[i] = w[i];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (e0 + i < E) store(row + e0 + i, v[i]);
+}
+
+// Softmax over the warp's logits s (cleaned): s becomes the scores, m and 1 / z its
+// statistics. A fully masked row has scores 0.
+template <int NV>
+__device__ __forceinline__ void warp_softmax(float* s, float& m, float& inv_z) {
+  m = s[0];
+#pragma unroll
+  for (int i = 1; i < NV; ++i) m = fmaxf(m, s[i]);
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.f;
+  float z = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    s[i] = expf(s[i] - m);
+    z += s[i];
+  }
+  z = warp_sum(z);
+  inv_z = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) s[i] *= inv_z;
+}
 
 template <int NV, typename LT>
 __global__ void __launch_bounds__(32 * kWarps)
@@ -67,119 +169,128 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= q.T) return;
   const LT* row = logits + (size_t)t * q.E;
+  const int e0 = lane * NV;
+  const uint32_t masked = order_key(-INFINITY);
 
   // scores; key = 0: no candidate (past E, in a dropped group, or taken)
   float s[NV];
   uint32_t key[NV];
+  load_row<NV>(row, e0, q.E, q.vec, -INFINITY, s);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    s[i] = e < q.E ? clean(load(row + e)) : -INFINITY;
+    s[i] = clean(s[i]);
+    key[i] = order_key(s[i]);
   }
-  float m = 0.f, z = 1.f;   // softmax statistics
+  float m = 0.f, inv_z = 0.f;
   const bool on_logits = !q.sigmoid && bias == nullptr;
+  if (!on_logits || (q.top_groups < q.groups && q.top2) || !q.renorm) {
+    if (q.sigmoid) {
+      // the choice needs the scores to a few ulp only (the gates below are full precision)
 #pragma unroll
-  for (int i = 0; i < NV; ++i) key[i] = order_key(s[i]);
-  if (!q.sigmoid) {
-    m = s[0];
-#pragma unroll
-    for (int i = 1; i < NV; ++i) m = fmaxf(m, s[i]);
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.f;   // every expert masked: all scores 0
-    z = 0.f;
+      for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + expf(-s[i]));
+    } else {
+      warp_softmax<NV>(s, m, inv_z);
+    }
+    // choice scores: s becomes s + bias, -inf for masked experts
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = expf(s[i] - m);
-      z += s[i];
+      if (key[i] == masked) {
+        s[i] = -INFINITY;
+      } else if (bias != nullptr) {
+        const float c = s[i] + bias[e0 + i];
+        s[i] = c > -INFINITY ? c : -INFINITY;   // a NaN bias masks the choice too
+      }
+      if (!on_logits) key[i] = order_key(s[i]);
     }
-    z = warp_sum(z);
-    const float d = z > 0.f ? z : 1.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = s[i] / d;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = sigmoid(s[i]);
   }
-  // choice scores: s becomes s + bias, -inf for masked experts
-  const uint32_t masked = order_key(-INFINITY);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    if (key[i] == masked) {
-      s[i] = -INFINITY;
-    } else if (bias != nullptr) {
-      const float c = s[i] + bias[e];
-      s[i] = c > -INFINITY ? c : -INFINITY;   // a NaN bias masks too
-    }
-    if (!on_logits) key[i] = order_key(s[i]);
-    if (e >= q.E) key[i] = 0;
-  }
+  for (int i = 0; i < NV; ++i)
+    if (e0 + i >= q.E) key[i] = 0;
 
   if (q.top_groups < q.groups) {
-    // score of group g in lane g
-    float gs = -INFINITY;
-    for (int g = 0; g < q.groups; ++g) {
-      const int e0 = g * q.per, e1 = e0 + q.per;
-      float v;
-      if (!q.top2) {
-        uint32_t b = 0;
+    uint32_t gkey;      // of the group of this lane (lanes_shift >= 0), else of group `lane`
+    if (q.lanes_shift >= 0) {
+      uint32_t b1 = 0, b2 = 0;   // the group's two largest choice scores
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = lane + 32 * i;
-          if (e >= e0 && e < e1) b = max(b, key[i]);
-        }
-        v = key_value(__reduce_max_sync(kAll, b));
-      } else {
-        // the two largest choice scores of this lane, then of the warp
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t x = e0 + i >= q.E ? 0u : q.top2 ? order_key(s[i]) : key[i];
+        b2 = max(b2, min(b1, x));
+        b1 = max(b1, x);
+      }
+      for (int sh = 0; sh < q.lanes_shift; ++sh) {
+        const uint32_t o1 = __shfl_xor_sync(kAll, b1, 1 << sh);
+        const uint32_t o2 = __shfl_xor_sync(kAll, b2, 1 << sh);
+        b2 = max(max(b2, o2), min(b1, o1));
+        b1 = max(b1, o1);
+      }
+      // masked experts add nothing to a sum
+      gkey = q.top2 && b2 > masked ? order_key(key_value(b1) + key_value(b2)) : b1;
+    } else {
+      gkey = 0;
+      for (int g = 0; g < q.groups; ++g) {
+        const int g0 = g * q.per, g1 = g0 + q.per;
         uint32_t b1 = 0, b2 = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int e = lane + 32 * i;
-          if (e >= e0 && e < e1) {
-            const uint32_t x = order_key(s[i]);
-            b2 = max(b2, min(b1, x));
-            b1 = max(b1, x);
-          }
+          const int e = e0 + i;
+          const uint32_t x = e < g0 || e >= g1 ? 0u : q.top2 ? order_key(s[i]) : key[i];
+          b2 = max(b2, min(b1, x));
+          b1 = max(b1, x);
         }
-        const uint32_t w1 = __reduce_max_sync(kAll, b1);
-        const unsigned have = __ballot_sync(kAll, b1 == w1);
-        const uint32_t w2 = __reduce_max_sync(kAll, lane == __ffs(have) - 1 ? b2 : b1);
-        v = key_value(w1);
-        if (w2 > masked) v += key_value(w2);   // masked experts add nothing
+        uint32_t w = __reduce_max_sync(kAll, b1);
+        if (q.top2) {
+          const unsigned have = __ballot_sync(kAll, b1 == w);
+          const uint32_t w2 = __reduce_max_sync(kAll, lane == __ffs(have) - 1 ? b2 : b1);
+          if (w2 > masked) w = order_key(key_value(w) + key_value(w2));
+        }
+        if (lane == g) gkey = w;
       }
-      if (lane == g) gs = v;
     }
-    uint32_t gkey = lane < q.groups ? order_key(gs) : 0;
+    // the best groups; every lane of a run carries its group's key, the lowest lane wins ties
     uint32_t live = 0;
+    const int shift = q.lanes_shift >= 0 ? q.lanes_shift : 0;
     for (int j = 0; j < q.top_groups; ++j) {
       const uint32_t w = __reduce_max_sync(kAll, gkey);
-      const int g = __ffs(__ballot_sync(kAll, gkey == w)) - 1;
+      const int g = (__ffs(__ballot_sync(kAll, gkey == w)) - 1) >> shift;
       live |= 1u << g;
-      if (lane == g) gkey = 0;
+      if ((lane >> shift) == g) gkey = 0;
     }
+    if (q.lanes_shift >= 0) {
+      if (!((live >> (lane >> shift)) & 1u)) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      if (e < q.E && !((live >> (e / q.per)) & 1u)) key[i] = 0;
+        for (int i = 0; i < NV; ++i) key[i] = 0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = e0 + i;
+        if (e < q.E && !((live >> (e / q.per)) & 1u)) key[i] = 0;
+      }
     }
   }
 
-  // the k largest; lane j keeps the j-th id
+  // the k largest; lane j keeps the j-th id. Only the winning lane's maximum changes.
   int mine = 0;
+  uint32_t b = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) b = max(b, key[i]);
   for (int j = 0; j < q.k; ++j) {
-    uint32_t b = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) b = max(b, key[i]);
     const uint32_t w = __reduce_max_sync(kAll, b);
-    int e = 0x7fffffff;
+    const int win = __ffs(__ballot_sync(kAll, b == w)) - 1;
+    int at = 0;
+    if (lane == win) {
 #pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
-      if (key[i] == w) e = lane + 32 * i;
-    e = __reduce_min_sync(kAll, e);
+      for (int i = NV - 1; i >= 0; --i)
+        if (key[i] == w) at = i;
+      b = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (e == lane + 32 * i) key[i] = 0;
-    if (lane == j) mine = e;
+      for (int i = 0; i < NV; ++i) {
+        if (i == at) key[i] = 0;
+        b = max(b, key[i]);
+      }
+    }
+    at = __shfl_sync(kAll, at, win);
+    if (lane == j) mine = win * NV + at;
   }
 
   // gates from the scores without the bias, one lane per slot
@@ -192,7 +303,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     const float mc = warp_max(l);
     w = l > -INFINITY ? expf(l - mc) : 0.f;
   } else {
-    w = l > -INFINITY ? expf(l - m) / z : 0.f;
+    w = l > -INFINITY ? expf(l - m) * inv_z : 0.f;
   }
   if (q.renorm) {
     const float sum = warp_sum(w);
@@ -209,51 +320,38 @@ __global__ void __launch_bounds__(32 * kWarps)
 //   sigmoid, renormalised   scale w_j (1 - s_j) (dg_j - sum_S w dg)
 //   sigmoid                 scale s_j (1 - s_j) dg_j
 //   softmax                 scale s_e ([e in S] dg_e - sum_S s dg)       for every expert e
-// Slot j's value d_j lives in lane j; the row is written once, zeros included.
+// The whole row is written first (zeros, or the dense part), then lane j puts slot j's value
+// in its place.
 template <int NV, typename LT, typename DT>
 __global__ void __launch_bounds__(32 * kWarps)
     route_bwd_kernel(const Rule q, const LT* __restrict__ logits,
                      const int32_t* __restrict__ topk_idx, const float* __restrict__ dgates,
-                     DT* __restrict__ dlogits) {
+                     DT* dlogits) {
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= q.T) return;
   const LT* row = logits + (size_t)t * q.E;
   DT* out = dlogits + (size_t)t * q.E;
+  const int e0 = lane * NV;
 
   int id = lane < q.k ? topk_idx[(size_t)t * q.k + lane] : -1;
   if (id < 0 || id >= q.E) id = -1;
   const float dg = id >= 0 ? q.scale * dgates[(size_t)t * q.k + lane] : 0.f;
   const float l = id >= 0 ? clean(load(row + id)) : -INFINITY;
 
-  const bool dense = !q.sigmoid && !q.renorm;
-  float d;              // lane j: the gradient of slot j's expert (dense: its own part)
-  float p[NV];          // dense: s_e
-  float dot = 0.f;
-  if (dense) {
+  float d;              // lane j: the gradient of slot j's expert
+  float p[NV];
+  if (!q.sigmoid && !q.renorm) {
+    load_row<NV>(row, e0, q.E, q.vec, -INFINITY, p);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      p[i] = e < q.E ? clean(load(row + e)) : -INFINITY;
-    }
-    float m = p[0];
-#pragma unroll
-    for (int i = 1; i < NV; ++i) m = fmaxf(m, p[i]);
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.f;
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      p[i] = expf(p[i] - m);
-      z += p[i];
-    }
-    z = warp_sum(z);
-    if (!(z > 0.f)) z = 1.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) p[i] = p[i] / z;
-    const float s = l > -INFINITY ? expf(l - m) / z : 0.f;
-    dot = warp_sum(s > 0.f ? s * dg : 0.f);   // a gate of 0 takes no part, whatever its dg
+    for (int i = 0; i < NV; ++i) p[i] = clean(p[i]);
+    float m, inv_z;
+    warp_softmax<NV>(p, m, inv_z);
+    const float s = l > -INFINITY ? expf(l - m) * inv_z : 0.f;
+    const float dot = warp_sum(s > 0.f ? s * dg : 0.f);   // a gate of 0 takes no part, whatever its dg
     d = s > 0.f ? s * (dg - dot) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) p[i] = -p[i] * dot;
   } else {
     float w, part = 1.f;
     if (q.sigmoid) {
@@ -271,22 +369,12 @@ __global__ void __launch_bounds__(32 * kWarps)
       d = w * dg;
     }
     d = w > 0.f ? d * part : 0.f;
-  }
-
 #pragma unroll
-  for (int i = 0; i < NV; ++i) p[i] = dense ? -p[i] * dot : 0.f;
-  for (int j = 0; j < q.k; ++j) {
-    const int e = __shfl_sync(kAll, id, j);
-    const float v = __shfl_sync(kAll, d, j);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (e == lane + 32 * i) p[i] = v;
+    for (int i = 0; i < NV; ++i) p[i] = 0.f;
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    if (e < q.E) store(out + e, p[i]);
-  }
+  store_row<NV>(out, e0, q.E, q.vec, p);
+  __syncwarp();   // orders the row's stores before the slots'
+  if (id >= 0) store(out + id, d);
 }
 
 template <typename LT, int NV>
@@ -304,16 +392,21 @@ void launch_bwd(const Rule& q, const void* logits, const int32_t* idx, const flo
       q, static_cast<const LT*>(logits), idx, dg, static_cast<DT*>(dl));
 }
 
-// Registers per lane: the smallest of the built sizes that holds E / 32 logits.
+// Logits per lane: the smallest of the built widths that holds a row in 32 lanes.
+int lane_width(int E) {
+  const int nv = (E + 31) / 32;
+  return nv <= 2 ? nv : nv <= 4 ? 4 : nv <= 8 ? 8 : nv <= 12 ? 12 : 16;
+}
 template <class F>
 void by_width(int E, F f) {
-  const int nv = (E + 31) / 32;
-  if (nv <= 1) f(std::integral_constant<int, 1>{});
-  else if (nv <= 2) f(std::integral_constant<int, 2>{});
-  else if (nv <= 4) f(std::integral_constant<int, 4>{});
-  else if (nv <= 8) f(std::integral_constant<int, 8>{});
-  else if (nv <= 12) f(std::integral_constant<int, 12>{});
-  else f(std::integral_constant<int, 16>{});
+  switch (lane_width(E)) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    case 8: f(std::integral_constant<int, 8>{}); break;
+    case 12: f(std::integral_constant<int, 12>{}); break;
+    default: f(std::integral_constant<int, 16>{}); break;
+  }
 }
 
 bool is_type(mok_out_dtype t) { return t == MOK_OUT_BF16 || t == MOK_OUT_F32; }
@@ -330,8 +423,19 @@ bool make_rule(const mok_routing* r, int T, Rule* q) {
   if (!std::isfinite(r->scale)) return false;
   *q = Rule{T, r->E, r->k, r->groups, r->E / r->groups, r->top_groups,
             r->score == MOK_SCORE_SIGMOID, r->group_score == MOK_GROUP_TOP2, r->renormalize != 0,
-            r->scale};
+            false, -1, r->scale};
+  const int nv = lane_width(r->E);
+  if (q->per % nv == 0)
+    for (int s = 0; s <= 5; ++s)
+      if (q->per / nv == 1 << s) q->lanes_shift = s;
   return true;
+}
+// Vector accesses to the rows of [T][E]: whole lanes only, aligned to the widest power of
+// two that divides a lane's bytes (at most 16).
+bool rows_vectorize(int E, const void* p, mok_out_dtype type) {
+  const int nv = lane_width(E), es = type == MOK_OUT_BF16 ? 2 : 4;
+  const int width = std::min(16, (nv * es) & -(nv * es));
+  return E % nv == 0 && (long long)E * es % width == 0 && aligned_to(p, width);
 }
 
 }  // namespace
@@ -348,6 +452,7 @@ extern "C" mok_status mok_route(const mok_routing* rule, int T, const void* logi
   if (!aligned_to(logits, logits_type == MOK_OUT_BF16 ? 2 : 4) || !aligned_to(bias, 4) ||
       !aligned_to(topk_idx, 4) || !aligned_to(gates, 4))
     return MOK_ERR_INVALID_ARG;
+  q.vec = rows_vectorize(q.E, logits, logits_type);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_width(q.E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
@@ -372,6 +477,7 @@ extern "C" mok_status mok_route_bwd(const mok_routing* rule, int T, const void* 
   if (!aligned_to(logits, logits_type == MOK_OUT_BF16 ? 2 : 4) || !aligned_to(topk_idx, 4) ||
       !aligned_to(dgates, 4) || !aligned_to(dlogits, dlogits_type == MOK_OUT_BF16 ? 2 : 4))
     return MOK_ERR_INVALID_ARG;
+  q.vec = rows_vectorize(q.E, logits, logits_type) && rows_vectorize(q.E, dlogits, dlogits_type);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_width(q.E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;

@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from . import mok
-from .layer import _dev, _result_code
+from .layer import _dev, _on_current_stream, _result_code
 
 
 def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
@@ -24,7 +24,5 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
     if y is None:
         y = torch.empty_like(x)
     py = _dev(y, "y", dt, n)
-    with torch.cuda.device(x.device):
-        mok.mok_dropout(px, pa, py, n, p, seed, offset, code,
-                        torch.cuda.current_stream().cuda_stream)
+    _on_current_stream(x.get_device(), mok.mok_dropout, px, pa, py, n, p, seed, offset, code)
     return y

@@ -47,6 +47,15 @@ def _result_code(dtype, name: str) -> int:
     return _RESULT_CODES[dtype]
 
 
+def _on_current_stream(index: int, fn, *args):
+    """``fn(*args, stream)`` with CUDA device ``index`` current and its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        return fn(*args, stream)
+    with torch.cuda.device(index):
+        return fn(*args, stream)
+
+
 class MoELayer:
     """One MoE SwiGLU layer of fixed dims on one CUDA device."""
 

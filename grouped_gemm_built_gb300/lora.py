@@ -7,13 +7,15 @@ from typing import Optional
 import torch
 
 from . import mok
-from .layer import _dev, _result_code
+from .layer import _dev, _on_current_stream, _result_code
 
 
 class AdaptedLinear:
     """``y = x W + scale[a] (x A_a^T) B_a`` with ``a = ids[t]`` for each row t of x: one frozen
     projection W [K,N], n adapters A [n,r,K] and B [n,r,N] (bf16), scale [n] fp32. The object
     keeps the tensors, not copies: updated weights are what the next call reads."""
+
+    _sized = (-1, None, None)     # rows of the last call, and its dims and buffer sizes
 
     def __init__(self, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor):
         for name, t, nd in (("W", W, 2), ("A", A, 3), ("B", B, 3)):
@@ -36,8 +38,10 @@ class AdaptedLinear:
         self._dims(1)           # checks the sizes
 
     def _dims(self, T):
-        d = mok.MokLoraDims(T=T, K=self.K, N=self.N, n=self.n, r=self.r)
-        return d, mok.mok_lora_get_sizes(d)
+        if self._sized[0] != T:
+            d = mok.MokLoraDims(T=T, K=self.K, N=self.N, n=self.n, r=self.r)
+            self._sized = (T, d, mok.mok_lora_get_sizes(d))
+        return self._sized[1:]
 
     def _rows(self, x, ids, x_ad):
         if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != self.K:
@@ -58,11 +62,10 @@ class AdaptedLinear:
         T, px, pi, pa = self._rows(x, ids, x_ad)
         code = _result_code(out, "y")
         dims, sizes = self._dims(T)
-        with torch.cuda.device(self.device):
-            y = torch.empty((T, self.N), dtype=out, device=self.device)
-            saved = self._scratch(sizes.saved_bytes)
-            mok.mok_lora_fwd(dims, self.w, px, pa, pi, y.data_ptr(), code, saved.data_ptr(),
-                             self._status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        y = torch.empty((T, self.N), dtype=out, device=self.device)
+        saved = self._scratch(sizes.saved_bytes)
+        _on_current_stream(x.get_device(), mok.mok_lora_fwd, dims, self.w, px, pa, pi, y.data_ptr(),
+                           code, saved.data_ptr(), self._status.data_ptr())
         return y, saved
 
     def backward(self, x: torch.Tensor, ids: torch.Tensor, saved: torch.Tensor,
@@ -75,22 +78,22 @@ class AdaptedLinear:
         dims, sizes = self._dims(T)
         ps = _dev(saved, "saved", torch.uint8, sizes.saved_bytes)
         pdy = _dev(dY, "dY", torch.bfloat16, T * self.N)
-        with torch.cuda.device(self.device):
-            def new(*shape):
-                return torch.empty(shape, dtype=out, device=self.device)
-            g = {"dX": new(T, self.K), "dA": new(self.n, self.r, self.K),
-                 "dB": new(self.n, self.r, self.N)}
-            if x_ad is not None:
-                g["dXa"] = new(T, self.K)
-            ws = self._scratch(sizes.workspace_bytes)
-            mok.mok_lora_bwd(dims, self.w, px, pa, pi, ps, pdy, g["dX"].data_ptr(),
-                             g["dXa"].data_ptr() if x_ad is not None else None,
-                             g["dA"].data_ptr(), g["dB"].data_ptr(), code, ws.data_ptr(),
-                             self._status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+
+        def new(*shape):
+            return torch.empty(shape, dtype=out, device=self.device)
+
+        g = {"dX": new(T, self.K), "dA": new(self.n, self.r, self.K),
+             "dB": new(self.n, self.r, self.N)}
+        if x_ad is not None:
+            g["dXa"] = new(T, self.K)
+        ws = self._scratch(sizes.workspace_bytes)
+        _on_current_stream(x.get_device(), mok.mok_lora_bwd, dims, self.w, px, pa, pi, ps, pdy,
+                           g["dX"].data_ptr(), g["dXa"].data_ptr() if x_ad is not None else None,
+                           g["dA"].data_ptr(), g["dB"].data_ptr(), code, ws.data_ptr(),
+                           self._status.data_ptr())
         return g
 
     def status(self) -> int:
         """Waits for the current stream; 0, or MOK_ERR_TIMEOUT after a device wait expired."""
-        with torch.cuda.device(self.device):
-            return mok.mok_lora_get_status(self._status.data_ptr(),
-                                           torch.cuda.current_stream().cuda_stream)
+        return _on_current_stream(self._status.get_device(), mok.mok_lora_get_status,
+                                  self._status.data_ptr())

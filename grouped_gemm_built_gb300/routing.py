@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import mok
-from .layer import _dev, _result_code
+from .layer import _dev, _on_current_stream, _result_code
 
 
 class Routing:
@@ -51,9 +51,8 @@ class Routing:
         pb = _dev(bias, "bias", torch.float32, self.E, optional=True)
         idx = torch.empty((T, self.k), dtype=torch.int32, device=logits.device)
         gates = torch.empty((T, self.k), dtype=torch.float32, device=logits.device)
-        with torch.cuda.device(logits.device):
-            mok.mok_route(self.rule, T, pl, code, pb, idx.data_ptr(), gates.data_ptr(),
-                          torch.cuda.current_stream().cuda_stream)
+        _on_current_stream(logits.get_device(), mok.mok_route, self.rule, T, pl, code, pb,
+                           idx.data_ptr(), gates.data_ptr())
         return idx, gates
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, dgates: torch.Tensor,
@@ -66,7 +65,6 @@ class Routing:
         pi = _dev(topk_idx, "topk_idx", torch.int32, T * self.k)
         pd = _dev(dgates, "dgates", torch.float32, T * self.k)
         out = torch.empty((T, self.E), dtype=dtype, device=logits.device)
-        with torch.cuda.device(logits.device):
-            mok.mok_route_bwd(self.rule, T, pl, code, pi, pd, out.data_ptr(), dcode,
-                              torch.cuda.current_stream().cuda_stream)
+        _on_current_stream(logits.get_device(), mok.mok_route_bwd, self.rule, T, pl, code, pi, pd,
+                           out.data_ptr(), dcode)
         return out
