@@ -46,9 +46,9 @@ constexpr int BM = 128;                 // rows of a tile (TMEM lanes)
 constexpr int BK = 64;                  // contraction elements per pipeline stage
 constexpr int A_BYTES = BM * BK * 2;    // 16 KB: 128 rows x 128 bytes
 constexpr int kThreads = 192;           // producer warp, MMA warp, four epilogue warps
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 16;
 constexpr int kStagingBox = 4096;       // 32 rows x 128 bytes, one epilogue store
-constexpr int kBarBytes = 256;
+constexpr int kBarBytes = 512;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr size_t kMaxSmem = 227 * 1024;
 
@@ -62,9 +62,10 @@ struct Slot {
 __device__ __forceinline__ void flag_timeout(uint32_t* status) {
   if (status != nullptr) atomicOr(status, kErrTimeout);
 }
-// mbar_wait with the deadline taken only when the first try fails
+// mbar_wait whose deadline is taken only when the wait turns out long
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait(bar, parity, globaltimer_ns() + kTimeoutNs);
 }
 
@@ -82,6 +83,20 @@ __device__ __forceinline__ void umma_bf16_rows(uint32_t tmem_d, uint64_t adesc, 
       "r"(off.w)
       : "memory");
 }
+// The same for an SM pair (M = 256): words 0-3 are the even CTA's lanes, 4-7 the odd one's.
+__device__ __forceinline__ void umma_bf16_rows_pair(uint32_t tmem_d, uint64_t adesc,
+                                                    uint64_t bdesc, uint32_t idesc,
+                                                    const uint4 off0, const uint4 off1,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, "
+      "%12}, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(off0.x), "r"(off0.y), "r"(off0.z),
+      "r"(off0.w), "r"(off1.x), "r"(off1.y), "r"(off1.z), "r"(off1.w)
+      : "memory");
+}
 // 3-D tiled load: c0 innermost (elements), then c1, c2.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar,
                                             int32_t c0, int32_t c1, int32_t c2) {
@@ -90,6 +105,23 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
+}
+// ... completing on an mbarrier of either CTA of a pair (bar: from mapa_rank).
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar,
+                                                 int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+// Programmatic dependent launch: let the next kernel of the stream start its own set-up, and
+// wait until the kernels before this one have finished and their writes are visible.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_prerequisites() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 // 16 consecutive TMEM columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
@@ -141,14 +173,15 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier area");
 
-__device__ __forceinline__ void init_bars(Bars* b) {
+// pair: one arrival per epilogue warp of both CTAs hands an accumulator back
+__device__ __forceinline__ void init_bars(Bars* b, bool pair = false) {
   for (int s = 0; s < kMaxStages; ++s) {
     mbar_init(&b->full[s], 1);
     mbar_init(&b->empty[s], 1);
   }
   for (int a = 0; a < 2; ++a) {
     mbar_init(&b->acc_full[a], 1);
-    mbar_init(&b->acc_empty[a], 128);
+    mbar_init(&b->acc_empty[a], pair ? 8 : 128);
   }
   mbar_init(&b->drain, 1);
   b->abort = 0;
@@ -171,7 +204,8 @@ struct Ring {
   }
 };
 
-// Producer: waits until the stage is free and announces the bytes that will land in it.
+// Producer: waits until the stage is free and announces the bytes that will land in it
+// (0: another CTA announces them).
 __device__ __forceinline__ bool open_stage(Bars* b, const Ring& r, uint32_t bytes,
                                            uint32_t* status) {
   if (b->abort) return false;
@@ -180,7 +214,7 @@ __device__ __forceinline__ bool open_stage(Bars* b, const Ring& r, uint32_t byte
     b->abort = 1;
     return false;
   }
-  mbar_arrive_expect_tx(&b->full[r.stage], bytes);
+  if (bytes) mbar_arrive_expect_tx(&b->full[r.stage], bytes);
   return true;
 }
 __device__ __forceinline__ bool await_stage(Bars* b, const Ring& r, uint32_t* status) {
@@ -200,8 +234,10 @@ __device__ void drain_copies(Bars* b, const Ring& r) {
     wait_bar(&b->full[s], last & 1);
   }
 }
+template <bool PAIR>
 __device__ void drain_mmas(Bars* b) {
-  umma_commit(&b->drain);
+  if constexpr (PAIR) umma_commit_pair(&b->drain);
+  else umma_commit(&b->drain);
   wait_bar(&b->drain, 0);
 }
 
@@ -271,7 +307,7 @@ __device__ void find_slots(TileSlots& s, int et, const int32_t* ids, int n, int 
 // columns: cols / rp adapters side by side, each rp columns wide.
 struct ShrinkParams {
   int T, n, r, rp, nb;
-  int kiters, split, cy, cols, stages, stage_bytes;
+  int kiters, split, cy, cols, stages, a_bytes, stage_bytes;
   const int32_t* ids;
   const float* scale;
   uint8_t* uq;        // [T][nb] blocks of 128 bytes
@@ -298,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int m = (int)(blockIdx.x / p.split) / p.cy;
   const int row0 = m * BM;
 
+  launch_dependents();
   if (threadIdx.x == 0) {
     init_bars(bars);
     tma_prefetch_desc(&xmap);
@@ -331,12 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       if (lane == 0) {
         for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-          if (!open_stage(bars, ring, A_BYTES + ns * p.rp * 128, p.status)) break;
+          if (!open_stage(bars, ring, p.a_bytes + ns * p.rp * 128, p.status)) break;
           uint8_t* sa = smem + ring.stage * p.stage_bytes;
           uint64_t* bar = &bars->full[ring.stage];
           tma_load_2d(sa, &xmap, bar, kb * BK, row0);
           for (int j = 0; j < ns; ++j)   // rp rows of 128 bytes per adapter (zeros past rank r)
-            tma_load_3d(sa + A_BYTES + j * p.rp * 128, &amap, bar, kb * BK, 0, ts.slot_id[s0 + j]);
+            tma_load_3d(sa + p.a_bytes + j * p.rp * 128, &amap, bar, kb * BK, 0, ts.slot_id[s0 + j]);
         }
       }
       __syncwarp();
@@ -351,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16(tmem, umma_desc_sw128(sa + kk * 32, 16, 1024),
-                      umma_desc_sw128(sa + A_BYTES + kk * 32, 16, 1024), idesc,
+                      umma_desc_sw128(sa + p.a_bytes + kk * 32, 16, 1024), idesc,
                       (kb > kb0 || kk > 0) ? 1u : 0u);
           umma_commit(&bars->empty[ring.stage]);
         }
@@ -411,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (bars->abort) {
     if (threadIdx.x == 0) drain_copies(bars, ring);
-    if (threadIdx.x == 32) drain_mmas(bars);
+    if (threadIdx.x == 32) drain_mmas<false>(bars);
   }
   tc_fence_before();
   __syncthreads();
@@ -419,19 +456,142 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, p.cols);
   }
+  if (threadIdx.x == 0) wait_prerequisites();   // what waits for this kernel waits for them too
+}
+
+// The same for a few rows: CTA t takes row t alone, its warps share the contraction in pieces
+// of 256 elements, 16 ranks at a time (16 independent 16-byte loads per lane, so a row costs
+// about one trip to memory), on the CUDA cores; no MMA tile to fill, no ring to start. The
+// last CTAs list the row tiles' adapters for proj_kernel.
+constexpr int kRowThreads = 1024;
+constexpr int kRowMaxPieces = 64;    // contraction up to 16384
+constexpr int kRowsMost = 192;       // rows of a batch that goes this way
+
+struct ShrinkRowsParams {
+  int T, C, n, r, nb;
+  const __nv_bfloat16* x;      // [T][C]
+  const __nv_bfloat16* w;      // [n][r][C]
+  const int32_t* ids;
+  const float* scale;
+  uint8_t* uq;
+  int32_t* n_slots;
+  Slot* slots;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 q, float* v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRowsParams p) {
+  __shared__ __align__(16) TileSlots ts;
+  __shared__ float part[kRowMaxPieces][16];
+  launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if ((int)blockIdx.x >= p.T) {
+    const int m = (int)blockIdx.x - p.T;
+    find_slots(ts, tid < BM ? tid : -1, p.ids, p.n, p.T, m * BM);
+    if (tid == 0) p.n_slots[m] = ts.count;
+    if (tid < ts.count) {
+      Slot s;
+      s.id = ts.slot_id[tid];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) s.off[w] = ts.off[tid][w];
+      s.pad[0] = s.pad[1] = s.pad[2] = 0;
+      p.slots[(size_t)m * BM + tid] = s;
+    }
+    if (tid == 0) wait_prerequisites();   // what waits for this kernel waits for them too
+    return;
+  }
+  const int t = blockIdx.x;
+  const int id = p.ids[t];
+  if (id < 0 || id >= p.n) return;
+  const __nv_bfloat16* x = p.x + (size_t)t * p.C;
+  const __nv_bfloat16* w = p.w + (size_t)id * p.r * p.C;
+  const int pieces = (p.C + 255) / 256;
+  const float scale = p.scale[id];
+  for (int i0 = 0; i0 < p.r; i0 += 16) {
+    for (int c = warp; c < pieces; c += kRowThreads / 32) {
+      const int k = c * 256 + lane * 8;
+      uint4 wq[16];
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      const uint4 xq = k < p.C ? *reinterpret_cast<const uint4*>(x + k) : none;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        wq[i] = k < p.C && i0 + i < p.r
+                    ? *reinterpret_cast<const uint4*>(w + (size_t)(i0 + i) * p.C + k) : none;
+      float xv[8], sum[16];
+      unpack8(xq, xv);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float wv[8];
+        unpack8(wq[i], wv);
+        sum[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[i] = fmaf(xv[j], wv[j], sum[i]);
+      }
+      // 16 sums over the 32 lanes: halve the sums with every step, so that lane l ends with
+      // sum l / 2 (both lanes of a pair the same)
+#pragma unroll
+      for (int h = 8; h > 0; h >>= 1) {
+        const bool up = lane & (2 * h);
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+          const float give = up ? sum[i] : sum[i + h];
+          const float keep = up ? sum[i + h] : sum[i];
+          sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * h);
+        }
+      }
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+      if ((lane & 1) == 0) part[c][lane >> 1] = sum[0];
+    }
+    __syncthreads();
+    if (tid < 8) {
+      float v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j] = 0.f;
+        for (int c = 0; c < pieces; ++c) v[j] += part[c][2 * tid + j];
+        // ranks past r are padding: 0 also where a row with an inf met their zero fill
+        v[j] = i0 + 2 * tid + j < p.r ? scale * v[j] : 0.f;
+      }
+      uint32_t hi, lo;
+      split_pair(v[0], v[1], hi, lo);
+      uint8_t* dst = p.uq + ((size_t)t * p.nb + i0 / 32) * 128 + (i0 % 32 + 2 * tid) * 2;
+      *reinterpret_cast<uint32_t*>(dst) = hi;
+      *reinterpret_cast<uint32_t*>(dst + 64) = lo;
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------ projection
-// out tile [128][NT] = X W (TRANS: X W^T) + the adapters' steps. split == 1: persistent, one
-// CTA per tile at a time, two accumulators so that a tile's epilogue overlaps the next
-// tile's MMAs, results staged in shared memory and stored by TMA. split > 1 (too few tiles
-// for the SMs): a cluster of `split` CTAs shares one tile's contraction, W's and the
-// adapters' steps alike, and the partial sums meet in rank order through distributed shared
-// memory.
+// out tile [128][NT] = X W (TRANS: X W^T) + the adapters' steps. Three forms:
+//   PAIR       large batches: the two CTAs of a cluster share M = 256 MMAs, each with its own
+//              128 rows of X and half of the tile's columns of W, which takes a third off the
+//              bytes a tile moves into its SM's shared memory (what bounds single CTAs);
+//   split = 1  one CTA per tile;
+//   split > 1  too few tiles for the SMs: a cluster of `split` CTAs shares one tile's
+//              contraction, W's and the adapters' steps alike, and the partial sums meet in
+//              rank order through distributed shared memory.
+// The first two are persistent, with two accumulators, so that a tile's epilogue overlaps the
+// next tile's MMAs; results are staged in shared memory and stored by TMA.
+//
+// The adapters' part of a tile goes 32 ranks (a block of u) at a time. Its first stage holds
+// that block of u for the tile's rows, and B rows of as many adapters as fit; further stages
+// hold B rows only. The stage with u is handed back last, so a group is at most stages - 1
+// stages long; a longer list loads u again for its next group.
+//
+// Launched with programmatic dependence on shrink_kernel: the steps over W need nothing from
+// it, so only the adapters' part waits.
 struct ProjParams {
   int T, out_cols, n;
   int kiters;               // steps over W (0: the adapters' part alone)
-  int NT, n_tiles, m_tiles, split, stages, stage_bytes;
+  int NT, n_tiles, m_tiles, split, stages, a_bytes, stage_bytes;
   int rp, nb, rb;           // padded rank, 32-rank blocks, ranks per adapter step
   int out_bf16;
   const int32_t* ids;
@@ -441,7 +601,54 @@ struct ProjParams {
   uint32_t* status;
 };
 
-template <bool TRANS>
+// The adapters that a CTA (or pair) runs for one tile, in a fixed order, 32 at a time in the
+// lanes of a warp. PAIR: the slots of the even row tile, then the odd one's; split: every
+// split-th slot from rank q.
+template <bool PAIR>
+struct SlotList {
+  const Slot* base0;
+  const Slot* base1;
+  int n0, count, q, split, window;
+  int id;
+  uint4 off;
+  __device__ void open(const ProjParams& p, int m, int rank) {   // m: (first) row tile
+    base0 = p.slots + (size_t)m * BM;
+    base1 = base0 + BM;
+    n0 = p.n_slots[m];
+    count = n0;
+    q = 0;
+    split = 1;
+    if (PAIR) {
+      if (m + 1 < p.m_tiles) count += p.n_slots[m + 1];
+    } else {
+      q = rank;
+      split = p.split;
+      count = n0 > q ? (n0 - q + split - 1) / split : 0;
+    }
+    window = -1;
+    if (count > 0) load(0);
+  }
+  __device__ void load(int w) {
+    window = w;
+    const int i = 32 * w + (int)(threadIdx.x & 31);
+    if (i >= count) return;
+    const Slot* s = PAIR ? (i < n0 ? base0 + i : base1 + (i - n0)) : base0 + (q + i * split);
+    id = s->id;
+    off = make_uint4(s->off[0], s->off[1], s->off[2], s->off[3]);
+  }
+  // whole warp: adapter and lane mask of entry i
+  __device__ int get_id(int i) {
+    if (i >> 5 != window) load(i >> 5);
+    return __shfl_sync(0xffffffffu, id, i & 31);
+  }
+  __device__ uint4 get_off(int i) {
+    if (i >> 5 != window) load(i >> 5);
+    return make_uint4(__shfl_sync(0xffffffffu, off.x, i & 31), __shfl_sync(0xffffffffu, off.y, i & 31),
+                      __shfl_sync(0xffffffffu, off.z, i & 31), __shfl_sync(0xffffffffu, off.w, i & 31));
+  }
+};
+
+template <bool TRANS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     proj_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                 const __grid_constant__ CUtensorMap umap, const __grid_constant__ CUtensorMap emap,
@@ -454,116 +661,214 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(staging + (p.split == 1 ? 8 * kStagingBox : 0));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = (int)(blockIdx.x % p.split);
-  const int tiles = p.m_tiles * p.n_tiles;
-  const int t0 = (int)(blockIdx.x / p.split), tstep = (int)(gridDim.x / p.split);
-  const int kb0 = (int)((long long)p.kiters * q / p.split);
-  const int kb1 = (int)((long long)p.kiters * (q + 1) / p.split);
+  const int csize = PAIR ? 2 : p.split;
+  const int q = (int)(blockIdx.x % csize);                  // rank in the cluster
+  const int m_step = PAIR ? 2 : 1;                          // row tiles of a tile
+  const int tiles = (p.m_tiles + m_step - 1) / m_step * p.n_tiles;
+  const int t0 = (int)(blockIdx.x / csize), tstep = (int)(gridDim.x / csize);
+  const int kb0 = PAIR ? 0 : (int)((long long)p.kiters * q / p.split);
+  const int kb1 = PAIR ? p.kiters : (int)((long long)p.kiters * (q + 1) / p.split);
+  const int nc = PAIR ? p.NT / 2 : p.NT;                    // columns this CTA loads
   const uint32_t tmem_cols = p.NT <= 64 ? 128 : p.NT <= 128 ? 256 : 512;   // two accumulators
+  const int per_stage = 64 / p.rb;                          // adapters of an adapter stage
+  const int group = p.stages - 1;
 
   if (threadIdx.x == 0) {
-    init_bars(bars);
+    init_bars(bars, PAIR);
     tma_prefetch_desc(&xmap);
     tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&umap);
+    tma_prefetch_desc(&emap);
   }
-  if (warp == 1) tmem_alloc(&bars->tmem, tmem_cols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(&bars->tmem, tmem_cols);
+    else tmem_alloc(&bars->tmem, tmem_cols);
+  }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();   // the other CTA's barriers are initialised
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
+    // ---- producer: the whole warp walks the adapter list, lane 0 loads
     Ring ring(p.stages);
+    SlotList<PAIR> list;
     bool ok = true;
-    for (int tile = t0; ok && tile < tiles; tile += tstep) {
-      const int row0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * p.NT;
-      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-        ok = open_stage(bars, ring, A_BYTES + p.NT * 128, p.status);
-        if (!ok) break;
-        uint8_t* sa = smem + ring.stage * p.stage_bytes;
-        uint64_t* bar = &bars->full[ring.stage];
-        tma_load_2d(sa, &xmap, bar, kb * BK, row0);
-        if (TRANS) {   // NT rows of W, contraction along the row (K-major)
-          tma_load_2d(sa + A_BYTES, &wmap, bar, kb * BK, n0);
-        } else {       // 64 rows of W, 64-column chunks (MN-major)
-          for (int j = 0; j < p.NT / 64; ++j)
-            tma_load_2d(sa + A_BYTES + j * 64 * 128, &wmap, bar, n0 + j * 64, kb * BK);
-        }
-      }
-      if (!ok || p.n_slots == nullptr) continue;
-      const int ns = p.n_slots[row0 / BM];
-      const Slot* sl = p.slots + (size_t)(row0 / BM) * BM;
-      for (int s = q; ok && s < ns; s += p.split) {
-        const int id = sl[s].id;
-        for (int b = 0; b < p.nb; ++b, ring.next()) {
-          ok = open_stage(bars, ring, A_BYTES + p.NT * p.rb * 2, p.status);
+    // one box of X's (or u's) rows, then the columns of W (or B) for this CTA
+    auto load2 = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
+      if constexpr (PAIR) tma_load_2d_pair(dst, m, mapa_rank(&bars->full[ring.stage], 0), c0, c1);
+      else tma_load_2d(dst, m, &bars->full[ring.stage], c0, c1);
+    };
+    auto load3 = [&](void* dst, const CUtensorMap* m, int c0, int c1, int c2) {
+      if constexpr (PAIR) tma_load_3d_pair(dst, m, mapa_rank(&bars->full[ring.stage], 0), c0, c1, c2);
+      else tma_load_3d(dst, m, &bars->full[ring.stage], c0, c1, c2);
+    };
+    auto open = [&](uint32_t bytes) {   // PAIR: rank 0 announces both CTAs' bytes
+      return open_stage(bars, ring, PAIR ? (q == 0 ? 2 * bytes : 0) : bytes, p.status);
+    };
+    for (int tile = t0; tile < tiles; tile += tstep) {
+      const int m = tile / p.n_tiles * m_step;
+      const int row0 = (m + (PAIR ? q : 0)) * BM;
+      const int n0 = tile % p.n_tiles * p.NT + (PAIR ? q * nc : 0);
+      if (p.n_slots != nullptr && tile != t0) list.open(p, m, q);   // ahead of the steps over W
+      if (lane == 0) {
+        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+          ok = open(p.a_bytes + nc * 128);
           if (!ok) break;
           uint8_t* sa = smem + ring.stage * p.stage_bytes;
-          uint64_t* bar = &bars->full[ring.stage];
-          tma_load_2d(sa, &umap, bar, b * 64, row0);
-          for (int j = 0; j < p.NT / 64; ++j)   // rb ranks x 64 columns (zeros past rank r)
-            tma_load_3d(sa + A_BYTES + j * p.rb * 128, &emap, bar, n0 + j * 64, b * 32, id);
-        }
-      }
-    }
-    if (bars->abort) drain_copies(bars, ring);
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_bf16(BM, p.NT, false, !TRANS);
-    const uint32_t idesc_e = idesc_bf16(BM, p.NT, false, true);
-    Ring ring(p.stages);
-    bool ok = true;
-    int local = 0;
-    for (int tile = t0; ok && tile < tiles; tile += tstep, ++local) {
-      const int acc = local & 1;
-      if (!wait_bar(&bars->acc_empty[acc], ((local >> 1) & 1) ^ 1)) {
-        flag_timeout(p.status);
-        bars->abort = 1;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem + acc * (tmem_cols / 2);
-      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-        ok = await_stage(bars, ring, p.status);
-        if (!ok) break;
-        const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16(d, umma_desc_sw128(sa + kk * 32, 16, 1024),
-                    TRANS ? umma_desc_sw128(sa + A_BYTES + kk * 32, 16, 1024)
-                          : umma_desc_sw128(sa + A_BYTES + kk * 2048, 64 * 128, 1024),
-                    idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-        umma_commit(&bars->empty[ring.stage]);
-      }
-      if (ok && p.n_slots != nullptr) {
-        const int m = tile / p.n_tiles, ns = p.n_slots[m];
-        const Slot* sl = p.slots + (size_t)m * BM;
-        for (int s = q; ok && s < ns; s += p.split) {
-          const uint4 off = make_uint4(sl[s].off[0], sl[s].off[1], sl[s].off[2], sl[s].off[3]);
-          for (int b = 0; b < p.nb; ++b, ring.next()) {
-            ok = await_stage(bars, ring, p.status);
-            if (!ok) break;
-            const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
-            for (int kk = 0; kk < p.rb / 16; ++kk) {   // hi and lo of 16 ranks, same rows of B
-              const uint64_t bd = umma_desc_sw128(sa + A_BYTES + kk * 2048, p.rb * 128, 1024);
-              // without W a row's first step starts its sum (each row is in one slot only)
-              umma_bf16_rows(d, umma_desc_sw128(sa + kk * 32, 16, 1024), bd, idesc_e, off,
-                             (p.kiters > 0 || b > 0 || kk > 0) ? 1u : 0u);
-              umma_bf16_rows(d, umma_desc_sw128(sa + 64 + kk * 32, 16, 1024), bd, idesc_e, off, 1u);
-            }
-            umma_commit(&bars->empty[ring.stage]);
+          uint8_t* sb = sa + p.a_bytes;
+          load2(sa, &xmap, kb * BK, row0);
+          if (TRANS) {   // nc rows of W, contraction along the row (K-major)
+            load2(sb, &wmap, kb * BK, n0);
+          } else {       // 64 rows of W, 64-column chunks (MN-major)
+            for (int j = 0; j < nc / 64; ++j) load2(sb + j * 64 * 128, &wmap, n0 + j * 64, kb * BK);
           }
         }
       }
-      if (ok) umma_commit(&bars->acc_full[acc]);
+      if (tile == t0) {
+        wait_prerequisites();
+        if (p.n_slots != nullptr) list.open(p, m, q);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (p.n_slots == nullptr) continue;
+      for (int b = 0; b < p.nb && ok; ++b) {
+        int in_group = 0;
+        for (int i0 = 0; i0 < list.count && ok; i0 += per_stage) {
+          const int cnt = min(per_stage, list.count - i0);
+          const bool head = in_group == 0;
+          uint8_t* sa = smem + ring.stage * p.stage_bytes;
+          if (lane == 0) {
+            ok = open((head ? p.a_bytes : 0) + cnt * nc * p.rb * 2);
+            sa = smem + ring.stage * p.stage_bytes;
+            if (ok && head) load2(sa, &umap, b * 64, row0);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          for (int j = 0; j < cnt; ++j) {
+            const int id = list.get_id(i0 + j);
+            if (lane == 0 && ok) {
+              uint8_t* sb = sa + p.a_bytes + j * nc * p.rb * 2;
+              for (int c = 0; c < nc / 64; ++c)   // rb ranks x 64 columns (zeros past rank r)
+                load3(sb + c * p.rb * 128, &emap, n0 + c * 64, b * 32, id);
+            }
+          }
+          if (lane == 0 && ok) ring.next();
+          if (++in_group == group) in_group = 0;
+        }
+      }
+      if (!ok) break;
     }
-    if (bars->abort) drain_mmas(bars);
-  } else if (warp >= 2) {
+    if (lane == 0 && bars->abort && (!PAIR || q == 0)) drain_copies(bars, ring);
+  } else if (warp == 1 && (!PAIR || q == 0)) {
+    // ---- MMA: the whole warp walks the adapter list, lane 0 issues
+    const int rows = PAIR ? 2 * BM : BM;
+    const uint32_t idesc = idesc_bf16(rows, p.NT, false, !TRANS);
+    const uint32_t idesc_e = idesc_bf16(rows, p.NT, false, true);
+    auto commit = [&](uint64_t* bar) {
+      if constexpr (PAIR) umma_commit_pair(bar);
+      else umma_commit(bar);
+    };
+    Ring ring(p.stages);
+    SlotList<PAIR> list;
+    bool ok = true;
+    int local = 0;
+    for (int tile = t0; tile < tiles; tile += tstep, ++local) {
+      const int m = tile / p.n_tiles * m_step;
+      const int acc = local & 1;
+      const uint32_t d = tmem + acc * (tmem_cols / 2);
+      if (p.n_slots != nullptr && tile != t0) list.open(p, m, q);
+      if (lane == 0) {
+        if (!wait_bar(&bars->acc_empty[acc], ((local >> 1) & 1) ^ 1)) {
+          flag_timeout(p.status);
+          bars->abort = 1;
+          ok = false;
+        }
+        tc_fence_after();
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+          ok = await_stage(bars, ring, p.status);
+          if (!ok) break;
+          const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+          const uint32_t sb = sa + p.a_bytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t ad = umma_desc_sw128(sa + kk * 32, 16, 1024);
+            const uint64_t bd = TRANS ? umma_desc_sw128(sb + kk * 32, 16, 1024)
+                                      : umma_desc_sw128(sb + kk * 2048, 64 * 128, 1024);
+            const uint32_t accumulate = (kb > kb0 || kk > 0) ? 1u : 0u;
+            if constexpr (PAIR) umma_bf16_pair(d, ad, bd, idesc, accumulate);
+            else umma_bf16(d, ad, bd, idesc, accumulate);
+          }
+          commit(&bars->empty[ring.stage]);
+          ring.next();
+        }
+      }
+      if (tile == t0) {
+        wait_prerequisites();
+        if (p.n_slots != nullptr) list.open(p, m, q);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (p.n_slots != nullptr) {
+        for (int b = 0; b < p.nb && ok; ++b) {
+          int in_group = 0, head_stage = 0;
+          for (int i0 = 0; i0 < list.count && ok; i0 += per_stage) {
+            const int cnt = min(per_stage, list.count - i0);
+            if (lane == 0) {
+              ok = await_stage(bars, ring, p.status);
+              if (in_group == 0) head_stage = ring.stage;
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const uint32_t su = smem_u32(smem + head_stage * p.stage_bytes);
+            const uint32_t sb = smem_u32(smem + ring.stage * p.stage_bytes) + p.a_bytes;
+            for (int j = 0; j < cnt; ++j) {
+              const uint4 off = list.get_off(i0 + j);
+              if (lane == 0) {
+                for (int kk = 0; kk < p.rb / 16; ++kk) {   // hi and lo of 16 ranks, same rows of B
+                  const uint64_t bd =
+                      umma_desc_sw128(sb + j * nc * p.rb * 2 + kk * 2048, p.rb * 128, 1024);
+                  const uint64_t hi = umma_desc_sw128(su + kk * 32, 16, 1024);
+                  const uint64_t lo = umma_desc_sw128(su + 64 + kk * 32, 16, 1024);
+                  // without W a row's first step starts its sum (a row is in one slot only)
+                  const uint32_t first = (p.kiters > 0 || b > 0 || kk > 0) ? 1u : 0u;
+                  if constexpr (PAIR) {
+                    const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);
+                    const bool odd = i0 + j >= list.n0;
+                    umma_bf16_rows_pair(d, hi, bd, idesc_e, odd ? none : off, odd ? off : none, first);
+                    umma_bf16_rows_pair(d, lo, bd, idesc_e, odd ? none : off, odd ? off : none, 1u);
+                  } else {
+                    umma_bf16_rows(d, hi, bd, idesc_e, off, first);
+                    umma_bf16_rows(d, lo, bd, idesc_e, off, 1u);
+                  }
+                }
+              }
+            }
+            if (lane == 0) {
+              const bool last = i0 + per_stage >= list.count || in_group + 1 == group;
+              if (in_group > 0) commit(&bars->empty[ring.stage]);
+              if (last) commit(&bars->empty[head_stage]);
+              ring.next();
+            }
+            if (++in_group == group) in_group = 0;
+          }
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) commit(&bars->acc_full[acc]);
+    }
+    if (lane == 0 && bars->abort) drain_mmas<PAIR>(bars);
+  } else if (warp == 1) {
+    wait_prerequisites();
+  } else {
+    // ---- epilogue
     const int quarter = warp & 3, row = quarter * 32 + lane;
     uint8_t* box = staging + quarter * 2 * kStagingBox;
     int local = 0, stored = 0;
     for (int tile = t0; tile < tiles; tile += tstep, ++local) {
       const int acc = local & 1;
-      const int row0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * p.NT;
+      const int row0 = (tile / p.n_tiles * m_step + (PAIR ? q : 0)) * BM;
+      const int n0 = tile % p.n_tiles * p.NT;
       bool ok = !bars->abort && wait_bar(&bars->acc_full[acc], (local >> 1) & 1);
       if (!ok) {
         if (!bars->abort) flag_timeout(p.status);
@@ -578,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int id = row0 + row < p.T ? p.ids[row0 + row] : -1;
         zero = id < 0 || id >= p.n;
       }
-      if (p.split > 1) {
+      if (!PAIR && p.split > 1) {
         float* red = reinterpret_cast<float*>(smem) + row * (p.NT + 4);
         for (int c = 0; rows_here && c < p.NT; c += 32) {
           float v[32];
@@ -625,13 +930,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&bars->acc_empty[acc]);
+      if constexpr (PAIR) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_rank(&bars->acc_empty[acc], 0));
+      } else {
+        mbar_arrive(&bars->acc_empty[acc]);
+      }
     }
     if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
 
-  if (p.split > 1) {   // one tile per cluster
+  if (!PAIR && p.split > 1) {   // one tile per cluster
     cluster_sync_all();
     if (warp >= 2) {
       const int et = (int)threadIdx.x - 64, tile = t0;
@@ -657,23 +967,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();   // no rank leaves while another reads its partial tile
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();   // no copy or commit of either CTA is on its way
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, tmem_cols);
+    else tmem_dealloc(tmem, tmem_cols);
   }
 }
 
 // ------------------------------------------------------------------ row lists
-// One CTA per adapter: its rows in ascending order at rows[off[a] .. off[a] + cnt[a]), where
-// off[a] counts the rows of lower adapters. Each CTA reads all ids, so that no CTA waits for
-// another.
+// One CTA per adapter: its rows in ascending order at rows[off[a] .. off[a + 1]), where off[a]
+// counts the rows of lower adapters. Each CTA reads all ids, so that no CTA waits for another.
 constexpr int kBucketThreads = 1024;
 
 __global__ void __launch_bounds__(kBucketThreads)
-    bucket_kernel(int T, const int32_t* __restrict__ ids, int32_t* __restrict__ off,
-                  int32_t* __restrict__ cnt, int32_t* __restrict__ rows) {
+    bucket_kernel(int T, int n, const int32_t* __restrict__ ids, int32_t* __restrict__ off,
+                  int32_t* __restrict__ rows) {
   __shared__ int s_less[32], s_eq[32];
+  launch_dependents();
   const int a = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int less = 0;
   for (int t = tid; t < T; t += kBucketThreads) {
@@ -704,17 +1016,22 @@ __global__ void __launch_bounds__(kBucketThreads)
   }
   if (tid == 0) {
     off[a] = start;
-    cnt[a] = base - start;
+    if (a == n - 1) off[n] = base;
   }
 }
 
 // ------------------------------------------------------------------ weight gradients
-// out[a] [r][C] = sum over adapter a's rows t of uq[t]^T g[t]: CTA = (adapter, 128 columns,
-// share of the rows); the shares of one block of columns are the ranks of a cluster, whose
-// partial sums meet in rank order through distributed shared memory. A pass over g: memory
-// bound, so the products run on warp-level MMAs (mma.sync m16n8k16), whose operands come
-// straight from the gathered rows: 64 rows per stage, cp.async, rows past the end zero-filled
-// (both operands, so that a stale value cannot meet a zero). MT = padded rank / 16.
+// dA[a] = sum over adapter a's rows t of vq[t]^T xa[t], and dB[a] the same of uq and dY, in one
+// launch. A CTA owns 128 columns of one of the two and an equal share of the row list
+// (adapter by adapter), whatever the adapters' sizes; the `split` shares of a block of columns
+// are the ranks of a cluster. An adapter that lies inside a share is finished there. One that
+// goes on into the next ranks' shares leaves partial sums in their shared memory, which the
+// rank where it starts adds up in rank order.
+//
+// One pass over xa and dY, memory bound, so the products run on warp-level MMAs (mma.sync
+// m16n8k16), whose operands come straight from the gathered rows: 64 rows per stage,
+// cp.async, rows past an adapter's end zero-filled (both operands, so that no stale or other
+// adapter's value can meet a zero). MT = padded rank / 16.
 constexpr int kWgCols = 128;
 constexpr int kWgRows = 64;
 constexpr int kWgStages = 3;
@@ -739,14 +1056,17 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-struct WgradParams {
-  int C, r, n, ctiles, split, out_bf16;
-  const int32_t* off;
-  const int32_t* cnt;
-  const int32_t* rows;
+struct WgradSide {
   const uint8_t* uq;             // [T][nb] blocks of 128 bytes
   const __nv_bfloat16* g;        // [T][C]
   void* out;                     // [n][r][C]
+  int C, ctiles;
+};
+struct WgradParams {
+  WgradSide side[2];
+  int r, n, split, out_bf16;
+  const int32_t* off;            // [n + 1]
+  const int32_t* rows;           // [off[n]]
 };
 
 template <int MT>
@@ -756,114 +1076,182 @@ __global__ void __launch_bounds__(kWgThreads) wgrad_kernel(const WgradParams p) 
   constexpr int U_ROW = NB * 128;
   constexpr int STAGE = G_BYTES + kWgRows * U_ROW;
   constexpr int RS = kWgCols + 4;                  // floats per row of the partial sums
+  constexpr int GI = kWgRows * 16 / kWgThreads;    // 16-byte pieces per thread and stage
+  constexpr int UI = kWgRows * NB * 8 / kWgThreads;
   extern __shared__ __align__(16) uint8_t smem[];
+  float* head = reinterpret_cast<float*>(smem);    // partial sums [16 MT][RS], see below
+  uint8_t* stages = smem + 16 * MT * RS * 4;
+  float* tail = reinterpret_cast<float*>(stages);  // over the stages, when they are done
+  launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int q = (int)(blockIdx.x % p.split);
-  const int ct = (int)(blockIdx.x / p.split) % p.ctiles;
-  const int a = (int)(blockIdx.x / p.split) / p.ctiles;
+  int ct = (int)(blockIdx.x / p.split);
+  const bool second = ct >= p.side[0].ctiles;
+  if (second) ct -= p.side[0].ctiles;
+  const uint8_t* uq = second ? p.side[1].uq : p.side[0].uq;
+  const __nv_bfloat16* g = second ? p.side[1].g : p.side[0].g;
+  void* out = second ? p.side[1].out : p.side[0].out;
+  const int C = second ? p.side[1].C : p.side[0].C;
   const int c0 = ct * kWgCols;
-  const int cnt = p.cnt[a];
-  const int32_t* rows = p.rows + p.off[a];
-  const int blocks = (cnt + kWgRows - 1) / kWgRows;
-  const int b0 = (int)((long long)blocks * q / p.split);
-  const int b1 = (int)((long long)blocks * (q + 1) / p.split);
+  wait_prerequisites();
 
-  auto fetch = [&](int b) {
-    uint8_t* sg = smem + (b - b0) % kWgStages * STAGE;
-    uint8_t* su = sg + G_BYTES;
-#pragma unroll
-    for (int i = 0; i < kWgRows * 16 / kWgThreads; ++i) {
-      const int e = tid + i * kWgThreads, rr = e >> 4, ch = e & 15;
-      const int at = b * kWgRows + rr;
-      const bool on = at < cnt && c0 + ch * 8 < p.C;
-      const __nv_bfloat16* src = on ? p.g + (size_t)rows[at] * p.C + c0 + ch * 8 : p.g;
-      cp_async16(sg + rr * 256 + ((ch ^ (rr & 7)) * 16), src, on);
-    }
-#pragma unroll
-    for (int i = 0; i < kWgRows * NB * 8 / kWgThreads; ++i) {
-      const int e = tid + i * kWgThreads, rr = e / (NB * 8), ch = e % (NB * 8);
-      const int at = b * kWgRows + rr;
-      const bool on = at < cnt;
-      const uint8_t* src = on ? p.uq + (size_t)rows[at] * U_ROW + ch * 16 : p.uq;
-      cp_async16(su + rr * U_ROW + ((ch ^ (rr & 7)) * 16), src, on);
-    }
-  };
+  const int total = p.off[p.n];
+  const int r0 = (int)((long long)total * q / p.split);
+  const int r1 = (int)((long long)total * (q + 1) / p.split);
 
   float acc[MT][4][4];
+  // rows [lo, hi) of the list (one adapter) into acc
+  auto accumulate = [&](int lo, int hi) {
+    const int blocks = (hi - lo + kWgRows - 1) / kWgRows;
+    int gi[GI], ui[UI];   // rows of the pieces this thread fetches next (-1: past the end)
+    auto index = [&](int b) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
-
-#pragma unroll
-  for (int s = 0; s < kWgStages - 1; ++s) {
-    if (b0 + s < b1) fetch(b0 + s);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  for (int b = b0; b < b1; ++b) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kWgStages - 2) : "memory");
-    __syncthreads();   // stage b is in; every warp is done with the stage that is refilled next
-    if (b + kWgStages - 1 < b1) fetch(b + kWgStages - 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    const uint8_t* sg = smem + (b - b0) % kWgStages * STAGE;
-    const uint8_t* su = sg + G_BYTES;
-#pragma unroll
-    for (int k0 = 0; k0 < kWgRows; k0 += 16) {
-      uint32_t bf[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rr = k0 + ((lane >> 3) & 1) * 8 + (lane & 7);
-        const int ch = warp * 4 + h * 2 + (lane >> 4);
-        ldsm4_t(bf + 4 * h, sg + rr * 256 + ((ch ^ (rr & 7)) * 16));
+      for (int i = 0; i < GI; ++i) {
+        const int at = lo + b * kWgRows + ((tid + i * kWgThreads) >> 4);
+        gi[i] = at < hi ? p.rows[at] : -1;
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int rr = k0 + (lane >> 4) * 8 + (lane & 7);
-        const int ch = (mt >> 1) * 8 + (mt & 1) * 2 + ((lane >> 3) & 1);
-        uint32_t hi[4], lo[4];
-        ldsm4_t(hi, su + rr * U_ROW + ((ch ^ (rr & 7)) * 16));
-        ldsm4_t(lo, su + rr * U_ROW + (((ch + 4) ^ (rr & 7)) * 16));
+      for (int i = 0; i < UI; ++i) {
+        const int at = lo + b * kWgRows + (tid + i * kWgThreads) / (NB * 8);
+        ui[i] = at < hi ? p.rows[at] : -1;
+      }
+    };
+    auto fetch = [&](int b) {
+      uint8_t* sg = stages + b % kWgStages * STAGE;
+      uint8_t* su = sg + G_BYTES;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma16816(acc[mt][j], hi, bf[2 * j], bf[2 * j + 1]);
-          mma16816(acc[mt][j], lo, bf[2 * j], bf[2 * j + 1]);
+      for (int i = 0; i < GI; ++i) {
+        const int e = tid + i * kWgThreads, rr = e >> 4, ch = e & 15;
+        const bool on = gi[i] >= 0 && c0 + ch * 8 < C;
+        cp_async16(sg + rr * 256 + ((ch ^ (rr & 7)) * 16),
+                   on ? g + (size_t)gi[i] * C + c0 + ch * 8 : g, on);
+      }
+#pragma unroll
+      for (int i = 0; i < UI; ++i) {
+        const int e = tid + i * kWgThreads, rr = e / (NB * 8), ch = e % (NB * 8);
+        const bool on = ui[i] >= 0;
+        cp_async16(su + rr * U_ROW + ((ch ^ (rr & 7)) * 16),
+                   on ? uq + (size_t)ui[i] * U_ROW + ch * 16 : uq, on);
+      }
+      if (b + 1 < blocks) index(b + 1);
+    };
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
+    index(0);
+#pragma unroll
+    for (int b = 0; b < kWgStages - 1; ++b) {
+      if (b < blocks) fetch(b);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int b = 0; b < blocks; ++b) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kWgStages - 2) : "memory");
+      __syncthreads();   // stage b is in; every warp is done with the stage refilled next
+      if (b + kWgStages - 1 < blocks) fetch(b + kWgStages - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const uint8_t* sg = stages + b % kWgStages * STAGE;
+      const uint8_t* su = sg + G_BYTES;
+#pragma unroll
+      for (int k0 = 0; k0 < kWgRows; k0 += 16) {
+        uint32_t bf[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int rr = k0 + ((lane >> 3) & 1) * 8 + (lane & 7);
+          const int ch = warp * 4 + h * 2 + (lane >> 4);
+          ldsm4_t(bf + 4 * h, sg + rr * 256 + ((ch ^ (rr & 7)) * 16));
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int rr = k0 + (lane >> 4) * 8 + (lane & 7);
+          const int ch = (mt >> 1) * 8 + (mt & 1) * 2 + ((lane >> 3) & 1);
+          uint32_t hi4[4], lo4[4];
+          ldsm4_t(hi4, su + rr * U_ROW + ((ch ^ (rr & 7)) * 16));
+          ldsm4_t(lo4, su + rr * U_ROW + (((ch + 4) ^ (rr & 7)) * 16));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma16816(acc[mt][j], hi4, bf[2 * j], bf[2 * j + 1]);
+            mma16816(acc[mt][j], lo4, bf[2 * j], bf[2 * j + 1]);
+          }
         }
       }
     }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();     // the stages are free
+  };
+  auto put = [&](float* dst) {   // acc -> shared memory
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int rr = mt * 16 + (lane >> 2), cc = warp * 32 + j * 8 + (lane & 3) * 2;
+        *reinterpret_cast<float2*>(dst + rr * RS + cc) = make_float2(acc[mt][j][0], acc[mt][j][1]);
+        *reinterpret_cast<float2*>(dst + (rr + 8) * RS + cc) =
+            make_float2(acc[mt][j][2], acc[mt][j][3]);
+      }
+  };
+  // out[a] = src of this CTA (null: zeros) + the heads of the next `more` ranks
+  auto write = [&](int a, const float* src, int more) {
+    for (int it = tid; it < p.r * (kWgCols / 4); it += kWgThreads) {
+      const int rr = it / (kWgCols / 4), cc = it % (kWgCols / 4) * 4;
+      if (c0 + cc >= C) continue;
+      float4 s = src ? *reinterpret_cast<const float4*>(src + rr * RS + cc)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 1; k <= more; ++k) {
+        const float4 v = ld_rank4(head + rr * RS + cc, q + k);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      const size_t at = ((size_t)a * p.r + rr) * C + c0 + cc;
+      if (p.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+            make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
+    }
+  };
 
-  float* red = reinterpret_cast<float*>(smem);   // [16 MT][RS], over the stages
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int rr = mt * 16 + (lane >> 2), cc = warp * 32 + j * 8 + (lane & 3) * 2;
-      red[rr * RS + cc] = acc[mt][j][0];
-      red[rr * RS + cc + 1] = acc[mt][j][1];
-      red[(rr + 8) * RS + cc] = acc[mt][j][2];
-      red[(rr + 8) * RS + cc + 1] = acc[mt][j][3];
+  // adapter of list row r0: the last one whose rows start at or before it and that has rows
+  int a = 0;
+  if (r0 < r1) {
+    int lo = 0, hi = p.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (p.off[mid] <= r0) lo = mid;
+      else hi = mid - 1;
     }
-  cluster_sync_all();
-  for (int it = q * kWgThreads + tid; it < p.r * (kWgCols / 4); it += kWgThreads * p.split) {
-    const int rr = it / (kWgCols / 4), cc = it % (kWgCols / 4) * 4;
-    if (c0 + cc >= p.C) continue;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.split; ++k) {
-      const float4 v = ld_rank4(red + rr * RS + cc, k);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
-    const size_t at = ((size_t)a * p.r + rr) * p.C + c0 + cc;
-    if (p.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-          make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = s;
+    a = lo;
   }
-  cluster_sync_all();
+  int last = -1, more = 0;   // the adapter that goes on into the next ranks, and how many of them
+  for (int at = r0; at < r1; ++a) {
+    const int begin = p.off[a], end = p.off[a + 1];
+    if (begin == end) continue;
+    const int stop = min(end, r1);
+    accumulate(at, stop);
+    at = stop;
+    if (begin < r0) {                 // began in an earlier rank, which adds this part
+      put(head);
+    } else {
+      put(tail);
+      if (end <= r1) {
+        __syncthreads();
+        write(a, tail, 0);
+        __syncthreads();              // before the stages are filled again
+      } else {
+        last = a;
+        while (q + more + 1 < p.split && (int)((long long)total * (q + more + 1) / p.split) < end)
+          ++more;
+      }
+    }
+  }
+  if (r0 == r1)                       // fewer rows than ranks: nothing to add here
+    for (int i = tid; i < 16 * MT * RS; i += kWgThreads) head[i] = 0.f;
+  cluster_sync_all();                 // every head is in place
+  if (last >= 0) write(last, tail, more);
+  for (int z = q; z < p.n; z += p.split)   // adapters without rows
+    if (p.off[z] == p.off[z + 1]) write(z, nullptr, 0);
+  cluster_sync_all();                 // no rank leaves while another reads its head
 }
 
 // ------------------------------------------------------------------ host side
@@ -921,102 +1309,204 @@ SavedParts saved_parts(const mok_lora_dims& d) {
 }
 struct WorkParts {
   SavedParts v;
-  size_t off, cnt, rows, total;
+  size_t off, rows, total;
 };
 WorkParts work_parts(const mok_lora_dims& d) {
   WorkParts w;
   w.v = saved_parts(d);
   w.off = w.v.total;
-  w.cnt = w.off + align_up((size_t)d.n * 4, 256);
-  w.rows = w.cnt + align_up((size_t)d.n * 4, 256);
+  w.rows = w.off + align_up(((size_t)d.n + 1) * 4, 256);
   w.total = w.rows + align_up((size_t)d.T * 4, 256);
   return w;
 }
 
-// SM count of the current device, and its kernels' shared-memory limits raised (once each).
-int device_sms() {
-  static std::atomic<int> sms[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev < 64 && sms[dev].load(std::memory_order_acquire)) return sms[dev].load();
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  const void* fns[] = {(const void*)shrink_kernel, (const void*)proj_kernel<false>,
-                       (const void*)proj_kernel<true>, (const void*)wgrad_kernel<1>,
-                       (const void*)wgrad_kernel<2>, (const void*)wgrad_kernel<4>,
-                       (const void*)wgrad_kernel<8>};
-  for (const void* f : fns) {
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, f) != cudaSuccess) return 0;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kMaxSmem - a.sharedSizeBytes)) != cudaSuccess)
-      return 0;
-  }
-  if (dev < 64) sms[dev].store(n, std::memory_order_release);
-  return n;
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), int grid, int threads, size_t smem, int cluster,
-                   cudaStream_t s, const Args&... args) {
+// The current device's SMs, and how many clusters of 1, 2, 4, 8 CTAs of proj_kernel (one CTA
+// per SM) it holds at once. Also raises the kernels' shared-memory limits. Once per device.
+struct Device {
+  int sms = 0;
+  int clusters[4];
+};
+template <typename K>
+int max_clusters(K kernel, int cluster, size_t smem) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.gridDim = dim3((unsigned)cluster * 64);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+bool init_device(Device& d, int dev) {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+  const void* fns[] = {(const void*)shrink_kernel,
+                       (const void*)proj_kernel<false, false>, (const void*)proj_kernel<true, false>,
+                       (const void*)proj_kernel<false, true>, (const void*)proj_kernel<true, true>,
+                       (const void*)wgrad_kernel<1>, (const void*)wgrad_kernel<2>,
+                       (const void*)wgrad_kernel<4>, (const void*)wgrad_kernel<8>};
+  for (const void* f : fns) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, f) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kMaxSmem - a.sharedSizeBytes)) != cudaSuccess)
+      return false;
+  }
+  for (int i = 0; i < 4; ++i) {
+    d.clusters[i] = max_clusters(proj_kernel<false, false>, 1 << i, kMaxSmem);
+    if (d.clusters[i] <= 0) return false;
+  }
+  d.sms = n;
+  return true;
+}
+const Device* current_device() {
+  constexpr int kMaxDevices = 64;
+  static Device devices[kMaxDevices];
+  static std::once_flag once[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::call_once(once[dev], [&] { init_device(devices[dev], dev); });
+  return devices[dev].sms > 0 ? &devices[dev] : nullptr;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int grid, int threads, size_t smem, int cluster,
+                   bool early, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // early: may start before
+  attr[1].val.programmaticStreamSerializationAllowed = 1;            // the last kernel ends
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The r values of every row: in [T][C] against w [n][r][C].
+// Rows of X (or u) that a tile loads: all 128, or the batch's own rounded up to 8 (the rows of
+// a swizzle atom).
+int tile_rows(int T) { return T >= BM ? BM : (T + 7) / 8 * 8; }
+
+// The r values of every row: in [T][C] against w [n][r][C]. early: the launch may start before
+// the stream's last kernel ends.
 mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void* w,
                       const float* scale, const int32_t* ids, char* saved, uint32_t* status,
-                      int sms, cudaStream_t s) {
+                      bool early, const Device& dev, cudaStream_t s) {
   const SavedParts sp = saved_parts(d);
   const int mt = (d.T + BM - 1) / BM;
+  const int rp = padded_rank(d.r), nb = (rp + 31) / 32;
+  uint8_t* uq = reinterpret_cast<uint8_t*>(saved + sp.uq);
+  int32_t* n_slots = reinterpret_cast<int32_t*>(saved + sp.n_slots);
+  Slot* slots = reinterpret_cast<Slot*>(saved + sp.slots);
+  if (d.T <= kRowsMost && C <= 256 * kRowMaxPieces) {
+    ShrinkRowsParams p = {d.T, C, d.n, d.r, nb, static_cast<const __nv_bfloat16*>(in),
+                          static_cast<const __nv_bfloat16*>(w), ids, scale, uq, n_slots, slots};
+    return launch(shrink_rows_kernel, d.T + mt, kRowThreads, 0, 1, early, s, p) == cudaSuccess
+               ? MOK_OK
+               : MOK_ERR_CUDA;
+  }
   ShrinkParams p = {};
   p.T = d.T;
   p.n = d.n;
   p.r = d.r;
-  p.rp = padded_rank(d.r);
-  p.nb = (p.rp + 31) / 32;
+  p.rp = rp;
+  p.nb = nb;
   p.kiters = (C + BK - 1) / BK;
-  p.cols = std::max(64, p.rp);
-  // CTAs: two per SM if there is work for them; a rank takes at least four steps
-  p.split = 1;
-  while (p.split < 8 && 2 * p.split * 4 <= p.kiters && mt * p.split < 2 * sms) p.split *= 2;
-  const int most = std::min(std::min(d.n, d.T), BM);   // distinct adapters of a tile
-  const int chunks = (most * p.rp + p.cols - 1) / p.cols;
-  p.cy = std::max(1, std::min(chunks, 2 * sms / (mt * p.split)));
-  p.stage_bytes = A_BYTES + p.cols * 128;
-  p.stages = 4;
+  p.cols = 128;
+  p.a_bytes = tile_rows(d.T) * BK * 2;
+  p.stage_bytes = p.a_bytes + p.cols * 128;
+  // an MMA reads 128 rows from a stage's start, past a short batch's own: in bounds for the
+  // last stage too
+  const size_t tail = A_BYTES - p.a_bytes;
+  const size_t fixed = align_up((size_t)BM * (p.rp + 1) * 4, 16) + tail + kBarBytes + 1024;
+  p.stages = std::min<int>(kMaxStages, (int)((kMaxSmem - sizeof(TileSlots) - fixed) / p.stage_bytes));
+  // one wave of clusters, a rank at least two steps
+  int i = 0;
+  while (i < 3 && 2 * (2 << i) <= p.kiters && mt <= dev.clusters[i + 1]) ++i;
+  p.split = 1 << i;
+  const int distinct = std::min(std::min(d.n, d.T), BM);   // adapters of a tile, at most
+  const int chunks = (distinct * p.rp + p.cols - 1) / p.cols;
+  p.cy = std::max(1, std::min(chunks, dev.clusters[i] / mt));
   p.ids = ids;
   p.scale = scale;
-  p.uq = reinterpret_cast<uint8_t*>(saved + sp.uq);
-  p.n_slots = reinterpret_cast<int32_t*>(saved + sp.n_slots);
-  p.slots = reinterpret_cast<Slot*>(saved + sp.slots);
+  p.uq = uq;
+  p.n_slots = n_slots;
+  p.slots = slots;
   p.status = status;
   CUtensorMap xm, am;
-  if (!make_map(&xm, in, true, C, d.T, 0, BM) || !make_map(&am, w, true, C, d.r, d.n, p.rp))
+  if (!make_map(&xm, in, true, C, d.T, 0, tile_rows(d.T)) || !make_map(&am, w, true, C, d.r, d.n, p.rp))
     return MOK_ERR_CUDA;
-  const size_t smem = (size_t)p.stages * p.stage_bytes + align_up((size_t)BM * (p.rp + 1) * 4, 16) +
-                      kBarBytes + 1024;
-  return launch(shrink_kernel, mt * p.cy * p.split, kThreads, smem, p.split, s, xm, am, p) ==
+  const size_t smem = (size_t)p.stages * p.stage_bytes + fixed;
+  return launch(shrink_kernel, mt * p.cy * p.split, kThreads, smem, p.split, early, s, xm, am, p) ==
                  cudaSuccess
              ? MOK_OK
              : MOK_ERR_CUDA;
+}
+
+// Form of the projection for [T][C] x [C][cols]: the candidate with the least estimated time,
+// in microseconds: waves x (steps x time of a step + fixed). A step's time is the largest of
+// the tensor core's (2.2 clocks per column at 1.9 GHz), its bytes' way into the SM's shared
+// memory (64 bytes a clock), W's out of HBM, and the memory's latency over the ring's stages.
+struct ProjForm {
+  int NT, split, pair, stages, stage_bytes;
+  size_t smem;
+};
+ProjForm choose_form(int T, int kiters, int cols, const Device& dev) {
+  const int mt = (T + BM - 1) / BM, a_bytes = tile_rows(T) * BK * 2;
+  ProjForm best = {};
+  double best_t = 0;
+  for (int nt : {256, 192, 128, 64}) {
+    for (int pair = 0; pair <= 1; ++pair) {
+      for (int i = 0; i < 4; ++i) {
+        const int split = 1 << i;
+        if (pair && (nt != 256 || split > 1 || mt < 2)) continue;
+        if (split > 1 && (kiters < 2 * split || nt > 128)) continue;
+        ProjForm f;
+        f.NT = nt;
+        f.split = split;
+        f.pair = pair;
+        f.stage_bytes = a_bytes + (pair ? nt / 2 : nt) * 128;
+        const size_t fixed = (split == 1 ? 8 * kStagingBox : 0) + kBarBytes + 1024;
+        const size_t tail = A_BYTES - a_bytes;   // an MMA reads 128 rows (see run_shrink)
+        // a cluster's partial tile lies over the stages
+        const size_t red = split == 1 ? 0 : (size_t)std::min(BM, (T + 31) / 32 * 32) * (nt + 4) * 4;
+        f.stages = std::min<int>(kMaxStages, (int)((kMaxSmem - fixed - tail) / f.stage_bytes));
+        if (f.stages < 3 || (size_t)f.stages * f.stage_bytes < red) continue;
+        f.smem = (size_t)f.stages * f.stage_bytes + tail + fixed;
+        const double tiles = (double)((cols + nt - 1) / nt) * (pair ? (mt + 1) / 2 : mt);
+        const double cap = dev.clusters[pair ? 1 : i];
+        const double waves = std::ceil(tiles / cap);
+        const double live = std::min(tiles, cap) * (pair ? 2 : split);   // CTAs at once
+        const double mma = 2.2 * nt / 1.9e3;
+        const double fill = f.stage_bytes / (64 * 1.9e3);
+        const double hbm = (double)(pair ? nt / 2 : nt) * 128 * live / mt / 6.0e6;
+        const double step = std::max(std::max(mma, fill), std::max(hbm, 2.0 / f.stages));
+        const double t = waves * (std::ceil((double)kiters / split) * step + (split > 1 ? 3.0 : 1.0));
+        if (best_t == 0 || t < best_t) {
+          best_t = t;
+          best = f;
+        }
+      }
+    }
+  }
+  return best;
 }
 
 // out [T][cols] = in [T][C] W (trans: W^T) + the low-rank part. W == null: that part alone;
 // parts == null: no such part.
 mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const void* in,
                     const void* W, const char* parts, const void* expand, const int32_t* ids,
-                    void* out, mok_out_dtype type, uint32_t* status, int sms, cudaStream_t s) {
+                    void* out, mok_out_dtype type, uint32_t* status, bool early, const Device& dev,
+                    cudaStream_t s) {
   const SavedParts sp = saved_parts(d);
   ProjParams p = {};
   p.T = d.T;
@@ -1028,28 +1518,13 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
   p.nb = (p.rp + 31) / 32;
   p.rb = std::min(p.rp, 32);
   p.out_bf16 = type == MOK_OUT_BF16;
-  // Tile width and contraction split: the pair with the least estimated time, waves x
-  // (steps x time of a step + fixed cost), in SM clocks. A step of NT columns takes the
-  // tensor core about 2.2 clocks per column, and never less than its loads need.
-  double best = 0;
-  for (int nt : {256, 192, 128, 64}) {
-    for (int split = 1; split <= 8; split *= 2) {
-      if (split > 1 && (p.kiters < 4 * split || nt > 128)) continue;
-      const double n_tiles = (cols + nt - 1) / nt, tiles = n_tiles * p.m_tiles;
-      const double waves = std::ceil(tiles * split / sms);
-      const double step = std::max(2.2 * nt, 250.0);
-      const double t = waves * (std::ceil((double)p.kiters / split) * step +
-                                (split > 1 ? 6000.0 : 1500.0));
-      if (best == 0 || t < best) {
-        best = t;
-        p.NT = nt;
-        p.split = split;
-      }
-    }
-  }
+  const ProjForm f = choose_form(d.T, p.kiters, cols, dev);
+  p.NT = f.NT;
+  p.split = f.split;
   p.n_tiles = (cols + p.NT - 1) / p.NT;
-  p.stage_bytes = A_BYTES + p.NT * 128;
-  p.stages = std::min(kMaxStages, (int)((kMaxSmem - 1024 - kBarBytes - 8 * kStagingBox) / p.stage_bytes));
+  p.a_bytes = tile_rows(d.T) * BK * 2;
+  p.stage_bytes = f.stage_bytes;
+  p.stages = f.stages;
   if (parts) {
     p.n_slots = reinterpret_cast<const int32_t*>(parts + sp.n_slots);
     p.slots = reinterpret_cast<const Slot*>(parts + sp.slots);
@@ -1057,61 +1532,65 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
   p.ids = ids;
   p.out = out;
   p.status = status;
+  const int rows = tile_rows(d.T);
   CUtensorMap xm, wm, um, em, om;
   bool ok = make_map(&om, out, p.out_bf16, cols, d.T, 0, 32);
   if (W) {
-    ok = ok && make_map(&xm, in, true, C, d.T, 0, BM);
-    ok = ok && (trans ? make_map(&wm, W, true, C, cols, 0, p.NT) : make_map(&wm, W, true, cols, C, 0, BK));
+    ok = ok && make_map(&xm, in, true, C, d.T, 0, rows);
+    ok = ok && (trans ? make_map(&wm, W, true, C, cols, 0, f.pair ? p.NT / 2 : p.NT)
+                      : make_map(&wm, W, true, cols, C, 0, BK));
   } else {
     xm = wm = om;   // not read
   }
   if (parts) {
-    ok = ok && make_map(&um, parts + sp.uq, true, (uint64_t)p.nb * 64, d.T, 0, BM);
+    ok = ok && make_map(&um, parts + sp.uq, true, (uint64_t)p.nb * 64, d.T, 0, rows);
     ok = ok && make_map(&em, expand, true, cols, d.r, d.n, p.rb);
   } else {
     um = em = om;
   }
   if (!ok) return MOK_ERR_CUDA;
-  const int tiles = p.m_tiles * p.n_tiles;
-  const size_t smem = (size_t)p.stages * p.stage_bytes + (p.split == 1 ? 8 * kStagingBox : 0) +
-                      kBarBytes + 1024;
-  const int grid = p.split == 1 ? std::min(tiles, sms) : tiles * p.split;
+  const int csize = f.pair ? 2 : f.split;
+  const int tiles = (f.pair ? (p.m_tiles + 1) / 2 : p.m_tiles) * p.n_tiles;
+  const int grid = f.split > 1 ? tiles * csize
+                               : std::min(tiles, dev.clusters[f.pair]) * csize;
+  auto go = [&](auto kernel) {
+    return launch(kernel, grid, kThreads, f.smem, csize, early, s, xm, wm, um, em, om, p);
+  };
   const cudaError_t e =
-      trans ? launch(proj_kernel<true>, grid, kThreads, smem, p.split, s, xm, wm, um, em, om, p)
-            : launch(proj_kernel<false>, grid, kThreads, smem, p.split, s, xm, wm, um, em, om, p);
+      trans ? (f.pair ? go(proj_kernel<true, true>) : go(proj_kernel<true, false>))
+            : (f.pair ? go(proj_kernel<false, true>) : go(proj_kernel<false, false>));
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
 
-mok_status run_wgrad(const mok_lora_dims& d, int C, const char* uq, const void* g, char* ws,
-                     const WorkParts& wp, void* out, mok_out_dtype type, int sms, cudaStream_t s) {
+mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, const void* xa,
+                     const void* dY, const char* ws, const WorkParts& wp, void* dA, void* dB,
+                     mok_out_dtype type, cudaStream_t s) {
   WgradParams p = {};
-  p.C = C;
+  auto side = [](const char* q, const void* g, void* out, int C) {
+    return WgradSide{reinterpret_cast<const uint8_t*>(q), static_cast<const __nv_bfloat16*>(g), out,
+                     C, (C + kWgCols - 1) / kWgCols};
+  };
+  p.side[0] = side(vq, xa, dA, d.K);
+  p.side[1] = side(uq, dY, dB, d.N);
   p.r = d.r;
   p.n = d.n;
-  p.ctiles = (C + kWgCols - 1) / kWgCols;
   p.out_bf16 = type == MOK_OUT_BF16;
   p.off = reinterpret_cast<const int32_t*>(ws + wp.off);
-  p.cnt = reinterpret_cast<const int32_t*>(ws + wp.cnt);
   p.rows = reinterpret_cast<const int32_t*>(ws + wp.rows);
-  p.uq = reinterpret_cast<const uint8_t*>(uq);
-  p.g = static_cast<const __nv_bfloat16*>(g);
-  p.out = out;
-  // row shares: enough CTAs to keep the SMs' loads in flight, and at least two stages each
+  // row shares of at least two stages
   p.split = 1;
-  const long long base = (long long)d.n * p.ctiles;
-  while (p.split < 8 && base * p.split < 6LL * sms && d.T / p.split > 2 * kWgRows) p.split *= 2;
+  while (p.split < 8 && d.T > 4 * p.split * kWgRows) p.split *= 2;
   const int mt = padded_rank(d.r) / 16, nb = (mt + 1) / 2;
+  const size_t part = (size_t)mt * 16 * (kWgCols + 4) * 4;
   const size_t stages = (size_t)kWgStages * kWgRows * (kWgCols * 2 + nb * 128);
-  const size_t red = (size_t)mt * 16 * (kWgCols + 4) * 4;
-  const size_t smem = std::max(stages, red);
-  const long long grid = base * p.split;
-  if (grid > 0x7fffffff) return MOK_ERR_UNSUPPORTED;
+  const size_t smem = part + std::max(stages, part);
+  const int grid = (p.side[0].ctiles + p.side[1].ctiles) * p.split;
   cudaError_t e;
   switch (mt) {
-    case 1: e = launch(wgrad_kernel<1>, (int)grid, kWgThreads, smem, p.split, s, p); break;
-    case 2: e = launch(wgrad_kernel<2>, (int)grid, kWgThreads, smem, p.split, s, p); break;
-    case 4: e = launch(wgrad_kernel<4>, (int)grid, kWgThreads, smem, p.split, s, p); break;
-    default: e = launch(wgrad_kernel<8>, (int)grid, kWgThreads, smem, p.split, s, p); break;
+    case 1: e = launch(wgrad_kernel<1>, grid, kWgThreads, smem, p.split, true, s, p); break;
+    case 2: e = launch(wgrad_kernel<2>, grid, kWgThreads, smem, p.split, true, s, p); break;
+    case 4: e = launch(wgrad_kernel<4>, grid, kWgThreads, smem, p.split, true, s, p); break;
+    default: e = launch(wgrad_kernel<8>, grid, kWgThreads, smem, p.split, true, s, p); break;
   }
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
@@ -1151,13 +1630,13 @@ extern "C" mok_status mok_lora_fwd(const mok_lora_dims* dims, const mok_lora_wei
       (status && !ok_ptr(status, 4)))
     return MOK_ERR_INVALID_ARG;
   if (!ok_ptr(saved, 256)) return MOK_ERR_WORKSPACE;
-  const int sms = device_sms();
-  if (sms <= 0) return MOK_ERR_CUDA;
+  const Device* dev = current_device();
+  if (!dev) return MOK_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* sv = static_cast<char*>(saved);
-  mok_status st = run_shrink(*dims, dims->K, x_ad ? x_ad : x, w->A, w->scale, ids, sv, status, sms, s);
+  mok_status st = run_shrink(*dims, dims->K, x_ad ? x_ad : x, w->A, w->scale, ids, sv, status, false, *dev, s);
   if (st != MOK_OK) return st;
-  return run_proj(*dims, dims->K, dims->N, false, x, w->W, sv, w->B, ids, y, out, status, sms, s);
+  return run_proj(*dims, dims->K, dims->N, false, x, w->W, sv, w->B, ids, y, out, status, true, *dev, s);
 }
 
 extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_weights* w,
@@ -1181,27 +1660,26 @@ extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_wei
     return MOK_ERR_INVALID_ARG;
   if (x_ad ? (!ok_ptr(x_ad, 16) || !ok_ptr(dXa, 16)) : dXa != nullptr) return MOK_ERR_INVALID_ARG;
   if (!ok_ptr(saved, 256) || !ok_ptr(workspace, 256)) return MOK_ERR_WORKSPACE;
-  const int sms = device_sms();
-  if (sms <= 0) return MOK_ERR_CUDA;
+  const Device* dev = current_device();
+  if (!dev) return MOK_ERR_CUDA;
   const mok_lora_dims& d = *dims;
   const char* sv = static_cast<const char*>(saved);
   char* ws = static_cast<char*>(workspace);
   const WorkParts wp = work_parts(d);
-  mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, status, sms, s);
-  if (st != MOK_OK) return st;
-  st = run_proj(d, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, sms, s);
-  if (st != MOK_OK) return st;
-  if (x_ad) {
-    st = run_proj(d, d.N, d.K, true, nullptr, nullptr, ws, w->A, ids, dXa, out, status, sms, s);
-    if (st != MOK_OK) return st;
-  }
-  bucket_kernel<<<d.n, kBucketThreads, 0, s>>>(d.T, ids, reinterpret_cast<int32_t*>(ws + wp.off),
-                                               reinterpret_cast<int32_t*>(ws + wp.cnt),
+  // row lists, v, weight gradients, dX: each launch starts its set-up while the one before it
+  // drains, and waits for it before it reads or writes anything that it produced
+  bucket_kernel<<<d.n, kBucketThreads, 0, s>>>(d.T, d.n, ids, reinterpret_cast<int32_t*>(ws + wp.off),
                                                reinterpret_cast<int32_t*>(ws + wp.rows));
   if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
-  st = run_wgrad(d, d.K, ws + wp.v.uq, x_ad ? x_ad : x, ws, wp, dA, out, sms, s);
+  mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, status, true, *dev, s);
   if (st != MOK_OK) return st;
-  return run_wgrad(d, d.N, sv + saved_parts(d).uq, dY, ws, wp, dB, out, sms, s);
+  st = run_wgrad(d, sv + wp.v.uq, ws + wp.v.uq, x_ad ? x_ad : x, dY, ws, wp, dA, dB, out, s);
+  if (st != MOK_OK) return st;
+  st = run_proj(d, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, true,
+                *dev, s);
+  if (st != MOK_OK || !x_ad) return st;
+  return run_proj(d, d.N, d.K, true, nullptr, nullptr, ws, w->A, ids, dXa, out, status, false, *dev,
+                  s);
 }
 
 extern "C" mok_status mok_lora_get_status(uint32_t* status, void* stream) {

@@ -106,6 +106,32 @@ def test_many_row_tiles_and_wide_outputs(rng):
     check(c, run(c))
 
 
+@pytest.mark.parametrize("T,K,N,n,r,order", [
+    (1500, 520, 2000, 40, 40, "rows"), (1409, 2056, 1544, 5, 16, "packed"),
+    (2304, 264, 3016, 3, 7, "packed")])
+def test_pairs_of_row_tiles(T, K, N, n, r, order, rng):
+    """Large enough for the two-CTA form in both directions, odd counts of row tiles among them."""
+    c = make(rng, T, K, N, n, r, order)
+    check(c, run(c))
+
+
+@pytest.mark.parametrize("used", [0, 1, 3, 70, 700])
+def test_few_rows_with_adapters(used, rng):
+    """The weight gradients share the rows that have an adapter, fewer than shares among them."""
+    c = make(rng, 3000, 72, 136, 6, 9, "none")
+    at = torch.tensor(rng.choice(3000, used, replace=False))
+    c["ids"][at] = torch.tensor(rng.choice([0, 2, 5], used), dtype=torch.int32)
+    check(c, run(c))
+
+
+def test_adapters_of_very_unequal_sizes(rng):
+    """One adapter's rows cover several shares, others end inside one."""
+    c = make(rng, 2000, 136, 200, 9, 20, "none")
+    c["ids"][:] = torch.tensor(np.repeat([3, 7, 1, 8], [1700, 90, 10, 200]), dtype=torch.int32)
+    c["ids"] = c["ids"][torch.tensor(rng.permutation(2000))].contiguous()
+    check(c, run(c))
+
+
 def test_long_contraction(rng):
     """Contraction shared between the CTAs of a cluster."""
     c = make(rng, 40, 4104, 136, 11, 16, "rows")
