@@ -68,6 +68,20 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait(bar, parity, globaltimer_ns() + kTimeoutNs);
 }
+// One lane of a converged warp, always the same one. The roles that issue TMA and MMA run as
+// whole warps and elect a lane only around those instructions: everything else is then
+// provably uniform, so their operands sit in uniform registers. (With the loops themselves
+// under "lane == 0" one step took 650 clocks to issue, longer than its MMAs: 0.33 us in every
+// shape.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 // tcgen05.mma (kind::f16) that leaves the accumulator rows (TMEM lanes) of `off` untouched:
 // bit i of word j stands for lane 32 j + i.
@@ -137,19 +151,28 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// fp32 loads from the shared memory of CTA `rank` of the cluster (p: this CTA's address).
-__device__ __forceinline__ float ld_rank(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_rank(p, rank)) : "memory");
-  return v;
-}
+// 4 floats from the shared memory of CTA `rank` of the cluster (p: this CTA's address).
+// Volatile, so it stays between the cluster barriers around it; several may be in flight.
 __device__ __forceinline__ float4 ld_rank4(const float* p, uint32_t rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(mapa_rank(p, rank))
-               : "memory");
+               : "r"(mapa_rank(p, rank)));
   return v;
+}
+// Sum over the ranks 0 .. n - 1 (n <= 8) in rank order, all loads issued before the first add.
+__device__ __forceinline__ float4 sum_ranks(const float* p, int n) {
+  float4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) v[k] = ld_rank4(p, k);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) {
+      s.x += v[k].x; s.y += v[k].y; s.z += v[k].z; s.w += v[k].w;
+    }
+  return s;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -188,14 +211,14 @@ __device__ __forceinline__ void init_bars(Bars* b, bool pair = false) {
   fence_mbar_init();
 }
 
-// The ring of pipeline stages as one role (producer or MMA lane) walks it.
+// The ring of pipeline stages as one role (producer or MMA warp) walks it.
 struct Ring {
   int stages;
   int stage = 0;
   uint32_t phase = 0;
   uint32_t used = 0;     // stages filled so far (producer)
   __device__ explicit Ring(int n) : stages(n) {}
-  __device__ void next() {
+  __device__ __forceinline__ void next() {
     ++used;
     if (++stage == stages) {
       stage = 0;
@@ -204,27 +227,29 @@ struct Ring {
   }
 };
 
-// Producer: waits until the stage is free and announces the bytes that will land in it
-// (0: another CTA announces them).
-__device__ __forceinline__ bool open_stage(Bars* b, const Ring& r, uint32_t bytes,
-                                           uint32_t* status) {
-  if (b->abort) return false;
-  if (!wait_bar(&b->empty[r.stage], r.phase ^ 1)) {   // passes at once in the first round
-    flag_timeout(status);
-    b->abort = 1;
-    return false;
+// A wait of a whole warp; every lane gets the same answer. False: the wait passed its bound
+// (the status word is set) or another warp's did.
+__device__ __noinline__ bool warp_wait_long(Bars* b, uint64_t* bar, uint32_t parity,
+                                            uint32_t* status) {
+  uint64_t deadline = 0;
+  bool done = false;
+  for (uint32_t i = 1;; ++i) {
+    done = done || mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (i % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (deadline == 0) deadline = now + kTimeoutNs;
+      const bool late = now > deadline;
+      if (late && !b->abort) flag_timeout(status);
+      if (late) b->abort = 1;
+      if (__any_sync(0xffffffffu, late || b->abort)) return false;
+    }
   }
-  if (bytes) mbar_arrive_expect_tx(&b->full[r.stage], bytes);
-  return true;
 }
-__device__ __forceinline__ bool await_stage(Bars* b, const Ring& r, uint32_t* status) {
-  if (b->abort || !wait_bar(&b->full[r.stage], r.phase)) {
-    if (!b->abort) flag_timeout(status);
-    b->abort = 1;
-    return false;
-  }
-  tc_fence_after();
-  return true;
+__device__ __forceinline__ bool warp_wait(Bars* b, uint64_t* bar, uint32_t parity,
+                                          uint32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_long(b, bar, parity, status);
 }
 // After an abort: every copy that was issued has landed (bounded), so that the shared memory
 // may go away.
@@ -235,10 +260,16 @@ __device__ void drain_copies(Bars* b, const Ring& r) {
   }
 }
 template <bool PAIR>
-__device__ void drain_mmas(Bars* b) {
+__device__ void drain_mmas(Bars* b) {   // from the lane that issued them
   if constexpr (PAIR) umma_commit_pair(&b->drain);
   else umma_commit(&b->drain);
   wait_bar(&b->drain, 0);
+}
+// Descriptor of the operand at shared-memory address `at`, from one with address 0. The mask
+// matters: in a cluster the address carries the CTA's rank above its 18 bits, which would
+// otherwise land in the descriptor's byte offsets.
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t at) {
+  return base + ((at & 0x3ffffu) >> 4);
 }
 
 // ------------------------------------------------------------------ distinct adapters
@@ -323,11 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) TileSlots ts;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  float* red = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);   // [128][rp + 1]
-  const int rs = p.rp + 1;
-  Bars* bars = reinterpret_cast<Bars*>(red + ((BM * rs + 3) & ~3));
+  float* red = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);   // [128][rp + 4]
+  const int rs = p.rp + 4;
+  Bars* bars = reinterpret_cast<Bars*>(red + BM * rs);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // known uniform
+  const int lane = threadIdx.x & 31;
   const int et = (int)threadIdx.x - 64;
   const int q = (int)(blockIdx.x % p.split);
   const int c0 = (int)(blockIdx.x / p.split) % p.cy;
@@ -366,34 +398,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int c = c0; c * per < count; c += p.cy, parity ^= 1) {   // the same chunks in every rank
     const int s0 = c * per, ns = min(per, count - s0);
     if (warp == 0) {
-      if (lane == 0) {
-        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-          if (!open_stage(bars, ring, p.a_bytes + ns * p.rp * 128, p.status)) break;
-          uint8_t* sa = smem + ring.stage * p.stage_bytes;
-          uint64_t* bar = &bars->full[ring.stage];
+      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+        if (!warp_wait(bars, &bars->empty[ring.stage], ring.phase ^ 1, p.status)) break;
+        uint8_t* sa = smem + ring.stage * p.stage_bytes;
+        uint64_t* bar = &bars->full[ring.stage];
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, p.a_bytes + ns * p.rp * 128);
           tma_load_2d(sa, &xmap, bar, kb * BK, row0);
+        }
+        __syncwarp();
+        if (elect_one())
           for (int j = 0; j < ns; ++j)   // rp rows of 128 bytes per adapter (zeros past rank r)
             tma_load_3d(sa + p.a_bytes + j * p.rp * 128, &amap, bar, kb * BK, 0, ts.slot_id[s0 + j]);
-        }
+        __syncwarp();
       }
-      __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
-        const uint32_t idesc = idesc_bf16(BM, ns * p.rp, false, false);
-        bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-          ok = await_stage(bars, ring, p.status);
-          if (!ok) break;
-          const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+      const uint32_t idesc = idesc_bf16(BM, ns * p.rp, false, false);
+      const uint64_t km = umma_desc_sw128(0, 16, 1024);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+        ok = warp_wait(bars, &bars->full[ring.stage], ring.phase, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+        const uint64_t ad = desc_at(km, sa), bd = desc_at(km, sa + p.a_bytes);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem, umma_desc_sw128(sa + kk * 32, 16, 1024),
-                      umma_desc_sw128(sa + p.a_bytes + kk * 32, 16, 1024), idesc,
-                      (kb > kb0 || kk > 0) ? 1u : 0u);
+            umma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
           umma_commit(&bars->empty[ring.stage]);
         }
-        if (ok) umma_commit(&bars->acc_full[0]);
+        __syncwarp();
       }
+      if (ok && elect_one()) umma_commit(&bars->acc_full[0]);
       __syncwarp();
     } else {
       bool ok = !bars->abort && wait_bar(&bars->acc_full[0], parity);
@@ -415,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (cur - s0) * p.rp + i0, v);
           if (sl == cur) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) red[row * rs + i0 + i] = v[i];
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(&red[row * rs + i0 + i]) =
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
       }
@@ -424,31 +463,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cluster_sync_all();
     if (et >= 0) {
-      const int rows = BM / p.split, half = p.rp / 2;
-      for (int it = et; it < rows * half; it += 128) {
-        const int row = q * rows + it / half, i = 2 * (it % half);
+      const int rows = BM / p.split, quads = p.rp / 4;
+      for (int it = et; it < rows * quads; it += 128) {
+        const int row = q * rows + it / quads, i = 4 * (it % quads);
         const int sl = ts.slot[row];
         if (sl < s0 || sl >= s0 + ns) continue;
-        float a = 0.f, b = 0.f;
-        for (int k = 0; k < p.split; ++k) {
-          a += ld_rank(&red[row * rs + i], k);
-          b += ld_rank(&red[row * rs + i + 1], k);
-        }
+        const float4 v = sum_ranks(&red[row * rs + i], p.split);
         const float f = p.scale[ts.id[row]];
-        uint32_t hi, lo;
         // ranks r .. rp - 1 are padding: 0 also where a row with an inf met A's zero fill
-        split_pair(i < p.r ? f * a : 0.f, i + 1 < p.r ? f * b : 0.f, hi, lo);
+        uint2 hi, lo;
+        split_pair(i < p.r ? f * v.x : 0.f, i + 1 < p.r ? f * v.y : 0.f, hi.x, lo.x);
+        split_pair(i + 2 < p.r ? f * v.z : 0.f, i + 3 < p.r ? f * v.w : 0.f, hi.y, lo.y);
         uint8_t* dst = p.uq + ((size_t)(row0 + row) * p.nb + i / 32) * 128 + (i % 32) * 2;
-        *reinterpret_cast<uint32_t*>(dst) = hi;
-        *reinterpret_cast<uint32_t*>(dst + 64) = lo;
+        *reinterpret_cast<uint2*>(dst) = hi;
+        *reinterpret_cast<uint2*>(dst + 64) = lo;
       }
     }
     cluster_sync_all();   // the partial sums may be overwritten, the accumulator reused
     tc_fence_after();
   }
   if (bars->abort) {
-    if (threadIdx.x == 0) drain_copies(bars, ring);
-    if (threadIdx.x == 32) drain_mmas<false>(bars);
+    if (warp == 0) drain_copies(bars, ring);
+    if (warp == 1 && elect_one()) drain_mmas<false>(bars);
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -579,7 +616,8 @@ __global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRo
 //              contraction, W's and the adapters' steps alike, and the partial sums meet in
 //              rank order through distributed shared memory.
 // The first two are persistent, with two accumulators, so that a tile's epilogue overlaps the
-// next tile's MMAs; results are staged in shared memory and stored by TMA.
+// next tile's MMAs; results are staged in shared memory and stored by TMA. Where the last wave
+// of pairs would be at most half full, its tiles are halved in width and fill it.
 //
 // The adapters' part of a tile goes 32 ranks (a block of u) at a time. Its first stage holds
 // that block of u for the tile's rows, and B rows of as many adapters as fit; further stages
@@ -592,6 +630,7 @@ struct ProjParams {
   int T, out_cols, n;
   int kiters;               // steps over W (0: the adapters' part alone)
   int NT, n_tiles, m_tiles, split, stages, a_bytes, stage_bytes;
+  int whole;                // PAIR: tiles from here on are run as two halves of NT / 2 columns
   int rp, nb, rb;           // padded rank, 32-rank blocks, ranks per adapter step
   int out_bf16;
   const int32_t* ids;
@@ -660,15 +699,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // split > 1: no staging boxes; the partial tile reuses the pipeline stages
   Bars* bars = reinterpret_cast<Bars*>(staging + (p.split == 1 ? 8 * kStagingBox : 0));
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // known uniform
+  const int lane = threadIdx.x & 31;
   const int csize = PAIR ? 2 : p.split;
   const int q = (int)(blockIdx.x % csize);                  // rank in the cluster
   const int m_step = PAIR ? 2 : 1;                          // row tiles of a tile
-  const int tiles = (p.m_tiles + m_step - 1) / m_step * p.n_tiles;
+  const int all = (p.m_tiles + m_step - 1) / m_step * p.n_tiles;
+  const int tiles = PAIR ? p.whole + 2 * (all - p.whole) : all;
   const int t0 = (int)(blockIdx.x / csize), tstep = (int)(gridDim.x / csize);
   const int kb0 = PAIR ? 0 : (int)((long long)p.kiters * q / p.split);
   const int kb1 = PAIR ? p.kiters : (int)((long long)p.kiters * (q + 1) / p.split);
-  const int nc = PAIR ? p.NT / 2 : p.NT;                    // columns this CTA loads
   const uint32_t tmem_cols = p.NT <= 64 ? 128 : p.NT <= 128 ? 256 : 512;   // two accumulators
   const int per_stage = 64 / p.rb;                          // adapters of an adapter stage
   const int group = p.stages - 1;
@@ -690,12 +730,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
 
+  // tile -> its (first) row tile, first column and width
+  auto place = [&](int tile, int& m, int& n0, int& width) {
+    width = p.NT;
+    int half = 0;
+    if (PAIR && tile >= p.whole) {
+      const int h = tile - p.whole;
+      tile = p.whole + h / 2;
+      width = p.NT / 2;
+      half = (h & 1) * width;
+    }
+    m = tile / p.n_tiles * m_step;
+    n0 = tile % p.n_tiles * p.NT + half;
+  };
+
   if (warp == 0) {
-    // ---- producer: the whole warp walks the adapter list, lane 0 loads
+    // ---- producer
     Ring ring(p.stages);
     SlotList<PAIR> list;
     bool ok = true;
-    // one box of X's (or u's) rows, then the columns of W (or B) for this CTA
+    // one box of X's (or u's) rows, or of the columns of W (or B) for this CTA
     auto load2 = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
       if constexpr (PAIR) tma_load_2d_pair(dst, m, mapa_rank(&bars->full[ring.stage], 0), c0, c1);
       else tma_load_2d(dst, m, &bars->full[ring.stage], c0, c1);
@@ -704,160 +758,160 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (PAIR) tma_load_3d_pair(dst, m, mapa_rank(&bars->full[ring.stage], 0), c0, c1, c2);
       else tma_load_3d(dst, m, &bars->full[ring.stage], c0, c1, c2);
     };
-    auto open = [&](uint32_t bytes) {   // PAIR: rank 0 announces both CTAs' bytes
-      return open_stage(bars, ring, PAIR ? (q == 0 ? 2 * bytes : 0) : bytes, p.status);
+    auto announce = [&](uint32_t bytes) {   // PAIR: rank 0 announces both CTAs' bytes
+      if (!PAIR || q == 0) mbar_arrive_expect_tx(&bars->full[ring.stage], PAIR ? 2 * bytes : bytes);
     };
-    for (int tile = t0; tile < tiles; tile += tstep) {
-      const int m = tile / p.n_tiles * m_step;
+    for (int tile = t0; ok && tile < tiles; tile += tstep) {
+      int m, n0, width;
+      place(tile, m, n0, width);
       const int row0 = (m + (PAIR ? q : 0)) * BM;
-      const int n0 = tile % p.n_tiles * p.NT + (PAIR ? q * nc : 0);
+      const int nc = PAIR ? width / 2 : width;   // columns this CTA loads
+      if (PAIR) n0 += q * nc;
       if (p.n_slots != nullptr && tile != t0) list.open(p, m, q);   // ahead of the steps over W
-      if (lane == 0) {
-        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-          ok = open(p.a_bytes + nc * 128);
-          if (!ok) break;
-          uint8_t* sa = smem + ring.stage * p.stage_bytes;
-          uint8_t* sb = sa + p.a_bytes;
+      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+        ok = warp_wait(bars, &bars->empty[ring.stage], ring.phase ^ 1, p.status);
+        if (!ok) break;
+        uint8_t* sa = smem + ring.stage * p.stage_bytes;
+        uint8_t* sb = sa + p.a_bytes;
+        if (elect_one()) {
+          announce(p.a_bytes + nc * 128);
           load2(sa, &xmap, kb * BK, row0);
-          if (TRANS) {   // nc rows of W, contraction along the row (K-major)
-            load2(sb, &wmap, kb * BK, n0);
-          } else {       // 64 rows of W, 64-column chunks (MN-major)
-            for (int j = 0; j < nc / 64; ++j) load2(sb + j * 64 * 128, &wmap, n0 + j * 64, kb * BK);
+          for (int j = 0; j < nc / 64; ++j) {
+            if (TRANS) load2(sb + j * 64 * 128, &wmap, kb * BK, n0 + j * 64);   // 64 rows of W (K-major)
+            else load2(sb + j * 64 * 128, &wmap, n0 + j * 64, kb * BK);         // 64 columns (MN-major)
           }
         }
+        __syncwarp();
       }
       if (tile == t0) {
         wait_prerequisites();
         if (p.n_slots != nullptr) list.open(p, m, q);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (p.n_slots == nullptr) continue;
+      if (!ok || p.n_slots == nullptr) continue;
       for (int b = 0; b < p.nb && ok; ++b) {
         int in_group = 0;
-        for (int i0 = 0; i0 < list.count && ok; i0 += per_stage) {
+        for (int i0 = 0; i0 < list.count; i0 += per_stage, ring.next()) {
           const int cnt = min(per_stage, list.count - i0);
           const bool head = in_group == 0;
+          ok = warp_wait(bars, &bars->empty[ring.stage], ring.phase ^ 1, p.status);
+          if (!ok) break;
           uint8_t* sa = smem + ring.stage * p.stage_bytes;
-          if (lane == 0) {
-            ok = open((head ? p.a_bytes : 0) + cnt * nc * p.rb * 2);
-            sa = smem + ring.stage * p.stage_bytes;
-            if (ok && head) load2(sa, &umap, b * 64, row0);
+          if (elect_one()) {
+            announce((head ? p.a_bytes : 0) + cnt * nc * p.rb * 2);
+            if (head) load2(sa, &umap, b * 64, row0);
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          __syncwarp();
           for (int j = 0; j < cnt; ++j) {
             const int id = list.get_id(i0 + j);
-            if (lane == 0 && ok) {
-              uint8_t* sb = sa + p.a_bytes + j * nc * p.rb * 2;
+            uint8_t* sb = sa + p.a_bytes + j * nc * p.rb * 2;
+            if (elect_one())
               for (int c = 0; c < nc / 64; ++c)   // rb ranks x 64 columns (zeros past rank r)
                 load3(sb + c * p.rb * 128, &emap, n0 + c * 64, b * 32, id);
-            }
+            __syncwarp();
           }
-          if (lane == 0 && ok) ring.next();
           if (++in_group == group) in_group = 0;
         }
       }
-      if (!ok) break;
     }
-    if (lane == 0 && bars->abort && (!PAIR || q == 0)) drain_copies(bars, ring);
+    if (bars->abort && (!PAIR || q == 0)) drain_copies(bars, ring);
   } else if (warp == 1 && (!PAIR || q == 0)) {
-    // ---- MMA: the whole warp walks the adapter list, lane 0 issues
+    // ---- MMA
     const int rows = PAIR ? 2 * BM : BM;
-    const uint32_t idesc = idesc_bf16(rows, p.NT, false, !TRANS);
-    const uint32_t idesc_e = idesc_bf16(rows, p.NT, false, true);
     auto commit = [&](uint64_t* bar) {
       if constexpr (PAIR) umma_commit_pair(bar);
       else umma_commit(bar);
     };
+    const uint64_t km = umma_desc_sw128(0, 16, 1024);              // K-major operand
+    const uint64_t wm = TRANS ? km : umma_desc_sw128(0, 64 * 128, 1024);
+    const uint64_t em = umma_desc_sw128(0, p.rb * 128, 1024);      // MN-major, rb rows a chunk
+    constexpr uint32_t wstep = TRANS ? 32 / 16 : 2048 / 16;        // 16 contraction elements on
     Ring ring(p.stages);
     SlotList<PAIR> list;
     bool ok = true;
     int local = 0;
     for (int tile = t0; tile < tiles; tile += tstep, ++local) {
-      const int m = tile / p.n_tiles * m_step;
+      int m, n0, width;
+      place(tile, m, n0, width);
+      const int nc = PAIR ? width / 2 : width;
+      const uint32_t idesc = idesc_bf16(rows, width, false, !TRANS);
+      const uint32_t idesc_e = idesc_bf16(rows, width, false, true);
       const int acc = local & 1;
       const uint32_t d = tmem + acc * (tmem_cols / 2);
       if (p.n_slots != nullptr && tile != t0) list.open(p, m, q);
-      if (lane == 0) {
-        if (!wait_bar(&bars->acc_empty[acc], ((local >> 1) & 1) ^ 1)) {
-          flag_timeout(p.status);
-          bars->abort = 1;
-          ok = false;
-        }
+      ok = warp_wait(bars, &bars->acc_empty[acc], ((local >> 1) & 1) ^ 1, p.status);
+      tc_fence_after();
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        ok = warp_wait(bars, &bars->full[ring.stage], ring.phase, p.status);
+        if (!ok) break;
         tc_fence_after();
-        for (int kb = kb0; ok && kb < kb1; ++kb) {
-          ok = await_stage(bars, ring, p.status);
-          if (!ok) break;
-          const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
-          const uint32_t sb = sa + p.a_bytes;
+        const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+        const uint64_t ad = desc_at(km, sa), bd = desc_at(wm, sa + p.a_bytes);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = umma_desc_sw128(sa + kk * 32, 16, 1024);
-            const uint64_t bd = TRANS ? umma_desc_sw128(sb + kk * 32, 16, 1024)
-                                      : umma_desc_sw128(sb + kk * 2048, 64 * 128, 1024);
             const uint32_t accumulate = (kb > kb0 || kk > 0) ? 1u : 0u;
-            if constexpr (PAIR) umma_bf16_pair(d, ad, bd, idesc, accumulate);
-            else umma_bf16(d, ad, bd, idesc, accumulate);
+            if constexpr (PAIR) umma_bf16_pair(d, ad + 2 * kk, bd + wstep * kk, idesc, accumulate);
+            else umma_bf16(d, ad + 2 * kk, bd + wstep * kk, idesc, accumulate);
           }
           commit(&bars->empty[ring.stage]);
-          ring.next();
         }
+        __syncwarp();
+        ring.next();
       }
       if (tile == t0) {
         wait_prerequisites();
         if (p.n_slots != nullptr) list.open(p, m, q);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       if (p.n_slots != nullptr) {
         for (int b = 0; b < p.nb && ok; ++b) {
           int in_group = 0, head_stage = 0;
-          for (int i0 = 0; i0 < list.count && ok; i0 += per_stage) {
+          for (int i0 = 0; i0 < list.count; i0 += per_stage) {
             const int cnt = min(per_stage, list.count - i0);
-            if (lane == 0) {
-              ok = await_stage(bars, ring, p.status);
-              if (in_group == 0) head_stage = ring.stage;
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(bars, &bars->full[ring.stage], ring.phase, p.status);
             if (!ok) break;
+            tc_fence_after();
+            if (in_group == 0) head_stage = ring.stage;
             const uint32_t su = smem_u32(smem + head_stage * p.stage_bytes);
             const uint32_t sb = smem_u32(smem + ring.stage * p.stage_bytes) + p.a_bytes;
             for (int j = 0; j < cnt; ++j) {
               const uint4 off = list.get_off(i0 + j);
-              if (lane == 0) {
+              const uint64_t hi = desc_at(km, su), bd = desc_at(em, sb + j * nc * p.rb * 2);
+              if (elect_one()) {
                 for (int kk = 0; kk < p.rb / 16; ++kk) {   // hi and lo of 16 ranks, same rows of B
-                  const uint64_t bd =
-                      umma_desc_sw128(sb + j * nc * p.rb * 2 + kk * 2048, p.rb * 128, 1024);
-                  const uint64_t hi = umma_desc_sw128(su + kk * 32, 16, 1024);
-                  const uint64_t lo = umma_desc_sw128(su + 64 + kk * 32, 16, 1024);
                   // without W a row's first step starts its sum (a row is in one slot only)
                   const uint32_t first = (p.kiters > 0 || b > 0 || kk > 0) ? 1u : 0u;
+                  const uint64_t h = hi + 2 * kk, l = h + 4, e = bd + 128 * kk;
                   if constexpr (PAIR) {
                     const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);
                     const bool odd = i0 + j >= list.n0;
-                    umma_bf16_rows_pair(d, hi, bd, idesc_e, odd ? none : off, odd ? off : none, first);
-                    umma_bf16_rows_pair(d, lo, bd, idesc_e, odd ? none : off, odd ? off : none, 1u);
+                    umma_bf16_rows_pair(d, h, e, idesc_e, odd ? none : off, odd ? off : none, first);
+                    umma_bf16_rows_pair(d, l, e, idesc_e, odd ? none : off, odd ? off : none, 1u);
                   } else {
-                    umma_bf16_rows(d, hi, bd, idesc_e, off, first);
-                    umma_bf16_rows(d, lo, bd, idesc_e, off, 1u);
+                    umma_bf16_rows(d, h, e, idesc_e, off, first);
+                    umma_bf16_rows(d, l, e, idesc_e, off, 1u);
                   }
                 }
               }
+              __syncwarp();
             }
-            if (lane == 0) {
-              const bool last = i0 + per_stage >= list.count || in_group + 1 == group;
+            const bool last = i0 + per_stage >= list.count || in_group + 1 == group;
+            if (elect_one()) {
               if (in_group > 0) commit(&bars->empty[ring.stage]);
               if (last) commit(&bars->empty[head_stage]);
-              ring.next();
             }
+            __syncwarp();
+            ring.next();
             if (++in_group == group) in_group = 0;
           }
         }
       }
       if (!ok) break;
-      if (lane == 0) commit(&bars->acc_full[acc]);
+      if (elect_one()) commit(&bars->acc_full[acc]);
+      __syncwarp();
     }
-    if (lane == 0 && bars->abort) drain_mmas<PAIR>(bars);
+    if (bars->abort && elect_one()) drain_mmas<PAIR>(bars);
+    __syncwarp();
   } else if (warp == 1) {
     wait_prerequisites();
   } else {
@@ -867,8 +921,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int local = 0, stored = 0;
     for (int tile = t0; tile < tiles; tile += tstep, ++local) {
       const int acc = local & 1;
-      const int row0 = (tile / p.n_tiles * m_step + (PAIR ? q : 0)) * BM;
-      const int n0 = tile % p.n_tiles * p.NT;
+      int m, n0, width;
+      place(tile, m, n0, width);
+      const int row0 = (m + (PAIR ? q : 0)) * BM;
       bool ok = !bars->abort && wait_bar(&bars->acc_full[acc], (local >> 1) & 1);
       if (!ok) {
         if (!bars->abort) flag_timeout(p.status);
@@ -895,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int step = p.out_bf16 ? 64 : 32;   // columns of a 128-byte box row
-      for (int c = 0; rows_here && c < p.NT && n0 + c < p.out_cols; c += step, ++stored) {
+      for (int c = 0; rows_here && c < width && n0 + c < p.out_cols; c += step, ++stored) {
         uint8_t* dst = box + (stored & 1) * kStagingBox;
         float v[32];
         if (stored >= 2) {
@@ -951,11 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = q * 128 + et; it < rows * groups; it += 128 * p.split) {
         const int r = it / groups, c = it % groups * 4;
         if (n0 + c >= p.out_cols) continue;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < p.split; ++k) {
-          const float4 v = ld_rank4(red + r * (p.NT + 4) + c, k);
-          a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-        }
+        const float4 a = sum_ranks(red + r * (p.NT + 4) + c, p.split);
         const size_t at = (size_t)(row0 + r) * p.out_cols + n0 + c;
         if (p.out_bf16)
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
@@ -1029,17 +1080,25 @@ __global__ void __launch_bounds__(kBucketThreads)
 // rank where it starts adds up in rank order.
 //
 // One pass over xa and dY, memory bound, so the products run on warp-level MMAs (mma.sync
-// m16n8k16), whose operands come straight from the gathered rows: 64 rows per stage,
-// cp.async, rows past an adapter's end zero-filled (both operands, so that no stale or other
-// adapter's value can meet a zero). MT = padded rank / 16.
+// m16n8k16), whose operands come straight from the gathered rows: four warps gather 64 rows a
+// stage with 16-byte asynchronous copies, four multiply, 32 columns each. (TMA's row gather,
+// four rows of 128 bytes per instruction, reached half the rate: 462 against 403 us for the
+// training step of 8192 rows, 7168 to 2048, rank 16.) Rows past an adapter's end are filled
+// with zeros in both operands, so that no other adapter's value can meet a zero.
+// MT = padded rank / 16.
 constexpr int kWgCols = 128;
 constexpr int kWgRows = 64;
-constexpr int kWgStages = 3;
-constexpr int kWgThreads = 128;
+constexpr int kWgThreads = 256;     // four warps that multiply, four that gather
+constexpr int kWgMaxStages = 6;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(on ? 16 : 0)
+               : "memory");
+}
+// Arrives on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
 __device__ __forceinline__ void ldsm4_t(uint32_t* r, const void* p) {
@@ -1064,24 +1123,25 @@ struct WgradSide {
 };
 struct WgradParams {
   WgradSide side[2];
-  int r, n, split, out_bf16;
+  int r, n, split, stages, out_bf16;
   const int32_t* off;            // [n + 1]
   const int32_t* rows;           // [off[n]]
+  uint32_t* status;
 };
 
 template <int MT>
-__global__ void __launch_bounds__(kWgThreads) wgrad_kernel(const WgradParams p) {
-  constexpr int NB = (MT + 1) / 2;                 // 32-rank blocks of a row of uq
-  constexpr int G_BYTES = kWgRows * kWgCols * 2;
-  constexpr int U_ROW = NB * 128;
-  constexpr int STAGE = G_BYTES + kWgRows * U_ROW;
+__global__ void __launch_bounds__(kWgThreads, MT <= 2 ? 2 : 1) wgrad_kernel(const WgradParams p) {
+  constexpr int NB = (MT + 1) / 2;                 // 32-rank blocks of a row of u
+  constexpr int BOX = kWgRows * 128;               // 64 rows x 128 bytes
+  constexpr int STAGE = (2 + NB) * BOX;            // two halves of the columns, then u's blocks
   constexpr int RS = kWgCols + 4;                  // floats per row of the partial sums
-  constexpr int GI = kWgRows * 16 / kWgThreads;    // 16-byte pieces per thread and stage
-  constexpr int UI = kWgRows * NB * 8 / kWgThreads;
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* head = reinterpret_cast<float*>(smem);    // partial sums [16 MT][RS], see below
-  uint8_t* stages = smem + 16 * MT * RS * 4;
-  float* tail = reinterpret_cast<float*>(stages);  // over the stages, when they are done
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kWgMaxStages], empty[kWgMaxStages];
+  __shared__ volatile int abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  float* tail = reinterpret_cast<float*>(smem);    // over the stages, when they are done
+  float* head = reinterpret_cast<float*>(smem + max(p.stages * STAGE, 16 * MT * RS * 4));
   launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int q = (int)(blockIdx.x % p.split);
@@ -1093,126 +1153,21 @@ __global__ void __launch_bounds__(kWgThreads) wgrad_kernel(const WgradParams p) 
   void* out = second ? p.side[1].out : p.side[0].out;
   const int C = second ? p.side[1].C : p.side[0].C;
   const int c0 = ct * kWgCols;
+  if (tid == 0) {
+    for (int i = 0; i < kWgMaxStages; ++i) {
+      mbar_init(&full[i], 128);
+      mbar_init(&empty[i], 4);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   wait_prerequisites();
 
   const int total = p.off[p.n];
   const int r0 = (int)((long long)total * q / p.split);
   const int r1 = (int)((long long)total * (q + 1) / p.split);
-
-  float acc[MT][4][4];
-  // rows [lo, hi) of the list (one adapter) into acc
-  auto accumulate = [&](int lo, int hi) {
-    const int blocks = (hi - lo + kWgRows - 1) / kWgRows;
-    int gi[GI], ui[UI];   // rows of the pieces this thread fetches next (-1: past the end)
-    auto index = [&](int b) {
-#pragma unroll
-      for (int i = 0; i < GI; ++i) {
-        const int at = lo + b * kWgRows + ((tid + i * kWgThreads) >> 4);
-        gi[i] = at < hi ? p.rows[at] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < UI; ++i) {
-        const int at = lo + b * kWgRows + (tid + i * kWgThreads) / (NB * 8);
-        ui[i] = at < hi ? p.rows[at] : -1;
-      }
-    };
-    auto fetch = [&](int b) {
-      uint8_t* sg = stages + b % kWgStages * STAGE;
-      uint8_t* su = sg + G_BYTES;
-#pragma unroll
-      for (int i = 0; i < GI; ++i) {
-        const int e = tid + i * kWgThreads, rr = e >> 4, ch = e & 15;
-        const bool on = gi[i] >= 0 && c0 + ch * 8 < C;
-        cp_async16(sg + rr * 256 + ((ch ^ (rr & 7)) * 16),
-                   on ? g + (size_t)gi[i] * C + c0 + ch * 8 : g, on);
-      }
-#pragma unroll
-      for (int i = 0; i < UI; ++i) {
-        const int e = tid + i * kWgThreads, rr = e / (NB * 8), ch = e % (NB * 8);
-        const bool on = ui[i] >= 0;
-        cp_async16(su + rr * U_ROW + ((ch ^ (rr & 7)) * 16),
-                   on ? uq + (size_t)ui[i] * U_ROW + ch * 16 : uq, on);
-      }
-      if (b + 1 < blocks) index(b + 1);
-    };
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
-    index(0);
-#pragma unroll
-    for (int b = 0; b < kWgStages - 1; ++b) {
-      if (b < blocks) fetch(b);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    for (int b = 0; b < blocks; ++b) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kWgStages - 2) : "memory");
-      __syncthreads();   // stage b is in; every warp is done with the stage refilled next
-      if (b + kWgStages - 1 < blocks) fetch(b + kWgStages - 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint8_t* sg = stages + b % kWgStages * STAGE;
-      const uint8_t* su = sg + G_BYTES;
-#pragma unroll
-      for (int k0 = 0; k0 < kWgRows; k0 += 16) {
-        uint32_t bf[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int rr = k0 + ((lane >> 3) & 1) * 8 + (lane & 7);
-          const int ch = warp * 4 + h * 2 + (lane >> 4);
-          ldsm4_t(bf + 4 * h, sg + rr * 256 + ((ch ^ (rr & 7)) * 16));
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int rr = k0 + (lane >> 4) * 8 + (lane & 7);
-          const int ch = (mt >> 1) * 8 + (mt & 1) * 2 + ((lane >> 3) & 1);
-          uint32_t hi4[4], lo4[4];
-          ldsm4_t(hi4, su + rr * U_ROW + ((ch ^ (rr & 7)) * 16));
-          ldsm4_t(lo4, su + rr * U_ROW + (((ch + 4) ^ (rr & 7)) * 16));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma16816(acc[mt][j], hi4, bf[2 * j], bf[2 * j + 1]);
-            mma16816(acc[mt][j], lo4, bf[2 * j], bf[2 * j + 1]);
-          }
-        }
-      }
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();     // the stages are free
-  };
-  auto put = [&](float* dst) {   // acc -> shared memory
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rr = mt * 16 + (lane >> 2), cc = warp * 32 + j * 8 + (lane & 3) * 2;
-        *reinterpret_cast<float2*>(dst + rr * RS + cc) = make_float2(acc[mt][j][0], acc[mt][j][1]);
-        *reinterpret_cast<float2*>(dst + (rr + 8) * RS + cc) =
-            make_float2(acc[mt][j][2], acc[mt][j][3]);
-      }
-  };
-  // out[a] = src of this CTA (null: zeros) + the heads of the next `more` ranks
-  auto write = [&](int a, const float* src, int more) {
-    for (int it = tid; it < p.r * (kWgCols / 4); it += kWgThreads) {
-      const int rr = it / (kWgCols / 4), cc = it % (kWgCols / 4) * 4;
-      if (c0 + cc >= C) continue;
-      float4 s = src ? *reinterpret_cast<const float4*>(src + rr * RS + cc)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 1; k <= more; ++k) {
-        const float4 v = ld_rank4(head + rr * RS + cc, q + k);
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-      }
-      const size_t at = ((size_t)a * p.r + rr) * C + c0 + cc;
-      if (p.out_bf16)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
-            make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-      else
-        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
-    }
-  };
-
-  // adapter of list row r0: the last one whose rows start at or before it and that has rows
+  // adapter of list row r0: the last one whose rows start at or before it
   int a = 0;
   if (r0 < r1) {
     int lo = 0, hi = p.n - 1;
@@ -1223,34 +1178,194 @@ __global__ void __launch_bounds__(kWgThreads) wgrad_kernel(const WgradParams p) 
     }
     a = lo;
   }
+
   int last = -1, more = 0;   // the adapter that goes on into the next ranks, and how many of them
-  for (int at = r0; at < r1; ++a) {
-    const int begin = p.off[a], end = p.off[a + 1];
-    if (begin == end) continue;
-    const int stop = min(end, r1);
-    accumulate(at, stop);
-    at = stop;
-    if (begin < r0) {                 // began in an earlier rank, which adds this part
-      put(head);
-    } else {
-      put(tail);
-      if (end <= r1) {
-        __syncthreads();
-        write(a, tail, 0);
-        __syncthreads();              // before the stages are filled again
-      } else {
+  int stage = 0;
+  uint32_t phase = 0;
+  if (warp >= 4) {
+    // ---- gather: a thread copies one 16-byte column of eight rows (and its part of u); the
+    // lanes of a warp hold the stage's 64 row numbers, the next stage's already on their way
+    const int gt = tid - 128;
+    const int gc = gt & 15;                                     // 16-byte column of the tile
+    const bool col_on = c0 + gc * 8 < C;
+    bool ok = true;
+    for (int at = r0; ok && at < r1; ++a) {
+      const int end = min(p.off[a + 1], r1);
+      int n0 = at + lane < end ? p.rows[at + lane] : -1;
+      int n1 = at + 32 + lane < end ? p.rows[at + 32 + lane] : -1;
+      for (int b = at; b < end; b += kWgRows) {
+        const int i0 = n0, i1 = n1;
+        const int nx = b + kWgRows + lane;
+        n0 = nx < end ? p.rows[nx] : -1;
+        n1 = nx + 32 < end ? p.rows[nx + 32] : -1;
+        ok = !abort_flag && wait_bar(&empty[stage], phase ^ 1);
+        if (!ok) {
+          if (!abort_flag) flag_timeout(p.status);
+          abort_flag = 1;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* sg = smem + stage * STAGE + (gc >> 3) * BOX;
+        uint8_t* su = smem + stage * STAGE + 2 * BOX;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = (gt >> 4) + 8 * i;
+          const int row = __shfl_sync(0xffffffffu, i < 4 ? i0 : i1, rr & 31);
+          const bool on = row >= 0 && col_on;
+          cp_async16(sg + rr * 128 + (((gc & 7) ^ (rr & 7)) * 16),
+                     on ? g + (size_t)row * C + c0 + gc * 8 : g, on);
+        }
+        // u: 16-byte pieces of a row that hold ranks below 16 MT
+        constexpr int PIECES = MT == 1 ? 4 : NB * 8;
+        constexpr int UI = kWgRows * PIECES / 128;
+#pragma unroll
+        for (int i = 0; i < UI; ++i) {
+          const int rr = gt / PIECES + 128 / PIECES * i, pc = gt % PIECES;
+          const int row = __shfl_sync(0xffffffffu, 2 * i < UI ? i0 : i1, rr & 31);
+          const int ch = MT == 1 ? (pc & 1) + (pc >> 1) * 4 : pc & 7;
+          const int blk = MT == 1 ? 0 : pc >> 3;
+          cp_async16(su + blk * BOX + rr * 128 + ((ch ^ (rr & 7)) * 16),
+                     row >= 0 ? uq + (size_t)row * (NB * 128) + blk * 128 + ch * 16 : uq, row >= 0);
+        }
+        cp_async_arrive(&full[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      at = max(at, end);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // none is on its way when this CTA ends
+    __syncwarp();
+  } else {
+    // ---- multiply
+    float acc[MT][4][4];
+    bool ok = true;
+    for (int at = r0; ok && at < r1; ++a) {
+      const int begin = p.off[a], end = p.off[a + 1], stop = min(end, r1);
+      if (begin == end) continue;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
+      for (int b = at; b < stop; b += kWgRows) {
+        ok = !abort_flag && wait_bar(&full[stage], phase);
+        if (!ok) {
+          if (!abort_flag) flag_timeout(p.status);
+          abort_flag = 1;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* sg = smem + stage * STAGE + (warp >> 1) * BOX;
+        const uint8_t* su = smem + stage * STAGE + 2 * BOX;
+#pragma unroll
+        for (int k0 = 0; k0 < kWgRows; k0 += 16) {
+          uint32_t bf[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int rr = k0 + ((lane >> 3) & 1) * 8 + (lane & 7);
+            const int ch = (warp & 1) * 4 + h * 2 + (lane >> 4);
+            ldsm4_t(bf + 4 * h, sg + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int rr = k0 + (lane >> 4) * 8 + (lane & 7);
+            const int ch = (mt & 1) * 2 + ((lane >> 3) & 1);
+            const uint8_t* sb = su + (mt >> 1) * BOX + rr * 128;
+            uint32_t hi4[4], lo4[4];
+            ldsm4_t(hi4, sb + ((ch ^ (rr & 7)) * 16));
+            ldsm4_t(lo4, sb + (((ch + 4) ^ (rr & 7)) * 16));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma16816(acc[mt][j], hi4, bf[2 * j], bf[2 * j + 1]);
+              mma16816(acc[mt][j], lo4, bf[2 * j], bf[2 * j + 1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      at = stop;
+      const bool began = begin >= r0, ends = end <= r1;
+      if (began && ends) {   // finished here: straight from the registers
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int rr = mt * 16 + (lane >> 2) + 8 * h;
+              const int cc = c0 + warp * 32 + j * 8 + (lane & 3) * 2;
+              if (rr >= p.r || cc >= C) continue;
+              const size_t o = ((size_t)a * p.r + rr) * C + cc;
+              if (p.out_bf16)
+                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(out) + o) =
+                    pack_bf16(acc[mt][j][2 * h], acc[mt][j][2 * h + 1]);
+              else
+                *reinterpret_cast<float2*>(static_cast<float*>(out) + o) =
+                    make_float2(acc[mt][j][2 * h], acc[mt][j][2 * h + 1]);
+            }
+        continue;
+      }
+      // began earlier: the rank where it began adds this part; else it goes on in the next
+      // ranks and is this CTA's last (all its stages are read when every warp is here)
+      if (began) {
         last = a;
         while (q + more + 1 < p.split && (int)((long long)total * (q + more + 1) / p.split) < end)
           ++more;
+        named_bar_sync(1, 128);
       }
+      float* dst = began ? tail : head;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rr = mt * 16 + (lane >> 2), cc = warp * 32 + j * 8 + (lane & 3) * 2;
+          *reinterpret_cast<float2*>(dst + rr * RS + cc) = make_float2(acc[mt][j][0], acc[mt][j][1]);
+          *reinterpret_cast<float2*>(dst + (rr + 8) * RS + cc) =
+              make_float2(acc[mt][j][2], acc[mt][j][3]);
+        }
     }
+    if (r0 == r1)                     // fewer rows than ranks: nothing to add here
+      for (int i = tid; i < 16 * MT * RS; i += 128) head[i] = 0.f;
   }
-  if (r0 == r1)                       // fewer rows than ranks: nothing to add here
-    for (int i = tid; i < 16 * MT * RS; i += kWgThreads) head[i] = 0.f;
+  // out[z] = this CTA's tail (or zeros) + the heads of the next ranks
+  auto write = [&](int z, bool own, int ranks) {
+    for (int it = tid; it < p.r * (kWgCols / 4); it += kWgThreads) {
+      const int rr = it / (kWgCols / 4), cc = it % (kWgCols / 4) * 4;
+      if (c0 + cc >= C) continue;
+      float4 s = own ? *reinterpret_cast<const float4*>(tail + rr * RS + cc)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 1; k <= ranks; ++k) {
+        const float4 v = ld_rank4(head + rr * RS + cc, q + k);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      const size_t o = ((size_t)z * p.r + rr) * C + c0 + cc;
+      if (p.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
+            make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = s;
+    }
+  };
+  last = __shfl_sync(0xffffffffu, last, 0);
+  __shared__ int s_last, s_more;      // known to the warps that multiply
+  if (tid == 0) {
+    s_last = last;
+    s_more = more;
+  }
+  __syncwarp();
   cluster_sync_all();                 // every head is in place
-  if (last >= 0) write(last, tail, more);
+  if (s_last >= 0) write(s_last, true, s_more);
   for (int z = q; z < p.n; z += p.split)   // adapters without rows
-    if (p.off[z] == p.off[z + 1]) write(z, nullptr, 0);
+    if (p.off[z] == p.off[z + 1]) write(z, false, 0);
   cluster_sync_all();                 // no rank leaves while another reads its head
 }
 
@@ -1427,7 +1542,7 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   // an MMA reads 128 rows from a stage's start, past a short batch's own: in bounds for the
   // last stage too
   const size_t tail = A_BYTES - p.a_bytes;
-  const size_t fixed = align_up((size_t)BM * (p.rp + 1) * 4, 16) + tail + kBarBytes + 1024;
+  const size_t fixed = (size_t)BM * (p.rp + 4) * 4 + tail + kBarBytes + 1024;
   p.stages = std::min<int>(kMaxStages, (int)((kMaxSmem - sizeof(TileSlots) - fixed) / p.stage_bytes));
   // one wave of clusters, a rank at least two steps
   int i = 0;
@@ -1460,6 +1575,12 @@ struct ProjForm {
   int NT, split, pair, stages, stage_bytes;
   size_t smem;
 };
+// Tiles of the last wave of pairs that are run as halves: all of them if they then still fit
+// one wave.
+int pair_tail(int tiles, const Device& dev) {
+  const int rest = tiles % dev.clusters[1];
+  return 2 * rest <= dev.clusters[1] ? rest : 0;
+}
 ProjForm choose_form(int T, int kiters, int cols, const Device& dev) {
   const int mt = (T + BM - 1) / BM, a_bytes = tile_rows(T) * BK * 2;
   ProjForm best = {};
@@ -1484,11 +1605,13 @@ ProjForm choose_form(int T, int kiters, int cols, const Device& dev) {
         f.smem = (size_t)f.stages * f.stage_bytes + tail + fixed;
         const double tiles = (double)((cols + nt - 1) / nt) * (pair ? (mt + 1) / 2 : mt);
         const double cap = dev.clusters[pair ? 1 : i];
-        const double waves = std::ceil(tiles / cap);
+        const double waves = std::ceil(tiles / cap) - (pair && pair_tail((int)tiles, dev) ? 0.4 : 0.0);
         const double live = std::min(tiles, cap) * (pair ? 2 : split);   // CTAs at once
         const double mma = 2.2 * nt / 1.9e3;
         const double fill = f.stage_bytes / (64 * 1.9e3);
-        const double hbm = (double)(pair ? nt / 2 : nt) * 128 * live / mt / 6.0e6;
+        const double w_bytes = (pair ? nt / 2 : nt) * 128;
+        // W's bytes from HBM: 6 TB/s shared by the CTAs, at most 55 GB/s into one SM
+        const double hbm = w_bytes / mt * std::max(live / 6.0e6, 1 / 5.5e4);
         const double step = std::max(std::max(mma, fill), std::max(hbm, 2.0 / f.stages));
         const double t = waves * (std::ceil((double)kiters / split) * step + (split > 1 ? 3.0 : 1.0));
         if (best_t == 0 || t < best_t) {
@@ -1537,8 +1660,7 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
   bool ok = make_map(&om, out, p.out_bf16, cols, d.T, 0, 32);
   if (W) {
     ok = ok && make_map(&xm, in, true, C, d.T, 0, rows);
-    ok = ok && (trans ? make_map(&wm, W, true, C, cols, 0, f.pair ? p.NT / 2 : p.NT)
-                      : make_map(&wm, W, true, cols, C, 0, BK));
+    ok = ok && (trans ? make_map(&wm, W, true, C, cols, 0, 64) : make_map(&wm, W, true, cols, C, 0, BK));
   } else {
     xm = wm = om;   // not read
   }
@@ -1550,7 +1672,11 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
   }
   if (!ok) return MOK_ERR_CUDA;
   const int csize = f.pair ? 2 : f.split;
-  const int tiles = (f.pair ? (p.m_tiles + 1) / 2 : p.m_tiles) * p.n_tiles;
+  int tiles = (f.pair ? (p.m_tiles + 1) / 2 : p.m_tiles) * p.n_tiles;
+  if (f.pair) {
+    p.whole = tiles - pair_tail(tiles, dev);
+    tiles += tiles - p.whole;
+  }
   const int grid = f.split > 1 ? tiles * csize
                                : std::min(tiles, dev.clusters[f.pair]) * csize;
   auto go = [&](auto kernel) {
@@ -1564,33 +1690,39 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
 
 mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, const void* xa,
                      const void* dY, const char* ws, const WorkParts& wp, void* dA, void* dB,
-                     mok_out_dtype type, cudaStream_t s) {
+                     mok_out_dtype type, uint32_t* status, cudaStream_t s) {
   WgradParams p = {};
-  auto side = [](const char* q, const void* g, void* out, int C) {
-    return WgradSide{reinterpret_cast<const uint8_t*>(q), static_cast<const __nv_bfloat16*>(g), out,
-                     C, (C + kWgCols - 1) / kWgCols};
-  };
-  p.side[0] = side(vq, xa, dA, d.K);
-  p.side[1] = side(uq, dY, dB, d.N);
+  p.side[0] = WgradSide{reinterpret_cast<const uint8_t*>(vq), static_cast<const __nv_bfloat16*>(xa),
+                        dA, d.K, (d.K + kWgCols - 1) / kWgCols};
+  p.side[1] = WgradSide{reinterpret_cast<const uint8_t*>(uq), static_cast<const __nv_bfloat16*>(dY),
+                        dB, d.N, (d.N + kWgCols - 1) / kWgCols};
   p.r = d.r;
   p.n = d.n;
   p.out_bf16 = type == MOK_OUT_BF16;
   p.off = reinterpret_cast<const int32_t*>(ws + wp.off);
   p.rows = reinterpret_cast<const int32_t*>(ws + wp.rows);
+  p.status = status;
   // row shares of at least two stages
   p.split = 1;
   while (p.split < 8 && d.T > 4 * p.split * kWgRows) p.split *= 2;
   const int mt = padded_rank(d.r) / 16, nb = (mt + 1) / 2;
   const size_t part = (size_t)mt * 16 * (kWgCols + 4) * 4;
-  const size_t stages = (size_t)kWgStages * kWgRows * (kWgCols * 2 + nb * 128);
-  const size_t smem = part + std::max(stages, part);
+  const size_t stage = (size_t)(2 + nb) * kWgRows * 128;
+  // two CTAs per SM where three stages allow it
+  const size_t fixed = part + 1024, half = 112 * 1024;
+  const size_t room = fixed + 3 * stage <= half ? half : kMaxSmem - 1024;
+  p.stages = std::min<int>(kWgMaxStages, (int)((room - fixed) / stage));
+  const size_t smem = std::max(p.stages * stage, part) + fixed;
   const int grid = (p.side[0].ctiles + p.side[1].ctiles) * p.split;
+  auto go = [&](auto kernel) {
+    return launch(kernel, grid, kWgThreads, smem, p.split, true, s, p);
+  };
   cudaError_t e;
   switch (mt) {
-    case 1: e = launch(wgrad_kernel<1>, grid, kWgThreads, smem, p.split, true, s, p); break;
-    case 2: e = launch(wgrad_kernel<2>, grid, kWgThreads, smem, p.split, true, s, p); break;
-    case 4: e = launch(wgrad_kernel<4>, grid, kWgThreads, smem, p.split, true, s, p); break;
-    default: e = launch(wgrad_kernel<8>, grid, kWgThreads, smem, p.split, true, s, p); break;
+    case 1: e = go(wgrad_kernel<1>); break;
+    case 2: e = go(wgrad_kernel<2>); break;
+    case 4: e = go(wgrad_kernel<4>); break;
+    default: e = go(wgrad_kernel<8>); break;
   }
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
@@ -1673,7 +1805,8 @@ extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_wei
   if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
   mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, status, true, *dev, s);
   if (st != MOK_OK) return st;
-  st = run_wgrad(d, sv + wp.v.uq, ws + wp.v.uq, x_ad ? x_ad : x, dY, ws, wp, dA, dB, out, s);
+  st = run_wgrad(d, sv + wp.v.uq, ws + wp.v.uq, x_ad ? x_ad : x, dY, ws, wp, dA, dB, out,
+                 status, s);
   if (st != MOK_OK) return st;
   st = run_proj(d, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, true,
                 *dev, s);

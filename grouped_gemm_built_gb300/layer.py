@@ -47,13 +47,16 @@ def _result_code(dtype, name: str) -> int:
     return _RESULT_CODES[dtype]
 
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _on_current_stream(index: int, fn, *args):
-    """``fn(*args, stream)`` with CUDA device ``index`` current and its current stream."""
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch.cuda.current_device():
-        return fn(*args, stream)
+    """``fn(*args, stream)`` with CUDA device ``index`` current and its current stream. (Raw
+    handles: building a stream object or entering a device context takes as long as a launch.)"""
+    if index == _current_device():
+        return fn(*args, _raw_stream(index))
     with torch.cuda.device(index):
-        return fn(*args, stream)
+        return fn(*args, _raw_stream(index))
 
 
 class MoELayer:

@@ -38,20 +38,24 @@ class Routing:
         mok.mok_route(self.rule, 0, None, mok.MOK_OUT_F32, None, None, None, None)  # checks it
 
     def _logits(self, logits):
+        """(rows, address, type code, device) of [T,E] logits."""
         dt = logits.dtype if isinstance(logits, torch.Tensor) else None
         code = _result_code(dt, "logits")
-        if logits.dim() != 2 or logits.shape[1] != self.E:
-            raise ValueError(f"logits must be [T, {self.E}], got {tuple(logits.shape)}")
-        return _dev(logits, "logits", dt, logits.numel()), code, logits.shape[0]
+        shape = logits.shape
+        if len(shape) != 2 or shape[1] != self.E:
+            raise ValueError(f"logits must be [T, {self.E}], got {tuple(shape)}")
+        T = shape[0]
+        return T, _dev(logits, "logits", dt, T * self.E), code, logits.device
 
     def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None):
         """(topk_idx [T,k] int32, gates [T,k] fp32) from logits [T,E] bf16 or fp32 and the
         selection bias [E] fp32."""
-        pl, code, T = self._logits(logits)
-        pb = _dev(bias, "bias", torch.float32, self.E, optional=True)
-        idx = torch.empty((T, self.k), dtype=torch.int32, device=logits.device)
-        gates = torch.empty((T, self.k), dtype=torch.float32, device=logits.device)
-        _on_current_stream(logits.get_device(), mok.mok_route, self.rule, T, pl, code, pb,
+        T, pl, code, device = self._logits(logits)
+        pb = None if bias is None else _dev(bias, "bias", torch.float32, self.E)
+        shape = (T, self.k)
+        idx = torch.empty(shape, dtype=torch.int32, device=device)
+        gates = torch.empty(shape, dtype=torch.float32, device=device)
+        _on_current_stream(device.index, mok.mok_route, self.rule, T, pl, code, pb,
                            idx.data_ptr(), gates.data_ptr())
         return idx, gates
 
@@ -59,12 +63,12 @@ class Routing:
                  dtype: Optional[torch.dtype] = None):
         """dlogits [T,E] (``dtype``, the logits' type by default) from dgates [T,k] fp32, at
         the choice that ``forward`` made from these logits."""
-        pl, code, T = self._logits(logits)
+        T, pl, code, device = self._logits(logits)
         dtype = dtype or logits.dtype
         dcode = _result_code(dtype, "dlogits")
         pi = _dev(topk_idx, "topk_idx", torch.int32, T * self.k)
         pd = _dev(dgates, "dgates", torch.float32, T * self.k)
-        out = torch.empty((T, self.E), dtype=dtype, device=logits.device)
-        _on_current_stream(logits.get_device(), mok.mok_route_bwd, self.rule, T, pl, code, pi, pd,
+        out = torch.empty((T, self.E), dtype=dtype, device=device)
+        _on_current_stream(device.index, mok.mok_route_bwd, self.rule, T, pl, code, pi, pd,
                            out.data_ptr(), dcode)
         return out
