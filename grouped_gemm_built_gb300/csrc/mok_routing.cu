@@ -31,12 +31,12 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 
 // A logit as the rule reads it: NaN masks like -inf, +inf is the largest finite value.
-__device__ __forceinline__ float clean(float l) { return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
 // Unsigned key in the order of v (equal for -0 and +0; -inf lowest, above 0 = "no candidate").
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
@@ -55,6 +55,7 @@ struct Rule {
   int T, E, k, groups, per, top_groups;
   bool sigmoid, top2, renorm;
   bool vec;          // rows of logits (and gradients) allow vector accesses
+  bool vec_bias;
   int lanes_shift;   // log2 of the lanes per group, -1: groups do not fall on such runs
   float scale;
 };
@@ -141,7 +142,8 @@ __device__ __forceinline__ void store_row(T* row, int e0, int E, bool vec, const
 }
 
 // Softmax over the warp's logits s (cleaned): s becomes the scores, m and 1 / z its
-// statistics. A fully masked row has scores 0.
+// statistics. A fully masked row has scores 0. __expf: 2^-22 relative near 0, where a sum's
+// weight is, and below 1e-5 down to the smallest normal score.
 template <int NV>
 __device__ __forceinline__ void warp_softmax(float* s, float& m, float& inv_z) {
   m = s[0];
@@ -152,7 +154,7 @@ __device__ __forceinline__ void warp_softmax(float* s, float& m, float& inv_z) {
   float z = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    s[i] = expf(s[i] - m);
+    s[i] = __expf(s[i] - m);
     z += s[i];
   }
   z = warp_sum(z);
@@ -171,41 +173,53 @@ __global__ void __launch_bounds__(32 * kWarps)
   const LT* row = logits + (size_t)t * q.E;
   const int e0 = lane * NV;
   const uint32_t masked = order_key(-INFINITY);
+  __shared__ uint2 s_list[kWarps][32];
 
   // scores; key = 0: no candidate (past E, in a dropped group, or taken)
   float s[NV];
   uint32_t key[NV];
   load_row<NV>(row, e0, q.E, q.vec, -INFINITY, s);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    s[i] = clean(s[i]);
-    key[i] = order_key(s[i]);
-  }
+  for (int i = 0; i < NV; ++i) s[i] = clean(s[i]);
   float m = 0.f, inv_z = 0.f;
   const bool on_logits = !q.sigmoid && bias == nullptr;
+  if (on_logits) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = order_key(s[i]);
+  }
   if (!on_logits || (q.top_groups < q.groups && q.top2) || !q.renorm) {
+    unsigned off = 0;   // masked experts of this lane
+#pragma unroll
+    for (int i = 0; i < NV; ++i) off |= s[i] == -INFINITY ? 1u << i : 0u;
     if (q.sigmoid) {
       // the choice needs the scores to a few ulp only (the gates below are full precision)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + expf(-s[i]));
+      for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-s[i]));
     } else {
       warp_softmax<NV>(s, m, inv_z);
     }
     // choice scores: s becomes s + bias, -inf for masked experts
+    if (bias != nullptr) {
+      float c[NV];
+      load_row<NV>(bias, e0, q.E, q.vec_bias, 0.f, c);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (key[i] == masked) {
-        s[i] = -INFINITY;
-      } else if (bias != nullptr) {
-        const float c = s[i] + bias[e0 + i];
-        s[i] = c > -INFINITY ? c : -INFINITY;   // a NaN bias masks the choice too
-      }
-      if (!on_logits) key[i] = order_key(s[i]);
+      for (int i = 0; i < NV; ++i) s[i] = fmaxf(s[i] + c[i], -INFINITY);   // a NaN bias masks the choice too
+    }
+    if (off) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (off >> i & 1u) s[i] = -INFINITY;
+    }
+    if (!on_logits) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = order_key(s[i]);
     }
   }
+  if (e0 + NV > q.E) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (e0 + i >= q.E) key[i] = 0;
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i >= q.E) key[i] = 0;
+  }
 
   if (q.top_groups < q.groups) {
     uint32_t gkey;      // of the group of this lane (lanes_shift >= 0), else of group `lane`
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       uint32_t b1 = 0, b2 = 0;   // the group's two largest choice scores
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const uint32_t x = e0 + i >= q.E ? 0u : q.top2 ? order_key(s[i]) : key[i];
+        const uint32_t x = on_logits && q.top2 && key[i] ? order_key(s[i]) : key[i];
         b2 = max(b2, min(b1, x));
         b1 = max(b1, x);
       }
@@ -233,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int e = e0 + i;
-          const uint32_t x = e < g0 || e >= g1 ? 0u : q.top2 ? order_key(s[i]) : key[i];
+          const uint32_t x = e < g0 || e >= g1 ? 0u : on_logits && q.top2 ? order_key(s[i]) : key[i];
           b2 = max(b2, min(b1, x));
           b1 = max(b1, x);
         }
@@ -269,28 +283,65 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
   }
 
-  // the k largest; lane j keeps the j-th id. Only the winning lane's maximum changes.
+  // the k largest; lane j keeps the j-th id
   int mine = 0;
-  uint32_t b = 0;
+  uint32_t b = 0;   // this lane's largest
 #pragma unroll
   for (int i = 0; i < NV; ++i) b = max(b, key[i]);
+  // The k-th largest of the lanes' maxima bounds the k-th largest score from below; what
+  // reaches it, little more than k, usually fits one candidate per lane. (Lanes with equal
+  // maxima leave together: the bound may come out lower, never higher.)
+  uint32_t bound = 0, left = b;
   for (int j = 0; j < q.k; ++j) {
-    const uint32_t w = __reduce_max_sync(kAll, b);
-    const int win = __ffs(__ballot_sync(kAll, b == w)) - 1;
-    int at = 0;
-    if (lane == win) {
+    bound = __reduce_max_sync(kAll, left);
+    if (left == bound) left = 0;
+  }
+  bound = max(bound, 1u);
+  int have = 0;
 #pragma unroll
-      for (int i = NV - 1; i >= 0; --i)
-        if (key[i] == w) at = i;
-      b = 0;
+  for (int i = 0; i < NV; ++i) have += key[i] >= bound;
+  int upto = have;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (i == at) key[i] = 0;
-        b = max(b, key[i]);
-      }
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(kAll, upto, off);
+    if (lane >= off) upto += o;
+  }
+  const int total = __shfl_sync(kAll, upto, 31);
+  if (total <= 32) {
+    uint2* list = s_list[threadIdx.x >> 5];
+    int at = upto - have;   // candidates in ascending id
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (key[i] >= bound) list[at++] = make_uint2(key[i], (uint32_t)(e0 + i));
+    __syncwarp();
+    const uint2 c = lane < total ? list[lane] : make_uint2(0u, 0u);
+    uint32_t mykey = c.x;
+    for (int j = 0; j < q.k; ++j) {
+      const uint32_t w = __reduce_max_sync(kAll, mykey);
+      const int win = __ffs(__ballot_sync(kAll, mykey == w)) - 1;
+      const int e = __shfl_sync(kAll, (int)c.y, win);
+      if (lane == j) mine = e;
+      if (lane == win) mykey = 0;
     }
-    at = __shfl_sync(kAll, at, win);
-    if (lane == j) mine = win * NV + at;
+  } else {   // many equal scores: one maximum of all at a time
+    for (int j = 0; j < q.k; ++j) {
+      const uint32_t w = __reduce_max_sync(kAll, b);
+      const int win = __ffs(__ballot_sync(kAll, b == w)) - 1;
+      int at = 0;
+      if (lane == win) {
+#pragma unroll
+        for (int i = NV - 1; i >= 0; --i)
+          if (key[i] == w) at = i;
+        b = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (i == at) key[i] = 0;
+          b = max(b, key[i]);
+        }
+      }
+      at = __shfl_sync(kAll, at, win);
+      if (lane == j) mine = win * NV + at;
+    }
   }
 
   // gates from the scores without the bias, one lane per slot
@@ -423,7 +474,7 @@ bool make_rule(const mok_routing* r, int T, Rule* q) {
   if (!std::isfinite(r->scale)) return false;
   *q = Rule{T, r->E, r->k, r->groups, r->E / r->groups, r->top_groups,
             r->score == MOK_SCORE_SIGMOID, r->group_score == MOK_GROUP_TOP2, r->renormalize != 0,
-            false, -1, r->scale};
+            false, false, -1, r->scale};
   const int nv = lane_width(r->E);
   if (q->per % nv == 0)
     for (int s = 0; s <= 5; ++s)
@@ -453,6 +504,7 @@ extern "C" mok_status mok_route(const mok_routing* rule, int T, const void* logi
       !aligned_to(topk_idx, 4) || !aligned_to(gates, 4))
     return MOK_ERR_INVALID_ARG;
   q.vec = rows_vectorize(q.E, logits, logits_type);
+  q.vec_bias = bias && rows_vectorize(q.E, bias, MOK_OUT_F32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_width(q.E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
