@@ -1568,9 +1568,12 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
 }
 
 // Form of the projection for [T][C] x [C][cols]: the candidate with the least estimated time,
-// in microseconds: waves x (steps x time of a step + fixed). A step's time is the largest of
-// the tensor core's (2.2 clocks per column at 1.9 GHz), its bytes' way into the SM's shared
-// memory (64 bytes a clock), W's out of HBM, and the memory's latency over the ring's stages.
+// in microseconds: waves x (steps x time of a step + fixed) + the last epilogue. A step's time
+// is the largest of the tensor core's, its bytes' way into the SM's shared memory, all SMs'
+// out of L2, W's out of HBM (narrow 64-column pieces of its rows at two thirds of the rate),
+// and the memory's latency over the ring's stages. The constants are fitted to the times of
+// every form at 112 shapes, 1 to 8192 rows and 256 x 256 to 7168 x 2048: the choice then costs
+// 1.7% against the best form on average.
 struct ProjForm {
   int NT, split, pair, stages, stage_bytes;
   size_t smem;
@@ -1605,15 +1608,17 @@ ProjForm choose_form(int T, int kiters, int cols, const Device& dev) {
         f.smem = (size_t)f.stages * f.stage_bytes + tail + fixed;
         const double tiles = (double)((cols + nt - 1) / nt) * (pair ? (mt + 1) / 2 : mt);
         const double cap = dev.clusters[pair ? 1 : i];
-        const double waves = std::ceil(tiles / cap) - (pair && pair_tail((int)tiles, dev) ? 0.4 : 0.0);
+        const double waves = std::ceil(tiles / cap);
         const double live = std::min(tiles, cap) * (pair ? 2 : split);   // CTAs at once
-        const double mma = 2.2 * nt / 1.9e3;
-        const double fill = f.stage_bytes / (64 * 1.9e3);
         const double w_bytes = (pair ? nt / 2 : nt) * 128;
-        // W's bytes from HBM: 6 TB/s shared by the CTAs, at most 55 GB/s into one SM
-        const double hbm = w_bytes / mt * std::max(live / 6.0e6, 1 / 5.5e4);
-        const double step = std::max(std::max(mma, fill), std::max(hbm, 2.0 / f.stages));
-        const double t = waves * (std::ceil((double)kiters / split) * step + (split > 1 ? 3.0 : 1.0));
+        double hbm = w_bytes / mt * std::max(live / 5.2e6, 1 / 6.6e4);
+        if (mt == 1 && nt == 64) hbm *= 1.5;
+        const double step = std::max({0.0014 * nt, f.stage_bytes / 1.8e5, live * f.stage_bytes / 1.32e7,
+                                      hbm, 0.42 / f.stages});
+        const double fill = std::min(T, BM) / (double)BM;   // of a tile's rows
+        const double fixed_t = pair ? 2.1 : split == 1 ? 1.7 : 2.8 + 4.3 * fill * nt / 128;
+        const double t = waves * (std::ceil((double)kiters / split) * step + fixed_t) +
+                         (split == 1 ? 2.75 * fill * nt / 256 : 0.0);
         if (best_t == 0 || t < best_t) {
           best_t = t;
           best = f;
