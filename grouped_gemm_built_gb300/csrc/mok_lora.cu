@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1073,46 +1074,46 @@ __global__ void __launch_bounds__(kBucketThreads)
 
 // ------------------------------------------------------------------ weight gradients
 // dA[a] = sum over adapter a's rows t of vq[t]^T xa[t], and dB[a] the same of uq and dY, in one
-// launch. A CTA owns 128 columns of one of the two and an equal share of the row list
-// (adapter by adapter), whatever the adapters' sizes; the `split` shares of a block of columns
-// are the ranks of a cluster. An adapter that lies inside a share is finished there. One that
-// goes on into the next ranks' shares leaves partial sums in their shared memory, which the
-// rank where it starts adds up in rank order.
+// launch. A CTA owns N columns of one of the two and an equal share of the row list (adapter
+// by adapter), whatever the adapters' sizes; the `split` shares of a block of columns are the
+// ranks of a cluster. An adapter that lies inside a share is finished there. One that goes on
+// into the next ranks' shares leaves partial sums in their shared memory, which the rank where
+// it starts adds up in rank order.
 //
-// One pass over xa and dY, memory bound, so the products run on warp-level MMAs (mma.sync
-// m16n8k16), whose operands come straight from the gathered rows: four warps gather 64 rows a
-// stage with 16-byte asynchronous copies, four multiply, 32 columns each. (TMA's row gather,
-// four rows of 128 bytes per instruction, reached half the rate: 462 against 403 us for the
-// training step of 8192 rows, 7168 to 2048, rank 16.) Rows past an adapter's end are filled
-// with zeros in both operands, so that no other adapter's value can meet a zero.
-// MT = padded rank / 16.
-constexpr int kWgCols = 128;
+// One pass over xa and dY, memory bound: 64 rows of the list a stage, gathered by four warps
+// with 16-byte asynchronous copies (TMA's row gather, four rows of 128 bytes an instruction,
+// reached half the rate). A stage holds xa or dY [64 rows][N], the rows' hi values [64][ranks]
+// and their lo values, all contraction-row by contraction-row (MN-major operands), so two MMAs
+// per 16 rows, hi and lo, sum D[rank][column] in TMEM. Two accumulators: an adapter's results
+// leave while the next one's rows are multiplied. (On warp-level MMAs the launch grew with the
+// rank, to 199 us at rank 128 for 8192 rows.) Rows past an adapter's end are filled with zeros in
+// both operands, so that no other adapter's value can meet a zero; ranks past RP and the
+// duplicate half of a short M are accumulator rows that nothing reads.
 constexpr int kWgRows = 64;
-constexpr int kWgThreads = 256;     // four warps that multiply, four that gather
-constexpr int kWgMaxStages = 6;
+constexpr int kWgThreads = 288;      // four warps that gather, one MMA, four epilogue
+constexpr int kWgBox = kWgRows * 128;
+
+template <int RP>
+struct WgShape {
+  static constexpr int N = RP <= 64 ? 256 : 128;        // columns of a CTA
+  static constexpr int UT = RP <= 64 ? 1 : 2;           // 64-rank tiles of hi (and of lo)
+  static constexpr int STAGE = (N / 64 + 2 * UT) * kWgBox;
+  static constexpr int STAGES = RP <= 32 ? 4 : 3;
+  static constexpr int LAG = STAGES - 2;                // copies in flight behind the newest
+  static constexpr int RS = N + 4;                      // floats per row of the partial sums
+  static constexpr int PART = RP * RS * 4;
+  static constexpr int SMEM = STAGES * STAGE + PART + kBarBytes + 1024;
+  static_assert(STAGES * STAGE >= PART && SMEM <= (int)kMaxSmem, "shared memory");
+};
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(on ? 16 : 0)
                : "memory");
 }
-// Arrives on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t* r, const void* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_u32(p))
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 struct WgradSide {
@@ -1123,27 +1124,25 @@ struct WgradSide {
 };
 struct WgradParams {
   WgradSide side[2];
-  int r, n, split, stages, out_bf16;
+  int r, n, split, out_bf16;
   const int32_t* off;            // [n + 1]
   const int32_t* rows;           // [off[n]]
   uint32_t* status;
 };
 
-template <int MT>
-__global__ void __launch_bounds__(kWgThreads, MT <= 2 ? 2 : 1) wgrad_kernel(const WgradParams p) {
-  constexpr int NB = (MT + 1) / 2;                 // 32-rank blocks of a row of u
-  constexpr int BOX = kWgRows * 128;               // 64 rows x 128 bytes
-  constexpr int STAGE = (2 + NB) * BOX;            // two halves of the columns, then u's blocks
-  constexpr int RS = kWgCols + 4;                  // floats per row of the partial sums
+template <int RP>
+__global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams p) {
+  using S = WgShape<RP>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kWgMaxStages], empty[kWgMaxStages];
-  __shared__ volatile int abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   float* tail = reinterpret_cast<float*>(smem);    // over the stages, when they are done
-  float* head = reinterpret_cast<float*>(smem + max(p.stages * STAGE, 16 * MT * RS * 4));
+  float* head = reinterpret_cast<float*>(smem + S::STAGES * S::STAGE);   // [RP][RS]
+  Bars* bars = reinterpret_cast<Bars*>(smem + S::STAGES * S::STAGE + S::PART);
+  __shared__ int s_last, s_more;
   launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known uniform
   const int q = (int)(blockIdx.x % p.split);
   int ct = (int)(blockIdx.x / p.split);
   const bool second = ct >= p.side[0].ctiles;
@@ -1152,16 +1151,27 @@ __global__ void __launch_bounds__(kWgThreads, MT <= 2 ? 2 : 1) wgrad_kernel(cons
   const __nv_bfloat16* g = second ? p.side[1].g : p.side[0].g;
   void* out = second ? p.side[1].out : p.side[0].out;
   const int C = second ? p.side[1].C : p.side[0].C;
-  const int c0 = ct * kWgCols;
+  const int c0 = ct * S::N;
   if (tid == 0) {
-    for (int i = 0; i < kWgMaxStages; ++i) {
-      mbar_init(&full[i], 128);
-      mbar_init(&empty[i], 4);
+    for (int i = 0; i < S::STAGES; ++i) {
+      mbar_init(&bars->full[i], 128);
+      mbar_init(&bars->empty[i], 1);
     }
-    abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->acc_full[i], 1);
+      mbar_init(&bars->acc_empty[i], 128);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    s_last = -1;
+    s_more = 0;
     fence_mbar_init();
   }
+  if (warp == 4) tmem_alloc(&bars->tmem, 512);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
   wait_prerequisites();
 
   const int total = p.off[p.n];
@@ -1179,15 +1189,15 @@ __global__ void __launch_bounds__(kWgThreads, MT <= 2 ? 2 : 1) wgrad_kernel(cons
     a = lo;
   }
 
-  int last = -1, more = 0;   // the adapter that goes on into the next ranks, and how many of them
-  int stage = 0;
-  uint32_t phase = 0;
-  if (warp >= 4) {
-    // ---- gather: a thread copies one 16-byte column of eight rows (and its part of u); the
-    // lanes of a warp hold the stage's 64 row numbers, the next stage's already on their way
-    const int gt = tid - 128;
-    const int gc = gt & 15;                                     // 16-byte column of the tile
+  if (warp < 4) {
+    // ---- gather: a thread copies one 16-byte column of the stage's rows (and its pieces of
+    // u); the lanes of a warp hold the 64 row numbers, the next stage's already on their way
+    constexpr int GC = S::N / 8;                       // 16-byte columns of a row
+    constexpr int GI = kWgRows * GC / 128, UP = RP / 4, UI = kWgRows * UP / 128;
+    const int gc = tid % GC;
     const bool col_on = c0 + gc * 8 < C;
+    Ring ring(S::STAGES);
+    int done = 0, pending = 0;                         // next stage to hand over, stages before it
     bool ok = true;
     for (int at = r0; ok && at < r1; ++a) {
       const int end = min(p.off[a + 1], r1);
@@ -1198,155 +1208,160 @@ __global__ void __launch_bounds__(kWgThreads, MT <= 2 ? 2 : 1) wgrad_kernel(cons
         const int nx = b + kWgRows + lane;
         n0 = nx < end ? p.rows[nx] : -1;
         n1 = nx + 32 < end ? p.rows[nx + 32] : -1;
-        ok = !abort_flag && wait_bar(&empty[stage], phase ^ 1);
-        if (!ok) {
-          if (!abort_flag) flag_timeout(p.status);
-          abort_flag = 1;
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(bars, &bars->empty[ring.stage], ring.phase ^ 1, p.status);
         if (!ok) break;
-        uint8_t* sg = smem + stage * STAGE + (gc >> 3) * BOX;
-        uint8_t* su = smem + stage * STAGE + 2 * BOX;
+        uint8_t* sg = smem + ring.stage * S::STAGE;
+        uint8_t* su = sg + S::N / 64 * kWgBox;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = (gt >> 4) + 8 * i;
-          const int row = __shfl_sync(0xffffffffu, i < 4 ? i0 : i1, rr & 31);
+        for (int i = 0; i < GI; ++i) {
+          const int rr = tid / GC + 128 / GC * i;
+          const int row = __shfl_sync(0xffffffffu, 2 * i < GI ? i0 : i1, rr & 31);
           const bool on = row >= 0 && col_on;
-          cp_async16(sg + rr * 128 + (((gc & 7) ^ (rr & 7)) * 16),
+          cp_async16(sg + (gc >> 3) * kWgBox + rr * 128 + (((gc & 7) ^ (rr & 7)) * 16),
                      on ? g + (size_t)row * C + c0 + gc * 8 : g, on);
         }
-        // u: 16-byte pieces of a row that hold ranks below 16 MT
-        constexpr int PIECES = MT == 1 ? 4 : NB * 8;
-        constexpr int UI = kWgRows * PIECES / 128;
 #pragma unroll
         for (int i = 0; i < UI; ++i) {
-          const int rr = gt / PIECES + 128 / PIECES * i, pc = gt % PIECES;
+          const int rr = tid / UP + 128 / UP * i, pc = tid % UP;
           const int row = __shfl_sync(0xffffffffu, 2 * i < UI ? i0 : i1, rr & 31);
-          const int ch = MT == 1 ? (pc & 1) + (pc >> 1) * 4 : pc & 7;
-          const int blk = MT == 1 ? 0 : pc >> 3;
-          cp_async16(su + blk * BOX + rr * 128 + ((ch ^ (rr & 7)) * 16),
-                     row >= 0 ? uq + (size_t)row * (NB * 128) + blk * 128 + ch * 16 : uq, row >= 0);
+          const int h = pc % (RP / 8), lo = pc / (RP / 8);   // eight ranks, hi or lo
+          cp_async16(su + (lo * S::UT + (h >> 3)) * kWgBox + rr * 128 + (((h & 7) ^ (rr & 7)) * 16),
+                     row >= 0 ? uq + ((size_t)row * ((RP + 31) / 32) + (h >> 2)) * 128 + lo * 64 +
+                                    (h & 3) * 16
+                              : uq,
+                     row >= 0);
         }
-        cp_async_arrive(&full[stage]);
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ring.next();
+        if (++pending > S::LAG) {                      // the oldest has landed: hand it over
+          cp_async_wait<S::LAG>();
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->full[done]);
+          done = done + 1 == S::STAGES ? 0 : done + 1;
+          --pending;
         }
       }
       at = max(at, end);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");   // none is on its way when this CTA ends
-    __syncwarp();
-  } else {
-    // ---- multiply
-    float acc[MT][4][4];
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    for (; pending > 0; --pending) {
+      mbar_arrive(&bars->full[done]);
+      done = done + 1 == S::STAGES ? 0 : done + 1;
+    }
+  } else if (warp == 4) {
+    // ---- MMA
+    const uint32_t idesc = idesc_bf16(128, S::N, true, true);
+    const uint64_t mn = umma_desc_sw128(0, kWgBox, 1024);
+    Ring ring(S::STAGES);
     bool ok = true;
+    int seg = 0;
     for (int at = r0; ok && at < r1; ++a) {
       const int begin = p.off[a], end = p.off[a + 1], stop = min(end, r1);
       if (begin == end) continue;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
-      for (int b = at; b < stop; b += kWgRows) {
-        ok = !abort_flag && wait_bar(&full[stage], phase);
-        if (!ok) {
-          if (!abort_flag) flag_timeout(p.status);
-          abort_flag = 1;
-        }
-        ok = __all_sync(0xffffffffu, ok);
+      const int buf = seg & 1;
+      const uint32_t d = tmem + buf * 256;
+      ok = warp_wait(bars, &bars->acc_empty[buf], ((seg >> 1) & 1) ^ 1, p.status);
+      tc_fence_after();
+      for (int b = at; ok && b < stop; b += kWgRows) {
+        ok = warp_wait(bars, &bars->full[ring.stage], ring.phase, p.status);
         if (!ok) break;
-        const uint8_t* sg = smem + stage * STAGE + (warp >> 1) * BOX;
-        const uint8_t* su = smem + stage * STAGE + 2 * BOX;
+        tc_fence_after();
+        const uint32_t sg = smem_u32(smem + ring.stage * S::STAGE);
+        const uint32_t su = sg + S::N / 64 * kWgBox;
+        const uint64_t bd = desc_at(mn, sg), hi = desc_at(mn, su),
+                       lo = desc_at(mn, su + S::UT * kWgBox);
+        if (elect_one()) {
 #pragma unroll
-        for (int k0 = 0; k0 < kWgRows; k0 += 16) {
-          uint32_t bf[8];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int rr = k0 + ((lane >> 3) & 1) * 8 + (lane & 7);
-            const int ch = (warp & 1) * 4 + h * 2 + (lane >> 4);
-            ldsm4_t(bf + 4 * h, sg + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          for (int kk = 0; kk < 4; ++kk) {
+            umma_bf16(d, hi + 128 * kk, bd + 128 * kk, idesc, (b > at || kk > 0) ? 1u : 0u);
+            umma_bf16(d, lo + 128 * kk, bd + 128 * kk, idesc, 1u);
           }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const int rr = k0 + (lane >> 4) * 8 + (lane & 7);
-            const int ch = (mt & 1) * 2 + ((lane >> 3) & 1);
-            const uint8_t* sb = su + (mt >> 1) * BOX + rr * 128;
-            uint32_t hi4[4], lo4[4];
-            ldsm4_t(hi4, sb + ((ch ^ (rr & 7)) * 16));
-            ldsm4_t(lo4, sb + (((ch + 4) ^ (rr & 7)) * 16));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma16816(acc[mt][j], hi4, bf[2 * j], bf[2 * j + 1]);
-              mma16816(acc[mt][j], lo4, bf[2 * j], bf[2 * j + 1]);
-            }
-          }
+          umma_commit(&bars->empty[ring.stage]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
+        ring.next();
       }
+      at = stop;
       if (!ok) break;
+      if (elect_one()) umma_commit(&bars->acc_full[buf]);
+      __syncwarp();
+      ++seg;
+    }
+    if (bars->abort && elect_one()) drain_mmas<false>(bars);
+    __syncwarp();
+  } else {
+    // ---- epilogue: lane = rank
+    const int quarter = warp & 3, rank = quarter * 32 + lane;
+    int seg = 0;
+    for (int at = r0; at < r1; ++a) {
+      const int begin = p.off[a], end = p.off[a + 1], stop = min(end, r1);
+      if (begin == end) continue;
+      const int buf = seg & 1;
+      if (!warp_wait(bars, &bars->acc_full[buf], (seg >> 1) & 1, p.status)) break;
+      tc_fence_after();
       at = stop;
       const bool began = begin >= r0, ends = end <= r1;
-      if (began && ends) {   // finished here: straight from the registers
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int rr = mt * 16 + (lane >> 2) + 8 * h;
-              const int cc = c0 + warp * 32 + j * 8 + (lane & 3) * 2;
-              if (rr >= p.r || cc >= C) continue;
-              const size_t o = ((size_t)a * p.r + rr) * C + cc;
-              if (p.out_bf16)
-                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(out) + o) =
-                    pack_bf16(acc[mt][j][2 * h], acc[mt][j][2 * h + 1]);
-              else
-                *reinterpret_cast<float2*>(static_cast<float*>(out) + o) =
-                    make_float2(acc[mt][j][2 * h], acc[mt][j][2 * h + 1]);
-            }
-        continue;
-      }
-      // began earlier: the rank where it began adds this part; else it goes on in the next
-      // ranks and is this CTA's last (all its stages are read when every warp is here)
-      if (began) {
-        last = a;
+      if (began && !ends && quarter == 0 && lane == 0) {   // goes on in the next ranks
+        int more = 0;
         while (q + more + 1 < p.split && (int)((long long)total * (q + more + 1) / p.split) < end)
           ++more;
-        named_bar_sync(1, 128);
+        s_last = a;
+        s_more = more;
       }
-      float* dst = began ? tail : head;
+      const uint32_t d = tmem + buf * 256 + ((uint32_t)(quarter * 32) << 16);
+      for (int c = 0; quarter * 32 < RP && c < S::N && c0 + c < C; c += 32) {
+        float v[32];
+        tmem_ld32(d + c, v);
+        if (began && ends) {   // finished here
+          const size_t o = ((size_t)a * p.r + rank) * C + c0 + c;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+          for (int j = 0; j < 4; ++j) {
+            if (rank < p.r && c0 + c + 8 * j < C) {
+              if (p.out_bf16) {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + o + 8 * j) =
+                    make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                               pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                               pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + o + 8 * j);
+                dst[0] = make_float4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
+                dst[1] = make_float4(v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]);
+              }
+            }
+          }
+        } else if (rank < RP) {   // to this rank's head, or (its last adapter) its tail
+          float* dst = (began ? tail : head) + rank * S::RS + c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int rr = mt * 16 + (lane >> 2), cc = warp * 32 + j * 8 + (lane & 3) * 2;
-          *reinterpret_cast<float2*>(dst + rr * RS + cc) = make_float2(acc[mt][j][0], acc[mt][j][1]);
-          *reinterpret_cast<float2*>(dst + (rr + 8) * RS + cc) =
-              make_float2(acc[mt][j][2], acc[mt][j][3]);
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
+        __syncwarp();
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->acc_empty[buf]);
+      ++seg;
     }
     if (r0 == r1)                     // fewer rows than ranks: nothing to add here
-      for (int i = tid; i < 16 * MT * RS; i += 128) head[i] = 0.f;
+      for (int i = tid - 160; i < RP * S::RS; i += 128) head[i] = 0.f;
   }
+  __syncwarp();
   // out[z] = this CTA's tail (or zeros) + the heads of the next ranks
   auto write = [&](int z, bool own, int ranks) {
-    for (int it = tid; it < p.r * (kWgCols / 4); it += kWgThreads) {
-      const int rr = it / (kWgCols / 4), cc = it % (kWgCols / 4) * 4;
+    for (int it = tid; it < p.r * (S::N / 4); it += kWgThreads) {
+      const int rr = it / (S::N / 4), cc = it % (S::N / 4) * 4;
       if (c0 + cc >= C) continue;
-      float4 s = own ? *reinterpret_cast<const float4*>(tail + rr * RS + cc)
+      float4 v[8];
+#pragma unroll
+      for (int k = 1; k < 8; ++k)
+        if (k <= ranks) v[k] = ld_rank4(head + rr * S::RS + cc, q + k);
+      float4 s = own ? *reinterpret_cast<const float4*>(tail + rr * S::RS + cc)
                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 1; k <= ranks; ++k) {
-        const float4 v = ld_rank4(head + rr * RS + cc, q + k);
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-      }
+#pragma unroll
+      for (int k = 1; k < 8; ++k)
+        if (k <= ranks) {
+          s.x += v[k].x; s.y += v[k].y; s.z += v[k].z; s.w += v[k].w;
+        }
       const size_t o = ((size_t)z * p.r + rr) * C + c0 + cc;
       if (p.out_bf16)
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
@@ -1355,18 +1370,16 @@ __global__ void __launch_bounds__(kWgThreads, MT <= 2 ? 2 : 1) wgrad_kernel(cons
         *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = s;
     }
   };
-  last = __shfl_sync(0xffffffffu, last, 0);
-  __shared__ int s_last, s_more;      // known to the warps that multiply
-  if (tid == 0) {
-    s_last = last;
-    s_more = more;
-  }
-  __syncwarp();
+  tc_fence_before();
   cluster_sync_all();                 // every head is in place
   if (s_last >= 0) write(s_last, true, s_more);
   for (int z = q; z < p.n; z += p.split)   // adapters without rows
     if (p.off[z] == p.off[z + 1]) write(z, false, 0);
   cluster_sync_all();                 // no rank leaves while another reads its head
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1462,8 +1475,8 @@ bool init_device(Device& d, int dev) {
   const void* fns[] = {(const void*)shrink_kernel,
                        (const void*)proj_kernel<false, false>, (const void*)proj_kernel<true, false>,
                        (const void*)proj_kernel<false, true>, (const void*)proj_kernel<true, true>,
-                       (const void*)wgrad_kernel<1>, (const void*)wgrad_kernel<2>,
-                       (const void*)wgrad_kernel<4>, (const void*)wgrad_kernel<8>};
+                       (const void*)wgrad_kernel<16>, (const void*)wgrad_kernel<32>,
+                       (const void*)wgrad_kernel<64>, (const void*)wgrad_kernel<128>};
   for (const void* f : fns) {
     cudaFuncAttributes a;
     if (cudaFuncGetAttributes(&a, f) != cudaSuccess) return false;
@@ -1695,39 +1708,34 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
 
 mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, const void* xa,
                      const void* dY, const char* ws, const WorkParts& wp, void* dA, void* dB,
-                     mok_out_dtype type, uint32_t* status, cudaStream_t s) {
-  WgradParams p = {};
-  p.side[0] = WgradSide{reinterpret_cast<const uint8_t*>(vq), static_cast<const __nv_bfloat16*>(xa),
-                        dA, d.K, (d.K + kWgCols - 1) / kWgCols};
-  p.side[1] = WgradSide{reinterpret_cast<const uint8_t*>(uq), static_cast<const __nv_bfloat16*>(dY),
-                        dB, d.N, (d.N + kWgCols - 1) / kWgCols};
-  p.r = d.r;
-  p.n = d.n;
-  p.out_bf16 = type == MOK_OUT_BF16;
-  p.off = reinterpret_cast<const int32_t*>(ws + wp.off);
-  p.rows = reinterpret_cast<const int32_t*>(ws + wp.rows);
-  p.status = status;
-  // row shares of at least two stages
-  p.split = 1;
-  while (p.split < 8 && d.T > 4 * p.split * kWgRows) p.split *= 2;
-  const int mt = padded_rank(d.r) / 16, nb = (mt + 1) / 2;
-  const size_t part = (size_t)mt * 16 * (kWgCols + 4) * 4;
-  const size_t stage = (size_t)(2 + nb) * kWgRows * 128;
-  // two CTAs per SM where three stages allow it
-  const size_t fixed = part + 1024, half = 112 * 1024;
-  const size_t room = fixed + 3 * stage <= half ? half : kMaxSmem - 1024;
-  p.stages = std::min<int>(kWgMaxStages, (int)((room - fixed) / stage));
-  const size_t smem = std::max(p.stages * stage, part) + fixed;
-  const int grid = (p.side[0].ctiles + p.side[1].ctiles) * p.split;
-  auto go = [&](auto kernel) {
-    return launch(kernel, grid, kWgThreads, smem, p.split, true, s, p);
+                     mok_out_dtype type, uint32_t* status, const Device& dev, cudaStream_t s) {
+  auto go = [&](auto rp) {
+    using S = WgShape<decltype(rp)::value>;
+    WgradParams p = {};
+    p.side[0] = WgradSide{reinterpret_cast<const uint8_t*>(vq), static_cast<const __nv_bfloat16*>(xa),
+                          dA, d.K, (d.K + S::N - 1) / S::N};
+    p.side[1] = WgradSide{reinterpret_cast<const uint8_t*>(uq), static_cast<const __nv_bfloat16*>(dY),
+                          dB, d.N, (d.N + S::N - 1) / S::N};
+    p.r = d.r;
+    p.n = d.n;
+    p.out_bf16 = type == MOK_OUT_BF16;
+    p.off = reinterpret_cast<const int32_t*>(ws + wp.off);
+    p.rows = reinterpret_cast<const int32_t*>(ws + wp.rows);
+    p.status = status;
+    // row shares: one wave of clusters, at least two stages a share
+    const int tiles = p.side[0].ctiles + p.side[1].ctiles;
+    int i = 0;
+    while (i < 3 && d.T > (2 << i) * kWgRows && tiles <= dev.clusters[i + 1]) ++i;
+    p.split = 1 << i;
+    return launch(wgrad_kernel<decltype(rp)::value>, tiles * p.split, kWgThreads, S::SMEM, p.split,
+                  true, s, p);
   };
   cudaError_t e;
-  switch (mt) {
-    case 1: e = go(wgrad_kernel<1>); break;
-    case 2: e = go(wgrad_kernel<2>); break;
-    case 4: e = go(wgrad_kernel<4>); break;
-    default: e = go(wgrad_kernel<8>); break;
+  switch (padded_rank(d.r)) {
+    case 16: e = go(std::integral_constant<int, 16>{}); break;
+    case 32: e = go(std::integral_constant<int, 32>{}); break;
+    case 64: e = go(std::integral_constant<int, 64>{}); break;
+    default: e = go(std::integral_constant<int, 128>{}); break;
   }
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
@@ -1811,7 +1819,7 @@ extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_wei
   mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, status, true, *dev, s);
   if (st != MOK_OK) return st;
   st = run_wgrad(d, sv + wp.v.uq, ws + wp.v.uq, x_ad ? x_ad : x, dY, ws, wp, dA, dB, out,
-                 status, s);
+                 status, *dev, s);
   if (st != MOK_OK) return st;
   st = run_proj(d, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, true,
                 *dev, s);
