@@ -497,16 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) wait_prerequisites();   // what waits for this kernel waits for them too
 }
 
-// The same for a few rows: CTA t takes row t alone, its warps share the contraction in pieces
-// of 256 elements, 16 ranks at a time (16 independent 16-byte loads per lane, so a row costs
-// about one trip to memory), on the CUDA cores; no MMA tile to fill, no ring to start. The
-// last CTAs list the row tiles' adapters for proj_kernel.
+// The same for a few rows: a CTA takes RG ranks of one row, its warps share the contraction in
+// pieces of 256 elements (RG independent 16-byte loads per lane, so the CTA costs about one
+// trip to memory), on the CUDA cores; no MMA tile to fill, no ring to start. Fewer rows, fewer
+// ranks a CTA: one SM takes in about 50 GB/s, so one row's 16 ranks of 7168 in one CTA took
+// 8 us. The last CTAs list the row tiles' adapters for proj_kernel.
 constexpr int kRowThreads = 1024;
 constexpr int kRowMaxPieces = 64;    // contraction up to 16384
 constexpr int kRowsMost = 192;       // rows of a batch that goes this way
 
 struct ShrinkRowsParams {
-  int T, C, n, r, nb;
+  int T, C, n, r, nb, groups;   // groups of RG ranks
   const __nv_bfloat16* x;      // [T][C]
   const __nv_bfloat16* w;      // [n][r][C]
   const int32_t* ids;
@@ -525,13 +526,15 @@ __device__ __forceinline__ void unpack8(const uint4 q, float* v) {
   }
 }
 
+template <int RG>
 __global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRowsParams p) {
   __shared__ __align__(16) TileSlots ts;
-  __shared__ float part[kRowMaxPieces][16];
+  __shared__ float part[kRowMaxPieces][RG];
   launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if ((int)blockIdx.x >= p.T) {
-    const int m = (int)blockIdx.x - p.T;
+  const int t = (int)blockIdx.x / p.groups;
+  if (t >= p.T) {
+    const int m = (int)blockIdx.x - p.T * p.groups;
     find_slots(ts, tid < BM ? tid : -1, p.ids, p.n, p.T, m * BM);
     if (tid == 0) p.n_slots[m] = ts.count;
     if (tid < ts.count) {
@@ -545,65 +548,65 @@ __global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRo
     if (tid == 0) wait_prerequisites();   // what waits for this kernel waits for them too
     return;
   }
-  const int t = blockIdx.x;
   const int id = p.ids[t];
   if (id < 0 || id >= p.n) return;
+  const int i0 = (int)blockIdx.x % p.groups * RG;
   const __nv_bfloat16* x = p.x + (size_t)t * p.C;
-  const __nv_bfloat16* w = p.w + (size_t)id * p.r * p.C;
+  const __nv_bfloat16* w = p.w + ((size_t)id * p.r + i0) * p.C;
   const int pieces = (p.C + 255) / 256;
   const float scale = p.scale[id];
-  for (int i0 = 0; i0 < p.r; i0 += 16) {
-    for (int c = warp; c < pieces; c += kRowThreads / 32) {
-      const int k = c * 256 + lane * 8;
-      uint4 wq[16];
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      const uint4 xq = k < p.C ? *reinterpret_cast<const uint4*>(x + k) : none;
+  for (int c = warp; c < pieces; c += kRowThreads / 32) {
+    const int k = c * 256 + lane * 8;
+    uint4 wq[RG];
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint4 xq = k < p.C ? *reinterpret_cast<const uint4*>(x + k) : none;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        wq[i] = k < p.C && i0 + i < p.r
-                    ? *reinterpret_cast<const uint4*>(w + (size_t)(i0 + i) * p.C + k) : none;
-      float xv[8], sum[16];
-      unpack8(xq, xv);
+    for (int i = 0; i < RG; ++i)
+      wq[i] = k < p.C && i0 + i < p.r ? *reinterpret_cast<const uint4*>(w + (size_t)i * p.C + k)
+                                      : none;
+    float xv[8], sum[RG];
+    unpack8(xq, xv);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float wv[8];
-        unpack8(wq[i], wv);
-        sum[i] = 0.f;
+    for (int i = 0; i < RG; ++i) {
+      float wv[8];
+      unpack8(wq[i], wv);
+      sum[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[i] = fmaf(xv[j], wv[j], sum[i]);
-      }
-      // 16 sums over the 32 lanes: halve the sums with every step, so that lane l ends with
-      // sum l / 2 (both lanes of a pair the same)
-#pragma unroll
-      for (int h = 8; h > 0; h >>= 1) {
-        const bool up = lane & (2 * h);
-#pragma unroll
-        for (int i = 0; i < h; ++i) {
-          const float give = up ? sum[i] : sum[i + h];
-          const float keep = up ? sum[i + h] : sum[i];
-          sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * h);
-        }
-      }
-      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-      if ((lane & 1) == 0) part[c][lane >> 1] = sum[0];
+      for (int j = 0; j < 8; ++j) sum[i] = fmaf(xv[j], wv[j], sum[i]);
     }
-    __syncthreads();
-    if (tid < 8) {
-      float v[2];
+    // RG sums over 32 lanes: a step halves the sums, then the rest is added up; lane l ends
+    // with sum l RG / 32
+    int dist = 16;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        v[j] = 0.f;
-        for (int c = 0; c < pieces; ++c) v[j] += part[c][2 * tid + j];
-        // ranks past r are padding: 0 also where a row with an inf met their zero fill
-        v[j] = i0 + 2 * tid + j < p.r ? scale * v[j] : 0.f;
+    for (int h = RG / 2; h > 0; h >>= 1, dist >>= 1) {
+      const bool up = lane & dist;
+#pragma unroll
+      for (int i = 0; i < h; ++i) {
+        const float give = up ? sum[i] : sum[i + h];
+        const float keep = up ? sum[i + h] : sum[i];
+        sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, dist);
       }
-      uint32_t hi, lo;
-      split_pair(v[0], v[1], hi, lo);
-      uint8_t* dst = p.uq + ((size_t)t * p.nb + i0 / 32) * 128 + (i0 % 32 + 2 * tid) * 2;
-      *reinterpret_cast<uint32_t*>(dst) = hi;
-      *reinterpret_cast<uint32_t*>(dst + 64) = lo;
     }
-    __syncthreads();
+#pragma unroll
+    for (; dist > 0; dist >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], dist);
+    if (lane % (32 / RG) == 0) part[c][lane / (32 / RG)] = sum[0];
+  }
+  __syncthreads();
+  if (tid < RG / 2) {
+    float v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v[j] = 0.f;
+      for (int c = 0; c < pieces; ++c) v[j] += part[c][2 * tid + j];
+      // ranks past r are padding: 0 also where a row with an inf met their zero fill
+      v[j] = i0 + 2 * tid + j < p.r ? scale * v[j] : 0.f;
+    }
+    uint32_t hi, lo;
+    split_pair(v[0], v[1], hi, lo);
+    const int i = i0 + 2 * tid;
+    uint8_t* dst = p.uq + ((size_t)t * p.nb + i / 32) * 128 + i % 32 * 2;
+    *reinterpret_cast<uint32_t*>(dst) = hi;
+    *reinterpret_cast<uint32_t*>(dst + 64) = lo;
   }
 }
 
@@ -1093,9 +1096,9 @@ constexpr int kWgRows = 64;
 constexpr int kWgThreads = 288;      // four warps that gather, one MMA, four epilogue
 constexpr int kWgBox = kWgRows * 128;
 
-template <int RP>
+template <int RP, int NCOLS>
 struct WgShape {
-  static constexpr int N = RP <= 64 ? 256 : 128;        // columns of a CTA
+  static constexpr int N = NCOLS;                       // columns of a CTA
   static constexpr int UT = RP <= 64 ? 1 : 2;           // 64-rank tiles of hi (and of lo)
   static constexpr int STAGE = (N / 64 + 2 * UT) * kWgBox;
   static constexpr int STAGES = RP <= 32 ? 4 : 3;
@@ -1130,9 +1133,9 @@ struct WgradParams {
   uint32_t* status;
 };
 
-template <int RP>
+template <int RP, int NCOLS>
 __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams p) {
-  using S = WgShape<RP>;
+  using S = WgShape<RP, NCOLS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -1475,8 +1478,10 @@ bool init_device(Device& d, int dev) {
   const void* fns[] = {(const void*)shrink_kernel,
                        (const void*)proj_kernel<false, false>, (const void*)proj_kernel<true, false>,
                        (const void*)proj_kernel<false, true>, (const void*)proj_kernel<true, true>,
-                       (const void*)wgrad_kernel<16>, (const void*)wgrad_kernel<32>,
-                       (const void*)wgrad_kernel<64>, (const void*)wgrad_kernel<128>};
+                       (const void*)wgrad_kernel<16, 256>, (const void*)wgrad_kernel<16, 128>,
+                       (const void*)wgrad_kernel<32, 256>, (const void*)wgrad_kernel<32, 128>,
+                       (const void*)wgrad_kernel<64, 256>, (const void*)wgrad_kernel<64, 128>,
+                       (const void*)wgrad_kernel<128, 128>};
   for (const void* f : fns) {
     cudaFuncAttributes a;
     if (cudaFuncGetAttributes(&a, f) != cudaSuccess) return false;
@@ -1536,11 +1541,20 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   int32_t* n_slots = reinterpret_cast<int32_t*>(saved + sp.n_slots);
   Slot* slots = reinterpret_cast<Slot*>(saved + sp.slots);
   if (d.T <= kRowsMost && C <= 256 * kRowMaxPieces) {
-    ShrinkRowsParams p = {d.T, C, d.n, d.r, nb, static_cast<const __nv_bfloat16*>(in),
-                          static_cast<const __nv_bfloat16*>(w), ids, scale, uq, n_slots, slots};
-    return launch(shrink_rows_kernel, d.T + mt, kRowThreads, 0, 1, early, s, p) == cudaSuccess
-               ? MOK_OK
-               : MOK_ERR_CUDA;
+    auto go = [&](auto rg) {
+      constexpr int RG = decltype(rg)::value;
+      // every rank that the MMAs read is written, padding too
+      const int groups = rp / RG;
+      ShrinkRowsParams p = {d.T, C, d.n, d.r, nb, groups, static_cast<const __nv_bfloat16*>(in),
+                            static_cast<const __nv_bfloat16*>(w), ids, scale, uq, n_slots, slots};
+      return launch(shrink_rows_kernel<RG>, d.T * groups + mt, kRowThreads, 0, 1, early, s, p);
+    };
+    // the fewest CTAs that still keep the SMs busy
+    const cudaError_t e = d.T * (rp / 16) >= dev.sms / 2  ? go(std::integral_constant<int, 16>{})
+                          : d.T * (rp / 8) >= dev.sms / 2 ? go(std::integral_constant<int, 8>{})
+                          : d.T * (rp / 4) >= dev.sms / 2 ? go(std::integral_constant<int, 4>{})
+                                                          : go(std::integral_constant<int, 2>{});
+    return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
   }
   ShrinkParams p = {};
   p.T = d.T;
@@ -1586,7 +1600,7 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
 // out of L2, W's out of HBM (narrow 64-column pieces of its rows at two thirds of the rate),
 // and the memory's latency over the ring's stages. The constants are fitted to the times of
 // every form at 112 shapes, 1 to 8192 rows and 256 x 256 to 7168 x 2048: the choice then costs
-// 1.7% against the best form on average.
+// 1.7% against the best form on average. ext: the adapters' stages of a tile, an estimate.
 struct ProjForm {
   int NT, split, pair, stages, stage_bytes;
   size_t smem;
@@ -1597,7 +1611,7 @@ int pair_tail(int tiles, const Device& dev) {
   const int rest = tiles % dev.clusters[1];
   return 2 * rest <= dev.clusters[1] ? rest : 0;
 }
-ProjForm choose_form(int T, int kiters, int cols, const Device& dev) {
+ProjForm choose_form(int T, int kiters, int ext, int cols, const Device& dev) {
   const int mt = (T + BM - 1) / BM, a_bytes = tile_rows(T) * BK * 2;
   ProjForm best = {};
   double best_t = 0;
@@ -1630,7 +1644,7 @@ ProjForm choose_form(int T, int kiters, int cols, const Device& dev) {
                                       hbm, 0.42 / f.stages});
         const double fill = std::min(T, BM) / (double)BM;   // of a tile's rows
         const double fixed_t = pair ? 2.1 : split == 1 ? 1.7 : 2.8 + 4.3 * fill * nt / 128;
-        const double t = waves * (std::ceil((double)kiters / split) * step + fixed_t) +
+        const double t = waves * (std::ceil((double)(kiters + ext) / split) * step + fixed_t) +
                          (split == 1 ? 2.75 * fill * nt / 256 : 0.0);
         if (best_t == 0 || t < best_t) {
           best_t = t;
@@ -1659,7 +1673,11 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
   p.nb = (p.rp + 31) / 32;
   p.rb = std::min(p.rp, 32);
   p.out_bf16 = type == MOK_OUT_BF16;
-  const ProjForm f = choose_form(d.T, p.kiters, cols, dev);
+  // short batches are mostly rows of different requests, long ones mostly long runs of one; an
+  // adapter stage takes about as long as two steps over W
+  const int slots = parts ? (d.T <= BM ? std::min(d.n, d.T) : 2) : 0;
+  const int ext = 2 * p.nb * ((slots * p.rb + 63) / 64);
+  const ProjForm f = choose_form(d.T, p.kiters, ext, cols, dev);
   p.NT = f.NT;
   p.split = f.split;
   p.n_tiles = (cols + p.NT - 1) / p.NT;
@@ -1709,8 +1727,8 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
 mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, const void* xa,
                      const void* dY, const char* ws, const WorkParts& wp, void* dA, void* dB,
                      mok_out_dtype type, uint32_t* status, const Device& dev, cudaStream_t s) {
-  auto go = [&](auto rp) {
-    using S = WgShape<decltype(rp)::value>;
+  auto go = [&](auto rp, auto cols) {
+    using S = WgShape<decltype(rp)::value, decltype(cols)::value>;
     WgradParams p = {};
     p.side[0] = WgradSide{reinterpret_cast<const uint8_t*>(vq), static_cast<const __nv_bfloat16*>(xa),
                           dA, d.K, (d.K + S::N - 1) / S::N};
@@ -1727,15 +1745,21 @@ mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, con
     int i = 0;
     while (i < 3 && d.T > (2 << i) * kWgRows && tiles <= dev.clusters[i + 1]) ++i;
     p.split = 1 << i;
-    return launch(wgrad_kernel<decltype(rp)::value>, tiles * p.split, kWgThreads, S::SMEM, p.split,
+    return launch(wgrad_kernel<decltype(rp)::value, decltype(cols)::value>, tiles * p.split, kWgThreads, S::SMEM, p.split,
                   true, s, p);
+  };
+  // 256 columns read u half as often; 128 make more CTAs of few rows
+  using std::integral_constant;
+  const bool wide = d.T >= 2048;
+  auto width = [&](auto rp) {
+    return wide ? go(rp, integral_constant<int, 256>{}) : go(rp, integral_constant<int, 128>{});
   };
   cudaError_t e;
   switch (padded_rank(d.r)) {
-    case 16: e = go(std::integral_constant<int, 16>{}); break;
-    case 32: e = go(std::integral_constant<int, 32>{}); break;
-    case 64: e = go(std::integral_constant<int, 64>{}); break;
-    default: e = go(std::integral_constant<int, 128>{}); break;
+    case 16: e = width(integral_constant<int, 16>{}); break;
+    case 32: e = width(integral_constant<int, 32>{}); break;
+    case 64: e = width(integral_constant<int, 64>{}); break;
+    default: e = go(integral_constant<int, 128>{}, integral_constant<int, 128>{}); break;
   }
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
