@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 import torch
 
+from grouped_gemm_built_gb300 import mok
 from grouped_gemm_built_gb300.lora import AdaptedLinear
 from tests import ops_reference as ref
 
@@ -205,6 +206,36 @@ def test_repeats_bitwise_on_another_stream(rng):
     for g in again:
         for k, v in first.items():
             assert torch.equal(v, g[k]), k
+
+
+def test_step_is_captured_in_a_graph(rng):
+    """A whole step (its launches depend on one another ahead of time) replays from a graph."""
+    c = {k: v.cuda() for k, v in make(rng, 520, 264, 328, 6, 24, "rows").items()}
+    L = AdaptedLinear(c["W"], c["A"], c["B"], c["scale"])
+
+    def step():
+        y, saved = L.forward(c["x"], c["ids"])
+        return dict(L.backward(c["x"], c["ids"], saved, c["dY"]), y=y)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    c["x"].copy_(torch.randn_like(c["x"]))
+    c["ids"].copy_(c["ids"].flip(0))
+    graph.replay()
+    graph.replay()
+    for k, v in step().items():
+        assert torch.equal(v, got[k]), k
+
+
+def test_status_word_is_read_and_cleared():
+    z = dict(dtype=torch.bfloat16, device="cuda")
+    L = AdaptedLinear(torch.ones(8, 8, **z), torch.ones(1, 1, 8, **z), torch.ones(1, 1, 8, **z),
+                      torch.ones(1, device="cuda"))
+    assert L.status() == 0
+    L._status.fill_(1)                        # what a kernel does when a wait passes its bound
+    assert L.status() == mok.MOK_ERR_TIMEOUT and L.status() == 0
 
 
 def test_updated_weights_are_read(rng):
