@@ -7,7 +7,16 @@ from typing import Optional
 import torch
 
 from . import mok
-from .layer import _dev, _on_current_stream, _result_code
+from .layer import _dev, _result_code, _results
+
+
+def _check(x, add, y):
+    dt = x.dtype if isinstance(x, torch.Tensor) else None
+    _result_code(dt, "x")
+    n = x.numel()
+    _dev(x, "x", dt, n)
+    _dev(add, "add", dt, n, optional=True)
+    _dev(y, "y", dt, n, optional=True)
 
 
 def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
@@ -16,13 +25,6 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
     probability round(65536 p) / 65536. The backward is the same call on the gradient. Calls
     that need masks of their own take different seeds, or offsets at least
     ``(x.numel() + 7) // 8`` apart. ``y`` may be ``x`` or ``add``."""
-    dt = x.dtype if isinstance(x, torch.Tensor) else None
-    code = _result_code(dt, "x")
-    n = x.numel()
-    px = _dev(x, "x", dt, n)
-    pa = _dev(add, "add", dt, n, optional=True)
-    if y is None:
-        y = torch.empty_like(x)
-    py = _dev(y, "y", dt, n)
-    _on_current_stream(x.get_device(), mok.mok_dropout, px, pa, py, n, p, seed, offset, code)
-    return y
+    got = mok.torch_calls().dropout(x, p, seed, offset, add, y)
+    out = _results(got, "mok_dropout", lambda: _check(x, add, y))[0]
+    return out if y is None else y

@@ -47,16 +47,15 @@ def _result_code(dtype, name: str) -> int:
     return _RESULT_CODES[dtype]
 
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
-def _on_current_stream(index: int, fn, *args):
-    """``fn(*args, stream)`` with CUDA device ``index`` current and its current stream. (Raw
-    handles: building a stream object or entering a device context takes as long as a launch.)"""
-    if index == _current_device():
-        return fn(*args, _raw_stream(index))
-    with torch.cuda.device(index):
-        return fn(*args, _raw_stream(index))
+def _results(got, what: str, check):
+    """What a call of mok_torch returned, or the reason why it did not: ``check`` repeats its
+    tests of the arguments one by one and raises for the first that fails."""
+    if type(got) is tuple:
+        return got
+    if got is None:
+        check()
+        raise ValueError(f"{what}: all tensors must be on one CUDA device")
+    raise mok.MokError(what, got)
 
 
 class MoELayer:

@@ -8,10 +8,12 @@ raises immediately; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 
-from .build import lib_path
+from .build import lib_path, torch_lib_path
 
 c_int, c_size_t, c_void_p, c_char_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
 
@@ -161,6 +163,28 @@ def lib():
         _declare(L)
         _LIB = L
     return _LIB
+
+
+_TORCH_CALLS = None
+
+
+def torch_calls():
+    """The extension module mok_torch, its calls bound to the loaded libmok (raises if it has
+    not been built)."""
+    global _TORCH_CALLS
+    if _TORCH_CALLS is None:
+        p, L = torch_lib_path(), lib()
+        if not os.path.exists(p):
+            raise RuntimeError(f"mok_torch is not built ({p}); run __graft_entry__.build()")
+        import torch  # noqa: F401  (the libraries that the module links against)
+        loader = importlib.machinery.ExtensionFileLoader("mok_torch", p)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("mok_torch", loader))
+        loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(L, "mok_" + f), c_void_p).value
+                 for f in ("route", "route_bwd", "dropout", "lora_get_sizes", "lora_fwd",
+                           "lora_bwd")))
+        _TORCH_CALLS = m
+    return _TORCH_CALLS
 
 
 def declared_symbols():

@@ -8,12 +8,13 @@ The results feed a layer without a router of its own (``MoELayer(router=False)``
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
 
 from . import mok
-from .layer import _dev, _on_current_stream, _result_code
+from .layer import _dev, _result_code, _results
 
 
 class Routing:
@@ -35,40 +36,33 @@ class Routing:
                                    top_groups=top_groups,
                                    group_score=self.GROUP_SCORES[group_score],
                                    renormalize=1 if renormalize else 0, scale=scale)
+        self._at = ctypes.addressof(self.rule)
         mok.mok_route(self.rule, 0, None, mok.MOK_OUT_F32, None, None, None, None)  # checks it
 
-    def _logits(self, logits):
-        """(rows, address, type code, device) of [T,E] logits."""
+    def _check(self, logits, bias=None, topk_idx=None, dgates=None, backward=False):
         dt = logits.dtype if isinstance(logits, torch.Tensor) else None
-        code = _result_code(dt, "logits")
-        shape = logits.shape
-        if len(shape) != 2 or shape[1] != self.E:
-            raise ValueError(f"logits must be [T, {self.E}], got {tuple(shape)}")
-        T = shape[0]
-        return T, _dev(logits, "logits", dt, T * self.E), code, logits.device
+        _result_code(dt, "logits")
+        if logits.dim() != 2 or logits.shape[1] != self.E:
+            raise ValueError(f"logits must be [T, {self.E}], got {tuple(logits.shape)}")
+        T = logits.shape[0]
+        _dev(logits, "logits", dt, T * self.E)
+        _dev(bias, "bias", torch.float32, self.E, optional=True)
+        if backward:
+            _dev(topk_idx, "topk_idx", torch.int32, T * self.k)
+            _dev(dgates, "dgates", torch.float32, T * self.k)
 
     def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None):
         """(topk_idx [T,k] int32, gates [T,k] fp32) from logits [T,E] bf16 or fp32 and the
         selection bias [E] fp32."""
-        T, pl, code, device = self._logits(logits)
-        pb = None if bias is None else _dev(bias, "bias", torch.float32, self.E)
-        shape = (T, self.k)
-        idx = torch.empty(shape, dtype=torch.int32, device=device)
-        gates = torch.empty(shape, dtype=torch.float32, device=device)
-        _on_current_stream(device.index, mok.mok_route, self.rule, T, pl, code, pb,
-                           idx.data_ptr(), gates.data_ptr())
-        return idx, gates
+        return _results(mok.torch_calls().route(self._at, logits, bias), "mok_route",
+                        lambda: self._check(logits, bias))
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, dgates: torch.Tensor,
                  dtype: Optional[torch.dtype] = None):
         """dlogits [T,E] (``dtype``, the logits' type by default) from dgates [T,k] fp32, at
         the choice that ``forward`` made from these logits."""
-        T, pl, code, device = self._logits(logits)
-        dtype = dtype or logits.dtype
-        dcode = _result_code(dtype, "dlogits")
-        pi = _dev(topk_idx, "topk_idx", torch.int32, T * self.k)
-        pd = _dev(dgates, "dgates", torch.float32, T * self.k)
-        out = torch.empty((T, self.E), dtype=dtype, device=device)
-        _on_current_stream(device.index, mok.mok_route_bwd, self.rule, T, pl, code, pi, pd,
-                           out.data_ptr(), dcode)
-        return out
+        dtype = dtype or getattr(logits, "dtype", None)
+        got = mok.torch_calls().route_bwd(self._at, logits, topk_idx, dgates,
+                                          _result_code(dtype, "dlogits"))
+        return _results(got, "mok_route_bwd", lambda: self._check(
+            logits, topk_idx=topk_idx, dgates=dgates, backward=True))[0]
