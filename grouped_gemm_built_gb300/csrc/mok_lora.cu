@@ -53,11 +53,12 @@ constexpr int kBarBytes = 512;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr size_t kMaxSmem = 227 * 1024;
 
-// A distinct adapter of a row tile: its id and the lanes (rows) that do NOT use it.
+// A distinct adapter of a row tile (or of a pair of them): its id and the lanes (rows) that do
+// NOT use it, four words for each of the row tiles.
 struct Slot {
   int32_t id;
-  uint32_t off[4];
   int32_t pad[3];
+  uint4 off[2];
 };
 
 __device__ __forceinline__ void flag_timeout(uint32_t* status) {
@@ -274,25 +275,27 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t at) {
 }
 
 // ------------------------------------------------------------------ distinct adapters
-// The distinct adapters among the 128 rows of a tile in order of first use, from 128
-// threads (et = 0 .. 127, one row each). Called by the whole CTA (it synchronises).
+// The distinct adapters among the 128 rows of a tile in order of first use, from 128 threads
+// (et = 0 .. 127, one row each; others et = -1). sync: a barrier of every thread that calls it.
 struct TileSlots {
   int32_t id[BM];        // adapter of each row, -1: none
   int32_t slot[BM];      // slot of each row's adapter, -1: none
   int32_t slot_id[BM];   // adapter of each slot
-  uint32_t off[BM][4];   // rows outside each slot
+  uint4 off[BM];         // rows outside each slot
   int32_t warp_count[4];
   int32_t count;
 };
 
-__device__ void find_slots(TileSlots& s, int et, const int32_t* ids, int n, int T, int row0) {
+template <class Sync>
+__device__ void find_slots(TileSlots& s, int et, const int32_t* ids, int n, int T, int row0,
+                           Sync sync) {
   int id = -1;
   if (et >= 0) {
     id = row0 + et < T ? ids[row0 + et] : -1;
     if (id < 0 || id >= n) id = -1;
     s.id[et] = id;
   }
-  __syncthreads();
+  sync();
   uint32_t eq[4] = {0, 0, 0, 0};
   int first = -1;
   bool leads = false;
@@ -314,37 +317,88 @@ __device__ void find_slots(TileSlots& s, int et, const int32_t* ids, int n, int 
   }
   const unsigned lead = __ballot_sync(0xffffffffu, leads);
   if (et >= 0 && (et & 31) == 0) s.warp_count[et >> 5] = __popc(lead);
-  __syncthreads();
+  sync();
   if (et >= 0 && leads) {
     int pos = __popc(lead & ((1u << (et & 31)) - 1));
     for (int w = 0; w < (et >> 5); ++w) pos += s.warp_count[w];
     s.slot_id[pos] = id;
     s.slot[et] = pos;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) s.off[pos][w] = ~eq[w];
+    s.off[pos] = make_uint4(~eq[0], ~eq[1], ~eq[2], ~eq[3]);
   }
   if (et == 0) s.count = s.warp_count[0] + s.warp_count[1] + s.warp_count[2] + s.warp_count[3];
-  __syncthreads();
+  sync();
   int mine = -1;
   if (et >= 0 && id >= 0) mine = s.slot[first];
-  __syncthreads();
+  sync();
   if (et >= 0) s.slot[et] = mine;
-  __syncthreads();
+  sync();
+}
+
+// What proj_kernel reads: the list of row tile m (128 entries each), or, where it runs SM pairs,
+// one list per pair of row tiles (256 entries each, from the even tile's CTA), in which an
+// adapter of both tiles stands once. Called by the 128 threads et = 0 .. 127, which share named
+// barrier 2; `even` holds row tile m's slots, `odd` is scratch.
+__device__ void publish_slots(bool pairs, int m, int et, const int32_t* ids, int n, int T,
+                              const TileSlots& even, TileSlots& odd, int32_t* n_slots,
+                              Slot* slots) {
+  const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);
+  Slot s;
+  s.pad[0] = s.pad[1] = s.pad[2] = 0;
+  s.off[1] = none;
+  if (!pairs) {
+    if (et == 0) n_slots[m] = even.count;
+    if (et < even.count) {
+      s.id = even.slot_id[et];
+      s.off[0] = even.off[et];
+      slots[(size_t)m * BM + et] = s;
+    }
+    return;
+  }
+  if (m & 1) return;
+  auto sync = [] { named_bar_sync(2, 128); };
+  find_slots(odd, et, ids, n, T, (m + 1) * BM, sync);
+  Slot* out = slots + (size_t)m * BM;
+  if (et < even.count) {
+    s.id = even.slot_id[et];
+    s.off[0] = even.off[et];
+    for (int j = 0; j < odd.count; ++j)
+      if (odd.slot_id[j] == s.id) s.off[1] = odd.off[j];
+    out[et] = s;
+  }
+  bool fresh = et < odd.count;   // the odd tile's own adapters follow
+  for (int j = 0; j < even.count; ++j) fresh = fresh && even.slot_id[j] != odd.slot_id[et];
+  const unsigned f = __ballot_sync(0xffffffffu, fresh);
+  sync();
+  if ((et & 31) == 0) odd.warp_count[et >> 5] = __popc(f);
+  sync();
+  int pos = even.count + __popc(f & ((1u << (et & 31)) - 1));
+  for (int w = 0; w < (et >> 5); ++w) pos += odd.warp_count[w];
+  if (fresh) {
+    s.id = odd.slot_id[et];
+    s.off[0] = none;
+    s.off[1] = odd.off[et];
+    out[pos] = s;
+  }
+  if (et == 0)
+    n_slots[m / 2] = even.count + odd.warp_count[0] + odd.warp_count[1] + odd.warp_count[2] +
+                     odd.warp_count[3];
 }
 
 // ------------------------------------------------------------------ shrink
 // u = scale (x A_a^T), as hi | lo. One cluster of `split` CTAs per row tile (and per `cy`-th
 // chunk of its adapters): each CTA takes a share of the contraction, the partial sums meet
 // through distributed shared memory in rank order. A chunk is at most p.cols accumulator
-// columns: cols / rp adapters side by side, each rp columns wide.
+// columns: cols / rp adapters side by side, each rp columns wide. The ring's stages are as large
+// as the tile's adapters need, and as many as then fit.
 struct ShrinkParams {
   int T, n, r, rp, nb;
-  int kiters, split, cy, cols, stages, a_bytes, stage_bytes;
+  int kiters, split, cy, cols, a_bytes, ring_bytes, tail;
+  int pairs;          // lists for pairs of row tiles
   const int32_t* ids;
   const float* scale;
   uint8_t* uq;        // [T][nb] blocks of 128 bytes
-  int32_t* n_slots;   // [row tiles]
-  Slot* slots;        // [row tiles][128]
+  int32_t* n_slots;
+  Slot* slots;
   uint32_t* status;
 };
 
@@ -352,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     shrink_kernel(const __grid_constant__ CUtensorMap xmap,
                   const __grid_constant__ CUtensorMap amap, const ShrinkParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) TileSlots ts;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  float* red = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);   // [128][rp + 4]
+  __shared__ __align__(16) TileSlots ts, ts_odd;
+  float* red = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                        ~uintptr_t(1023));   // [128][rp + 4], whole KB
   const int rs = p.rp + 4;
-  Bars* bars = reinterpret_cast<Bars*>(red + BM * rs);
+  uint8_t* smem = reinterpret_cast<uint8_t*>(red + BM * rs);
+  Bars* bars = reinterpret_cast<Bars*>(smem + p.ring_bytes + p.tail);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // known uniform
   const int lane = threadIdx.x & 31;
@@ -375,33 +429,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc(&bars->tmem, p.cols);
   tc_fence_before();
-  find_slots(ts, et, p.ids, p.n, p.T, row0);
+  find_slots(ts, et, p.ids, p.n, p.T, row0, [] { __syncthreads(); });
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   const int count = ts.count, per = p.cols / p.rp;
+  const int stage_bytes = p.a_bytes + min(count, per) * p.rp * 128;
 
-  if (c0 == 0 && q == 0 && et >= 0) {
-    if (et == 0) p.n_slots[m] = count;
-    if (et < count) {
-      Slot s;
-      s.id = ts.slot_id[et];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) s.off[w] = ts.off[et][w];
-      s.pad[0] = s.pad[1] = s.pad[2] = 0;
-      p.slots[(size_t)m * BM + et] = s;
-    }
-  }
+  if (c0 == 0 && q == 0 && warp >= 2)   // while the others start the ring
+    publish_slots(p.pairs, m, et, p.ids, p.n, p.T, ts, ts_odd, p.n_slots, p.slots);
 
   const int kb0 = (int)((long long)p.kiters * q / p.split);
   const int kb1 = (int)((long long)p.kiters * (q + 1) / p.split);
-  Ring ring(p.stages);
+  Ring ring(min(kMaxStages, p.ring_bytes / stage_bytes));
   uint32_t parity = 0;
   for (int c = c0; c * per < count; c += p.cy, parity ^= 1) {   // the same chunks in every rank
     const int s0 = c * per, ns = min(per, count - s0);
     if (warp == 0) {
       for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
         if (!warp_wait(bars, &bars->empty[ring.stage], ring.phase ^ 1, p.status)) break;
-        uint8_t* sa = smem + ring.stage * p.stage_bytes;
+        uint8_t* sa = smem + ring.stage * stage_bytes;
         uint64_t* bar = &bars->full[ring.stage];
         if (elect_one()) {
           mbar_arrive_expect_tx(bar, p.a_bytes + ns * p.rp * 128);
@@ -421,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(bars, &bars->full[ring.stage], ring.phase, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + ring.stage * p.stage_bytes);
+        const uint32_t sa = smem_u32(smem + ring.stage * stage_bytes);
         const uint64_t ad = desc_at(km, sa), bd = desc_at(km, sa + p.a_bytes);
         if (elect_one()) {
 #pragma unroll
@@ -521,6 +567,7 @@ struct ShrinkRowsParams {
   uint8_t* uq;
   int32_t* n_slots;
   Slot* slots;
+  int pairs;
 };
 
 __device__ __forceinline__ void unpack8(const uint4 q, float* v) {
@@ -534,23 +581,16 @@ __device__ __forceinline__ void unpack8(const uint4 q, float* v) {
 
 template <int RG>
 __global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRowsParams p) {
-  __shared__ __align__(16) TileSlots ts;
+  __shared__ __align__(16) TileSlots ts, ts_odd;
   __shared__ float part[kRowMaxPieces][RG];
   launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = (int)blockIdx.x / p.groups;
   if (t >= p.T) {
     const int m = (int)blockIdx.x - p.T * p.groups;
-    find_slots(ts, tid < BM ? tid : -1, p.ids, p.n, p.T, m * BM);
-    if (tid == 0) p.n_slots[m] = ts.count;
-    if (tid < ts.count) {
-      Slot s;
-      s.id = ts.slot_id[tid];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) s.off[w] = ts.off[tid][w];
-      s.pad[0] = s.pad[1] = s.pad[2] = 0;
-      p.slots[(size_t)m * BM + tid] = s;
-    }
+    find_slots(ts, tid < BM ? tid : -1, p.ids, p.n, p.T, m * BM, [] { __syncthreads(); });
+    if (tid < BM)
+      publish_slots(p.pairs, m, tid, p.ids, p.n, p.T, ts, ts_odd, p.n_slots, p.slots);
     if (tid == 0) wait_prerequisites();   // what waits for this kernel waits for them too
     return;
   }
@@ -657,29 +697,19 @@ struct ProjParams {
 };
 
 // The adapters that a CTA (or pair) runs for one tile, in a fixed order, 32 at a time in the
-// lanes of a warp. PAIR: the slots of the even row tile, then the odd one's; split: every
-// split-th slot from rank q.
+// lanes of a warp. split: every split-th slot from rank q.
 template <bool PAIR>
 struct SlotList {
-  const Slot* base0;
-  const Slot* base1;
-  int n0, count, q, split, window;
+  const Slot* base;
+  int count, q, split, window;
   int id;
-  uint4 off;
+  uint4 off0, off1;
   __device__ void open(const ProjParams& p, int m, int rank) {   // m: (first) row tile
-    base0 = p.slots + (size_t)m * BM;
-    base1 = base0 + BM;
-    n0 = p.n_slots[m];
-    count = n0;
-    q = 0;
-    split = 1;
-    if (PAIR) {
-      if (m + 1 < p.m_tiles) count += p.n_slots[m + 1];
-    } else {
-      q = rank;
-      split = p.split;
-      count = n0 > q ? (n0 - q + split - 1) / split : 0;
-    }
+    base = p.slots + (size_t)m * BM;
+    const int n = p.n_slots[PAIR ? m / 2 : m];
+    q = PAIR ? 0 : rank;
+    split = PAIR ? 1 : p.split;
+    count = n > q ? (n - q + split - 1) / split : 0;
     window = -1;
     if (count > 0) load(0);
   }
@@ -687,19 +717,24 @@ struct SlotList {
     window = w;
     const int i = 32 * w + (int)(threadIdx.x & 31);
     if (i >= count) return;
-    const Slot* s = PAIR ? (i < n0 ? base0 + i : base1 + (i - n0)) : base0 + (q + i * split);
+    const Slot* s = base + (q + i * split);
     id = s->id;
-    off = make_uint4(s->off[0], s->off[1], s->off[2], s->off[3]);
+    off0 = s->off[0];
+    if (PAIR) off1 = s->off[1];
   }
-  // whole warp: adapter and lane mask of entry i
+  // whole warp: adapter and lane masks of entry i
   __device__ int get_id(int i) {
     if (i >> 5 != window) load(i >> 5);
     return __shfl_sync(0xffffffffu, id, i & 31);
   }
-  __device__ uint4 get_off(int i) {
+  __device__ static uint4 pick(const uint4& v, int lane) {
+    return make_uint4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
+                      __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
+  }
+  __device__ void get_off(int i, uint4& a, uint4& b) {
     if (i >> 5 != window) load(i >> 5);
-    return make_uint4(__shfl_sync(0xffffffffu, off.x, i & 31), __shfl_sync(0xffffffffu, off.y, i & 31),
-                      __shfl_sync(0xffffffffu, off.z, i & 31), __shfl_sync(0xffffffffu, off.w, i & 31));
+    a = pick(off0, i & 31);
+    if (PAIR) b = pick(off1, i & 31);
   }
 };
 
@@ -891,7 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t su = smem_u32(smem + head_stage * p.stage_bytes);
             const uint32_t sb = smem_u32(smem + ring.stage * p.stage_bytes) + p.a_bytes;
             for (int j = 0; j < cnt; ++j) {
-              const uint4 off = list.get_off(i0 + j);
+              uint4 off, off_odd;
+              list.get_off(i0 + j, off, off_odd);
               const uint64_t hi = desc_at(km, su), bd = desc_at(em, sb + j * nc * p.rb * 2);
               if (elect_one()) {
                 for (int kk = 0; kk < p.rb / 16; ++kk) {   // hi and lo of 16 ranks, same rows of B
@@ -899,10 +935,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t first = (p.kiters > 0 || b > 0 || kk > 0) ? 1u : 0u;
                   const uint64_t h = hi + 2 * kk, l = h + 4, e = bd + 128 * kk;
                   if constexpr (PAIR) {
-                    const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);
-                    const bool odd = i0 + j >= list.n0;
-                    umma_bf16_rows_pair(d, h, e, idesc_e, odd ? none : off, odd ? off : none, first);
-                    umma_bf16_rows_pair(d, l, e, idesc_e, odd ? none : off, odd ? off : none, 1u);
+                    umma_bf16_rows_pair(d, h, e, idesc_e, off, off_odd, first);
+                    umma_bf16_rows_pair(d, l, e, idesc_e, off, off_odd, 1u);
                   } else {
                     umma_bf16_rows(d, h, e, idesc_e, off, first);
                     umma_bf16_rows(d, l, e, idesc_e, off, 1u);
@@ -1449,7 +1483,7 @@ struct SavedParts {
   size_t n_slots, slots, uq, total;
 };
 SavedParts saved_parts(const mok_lora_dims& d) {
-  const size_t mt = (size_t)(d.T + BM - 1) / BM, nb = (padded_rank(d.r) + 31) / 32;
+  const size_t mt = (size_t)(d.T + 2 * BM - 1) / (2 * BM) * 2, nb = (padded_rank(d.r) + 31) / 32;
   SavedParts s;
   s.n_slots = 0;
   s.slots = align_up(mt * 4, 256);
@@ -1551,8 +1585,8 @@ int tile_rows(int T) { return T >= BM ? BM : (T + 7) / 8 * 8; }
 // The r values of every row: in [T][C] against w [n][r][C]. early: the launch may start before
 // the stream's last kernel ends.
 mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void* w,
-                      const float* scale, const int32_t* ids, char* saved, uint32_t* status,
-                      bool early, const Device& dev, cudaStream_t s) {
+                      const float* scale, const int32_t* ids, char* saved, bool pairs,
+                      uint32_t* status, bool early, const Device& dev, cudaStream_t s) {
   const SavedParts sp = saved_parts(d);
   const int mt = (d.T + BM - 1) / BM;
   const int rp = padded_rank(d.r), nb = (rp + 31) / 32;
@@ -1565,7 +1599,7 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
       // every rank that the MMAs read is written, padding too
       const int groups = rp / RG;
       ShrinkRowsParams p = {d.T, C, d.n, d.r, nb, groups, static_cast<const __nv_bfloat16*>(in),
-                            static_cast<const __nv_bfloat16*>(w), ids, scale, uq, n_slots, slots};
+                            static_cast<const __nv_bfloat16*>(w), ids, scale, uq, n_slots, slots, pairs};
       return launch(shrink_rows_kernel<RG>, d.T * groups + mt, kRowThreads, 0, 1, early, s, p);
     };
     // the fewest CTAs that still keep the SMs busy
@@ -1582,19 +1616,19 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   p.rp = rp;
   p.nb = nb;
   p.kiters = (C + BK - 1) / BK;
-  p.cols = 128;
+  const int distinct = std::min(std::min(d.n, d.T), BM);   // adapters of a tile, at most
+  p.cols = distinct * rp <= 64 ? 64 : distinct * rp <= 128 ? 128 : 256;
   p.a_bytes = tile_rows(d.T) * BK * 2;
-  p.stage_bytes = p.a_bytes + p.cols * 128;
   // an MMA reads 128 rows from a stage's start, past a short batch's own: in bounds for the
   // last stage too
-  const size_t tail = A_BYTES - p.a_bytes;
-  const size_t fixed = (size_t)BM * (p.rp + 4) * 4 + tail + kBarBytes + 1024;
-  p.stages = std::min<int>(kMaxStages, (int)((kMaxSmem - sizeof(TileSlots) - fixed) / p.stage_bytes));
+  p.tail = A_BYTES - p.a_bytes;
+  const int fixed = BM * (rp + 4) * 4 + p.tail + kBarBytes + 1024;
+  p.ring_bytes = (int)((kMaxSmem - 2 * sizeof(TileSlots) - fixed) / 1024 * 1024);
+  p.pairs = pairs;
   // one wave of clusters, a rank at least two steps
   int i = 0;
   while (i < 3 && 2 * (2 << i) <= p.kiters && mt <= dev.clusters[i + 1]) ++i;
   p.split = 1 << i;
-  const int distinct = std::min(std::min(d.n, d.T), BM);   // adapters of a tile, at most
   const int chunks = (distinct * p.rp + p.cols - 1) / p.cols;
   p.cy = std::max(1, std::min(chunks, dev.clusters[i] / mt));
   p.ids = ids;
@@ -1606,7 +1640,7 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   CUtensorMap xm, am;
   if (!make_map(&xm, in, true, C, d.T, 0, tile_rows(d.T)) || !make_map(&am, w, true, C, d.r, d.n, p.rp))
     return MOK_ERR_CUDA;
-  const size_t smem = (size_t)p.stages * p.stage_bytes + fixed;
+  const size_t smem = (size_t)p.ring_bytes + fixed;
   return launch(shrink_kernel, mt * p.cy * p.split, kThreads, smem, p.split, early, s, xm, am, p) ==
                  cudaSuccess
              ? MOK_OK
@@ -1675,12 +1709,21 @@ ProjForm choose_form(int T, int kiters, int ext, int cols, const Device& dev) {
   return best;
 }
 
+// The form of [T][C] W (C = 0: no W), with or without the adapters' part.
+ProjForm form_of(const mok_lora_dims& d, int C, int cols, bool adapters, const Device& dev) {
+  const int rp = padded_rank(d.r), nb = (rp + 31) / 32, rb = std::min(rp, 32);
+  // short batches are mostly rows of different requests, long ones mostly long runs of one; an
+  // adapter stage takes about as long as two steps over W
+  const int slots = adapters ? (d.T <= BM ? std::min(d.n, d.T) : 2) : 0;
+  return choose_form(d.T, (C + BK - 1) / BK, 2 * nb * ((slots * rb + 63) / 64), cols, dev);
+}
+
 // out [T][cols] = in [T][C] W (trans: W^T) + the low-rank part. W == null: that part alone;
 // parts == null: no such part.
-mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const void* in,
-                    const void* W, const char* parts, const void* expand, const int32_t* ids,
-                    void* out, mok_out_dtype type, uint32_t* status, bool early, const Device& dev,
-                    cudaStream_t s) {
+mok_status run_proj(const mok_lora_dims& d, const ProjForm& f, int C, int cols, bool trans,
+                    const void* in, const void* W, const char* parts, const void* expand,
+                    const int32_t* ids, void* out, mok_out_dtype type, uint32_t* status, bool early,
+                    const Device& dev, cudaStream_t s) {
   const SavedParts sp = saved_parts(d);
   ProjParams p = {};
   p.T = d.T;
@@ -1692,11 +1735,6 @@ mok_status run_proj(const mok_lora_dims& d, int C, int cols, bool trans, const v
   p.nb = (p.rp + 31) / 32;
   p.rb = std::min(p.rp, 32);
   p.out_bf16 = type == MOK_OUT_BF16;
-  // short batches are mostly rows of different requests, long ones mostly long runs of one; an
-  // adapter stage takes about as long as two steps over W
-  const int slots = parts ? (d.T <= BM ? std::min(d.n, d.T) : 2) : 0;
-  const int ext = 2 * p.nb * ((slots * p.rb + 63) / 64);
-  const ProjForm f = choose_form(d.T, p.kiters, ext, cols, dev);
   p.NT = f.NT;
   p.split = f.split;
   p.n_tiles = (cols + p.NT - 1) / p.NT;
@@ -1823,9 +1861,12 @@ extern "C" mok_status mok_lora_fwd(const mok_lora_dims* dims, const mok_lora_wei
   if (!dev) return MOK_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* sv = static_cast<char*>(saved);
-  mok_status st = run_shrink(*dims, dims->K, x_ad ? x_ad : x, w->A, w->scale, ids, sv, status, false, *dev, s);
+  const ProjForm f = form_of(*dims, dims->K, dims->N, true, *dev);
+  mok_status st = run_shrink(*dims, dims->K, x_ad ? x_ad : x, w->A, w->scale, ids, sv, f.pair, status,
+                             false, *dev, s);
   if (st != MOK_OK) return st;
-  return run_proj(*dims, dims->K, dims->N, false, x, w->W, sv, w->B, ids, y, out, status, true, *dev, s);
+  return run_proj(*dims, f, dims->K, dims->N, false, x, w->W, sv, w->B, ids, y, out, status, true,
+                  *dev, s);
 }
 
 extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_weights* w,
@@ -1860,15 +1901,18 @@ extern "C" mok_status mok_lora_bwd(const mok_lora_dims* dims, const mok_lora_wei
   bucket_kernel<<<d.n, kBucketThreads, 0, s>>>(d.T, d.n, ids, reinterpret_cast<int32_t*>(ws + wp.off),
                                                reinterpret_cast<int32_t*>(ws + wp.rows));
   if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
-  mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, status, true, *dev, s);
+  // with x_ad the adapters' part is a product of its own
+  const ProjForm f = form_of(d, d.N, d.K, !x_ad, *dev);
+  const ProjForm fa = x_ad ? form_of(d, 0, d.K, true, *dev) : f;
+  mok_status st = run_shrink(d, d.N, dY, w->B, w->scale, ids, ws, fa.pair, status, true, *dev, s);
   if (st != MOK_OK) return st;
   st = run_wgrad(d, sv + wp.v.uq, ws + wp.v.uq, x_ad ? x_ad : x, dY, ws, wp, dA, dB, out,
                  status, *dev, s);
   if (st != MOK_OK) return st;
-  st = run_proj(d, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, true,
+  st = run_proj(d, f, d.N, d.K, true, dY, w->W, x_ad ? nullptr : ws, w->A, ids, dX, out, status, true,
                 *dev, s);
   if (st != MOK_OK || !x_ad) return st;
-  return run_proj(d, d.N, d.K, true, nullptr, nullptr, ws, w->A, ids, dXa, out, status, false, *dev,
+  return run_proj(d, fa, 0, d.K, true, nullptr, nullptr, ws, w->A, ids, dXa, out, status, false, *dev,
                   s);
 }
 
