@@ -1625,12 +1625,24 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   const int fixed = BM * (rp + 4) * 4 + p.tail + kBarBytes + 1024;
   p.ring_bytes = (int)((kMaxSmem - 2 * sizeof(TileSlots) - fixed) / 1024 * 1024);
   p.pairs = pairs;
-  // one wave of clusters, a rank at least two steps
-  int i = 0;
-  while (i < 3 && 2 * (2 << i) <= p.kiters && mt <= dev.clusters[i + 1]) ++i;
-  p.split = 1 << i;
+  // How many ranks share a tile's contraction (a rank takes at least two steps), against how many
+  // clusters share its chunks: the least estimated time in microseconds, 0.35 a step and 5 for
+  // the start and the join of a chunk, over a batch whose tiles hold every adapter they can and
+  // one of long runs (a single chunk), which the host cannot tell apart.
   const int chunks = (distinct * p.rp + p.cols - 1) / p.cols;
-  p.cy = std::max(1, std::min(chunks, dev.clusters[i] / mt));
+  double best = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int split = 1 << i, fit = dev.clusters[i];
+    if (i > 0 && 2 * split > p.kiters) break;
+    const int cy = std::max(1, std::min(chunks, fit / mt));
+    const double waves = (mt + fit - 1) / fit, rounds = (chunks + cy - 1) / cy;
+    const double t = waves * (rounds + 1) * ((p.kiters + split - 1) / split * 0.35 + 5.0);
+    if (best == 0 || t < best) {
+      best = t;
+      p.split = split;
+      p.cy = cy;
+    }
+  }
   p.ids = ids;
   p.scale = scale;
   p.uq = uq;
