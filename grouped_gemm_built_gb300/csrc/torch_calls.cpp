@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <cstring>
 
 #include "mok_ops.h"
 
@@ -73,6 +74,17 @@ template <typename S>
 S* at_address(PyObject* o) {
   return static_cast<S*>(PyLong_AsVoidPtr(o));
 }
+// The ABI struct that a ctypes object holds, copied; false (with a Python error) for others.
+template <typename S>
+bool read_struct(PyObject* o, S* out) {
+  Py_buffer b;
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) return false;
+  const bool ok = b.len == (Py_ssize_t)sizeof(S);
+  if (ok) std::memcpy(out, b.buf, sizeof(S));
+  else PyErr_Format(PyExc_TypeError, "expected a struct of %zu bytes, got %zd", sizeof(S), b.len);
+  PyBuffer_Release(&b);
+  return ok;
+}
 
 // bind(route, route_bwd, dropout, lora_get_sizes, lora_fwd, lora_bwd): addresses in libmok
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -87,20 +99,21 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-// route(&rule, logits, bias | None) -> (topk_idx, gates)
+// route(rule, logits, bias | None) -> (topk_idx, gates)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 3)) return nullptr;
-  const auto* rule = at_address<const mok_routing>(a[0]);
+  mok_routing rule;
+  if (!read_struct(a[0], &rule)) return nullptr;
   const at::Tensor* l = dense(a[1]);
-  if (!l || l->dim() != 2 || l->size(1) != rule->E || l->size(0) > INT_MAX) Py_RETURN_NONE;
+  if (!l || l->dim() != 2 || l->size(1) != rule.E || l->size(0) > INT_MAX) Py_RETURN_NONE;
   const int code = code_of(l->scalar_type());
-  const at::Tensor* b = a[2] == Py_None ? nullptr : dense(a[2], at::kFloat, rule->E, *l);
+  const at::Tensor* b = a[2] == Py_None ? nullptr : dense(a[2], at::kFloat, rule.E, *l);
   if (code < 0 || (!b && a[2] != Py_None)) Py_RETURN_NONE;
   const int T = (int)l->size(0);
   c10::cuda::OptionalCUDAGuard guard(l->device());
-  at::Tensor idx = make({T, rule->k}, at::kInt, *l), gates = make({T, rule->k}, at::kFloat, *l);
-  const mok_status st = api.route(rule, T, l->data_ptr(), (mok_out_dtype)code,
+  at::Tensor idx = make({T, rule.k}, at::kInt, *l), gates = make({T, rule.k}, at::kFloat, *l);
+  const mok_status st = api.route(&rule, T, l->data_ptr(), (mok_out_dtype)code,
                                   b ? b->data_ptr<float>() : nullptr, idx.data_ptr<int32_t>(),
                                   gates.data_ptr<float>(), stream_of(*l));
   if (st != MOK_OK) return PyLong_FromLong(st);
@@ -108,23 +121,24 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// route_bwd(&rule, logits, topk_idx, dgates, code of dlogits) -> (dlogits,)
+// route_bwd(rule, logits, topk_idx, dgates, code of dlogits) -> (dlogits,)
 PyObject* route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 5)) return nullptr;
-  const auto* rule = at_address<const mok_routing>(a[0]);
+  mok_routing rule;
+  if (!read_struct(a[0], &rule)) return nullptr;
   const at::Tensor* l = dense(a[1]);
-  if (!l || l->dim() != 2 || l->size(1) != rule->E || l->size(0) > INT_MAX) Py_RETURN_NONE;
+  if (!l || l->dim() != 2 || l->size(1) != rule.E || l->size(0) > INT_MAX) Py_RETURN_NONE;
   const int code = code_of(l->scalar_type());
   const int T = (int)l->size(0);
-  const at::Tensor* idx = dense(a[2], at::kInt, (int64_t)T * rule->k, *l);
-  const at::Tensor* dg = dense(a[3], at::kFloat, (int64_t)T * rule->k, *l);
+  const at::Tensor* idx = dense(a[2], at::kInt, (int64_t)T * rule.k, *l);
+  const at::Tensor* dg = dense(a[3], at::kFloat, (int64_t)T * rule.k, *l);
   const long out_code = PyLong_AsLong(a[4]);
   if (PyErr_Occurred()) return nullptr;
   if (code < 0 || !idx || !dg) Py_RETURN_NONE;
   c10::cuda::OptionalCUDAGuard guard(l->device());
-  at::Tensor out = make({T, rule->E}, type_of(out_code), *l);
-  const mok_status st = api.route_bwd(rule, T, l->data_ptr(), (mok_out_dtype)code,
+  at::Tensor out = make({T, rule.E}, type_of(out_code), *l);
+  const mok_status st = api.route_bwd(&rule, T, l->data_ptr(), (mok_out_dtype)code,
                                       idx->data_ptr<int32_t>(), dg->data_ptr<float>(),
                                       out.data_ptr(), (mok_out_dtype)out_code, stream_of(*l));
   if (st != MOK_OK) return PyLong_FromLong(st);

@@ -8,7 +8,6 @@ The results feed a layer without a router of its own (``MoELayer(router=False)``
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional
 
 import torch
@@ -36,7 +35,6 @@ class Routing:
                                    top_groups=top_groups,
                                    group_score=self.GROUP_SCORES[group_score],
                                    renormalize=1 if renormalize else 0, scale=scale)
-        self._at = ctypes.addressof(self.rule)
         mok.mok_route(self.rule, 0, None, mok.MOK_OUT_F32, None, None, None, None)  # checks it
 
     def _check(self, logits, bias=None, topk_idx=None, dgates=None, backward=False):
@@ -54,7 +52,7 @@ class Routing:
     def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None):
         """(topk_idx [T,k] int32, gates [T,k] fp32) from logits [T,E] bf16 or fp32 and the
         selection bias [E] fp32."""
-        return _results(mok.torch_calls().route(self._at, logits, bias), "mok_route",
+        return _results(mok.torch_calls().route(self.rule, logits, bias), "mok_route",
                         lambda: self._check(logits, bias))
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, dgates: torch.Tensor,
@@ -62,7 +60,7 @@ class Routing:
         """dlogits [T,E] (``dtype``, the logits' type by default) from dgates [T,k] fp32, at
         the choice that ``forward`` made from these logits."""
         dtype = dtype or getattr(logits, "dtype", None)
-        got = mok.torch_calls().route_bwd(self._at, logits, topk_idx, dgates,
+        got = mok.torch_calls().route_bwd(self.rule, logits, topk_idx, dgates,
                                           _result_code(dtype, "dlogits"))
         return _results(got, "mok_route_bwd", lambda: self._check(
             logits, topk_idx=topk_idx, dgates=dgates, backward=True))[0]
