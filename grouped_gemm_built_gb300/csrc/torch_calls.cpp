@@ -170,15 +170,18 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The rows of an adapted projection: x [T][K] bf16, ids [T] int32, x_ad like x or None.
+// The rows of an adapted projection: x [T][K] bf16, ids [T] int32, x_ad like x or None; and the
+// status word, which lies on the weights' device and ties x to it.
 struct Rows {
   mok_lora_dims dims;
-  const at::Tensor *x, *ids, *x_ad;
-  bool read(PyObject* dims_at, PyObject* px, PyObject* pids, PyObject* pad) {
+  const at::Tensor *status, *x, *ids, *x_ad;
+  bool read(PyObject* dims_at, PyObject* pstatus, PyObject* px, PyObject* pids, PyObject* pad) {
     const auto* d = at_address<const mok_lora_dims>(dims_at);
     x = dense(px);
     if (!d || !x) return false;
     dims = *d;
+    status = dense(pstatus, at::kInt, 1, *x);
+    if (!status) return false;
     if (x->scalar_type() != at::kBFloat16 || x->dim() != 2 || x->size(1) != dims.K ||
         x->size(0) > INT_MAX)
       return false;
@@ -187,14 +190,15 @@ struct Rows {
     x_ad = pad == Py_None ? nullptr : dense(pad, at::kBFloat16, x->numel(), *x);
     return ids && (x_ad || pad == Py_None);
   }
+  uint32_t* status_word() const { return static_cast<uint32_t*>(status->data_ptr()); }
 };
 
-// lora_fwd(&dims, &weights, status address, x, ids, x_ad | None, code of y) -> (y, saved)
+// lora_fwd(&dims, &weights, status, x, ids, x_ad | None, code of y) -> (y, saved)
 PyObject* lora_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 7)) return nullptr;
   Rows r;
-  if (!r.read(a[0], a[3], a[4], a[5])) Py_RETURN_NONE;
+  if (!r.read(a[0], a[2], a[3], a[4], a[5])) Py_RETURN_NONE;
   const long code = PyLong_AsLong(a[6]);
   if (PyErr_Occurred()) return nullptr;
   mok_lora_sizes sizes;
@@ -205,20 +209,20 @@ PyObject* lora_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor saved = make({(int64_t)sizes.saved_bytes}, at::kByte, *r.x);
   st = api.lora_fwd(&r.dims, at_address<const mok_lora_weights>(a[1]), r.x->data_ptr(),
                     r.x_ad ? r.x_ad->data_ptr() : nullptr, r.ids->data_ptr<int32_t>(), y.data_ptr(),
-                    (mok_out_dtype)code, saved.data_ptr(), at_address<uint32_t>(a[2]),
+                    (mok_out_dtype)code, saved.data_ptr(), r.status_word(),
                     stream_of(*r.x));
   if (st != MOK_OK) return PyLong_FromLong(st);
   return results(std::move(y), std::move(saved));
   END_HANDLE_TH_ERRORS
 }
 
-// lora_bwd(&dims, &weights, status address, x, ids, x_ad | None, saved, dY, code of the
+// lora_bwd(&dims, &weights, status, x, ids, x_ad | None, saved, dY, code of the
 // gradients) -> (dX, dA, dB[, dXa])
 PyObject* lora_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 9)) return nullptr;
   Rows r;
-  if (!r.read(a[0], a[3], a[4], a[5])) Py_RETURN_NONE;
+  if (!r.read(a[0], a[2], a[3], a[4], a[5])) Py_RETURN_NONE;
   const long code = PyLong_AsLong(a[8]);
   if (PyErr_Occurred()) return nullptr;
   const mok_lora_dims& d = r.dims;
@@ -238,7 +242,7 @@ PyObject* lora_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     r.x_ad ? r.x_ad->data_ptr() : nullptr, r.ids->data_ptr<int32_t>(),
                     saved->data_ptr(), dY->data_ptr(), dX.data_ptr(),
                     r.x_ad ? dXa.data_ptr() : nullptr, dA.data_ptr(), dB.data_ptr(),
-                    (mok_out_dtype)code, ws.data_ptr(), at_address<uint32_t>(a[2]), stream_of(*r.x));
+                    (mok_out_dtype)code, ws.data_ptr(), r.status_word(), stream_of(*r.x));
   if (st != MOK_OK) return PyLong_FromLong(st);
   if (r.x_ad) return results(std::move(dX), std::move(dA), std::move(dB), std::move(dXa));
   return results(std::move(dX), std::move(dA), std::move(dB));

@@ -16,7 +16,8 @@ class AdaptedLinear:
     projection W [K,N], n adapters A [n,r,K] and B [n,r,N] (bf16), scale [n] fp32. The object
     keeps the tensors, not copies: updated weights are what the next call reads."""
 
-    _at = (0, 0, 0)      # addresses of the dims, the weights and the status word
+    _at = (0, 0)         # addresses of the dims and the weights
+    _status = device = None
 
     def __init__(self, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor):
         for name, t, nd in (("W", W, 2), ("A", A, 3), ("B", B, 3)):
@@ -29,6 +30,9 @@ class AdaptedLinear:
         if A.shape[2] != self.K or tuple(B.shape) != (self.n, self.r, self.N):
             raise ValueError(f"W {tuple(W.shape)}, A {tuple(A.shape)} and B {tuple(B.shape)} "
                              "must be [K,N], [n,r,K] and [n,r,N]")
+        for name, t in (("A", A), ("B", B), ("scale", scale)):
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.device != W.device:
+                raise ValueError(f"{name} must be on W's device {W.device}, got {t.device}")
         bf = torch.bfloat16
         self.w = mok.MokLoraWeights(W=_dev(W, "W", bf, W.numel()), A=_dev(A, "A", bf, A.numel()),
                                     B=_dev(B, "B", bf, B.numel()),
@@ -38,7 +42,7 @@ class AdaptedLinear:
         self._status = torch.zeros(1, dtype=torch.int32, device=W.device)
         self.dims = mok.MokLoraDims(T=1, K=self.K, N=self.N, n=self.n, r=self.r)
         mok.mok_lora_get_sizes(self.dims)           # checks the sizes
-        self._at = (ctypes.addressof(self.dims), ctypes.addressof(self.w), self._status.data_ptr())
+        self._at = (ctypes.addressof(self.dims), ctypes.addressof(self.w))
 
     def _check(self, x, ids, x_ad, saved=None, dY=None, backward=False):
         if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != self.K:
@@ -51,6 +55,8 @@ class AdaptedLinear:
             dims = mok.MokLoraDims(T=T, K=self.K, N=self.N, n=self.n, r=self.r)
             _dev(saved, "saved", torch.uint8, mok.mok_lora_get_sizes(dims).saved_bytes)
             _dev(dY, "dY", bf, T * self.N)
+        if x.device != self.device:
+            raise ValueError(f"x must be on the weights' device {self.device}, got {x.device}")
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, x_ad: Optional[torch.Tensor] = None,
                 out: torch.dtype = torch.bfloat16):
@@ -58,7 +64,7 @@ class AdaptedLinear:
         ``x_ad``: the adapters' own input when it is not x (x after dropout). ``saved`` is
         what ``backward`` takes."""
         code = _result_code(out, "y")
-        return _results(mok.torch_calls().lora_fwd(*self._at, x, ids, x_ad, code), "mok_lora_fwd",
+        return _results(mok.torch_calls().lora_fwd(*self._at, self._status, x, ids, x_ad, code), "mok_lora_fwd",
                         lambda: self._check(x, ids, x_ad))
 
     def backward(self, x: torch.Tensor, ids: torch.Tensor, saved: torch.Tensor,
@@ -67,7 +73,7 @@ class AdaptedLinear:
         """{"dX", "dA", "dB"} for dY [T,N] bf16, after ``forward`` with the same x, ids and
         x_ad; with x_ad, "dXa" holds its gradient and "dX" only the shared projection's."""
         code = _result_code(out, "gradients")
-        got = _results(mok.torch_calls().lora_bwd(*self._at, x, ids, x_ad, saved, dY, code),
+        got = _results(mok.torch_calls().lora_bwd(*self._at, self._status, x, ids, x_ad, saved, dY, code),
                        "mok_lora_bwd", lambda: self._check(x, ids, x_ad, saved, dY, backward=True))
         return dict(zip(("dX", "dA", "dB", "dXa"), got))
 

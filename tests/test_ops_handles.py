@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from grouped_gemm_built_gb300 import build, mok
+from grouped_gemm_built_gb300.lora import AdaptedLinear
 from grouped_gemm_built_gb300.routing import Routing
 
 
@@ -34,3 +35,40 @@ def test_a_call_reads_the_rule_object_itself():
             calls.route(wrong, torch.zeros(3, 64), None)
         with pytest.raises(TypeError):
             calls.route_bwd(wrong, torch.zeros(3, 64), None, None, mok.MOK_OUT_F32)
+
+
+class _On(torch.Tensor):
+    """A host tensor that claims to be on a CUDA device of its own, for the checks only."""
+
+    is_cuda = True
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index_)
+
+
+def on(index, *shape, dtype=torch.bfloat16):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(_On)
+    t.index_ = index
+    return t
+
+
+@pytest.mark.parametrize("name", ["A", "B", "scale"])
+def test_weights_share_a_device(name):
+    w = dict(W=on(0, 64, 32), A=on(0, 2, 4, 64), B=on(0, 2, 4, 32),
+             scale=on(0, 2, dtype=torch.float32))
+    w[name].index_ = 1
+    with pytest.raises(ValueError, match=f"{name} must be on W's device cuda:0, got cuda:1"):
+        AdaptedLinear(**w)
+
+
+def test_rows_are_on_the_device_of_the_weights():
+    L = AdaptedLinear.__new__(AdaptedLinear)
+    L.K, L.N, L.n, L.r, L.device = 64, 32, 2, 4, torch.device("cuda", 0)
+    x, ids = on(1, 3, 64), on(1, 3, dtype=torch.int32)
+    saved = on(1, mok.mok_lora_get_sizes(mok.MokLoraDims(T=3, K=64, N=32, n=2, r=4)).saved_bytes,
+               dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x must be on the weights' device cuda:0, got cuda:1"):
+        L.forward(x, ids)
+    with pytest.raises(ValueError, match="x must be on the weights' device cuda:0, got cuda:1"):
+        L.backward(x, ids, saved, on(1, 3, 32))
