@@ -70,10 +70,6 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
   PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
   return false;
 }
-template <typename S>
-S* at_address(PyObject* o) {
-  return static_cast<S*>(PyLong_AsVoidPtr(o));
-}
 // The ABI struct that a ctypes object holds, copied; false (with a Python error) for others.
 template <typename S>
 bool read_struct(PyObject* o, S* out) {
@@ -170,19 +166,38 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The rows of an adapted projection: x [T][K] bf16, ids [T] int32, x_ad like x or None; and the
-// status word, which lies on the weights' device and ties x to it.
-struct Rows {
+// An adapted projection and its rows. weights: the tuple (W [K][N], A [n][r][K], B [n][r][N],
+// scale [n], status word, (K, N, n, r)), whose tensors say at every call where they lie now; then
+// x [T][K] bf16, ids [T] int32, x_ad like x or None, all on one device.
+struct Adapted {
   mok_lora_dims dims;
-  const at::Tensor *status, *x, *ids, *x_ad;
-  bool read(PyObject* dims_at, PyObject* pstatus, PyObject* px, PyObject* pids, PyObject* pad) {
-    const auto* d = at_address<const mok_lora_dims>(dims_at);
+  mok_lora_weights w;
+  uint32_t* status;
+  const at::Tensor *x, *ids, *x_ad;
+  bool read(PyObject* weights, PyObject* px, PyObject* pids, PyObject* pad) {
     x = dense(px);
-    if (!d || !x) return false;
-    dims = *d;
-    status = dense(pstatus, at::kInt, 1, *x);
-    if (!status) return false;
-    if (x->scalar_type() != at::kBFloat16 || x->dim() != 2 || x->size(1) != dims.K ||
+    if (!x || !PyTuple_Check(weights) || PyTuple_GET_SIZE(weights) != 6) return false;
+    PyObject* sizes = PyTuple_GET_ITEM(weights, 5);
+    if (!PyTuple_Check(sizes) || PyTuple_GET_SIZE(sizes) != 4) return false;
+    long v[4];
+    for (int i = 0; i < 4; ++i) {
+      v[i] = PyLong_AsLong(PyTuple_GET_ITEM(sizes, i));
+      if (v[i] < 0 || v[i] > INT_MAX) return false;
+    }
+    const int64_t K = v[0], N = v[1], n = v[2], r = v[3];
+    auto weight = [&](int i, at::IntArrayRef shape) {
+      const at::Tensor* t =
+          dense(PyTuple_GET_ITEM(weights, i), at::kBFloat16, c10::multiply_integers(shape), *x);
+      return t && t->sizes() == shape ? t : nullptr;
+    };
+    const at::Tensor *W = weight(0, {K, N}), *A = weight(1, {n, r, K}), *B = weight(2, {n, r, N}),
+                     *scale = dense(PyTuple_GET_ITEM(weights, 3), at::kFloat, n, *x),
+                     *word = dense(PyTuple_GET_ITEM(weights, 4), at::kInt, 1, *x);
+    if (!W || !A || !B || !scale || !word) return false;
+    dims = {0, (int)K, (int)N, (int)n, (int)r};
+    w = {W->data_ptr(), A->data_ptr(), B->data_ptr(), scale->data_ptr<float>()};
+    status = static_cast<uint32_t*>(word->data_ptr());
+    if (x->scalar_type() != at::kBFloat16 || x->dim() != 2 || x->size(1) != K ||
         x->size(0) > INT_MAX)
       return false;
     dims.T = (int)x->size(0);
@@ -190,16 +205,18 @@ struct Rows {
     x_ad = pad == Py_None ? nullptr : dense(pad, at::kBFloat16, x->numel(), *x);
     return ids && (x_ad || pad == Py_None);
   }
-  uint32_t* status_word() const { return static_cast<uint32_t*>(status->data_ptr()); }
 };
 
-// lora_fwd(&dims, &weights, status, x, ids, x_ad | None, code of y) -> (y, saved)
+// lora_fwd(weights, x, ids, x_ad | None, code of y) -> (y, saved)
 PyObject* lora_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 7)) return nullptr;
-  Rows r;
-  if (!r.read(a[0], a[2], a[3], a[4], a[5])) Py_RETURN_NONE;
-  const long code = PyLong_AsLong(a[6]);
+  if (!count(n, 5)) return nullptr;
+  Adapted r;
+  if (!r.read(a[0], a[1], a[2], a[3])) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  const long code = PyLong_AsLong(a[4]);
   if (PyErr_Occurred()) return nullptr;
   mok_lora_sizes sizes;
   mok_status st = api.lora_get_sizes(&r.dims, &sizes);
@@ -207,30 +224,32 @@ PyObject* lora_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::cuda::OptionalCUDAGuard guard(r.x->device());
   at::Tensor y = make({r.dims.T, r.dims.N}, type_of(code), *r.x);
   at::Tensor saved = make({(int64_t)sizes.saved_bytes}, at::kByte, *r.x);
-  st = api.lora_fwd(&r.dims, at_address<const mok_lora_weights>(a[1]), r.x->data_ptr(),
-                    r.x_ad ? r.x_ad->data_ptr() : nullptr, r.ids->data_ptr<int32_t>(), y.data_ptr(),
-                    (mok_out_dtype)code, saved.data_ptr(), r.status_word(),
-                    stream_of(*r.x));
+  st = api.lora_fwd(&r.dims, &r.w, r.x->data_ptr(), r.x_ad ? r.x_ad->data_ptr() : nullptr,
+                    r.ids->data_ptr<int32_t>(), y.data_ptr(), (mok_out_dtype)code, saved.data_ptr(),
+                    r.status, stream_of(*r.x));
   if (st != MOK_OK) return PyLong_FromLong(st);
   return results(std::move(y), std::move(saved));
   END_HANDLE_TH_ERRORS
 }
 
-// lora_bwd(&dims, &weights, status, x, ids, x_ad | None, saved, dY, code of the
-// gradients) -> (dX, dA, dB[, dXa])
+// lora_bwd(weights, x, ids, x_ad | None, saved, dY, code of the gradients)
+//   -> (dX, dA, dB[, dXa])
 PyObject* lora_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 9)) return nullptr;
-  Rows r;
-  if (!r.read(a[0], a[2], a[3], a[4], a[5])) Py_RETURN_NONE;
-  const long code = PyLong_AsLong(a[8]);
+  if (!count(n, 7)) return nullptr;
+  Adapted r;
+  if (!r.read(a[0], a[1], a[2], a[3])) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  const long code = PyLong_AsLong(a[6]);
   if (PyErr_Occurred()) return nullptr;
   const mok_lora_dims& d = r.dims;
   mok_lora_sizes sizes;
   mok_status st = api.lora_get_sizes(&d, &sizes);
   if (st != MOK_OK) return PyLong_FromLong(st);
-  const at::Tensor* saved = dense(a[6], at::kByte, (int64_t)sizes.saved_bytes, *r.x);
-  const at::Tensor* dY = dense(a[7], at::kBFloat16, (int64_t)d.T * d.N, *r.x);
+  const at::Tensor* saved = dense(a[4], at::kByte, (int64_t)sizes.saved_bytes, *r.x);
+  const at::Tensor* dY = dense(a[5], at::kBFloat16, (int64_t)d.T * d.N, *r.x);
   if (!saved || !dY) Py_RETURN_NONE;
   const at::ScalarType type = type_of(code);
   c10::cuda::OptionalCUDAGuard guard(r.x->device());
@@ -238,11 +257,10 @@ PyObject* lora_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
              dB = make({d.n, d.r, d.N}, type, *r.x), dXa;
   if (r.x_ad) dXa = make({d.T, d.K}, type, *r.x);
   const at::Tensor ws = make({(int64_t)sizes.workspace_bytes}, at::kByte, *r.x);
-  st = api.lora_bwd(&d, at_address<const mok_lora_weights>(a[1]), r.x->data_ptr(),
-                    r.x_ad ? r.x_ad->data_ptr() : nullptr, r.ids->data_ptr<int32_t>(),
-                    saved->data_ptr(), dY->data_ptr(), dX.data_ptr(),
+  st = api.lora_bwd(&d, &r.w, r.x->data_ptr(), r.x_ad ? r.x_ad->data_ptr() : nullptr,
+                    r.ids->data_ptr<int32_t>(), saved->data_ptr(), dY->data_ptr(), dX.data_ptr(),
                     r.x_ad ? dXa.data_ptr() : nullptr, dA.data_ptr(), dB.data_ptr(),
-                    (mok_out_dtype)code, ws.data_ptr(), r.status_word(), stream_of(*r.x));
+                    (mok_out_dtype)code, ws.data_ptr(), r.status, stream_of(*r.x));
   if (st != MOK_OK) return PyLong_FromLong(st);
   if (r.x_ad) return results(std::move(dX), std::move(dA), std::move(dB), std::move(dXa));
   return results(std::move(dX), std::move(dA), std::move(dB));

@@ -2,7 +2,6 @@
 (``mok_lora_fwd`` and ``mok_lora_bwd`` in include/mok_ops.h)."""
 from __future__ import annotations
 
-import ctypes
 from typing import Optional
 
 import torch
@@ -14,10 +13,11 @@ from .layer import _dev, _result_code, _results
 class AdaptedLinear:
     """``y = x W + scale[a] (x A_a^T) B_a`` with ``a = ids[t]`` for each row t of x: one frozen
     projection W [K,N], n adapters A [n,r,K] and B [n,r,N] (bf16), scale [n] fp32. The object
-    keeps the tensors, not copies: updated weights are what the next call reads."""
+    keeps the tensors, not copies or addresses: what W, A, B and scale hold at a call is what it
+    reads, also after another tensor of the same shape has taken their place."""
 
-    _at = (0, 0)         # addresses of the dims and the weights
-    _status = device = None
+    W = A = B = scale = _status = device = None
+    _shape = (0, 0, 0, 0)       # K, N, n, r
 
     def __init__(self, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor):
         for name, t, nd in (("W", W, 2), ("A", A, 3), ("B", B, 3)):
@@ -27,22 +27,28 @@ class AdaptedLinear:
                 raise ValueError(f"{name} must have {nd} dimensions, got {tuple(t.shape)}")
         self.K, self.N = W.shape
         self.n, self.r = A.shape[:2]
+        self._shape = (self.K, self.N, self.n, self.r)
         if A.shape[2] != self.K or tuple(B.shape) != (self.n, self.r, self.N):
             raise ValueError(f"W {tuple(W.shape)}, A {tuple(A.shape)} and B {tuple(B.shape)} "
                              "must be [K,N], [n,r,K] and [n,r,N]")
-        for name, t in (("A", A), ("B", B), ("scale", scale)):
-            if isinstance(t, torch.Tensor) and t.is_cuda and t.device != W.device:
-                raise ValueError(f"{name} must be on W's device {W.device}, got {t.device}")
-        bf = torch.bfloat16
-        self.w = mok.MokLoraWeights(W=_dev(W, "W", bf, W.numel()), A=_dev(A, "A", bf, A.numel()),
-                                    B=_dev(B, "B", bf, B.numel()),
-                                    scale=_dev(scale, "scale", torch.float32, self.n))
         self.W, self.A, self.B, self.scale = W, A, B, scale
         self.device = W.device
+        self._check_weights()
+        mok.mok_lora_get_sizes(mok.MokLoraDims(T=1, K=self.K, N=self.N, n=self.n, r=self.r))
         self._status = torch.zeros(1, dtype=torch.int32, device=W.device)
-        self.dims = mok.MokLoraDims(T=1, K=self.K, N=self.N, n=self.n, r=self.r)
-        mok.mok_lora_get_sizes(self.dims)           # checks the sizes
-        self._at = (ctypes.addressof(self.dims), ctypes.addressof(self.w))
+
+    def _check_weights(self):
+        K, N, n, r = self._shape
+        for name, shape in (("W", (K, N)), ("A", (n, r, K)), ("B", (n, r, N)), ("scale", (n,))):
+            t, kind = getattr(self, name), torch.float32 if name == "scale" else torch.bfloat16
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.device != self.device:
+                raise ValueError(f"{name} must be on W's device {self.device}, got {t.device}")
+            numel = 1
+            for d in shape:
+                numel *= d
+            _dev(t, name, kind, numel)
+            if name != "scale" and tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
 
     def _check(self, x, ids, x_ad, saved=None, dY=None, backward=False):
         if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != self.K:
@@ -57,6 +63,10 @@ class AdaptedLinear:
             _dev(dY, "dY", bf, T * self.N)
         if x.device != self.device:
             raise ValueError(f"x must be on the weights' device {self.device}, got {x.device}")
+        self._check_weights()
+
+    def _weights(self):
+        return self.W, self.A, self.B, self.scale, self._status, self._shape
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, x_ad: Optional[torch.Tensor] = None,
                 out: torch.dtype = torch.bfloat16):
@@ -64,16 +74,16 @@ class AdaptedLinear:
         ``x_ad``: the adapters' own input when it is not x (x after dropout). ``saved`` is
         what ``backward`` takes."""
         code = _result_code(out, "y")
-        return _results(mok.torch_calls().lora_fwd(*self._at, self._status, x, ids, x_ad, code), "mok_lora_fwd",
-                        lambda: self._check(x, ids, x_ad))
+        return _results(mok.torch_calls().lora_fwd(self._weights(), x, ids, x_ad, code),
+                        "mok_lora_fwd", lambda: self._check(x, ids, x_ad))
 
     def backward(self, x: torch.Tensor, ids: torch.Tensor, saved: torch.Tensor,
                  dY: torch.Tensor, x_ad: Optional[torch.Tensor] = None,
                  out: torch.dtype = torch.bfloat16):
-        """{"dX", "dA", "dB"} for dY [T,N] bf16, after ``forward`` with the same x, ids and
-        x_ad; with x_ad, "dXa" holds its gradient and "dX" only the shared projection's."""
+        """{"dX", "dA", "dB"} for dY [T,N] bf16, after ``forward`` with the same x, ids, x_ad and
+        weights; with x_ad, "dXa" holds its gradient and "dX" only the shared projection's."""
         code = _result_code(out, "gradients")
-        got = _results(mok.torch_calls().lora_bwd(*self._at, self._status, x, ids, x_ad, saved, dY, code),
+        got = _results(mok.torch_calls().lora_bwd(self._weights(), x, ids, x_ad, saved, dY, code),
                        "mok_lora_bwd", lambda: self._check(x, ids, x_ad, saved, dY, backward=True))
         return dict(zip(("dX", "dA", "dB", "dXa"), got))
 

@@ -72,3 +72,22 @@ def test_rows_are_on_the_device_of_the_weights():
         L.forward(x, ids)
     with pytest.raises(ValueError, match="x must be on the weights' device cuda:0, got cuda:1"):
         L.backward(x, ids, saved, on(1, 3, 32))
+
+
+def test_replaced_weights_are_checked_at_the_call(monkeypatch):
+    """Weights that another tensor has replaced: the call looks at that one."""
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, _z=torch.zeros, **k: _z(*a, **k))
+    W, A = on(0, 64, 32), on(0, 2, 4, 64)
+    L = AdaptedLinear(W, A, on(0, 2, 4, 32), on(0, 2, dtype=torch.float32))
+    x, ids = on(0, 3, 64), on(0, 3, dtype=torch.int32)
+    for name, wrong, what in (("A", on(1, 2, 4, 64), "A must be on"), ("A", on(0, 2, 64, 4), r"A must be \["),
+                              ("W", on(0, 64, 40), "W must have"), ("scale", on(0, 2), "scale must be"),
+                              ("B", torch.zeros(2, 4, 32, dtype=torch.bfloat16), "B must be on a CUDA")):
+        right = getattr(L, name)
+        setattr(L, name, wrong)
+        with pytest.raises(ValueError, match=what):
+            L.forward(x, ids)
+        setattr(L, name, right)
+    A.set_(on(0, 2, 3, 64))
+    with pytest.raises(ValueError, match="A must have"):
+        L.forward(x, ids)
