@@ -166,6 +166,19 @@ __device__ __forceinline__ void warp_softmax(float* s, float& m, float& inv_z) {
   for (int i = 0; i < NV; ++i) s[i] *= inv_z;
 }
 
+// Renormalised gates from the chosen logits, one per lane (-inf: none): each score over the sum of
+// all. Softmax scores are taken relative to the largest chosen one, so that their sum cannot
+// underflow; so are sigmoid scores where the largest chosen logit is below -17 (there 1 + e^l is 1
+// in fp32 and sigmoid(l) is e^l, which is 0 below -104).
+__device__ __forceinline__ float renormalized(bool is_sigmoid, float l) {
+  const float mc = warp_max(l);
+  float w;
+  if (is_sigmoid && mc > -17.f) w = sigmoid(l);
+  else w = l > -INFINITY ? expf(l - mc) : 0.f;
+  const float sum = warp_sum(w);
+  return sum > 0.f ? w / sum : 0.f;
+}
+
 template <int NV, typename LT>
 __global__ void __launch_bounds__(32 * kWarps)
     route_kernel(const Rule q, const LT* __restrict__ logits, const float* __restrict__ bias,
@@ -351,18 +364,9 @@ __global__ void __launch_bounds__(32 * kWarps)
   const bool on = lane < q.k;
   const float l = on ? clean(load(row + mine)) : -INFINITY;
   float w;
-  if (q.sigmoid) {
-    w = on ? sigmoid(l) : 0.f;
-  } else if (q.renorm) {   // relative to the largest chosen logit: no underflow of the sum
-    const float mc = warp_max(l);
-    w = l > -INFINITY ? expf(l - mc) : 0.f;
-  } else {
-    w = l > -INFINITY ? expf(l - m) * inv_z : 0.f;
-  }
-  if (q.renorm) {
-    const float sum = warp_sum(w);
-    w = sum > 0.f ? w / sum : 0.f;
-  }
+  if (q.renorm) w = renormalized(q.sigmoid, l);
+  else if (q.sigmoid) w = sigmoid(l);
+  else w = l > -INFINITY ? expf(l - m) * inv_z : 0.f;
   if (on) {
     topk_idx[(size_t)t * q.k + lane] = mine;
     gates[(size_t)t * q.k + lane] = q.scale * w;
@@ -407,19 +411,13 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
     for (int i = 0; i < NV; ++i) p[i] = -p[i] * dot;
   } else {
-    float w, part = 1.f;
-    if (q.sigmoid) {
-      w = id >= 0 ? sigmoid(l) : 0.f;
-      part = sigmoid(-l);
-    } else {
-      const float mc = warp_max(l);
-      w = l > -INFINITY ? expf(l - mc) : 0.f;
-    }
+    const float part = q.sigmoid ? sigmoid(-l) : 1.f;
+    float w;
     if (q.renorm) {
-      const float sum = warp_sum(w);
-      w = sum > 0.f ? w / sum : 0.f;
+      w = renormalized(q.sigmoid, l);
       d = w * (dg - warp_sum(w > 0.f ? w * dg : 0.f));
     } else {
+      w = sigmoid(l);
       d = w * dg;
     }
     d = w > 0.f ? d * part : 0.f;

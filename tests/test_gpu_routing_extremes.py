@@ -1,0 +1,44 @@
+"""Routing at logits far from zero, on the GPU, against the 64-bit form in ops_reference.py."""
+import numpy as np
+import pytest
+import torch
+
+from grouped_gemm_built_gb300.routing import Routing
+from tests import ops_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("top", [-10.0, -16.5, -17.5, -60.0, -86.0, -95.0, -150.0, -1e4])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_renormalised_sigmoid_gates_of_very_negative_logits(top, dtype):
+    """Scores that are tiny in fp32, or 0, have ratios that are not. The logits of a row are `top`,
+    and lower by 0.5 or 3 (by 64 and 128 at -1e4, where bf16's step is 64). Per gate: the scores to
+    3 ulp each (2^-22 relative), a sum of three and a quotient: 2^-20. Gradients: sums of products
+    of such gates with |dg| <= 1, 2^-19 of the scale."""
+    E, k, scale = 40, 3, 2.5
+    l = torch.full((1, E), -float("inf"))
+    steps = [0.0, 0.5, 3.0] if top > -1e3 else [0.0, 64.0, 128.0]
+    if dtype == torch.bfloat16 and top != -1e4:
+        steps = [0.0, 1.0, 3.0]
+    l[0, [31, 4, 17]] = torch.tensor([top - s for s in steps])
+    l = l.to(dtype)
+    x = l[0].double().numpy()
+    # the same order as the scores', whichever way the choice compares them
+    bias = torch.zeros(E)
+    bias[[31, 4, 17]] = torch.tensor([3.0, 2.0, 1.0])
+    R = Routing(E, k, score="sigmoid", scale=scale)
+    idx, g = R.forward(l.cuda(), bias.cuda())
+    assert idx.tolist() == [[31, 4, 17]]
+    with np.errstate(over="ignore"):
+        want = ref.gates(np.maximum(x, -700), [31, 4, 17], "sigmoid", True, scale)
+    if top == -1e4:       # e^-64 and e^-128 of the largest
+        want = np.array([scale, scale * np.exp(-64.0), 0.0])
+    assert np.abs(g[0].cpu().numpy() - want).max() <= 2.0 ** -20 * scale
+    dg = torch.tensor([[1.0, -0.5, 0.75]])
+    dl = R.backward(l.cuda(), idx, dg.cuda(), dtype=torch.float32)[0].cpu().numpy()
+    w = want / scale
+    d = scale * w * (dg[0].double().numpy() - (w * dg[0].double().numpy()).sum())
+    d = d / (1 + np.exp(x[[31, 4, 17]]))
+    assert np.abs(dl[[31, 4, 17]] - d).max() <= 2.0 ** -19 * scale
+    assert np.count_nonzero(np.delete(dl, [31, 4, 17])) == 0
