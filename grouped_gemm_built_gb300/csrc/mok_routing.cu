@@ -198,12 +198,14 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
   for (int i = 0; i < NV; ++i) s[i] = clean(s[i]);
   float m = 0.f, inv_z = 0.f;
-  const bool on_logits = !q.sigmoid && bias == nullptr;
+  // without a bias the logits have the scores' order, and keep it where scores round to one value
+  const bool on_logits = bias == nullptr;
+  const bool group_sums = q.top_groups < q.groups && q.top2;
   if (on_logits) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = order_key(s[i]);
   }
-  if (!on_logits || (q.top_groups < q.groups && q.top2) || !q.renorm) {
+  if (!on_logits || group_sums || (!q.sigmoid && !q.renorm)) {
     unsigned off = 0;   // masked experts of this lane
 #pragma unroll
     for (int i = 0; i < NV; ++i) off |= s[i] == -INFINITY ? 1u << i : 0u;

@@ -33,10 +33,11 @@ typedef enum { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
 /* Score of an expert group: its largest choice score, or the sum of its two largest. */
 typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
 
-/* Routing rule. Choice scores are c = s + bias (softmax without a bias: the logits, which
- * have the same order). With groups > 1 the E experts form `groups` groups of E / groups
- * consecutive ids, and only experts of the top_groups best groups can be chosen. The k
- * largest choice scores are chosen; equal scores go to the lower id (group or expert).
+/* Routing rule. Choice scores are c = s + bias, or without a bias the logits, which have the
+ * scores' order (MOK_GROUP_TOP2 sums s also then). With groups > 1 the E experts form `groups`
+ * groups of E / groups consecutive ids, and only experts of the top_groups best groups can be
+ * chosen. The k largest choice scores are chosen; equal scores go to the lower id (group or
+ * expert).
  * gates_j = scale * s_j, divided by the sum of the k chosen scores when renormalize != 0
  * (the bias steers the choice only). A logit of -inf or NaN masks its expert: score 0,
  * chosen only when fewer than k unmasked experts are left (lowest id first), then with gate

@@ -42,3 +42,23 @@ def test_renormalised_sigmoid_gates_of_very_negative_logits(top, dtype):
     d = d / (1 + np.exp(x[[31, 4, 17]]))
     assert np.abs(dl[[31, 4, 17]] - d).max() <= 2.0 ** -19 * scale
     assert np.count_nonzero(np.delete(dl, [31, 4, 17])) == 0
+
+
+@pytest.mark.parametrize("rule", [dict(k=5), dict(k=3, groups=8, top_groups=3),
+                                  dict(k=4, groups=6, top_groups=2, E=60)])
+@pytest.mark.parametrize("around", [[17.5, 20.0, 24.0, 18.0, 30.0, 22.0, 19.0],
+                                    [-96.0, -91.0, -105.0, -100.0, -93.0, -88.5, -110.0]])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sigmoid_without_a_bias_keeps_the_order_of_its_logits(rule, around, dtype, rng):
+    """Logits whose fp32 scores are all 1, or all 0, are still in order; the rest lies below."""
+    E = rule.get("E", 64)
+    rule = {k: v for k, v in rule.items() if k != "E"}
+    for trial in range(8):
+        l = np.full(E, min(around) - 8.0)
+        l[rng.choice(E, len(around), replace=False)] = around
+        logits = torch.tensor(l[None], dtype=dtype)
+        assert (logits[0].double().numpy() == l).all()
+        idx, _ = Routing(E, score="sigmoid", **rule).forward(logits.cuda())
+        want = ref.choose(l, rule["k"], "softmax", None, rule.get("groups", 1),
+                          rule.get("top_groups", 1), "max")     # softmax compares the logits
+        assert idx[0].tolist() == want
