@@ -62,3 +62,26 @@ def test_sigmoid_without_a_bias_keeps_the_order_of_its_logits(rule, around, dtyp
         want = ref.choose(l, rule["k"], "softmax", None, rule.get("groups", 1),
                           rule.get("top_groups", 1), "max")     # softmax compares the logits
         assert idx[0].tolist() == want
+
+
+def choice_score_errors(score, logits, bias, at, other):
+    """For each exact score s of expert `at` in the rows of logits: does the choice between it and
+    expert `other`, whose own score is 0 and whose bias is s off by 8 ulp, go the right way?"""
+    wrong = []
+    for l in logits:
+        x = ref.scores(l.double().numpy(), score)[2][at]
+        R = Routing(len(l), 1, score=score)
+        for off, first in ((1 - 2.0 ** -20, at), (1 + 2.0 ** -20, other)):
+            b = bias.clone()
+            b[other] = float(np.float32(x * off))
+            idx, _ = R.forward(l[None].cuda(), b.cuda())
+            if idx.item() != first:
+                wrong.append((l[at].item(), off))
+    return wrong
+
+
+def test_sigmoid_choice_scores_are_good_to_a_few_ulp(rng):
+    """exp to 1 ulp, a sum to half, a quotient to 2: 3.5 ulp, where 8 (2^-20) decide."""
+    at = torch.tensor(rng.uniform(-24.0, 6.0, 400), dtype=torch.float32)
+    logits = torch.stack([at, torch.full((400,), -200.0)], 1)
+    assert choice_score_errors("sigmoid", logits, torch.zeros(2), 0, 1) == []
