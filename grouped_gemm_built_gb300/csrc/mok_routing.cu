@@ -145,8 +145,8 @@ __device__ __forceinline__ void store_row(T* row, int e0, int E, bool vec, const
 }
 
 // Softmax over the warp's logits s (cleaned): s becomes the scores, m and 1 / z its
-// statistics. A fully masked row has scores 0. __expf: 2^-22 relative near 0, where a sum's
-// weight is, and below 1e-5 down to the smallest normal score.
+// statistics. A fully masked row has scores 0. expf, not __expf, whose error grows with the
+// argument (to 1e-5 of the smallest scores, all of which the dense gradient writes).
 template <int NV>
 __device__ __forceinline__ void warp_softmax(float* s, float& m, float& inv_z) {
   m = s[0];
@@ -157,7 +157,7 @@ __device__ __forceinline__ void warp_softmax(float* s, float& m, float& inv_z) {
   float z = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    s[i] = __expf(s[i] - m);
+    s[i] = expf(s[i] - m);
     z += s[i];
   }
   z = warp_sum(z);

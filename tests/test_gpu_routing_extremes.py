@@ -85,3 +85,32 @@ def test_sigmoid_choice_scores_are_good_to_a_few_ulp(rng):
     at = torch.tensor(rng.uniform(-24.0, 6.0, 400), dtype=torch.float32)
     logits = torch.stack([at, torch.full((400,), -200.0)], 1)
     assert choice_score_errors("sigmoid", logits, torch.zeros(2), 0, 1) == []
+
+
+def test_softmax_choice_scores_are_good_to_a_few_ulp(rng):
+    """exp to 1 ulp, a sum of two terms and its inverse to half an ulp each, a product to half:
+    2.5 ulp and the sum's share of exp's, where 8 (2^-20) decide. The largest logit is 0, so the
+    differences are exact; a bias keeps its expert out of the choice."""
+    at = torch.tensor(rng.uniform(-60.0, -1.0, 400), dtype=torch.float32)
+    logits = torch.stack([torch.zeros(400), at, torch.full((400,), -200.0)], 1)
+    assert choice_score_errors("softmax", logits, torch.tensor([-10.0, 0.0, 0.0]), 1, 2) == []
+
+
+def test_dense_gradient_of_unchosen_experts_is_good_to_a_few_ulp(rng):
+    """dl_e = -scale s_e sum_S s dg for e outside S: two of them have the ratio of their scores.
+    Each entry is an exp to 1 ulp and two products to half an ulp, a ratio at most 2 x 2 ulp (2^-23
+    each) off: 4 x 2^-23 and their products, so 2^-20 with room. Logits on a grid of 1/16 and a
+    largest one of 0 make the differences exact; reference entry: the largest unchosen one."""
+    E, k = 384, 2
+    l = np.round(rng.uniform(-80.0, -2.0, E) * 16) / 16
+    l[[7, 200]] = 0.0, -0.5
+    l[100] = -1.0
+    R = Routing(E, k, renormalize=False, scale=1.0)
+    logits = torch.tensor(l[None], dtype=torch.float32, device="cuda")
+    idx, _ = R.forward(logits)
+    assert idx.tolist() == [[7, 200]]
+    # 2^40: the smallest products stay normal numbers
+    dl = R.backward(logits, idx, torch.full((1, k), 2.0 ** 40, device="cuda"))[0].double().cpu().numpy()
+    rest = [e for e in range(E) if e not in (7, 200)]
+    want = np.exp(l[rest] - l[100])
+    assert np.abs(dl[rest] / dl[100] / want - 1).max() <= 2.0 ** -20
