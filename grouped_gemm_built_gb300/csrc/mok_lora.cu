@@ -21,9 +21,9 @@
 // (shrink_rows_kernel finds u for small batches.) The weight gradients sum over the rows of one
 // adapter: bucket_kernel lists each adapter's rows in ascending order, wgrad_kernel gathers them.
 //
-// u and v are kept as hi = bf16(u), lo = bf16(u - hi): the tensor cores take bf16, and the
-// pair carries 16 significant bits, so the low-rank path adds no visible rounding to the
-// bf16 inputs and results. Per 32 ranks a row holds 128 bytes: 32 hi, then 32 lo values.
+// u and v are kept as two bf16 values, hi = u cut to bf16 and lo = bf16(u - hi): the tensor cores
+// take bf16, and the pair carries 16 significant bits, so the low-rank path adds no visible
+// rounding to the bf16 inputs and results. Per 32 ranks a row holds 128 bytes: 32 hi, then 32 lo values.
 //
 // Every mbarrier wait is bounded (kTimeoutNs); on expiry the kernel sets the status word,
 // lets its copies and MMAs in flight finish, and returns.
@@ -180,12 +180,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// hi and lo of two neighbours. lo is 0 where hi is not finite: an inf stays an inf.
+// hi and lo of two neighbours. hi is cut towards zero, and lo, which then has hi's sign, is never 0
+// beside a hi that is not (2^-24 of it, below fp32's rounding, where nothing is left), and is
+// infinite with hi: so hi x + lo x is infinite where u x is, and NaN only where that is NaN.
+__device__ __forceinline__ float low_part(float a, float hi) {
+  const float rest = a - hi;
+  return isinf(a) ? a : rest != 0.f ? rest : hi * 0x1p-24f;
+}
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  const float ha = __low2float(h), hb = __high2float(h);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack_bf16(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f);
+  const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
+  hi = ha >> 16 | hb;
+  lo = pack_bf16(low_part(a, __uint_as_float(ha)), low_part(b, __uint_as_float(hb)));
 }
 
 // ------------------------------------------------------------------ barriers of a CTA
