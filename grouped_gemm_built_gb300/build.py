@@ -49,6 +49,23 @@ def torch_lib_path() -> str:
     return os.path.join(OUT_DIR, TORCH_NAME)
 
 
+def torch_tag() -> str:
+    """What mok_torch is compiled against: the installed torch, its C++ ABI and this Python's."""
+    import torch
+
+    return (f"{torch.__version__} abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"{sysconfig.get_config_var('SOABI')} {os.path.dirname(torch.__file__)}")
+
+
+def torch_calls_tag() -> str:
+    """The tag that the mok_torch in the tree was built with ("" without one)."""
+    try:
+        with open(torch_lib_path() + ".tag") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _build_torch_calls(target: str) -> None:
     """csrc/torch_calls.cpp -> the extension module mok_torch, for the installed torch."""
     import torch
@@ -67,6 +84,8 @@ def _build_torch_calls(target: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(target + ".tmp", target)
+    with open(target + ".tag", "w") as f:
+        f.write(torch_tag())
 
 
 def _needs_build(objs_src, target):
@@ -85,6 +104,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     srcs = sources()
     target = lib_path()
     if not force and not _needs_build(srcs, target) and not _needs_build(srcs, torch_lib_path()):
+        if torch_calls_tag() != torch_tag():      # another torch than it was built for
+            _build_torch_calls(torch_lib_path())
         return target
     cc = nvcc()
     objs = []

@@ -13,7 +13,7 @@ import importlib.util
 import os
 import re
 
-from .build import lib_path, torch_lib_path
+from .build import lib_path, torch_calls_tag, torch_lib_path, torch_tag
 
 c_int, c_size_t, c_void_p, c_char_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
 
@@ -176,6 +176,9 @@ def torch_calls():
         p, L = torch_lib_path(), lib()
         if not os.path.exists(p):
             raise RuntimeError(f"mok_torch is not built ({p}); run __graft_entry__.build()")
+        if torch_calls_tag() != torch_tag():
+            raise RuntimeError(f"mok_torch was built for another torch ({torch_calls_tag()!r}, not "
+                               f"{torch_tag()!r}); run __graft_entry__.build()")
         import torch  # noqa: F401  (the libraries that the module links against)
         loader = importlib.machinery.ExtensionFileLoader("mok_torch", p)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("mok_torch", loader))
