@@ -123,7 +123,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
         calls = ex.submit(_build_torch_calls, torch_lib_path())
         objs = list(ex.map(compile_one, srcs))
-        calls.result()
     tmp = target + ".tmp"
     # No -lcuda: the tensor-map encoder is fetched through the runtime's driver entry
     # points, so the library loads on machines without a driver too.
@@ -132,6 +131,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, target)
+    calls.result()      # last: the C library does not depend on torch or its headers
     return target
 
 

@@ -47,3 +47,17 @@ def test_a_module_of_another_torch_is_not_loaded(tree, monkeypatch):
     monkeypatch.setattr(torch, "__version__", "2.0.0+other")
     with pytest.raises(RuntimeError, match="another torch"):
         mok.torch_calls()
+
+
+def test_the_library_is_built_where_the_module_cannot_be(tmp_path, monkeypatch):
+    """Programs that use the C ABI alone need neither torch's headers nor torch."""
+    def no_headers(target):
+        raise RuntimeError("g++ failed")
+
+    one = [s for s in build.sources() if s.endswith("mok_dropout.cu")]
+    monkeypatch.setattr(build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "sources", lambda: one)
+    monkeypatch.setattr(build, "_build_torch_calls", no_headers)
+    with pytest.raises(RuntimeError, match="failed"):
+        build.build()
+    assert os.path.exists(tmp_path / build.LIB_NAME)
