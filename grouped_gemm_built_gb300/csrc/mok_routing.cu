@@ -436,14 +436,14 @@ __global__ void __launch_bounds__(32 * kWarps)
 template <typename LT, int NV>
 void launch_fwd(const Rule& q, const void* logits, const float* bias, int32_t* idx, float* gates,
                 cudaStream_t s) {
-  const unsigned blocks = (unsigned)((q.T + kWarps - 1) / kWarps);
+  const unsigned blocks = ((unsigned)q.T + kWarps - 1) / kWarps;
   route_kernel<NV, LT><<<blocks, 32 * kWarps, 0, s>>>(q, static_cast<const LT*>(logits), bias, idx,
                                                       gates);
 }
 template <typename LT, typename DT, int NV>
 void launch_bwd(const Rule& q, const void* logits, const int32_t* idx, const float* dg, void* dl,
                 cudaStream_t s) {
-  const unsigned blocks = (unsigned)((q.T + kWarps - 1) / kWarps);
+  const unsigned blocks = ((unsigned)q.T + kWarps - 1) / kWarps;
   route_bwd_kernel<NV, LT, DT><<<blocks, 32 * kWarps, 0, s>>>(
       q, static_cast<const LT*>(logits), idx, dg, static_cast<DT*>(dl));
 }

@@ -114,3 +114,18 @@ def test_dense_gradient_of_unchosen_experts_is_good_to_a_few_ulp(rng):
     rest = [e for e in range(E) if e not in (7, 200)]
     want = np.exp(l[rest] - l[100])
     assert np.abs(dl[rest] / dl[100] / want - 1).max() <= 2.0 ** -20
+
+
+def test_the_largest_row_count():
+    """T is an int: rows up to 2^31 - 1 are counted without overflow."""
+    T = 2 ** 31 - 1
+    l = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    R = Routing(1, 1, renormalize=False, scale=0.5)
+    idx, g = R.forward(l)
+    assert (idx[-4:] == 0).all() and (g[-4:] == 0.5).all() and (g[:4] == 0.5).all()
+    assert g.amin() == 0.5 and g.amax() == 0.5
+    del idx, g
+    torch.cuda.empty_cache()
+    some = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    dl = R.backward(l, some, torch.ones(T, 1, device="cuda"))
+    assert dl.abs().amax() == 0           # one expert: its softmax is 1 whatever the logit
