@@ -38,6 +38,7 @@
 
 #include "mok_internal.h"
 #include "mok_ops.h"
+#include "mok_profile.h"
 #include "mok_ptx.cuh"
 
 namespace mok {
@@ -1587,6 +1588,42 @@ cudaError_t launch(void (*kernel)(Params...), int grid, int threads, size_t smem
 // a swizzle atom).
 int tile_rows(int T) { return T >= BM ? BM : (T + 7) / 8 * 8; }
 
+// How the r values of [T][C] are found: by rows on the CUDA cores (rg ranks a CTA), or in tiles, whose
+// contraction `split` CTAs of a cluster share and whose adapters' chunks `cy` clusters do.
+struct ShrinkForm {
+  int rg, split, cy, cols;
+};
+ShrinkForm shrink_form(const mok_lora_dims& d, int C, const Device& dev) {
+  const int mt = (d.T + BM - 1) / BM, rp = padded_rank(d.r);
+  ShrinkForm f = {};
+  if (d.T <= kRowsMost && C <= 256 * kRowMaxPieces && (long long)d.T * rp * C <= kRowsProducts) {
+    f.rg = 16;   // the fewest CTAs that still keep the SMs busy
+    while (f.rg > 2 && d.T * (rp / f.rg) < dev.sms / 2) f.rg /= 2;
+    return f;
+  }
+  const int distinct = std::min(std::min(d.n, d.T), BM);   // adapters of a tile, at most
+  f.cols = distinct * rp <= 64 ? 64 : distinct * rp <= 128 ? 128 : 256;
+  // How many ranks share a tile's contraction (a rank takes at least two steps), against how many
+  // clusters share its chunks: the least estimated time in microseconds, 0.35 a step and 5 for
+  // the start and the join of a chunk, over a batch whose tiles hold every adapter they can and
+  // one of long runs (a single chunk), which the host cannot tell apart.
+  const int kiters = (C + BK - 1) / BK, chunks = (distinct * rp + f.cols - 1) / f.cols;
+  double best = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int split = 1 << i, fit = dev.clusters[i];
+    if (i > 0 && 2 * split > kiters) break;
+    const int cy = std::max(1, std::min(chunks, fit / mt));
+    const double waves = (mt + fit - 1) / fit, rounds = (chunks + cy - 1) / cy;
+    const double t = waves * (rounds + 1) * ((kiters + split - 1) / split * 0.35 + 5.0);
+    if (best == 0 || t < best) {
+      best = t;
+      f.split = split;
+      f.cy = cy;
+    }
+  }
+  return f;
+}
+
 // The r values of every row: in [T][C] against w [n][r][C]. early: the launch may start before
 // the stream's last kernel ends.
 mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void* w,
@@ -1595,10 +1632,11 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   const SavedParts sp = saved_parts(d);
   const int mt = (d.T + BM - 1) / BM;
   const int rp = padded_rank(d.r), nb = (rp + 31) / 32;
+  const ShrinkForm f = shrink_form(d, C, dev);
   uint8_t* uq = reinterpret_cast<uint8_t*>(saved + sp.uq);
   int32_t* n_slots = reinterpret_cast<int32_t*>(saved + sp.n_slots);
   Slot* slots = reinterpret_cast<Slot*>(saved + sp.slots);
-  if (d.T <= kRowsMost && C <= 256 * kRowMaxPieces && (long long)d.T * rp * C <= kRowsProducts) {
+  if (f.rg > 0) {
     auto go = [&](auto rg) {
       constexpr int RG = decltype(rg)::value;
       // every rank that the MMAs read is written, padding too
@@ -1607,11 +1645,10 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
                             static_cast<const __nv_bfloat16*>(w), ids, scale, uq, n_slots, slots, pairs};
       return launch(shrink_rows_kernel<RG>, d.T * groups + mt, kRowThreads, 0, 1, early, s, p);
     };
-    // the fewest CTAs that still keep the SMs busy
-    const cudaError_t e = d.T * (rp / 16) >= dev.sms / 2  ? go(std::integral_constant<int, 16>{})
-                          : d.T * (rp / 8) >= dev.sms / 2 ? go(std::integral_constant<int, 8>{})
-                          : d.T * (rp / 4) >= dev.sms / 2 ? go(std::integral_constant<int, 4>{})
-                                                          : go(std::integral_constant<int, 2>{});
+    const cudaError_t e = f.rg == 16  ? go(std::integral_constant<int, 16>{})
+                          : f.rg == 8 ? go(std::integral_constant<int, 8>{})
+                          : f.rg == 4 ? go(std::integral_constant<int, 4>{})
+                                      : go(std::integral_constant<int, 2>{});
     return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
   }
   ShrinkParams p = {};
@@ -1621,8 +1658,9 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   p.rp = rp;
   p.nb = nb;
   p.kiters = (C + BK - 1) / BK;
-  const int distinct = std::min(std::min(d.n, d.T), BM);   // adapters of a tile, at most
-  p.cols = distinct * rp <= 64 ? 64 : distinct * rp <= 128 ? 128 : 256;
+  p.cols = f.cols;
+  p.split = f.split;
+  p.cy = f.cy;
   p.a_bytes = tile_rows(d.T) * BK * 2;
   // an MMA reads 128 rows from a stage's start, past a short batch's own: in bounds for the
   // last stage too
@@ -1630,24 +1668,6 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
   const int fixed = BM * (rp + 4) * 4 + p.tail + kBarBytes + 1024;
   p.ring_bytes = (int)((kMaxSmem - 2 * sizeof(TileSlots) - fixed) / 1024 * 1024);
   p.pairs = pairs;
-  // How many ranks share a tile's contraction (a rank takes at least two steps), against how many
-  // clusters share its chunks: the least estimated time in microseconds, 0.35 a step and 5 for
-  // the start and the join of a chunk, over a batch whose tiles hold every adapter they can and
-  // one of long runs (a single chunk), which the host cannot tell apart.
-  const int chunks = (distinct * p.rp + p.cols - 1) / p.cols;
-  double best = 0;
-  for (int i = 0; i < 4; ++i) {
-    const int split = 1 << i, fit = dev.clusters[i];
-    if (i > 0 && 2 * split > p.kiters) break;
-    const int cy = std::max(1, std::min(chunks, fit / mt));
-    const double waves = (mt + fit - 1) / fit, rounds = (chunks + cy - 1) / cy;
-    const double t = waves * (rounds + 1) * ((p.kiters + split - 1) / split * 0.35 + 5.0);
-    if (best == 0 || t < best) {
-      best = t;
-      p.split = split;
-      p.cy = cy;
-    }
-  }
   p.ids = ids;
   p.scale = scale;
   p.uq = uq;
@@ -1735,6 +1755,11 @@ ProjForm form_of(const mok_lora_dims& d, int C, int cols, bool adapters, const D
   return choose_form(d.T, (C + BK - 1) / BK, 2 * nb * ((slots * rb + 63) / 64), cols, dev);
 }
 
+int form_tiles(const mok_lora_dims& d, const ProjForm& f, int cols) {
+  const int mt = (d.T + BM - 1) / BM;
+  return (f.pair ? (mt + 1) / 2 : mt) * ((cols + f.NT - 1) / f.NT);
+}
+
 // out [T][cols] = in [T][C] W (trans: W^T) + the low-rank part. W == null: that part alone;
 // parts == null: no such part.
 mok_status run_proj(const mok_lora_dims& d, const ProjForm& f, int C, int cols, bool trans,
@@ -1782,7 +1807,7 @@ mok_status run_proj(const mok_lora_dims& d, const ProjForm& f, int C, int cols, 
   }
   if (!ok) return MOK_ERR_CUDA;
   const int csize = f.pair ? 2 : f.split;
-  int tiles = (f.pair ? (p.m_tiles + 1) / 2 : p.m_tiles) * p.n_tiles;
+  int tiles = form_tiles(d, f, cols);
   if (f.pair) {
     p.whole = tiles - pair_tail(tiles, dev);
     tiles += tiles - p.whole;
@@ -1798,9 +1823,27 @@ mok_status run_proj(const mok_lora_dims& d, const ProjForm& f, int C, int cols, 
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
 
+// Columns of a CTA of the weight gradients, and the row shares of a block of columns: one wave of
+// clusters, at least two stages a share.
+// 256 columns read u half as often (8192 rows, training step: rank 16 340 against 347 us,
+// rank 64 369 against 389); 128 make more CTAs of few rows (300 rows: 31.4 against 34.8)
+struct WgradForm {
+  int cols, split;
+};
+WgradForm wgrad_form(const mok_lora_dims& d, const Device& dev) {
+  WgradForm f;
+  f.cols = d.T >= 2048 && padded_rank(d.r) <= 64 ? 256 : 128;
+  const int tiles = (d.K + f.cols - 1) / f.cols + (d.N + f.cols - 1) / f.cols;
+  int i = 0;
+  while (i < 3 && d.T > (2 << i) * kWgRows && tiles <= dev.clusters[i + 1]) ++i;
+  f.split = 1 << i;
+  return f;
+}
+
 mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, const void* xa,
                      const void* dY, const char* ws, const WorkParts& wp, void* dA, void* dB,
                      mok_out_dtype type, uint32_t* status, const Device& dev, cudaStream_t s) {
+  const WgradForm f = wgrad_form(d, dev);
   auto go = [&](auto rp, auto cols) {
     using S = WgShape<decltype(rp)::value, decltype(cols)::value>;
     WgradParams p = {};
@@ -1810,24 +1853,18 @@ mok_status run_wgrad(const mok_lora_dims& d, const char* uq, const char* vq, con
                           dB, d.N, (d.N + S::N - 1) / S::N};
     p.r = d.r;
     p.n = d.n;
+    p.split = f.split;
     p.out_bf16 = type == MOK_OUT_BF16;
     p.off = reinterpret_cast<const int32_t*>(ws + wp.off);
     p.rows = reinterpret_cast<const int32_t*>(ws + wp.rows);
     p.status = status;
-    // row shares: one wave of clusters, at least two stages a share
     const int tiles = p.side[0].ctiles + p.side[1].ctiles;
-    int i = 0;
-    while (i < 3 && d.T > (2 << i) * kWgRows && tiles <= dev.clusters[i + 1]) ++i;
-    p.split = 1 << i;
-    return launch(wgrad_kernel<decltype(rp)::value, decltype(cols)::value>, tiles * p.split, kWgThreads, S::SMEM, p.split,
-                  true, s, p);
+    return launch(wgrad_kernel<decltype(rp)::value, decltype(cols)::value>, tiles * p.split,
+                  kWgThreads, S::SMEM, p.split, true, s, p);
   };
-  // 256 columns read u half as often (8192 rows, training step: rank 16 340 against 347 us,
-  // rank 64 369 against 389); 128 make more CTAs of few rows (300 rows: 31.4 against 34.8)
   using std::integral_constant;
-  const bool wide = d.T >= 2048;
   auto width = [&](auto rp) {
-    return wide ? go(rp, integral_constant<int, 256>{}) : go(rp, integral_constant<int, 128>{});
+    return f.cols == 256 ? go(rp, integral_constant<int, 256>{}) : go(rp, integral_constant<int, 128>{});
   };
   cudaError_t e;
   switch (padded_rank(d.r)) {
@@ -1942,4 +1979,34 @@ extern "C" mok_status mok_lora_get_status(uint32_t* status, void* stream) {
       cudaMemsetAsync(status, 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
     return MOK_ERR_CUDA;
   return (bits & kErrTimeout) ? MOK_ERR_TIMEOUT : MOK_OK;
+}
+
+extern "C" mok_status mok_lora_get_forms(const mok_lora_dims* dims, int backward, int own_input,
+                                         mok_lora_forms* out) {
+  using namespace mok;
+  if (!ok_dims(dims) || !out) return MOK_ERR_INVALID_ARG;
+  const Device* dev = current_device();
+  if (!dev) return MOK_ERR_CUDA;
+  *out = {};
+  if (dims->T == 0) return MOK_OK;
+  const mok_lora_dims& d = *dims;
+  const int C = backward ? d.N : d.K, cols = backward ? d.K : d.N;
+  auto describe = [&](const ProjForm& f) {
+    mok_lora_proj_form o = {f.NT, f.split, f.pair, 0};
+    if (f.pair) o.halved = pair_tail(form_tiles(d, f, cols), *dev);
+    return o;
+  };
+  const bool apart = backward && own_input;
+  out->proj = describe(form_of(d, C, cols, !apart, *dev));
+  if (apart) out->adapters = describe(form_of(d, 0, cols, true, *dev));
+  const ShrinkForm s = shrink_form(d, C, *dev);
+  out->u_ranks = s.rg;
+  out->u_split = s.split;
+  out->u_chunks = s.cy;
+  if (backward) {
+    const WgradForm w = wgrad_form(d, *dev);
+    out->grad_columns = w.cols;
+    out->grad_split = w.split;
+  }
+  return MOK_OK;
 }

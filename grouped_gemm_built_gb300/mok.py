@@ -93,6 +93,15 @@ class MokLoraSizes(ctypes.Structure):
     _fields_ = [("saved_bytes", c_size_t), ("workspace_bytes", c_size_t)]
 
 
+class MokLoraProjForm(ctypes.Structure):
+    _fields_ = [(n, c_int) for n in ("columns", "split", "pair", "halved")]
+
+
+class MokLoraForms(ctypes.Structure):
+    _fields_ = [("proj", MokLoraProjForm), ("adapters", MokLoraProjForm)] + [
+        (n, c_int) for n in ("u_ranks", "u_split", "u_chunks", "grad_columns", "grad_split")]
+
+
 class MokError(RuntimeError):
     def __init__(self, what, status):
         super().__init__(f"{what}: {mok_status_string(status)} ({status})")
@@ -144,6 +153,7 @@ def _declare(L):
                                  c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
         "mok_lora_get_status": (c_int, [c_void_p, c_void_p]),
         "mok_profile_enable": (c_int, [c_void_p, c_int]),
+        "mok_lora_get_forms": (c_int, [_P(MokLoraDims), c_int, c_int, _P(MokLoraForms)]),
         "mok_profile_report": (c_int, [c_void_p, c_char_p, c_size_t, _P(c_int)]),
     }
     for name, (res, args) in sig.items():
@@ -346,6 +356,13 @@ def mok_lora_bwd(dims: MokLoraDims, w: MokLoraWeights, x, x_ad, ids, saved, dY, 
 def mok_lora_get_status(status, stream) -> int:
     """Synchronises the stream; returns the status (0 = ok) and clears it."""
     return lib().mok_lora_get_status(status, stream)
+
+
+def mok_lora_get_forms(dims: MokLoraDims, backward=False, own_input=False) -> MokLoraForms:
+    f = MokLoraForms()
+    _check(lib().mok_lora_get_forms(ctypes.byref(dims), int(backward), int(own_input),
+                                    ctypes.byref(f)), "mok_lora_get_forms")
+    return f
 
 
 def mok_profile_enable(ctx, enable: bool) -> None:
