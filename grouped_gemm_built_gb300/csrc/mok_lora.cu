@@ -558,9 +558,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kRowThreads = 1024;
 constexpr int kRowMaxPieces = 64;    // contraction up to 16384
 // A batch goes this way up to 256 rows and 24 M products (rows x ranks x C): each row reads its
-// adapter by itself. Forward of 7168 to 2048, this way against the tiles: rank 16, 16 rows 13.7
-// and 17.0 us, 256 rows 24.5 and 25.6, 512 rows 44.5 and 40.1; rank 64, 16 rows 15.3 and 15.2,
-// 128 rows 31.8 and 25.6.
+// adapter by itself. Forward with 32 adapters, this way against the tiles, in us:
+//   7168 to 2048  rank 16: 16 rows 14.5 and 19.2, 192 rows 23.5 and 27.3, 384 rows 36.9 and 27.4
+//                 rank 64: 16 rows 18.5 and 19.0, 64 rows 26.2 and 23.8
+//   1024 to 1024  rank 16: 64 rows 10.2 and 13.4, 256 rows 15.6 and 16.1, 384 rows 18.1 and 16.5
+// The bounds are too wide at high ranks of short contractions (1024 to 1024, rank 64: 64 rows 13.0
+// and 13.5, 128 rows 18.3 and 15.2, 256 rows 35.1 and 24.4) and beside wide outputs (2048 to 7168,
+// rank 16: 64 rows 18.1 and 19.5, 128 rows 21.8 and 19.8).
 constexpr int kRowsMost = 256;
 constexpr long long kRowsProducts = 24 << 20;
 
@@ -680,14 +684,16 @@ __global__ void __launch_bounds__(kRowThreads) shrink_rows_kernel(const ShrinkRo
 // hold B rows only. The stage with u is handed back last, so a group is at most stages - 1
 // stages long; a longer list loads u again for its next group.
 //
-// Launched with programmatic dependence on shrink_kernel: the steps over W need nothing from
-// it, so only the adapters' part waits.
+// Launched with programmatic dependence on u's kernel: the steps over W need nothing from it, so
+// only the adapters' part waits. A CTA can start only where it has room: shrink_kernel takes its
+// SM's shared memory and shrink_rows_kernel<16> its registers, so that is on the SMs that they do
+// not use (24 of 152 beside the 128 tiles of 8192 rows) or have left.
 //
-// Alone, 8192 rows of 7168 to 2048 with a dozen adapters of rank 32 take 127 us, 1.9 PFLOP/s,
-// 0.99 of cuBLAS's burst rate (the transposed product 124): bound by the tensor cores. One row
-// of the same takes 10.5 us, half of it W's 29 MB at 5.7 TB/s, the rest the start, the join and
-// the launch. 96 rows with 42 adapters, 2048 to 7168: 15.8 us, four of them the adapters' steps
-// and three the join through distributed shared memory.
+// By itself under a profiler, 8192 rows of 7168 to 2048 with a dozen adapters of rank 32 take 132
+// us, 1.82 PFLOP/s, 0.95 of cuBLAS's burst rate (the transposed product, rank 16, 127 us, 0.98):
+// bound by the tensor cores, whose pipe is 84% (86%) busy. The whole forward of one such row, rank
+// 16, takes 11.6 us, where W's 29 MB need 4.4: the rest is the start, the join and the launches.
+// 96 rows with 48 adapters, 2048 to 7168: 19.9 us, u and then the adapters' steps and the join.
 struct ProjParams {
   int T, out_cols, n;
   int kiters;               // steps over W (0: the adapters' part alone)
@@ -1085,8 +1091,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ row lists
 // One CTA per adapter: its rows in ascending order at rows[off[a] .. off[a + 1]), where off[a]
-// counts the rows of lower adapters. Each CTA reads all ids, so that no CTA waits for another.
-// 10 us for 8192 rows, beside shrink_kernel, which needs nothing from it.
+// counts the rows of lower adapters. Each CTA reads all ids, so that no CTA waits for another, and
+// the work grows with n T: 8192 rows take 10 us for 48 adapters, 53 for 1024, 200 for 4096 and 790
+// for 16384 (of backwards of 73, 414, 1208 and 2950 us, 512 to 512, rank 8). Runs beside
+// shrink_kernel, which needs nothing from it.
 constexpr int kBucketThreads = 1024;
 
 __global__ void __launch_bounds__(kBucketThreads)
@@ -1137,8 +1145,8 @@ __global__ void __launch_bounds__(kBucketThreads)
 // it starts adds up in rank order.
 //
 // One pass over xa and dY, memory bound: 64 rows of the list a stage, gathered by eight warps
-// (four: 368 against 353 us for a training step at rank 64) with 16-byte asynchronous copies (TMA's row gather, four rows of 128 bytes an instruction,
-// reached half the rate). A stage holds xa or dY [64 rows][N], the rows' hi values [64][ranks]
+// (four: 368 against 353 us for a training step at rank 64) with 16-byte asynchronous copies
+// (TMA's row gather, four rows of 128 bytes an instruction, reached half the rate). A stage holds xa or dY [64 rows][N], the rows' hi values [64][ranks]
 // and their lo values, all contraction-row by contraction-row (MN-major operands), so two MMAs
 // per 16 rows, hi and lo, sum D[rank][column] in TMEM. Two accumulators: an adapter's results
 // leave while the next one's rows are multiplied. Rows past an adapter's end are filled with
@@ -1689,8 +1697,10 @@ mok_status run_shrink(const mok_lora_dims& d, int C, const void* in, const void*
 // is the largest of the tensor core's, its bytes' way into the SM's shared memory, all SMs'
 // out of L2, W's out of HBM (narrow 64-column pieces of its rows at two thirds of the rate),
 // and the memory's latency over the ring's stages. The constants are fitted to the times of
-// every form at 112 shapes, 1 to 8192 rows and 256 x 256 to 7168 x 2048: the choice then costs
-// 1.7% against the best form on average. ext: the adapters' stages of a tile, an estimate.
+// every form, 1 to 8192 rows and 256 x 256 to 7168 x 2048. At 96 shapes of that range (eight
+// adapters of rank 16, in any order up to 128 rows and packed above) the choice costs 2.1% against
+// the best form on average, at most 3% at 82 of them and 26% at the worst (2048 rows, 4096 to 1000:
+// 192 columns 35.5 us, pairs 28.2). ext: the adapters' stages of a tile, an estimate.
 struct ProjForm {
   int NT, split, pair, stages, stage_bytes;
   size_t smem;
@@ -1749,8 +1759,9 @@ ProjForm choose_form(int T, int kiters, int ext, int cols, const Device& dev) {
 // The form of [T][C] W (C = 0: no W), with or without the adapters' part.
 ProjForm form_of(const mok_lora_dims& d, int C, int cols, bool adapters, const Device& dev) {
   const int rp = padded_rank(d.r), nb = (rp + 31) / 32, rb = std::min(rp, 32);
-  // short batches are mostly rows of different requests, long ones mostly long runs of one; an
-  // adapter stage takes about as long as two steps over W
+  // Short batches are mostly rows of different requests, long ones mostly long runs of one; an
+  // adapter stage takes about as long as two steps over W. A long batch of many adapters in any
+  // order runs more steps than it is counted for here.
   const int slots = adapters ? (d.T <= BM ? std::min(d.n, d.T) : 2) : 0;
   return choose_form(d.T, (C + BK - 1) / BK, 2 * nb * ((slots * rb + 63) / 64), cols, dev);
 }
@@ -1824,9 +1835,15 @@ mok_status run_proj(const mok_lora_dims& d, const ProjForm& f, int C, int cols, 
 }
 
 // Columns of a CTA of the weight gradients, and the row shares of a block of columns: one wave of
-// clusters, at least two stages a share.
-// 256 columns read u half as often (8192 rows, training step: rank 16 340 against 347 us,
-// rank 64 369 against 389); 128 make more CTAs of few rows (300 rows: 31.4 against 34.8)
+// clusters, at least two stages a share. 256 columns read u half as often, 128 make more CTAs of few
+// rows. Backward with four packed adapters, 128 against 256 columns, in us:
+//   7168 and 2048  rank 16: 512 rows 31.7 and 33.6, 1536 rows 52.6 and 52.9, 2048 rows 60.4 and
+//                  60.1, 8192 rows 181.7 and 170.1; rank 64: 512 rows 36.5 and 38.8, 2048 rows 66.8
+//                  and 65.7, 8192 rows 193.5 and 181.0
+//   1000 and 1000  rank 16: 512 rows 18.7 and 21.1, 2048 rows 30.0 and 28.8, 8192 rows 53.7 and 50.0
+// At 2048 and 2048 the columns also decide how many CTAs share the rows, and the rule is off by up to
+// 20%: rank 16, 512 rows 24.7 and 21.0, 1024 rows 28.4 and 23.8, 2048 rows 34.3 and 35.5, 8192 rows
+// 77.5 and 80.2.
 struct WgradForm {
   int cols, split;
 };

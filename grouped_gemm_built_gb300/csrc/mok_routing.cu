@@ -8,9 +8,10 @@
 // the maximum over the warp is one integer reduction instruction per chosen expert. A group
 // of experts is a run of lanes, its score a lane-local pass and a few shuffles. Bound by
 // latency for few tokens (one token over 384 experts 3.4 us, the launch included) and by
-// instruction issue for many: 16384 tokens over 256 experts in 8 groups 15.0 us, about 770
-// instructions a token, where reading the logits once would take 2.6; 8192 tokens over 384
-// experts 8.4 us, and 4.8 for the dense gradient, which mostly waits for its loads.
+// instruction issue for many: 16384 tokens over 256 experts in 8 groups with a bias 16.4 us, about
+// 840 instructions a token, where reading the logits once would take 2.6 (15.0 and 770 with the fast
+// exponential, see the choice scores). 8192 tokens over 384 experts and their dense gradient 13.0
+// us; the gradient's launch mostly waits for its loads.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -211,8 +212,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     for (int i = 0; i < NV; ++i) off |= s[i] == -INFINITY ? 1u << i : 0u;
     if (q.sigmoid) {
       // The choice needs the scores to a few ulp (the gates below are full precision): 4, of which
-      // the quotient takes 2 (IEEE division: 0.5). __expf's error grows with the argument instead,
-      // 13 ulp at a logit of -10.
+      // the quotient takes 2 (IEEE division: 0.5). __expf's documented error grows with the
+      // argument instead, 13 ulp at a logit of -10.
 #pragma unroll
       for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + expf(-s[i]));
     } else {

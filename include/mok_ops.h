@@ -82,7 +82,8 @@ mok_status mok_dropout(const void* x, const void* add, void* y, size_t n, float 
 /* ---- low-rank adapters beside a shared projection --------------------------------- */
 
 /* T rows, K input and N output features (multiples of 8), n adapters of rank r
- * (1 <= r <= 128; adapters of smaller rank are padded with zeros). */
+ * (1 <= r <= 128; adapters of smaller rank are padded with zeros). T up to 2^24, K, N and n up to
+ * 2^20. The backward reads the ids once per adapter: its cost has a part that grows with n T. */
 typedef struct {
   int T, K, N, n, r;
 } mok_lora_dims;
