@@ -21,9 +21,10 @@
 // (shrink_rows_kernel finds u for small batches.) The weight gradients sum over the rows of one
 // adapter: bucket_kernel lists each adapter's rows in ascending order, wgrad_kernel gathers them.
 //
-// u and v are kept as two bf16 values, hi = u cut to bf16 and lo = bf16(u - hi): the tensor cores
-// take bf16, and the pair carries 16 significant bits, so the low-rank path adds no visible
-// rounding to the bf16 inputs and results. Per 32 ranks a row holds 128 bytes: 32 hi, then 32 lo values.
+// u and v are kept as two bf16 values, hi = u cut to bf16 and lo = bf16(u - hi): the tensor
+// cores take bf16, and the pair carries 16 significant bits, so the low-rank path adds no
+// visible rounding to the bf16 inputs and results. Per 32 ranks a row holds 128 bytes: 32 hi,
+// then 32 lo values.
 //
 // Every mbarrier wait is bounded (kTimeoutNs); on expiry the kernel sets the status word,
 // lets its copies and MMAs in flight finish, and returns.
@@ -1146,12 +1147,13 @@ __global__ void __launch_bounds__(kBucketThreads)
 //
 // One pass over xa and dY, memory bound: 64 rows of the list a stage, gathered by eight warps
 // (four: 368 against 353 us for a training step at rank 64) with 16-byte asynchronous copies
-// (TMA's row gather, four rows of 128 bytes an instruction, reached half the rate). A stage holds xa or dY [64 rows][N], the rows' hi values [64][ranks]
-// and their lo values, all contraction-row by contraction-row (MN-major operands), so two MMAs
-// per 16 rows, hi and lo, sum D[rank][column] in TMEM. Two accumulators: an adapter's results
-// leave while the next one's rows are multiplied. Rows past an adapter's end are filled with
-// zeros in both operands, so that no other adapter's value can meet a zero; ranks past RP and
-// the duplicate half of a short M are accumulator rows that nothing reads.
+// (TMA's row gather, four rows of 128 bytes an instruction, reached half the rate). A stage
+// holds xa or dY [64 rows][N], the rows' hi values [64][ranks] and their lo values, all
+// contraction-row by contraction-row (MN-major operands), so two MMAs per 16 rows, hi and lo,
+// sum D[rank][column] in TMEM. Two accumulators: an adapter's results leave while the next one's
+// rows are multiplied. Rows past an adapter's end are filled with zeros in both operands, so
+// that no other adapter's value can meet a zero; ranks past RP and the duplicate half of a short
+// M are accumulator rows that nothing reads.
 //
 // 8192 rows, 7168 and 2048 columns, four adapters: 37 us at rank 16 (4.1 TB/s), 49 at rank 64,
 // 89 at rank 128, where 128 columns a CTA read u twice as often. (On warp-level MMAs the launch
