@@ -1,0 +1,514 @@
+// The norm of many gradients and the AdamW step over many tensors (include/mok_ops.h).
+//
+// The tensors' addresses and sizes travel in the kernel's parameters (up to 32 KB of them), so a
+// call copies nothing to the device and a captured graph holds its own table.
+#include <memory>
+#include <new>
+
+#include "mok_internal.h"
+#include "mok_ops.h"
+#include "mok_rows.cuh"
+
+namespace mok {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlock = 256;           // state elements that share the scales of 8-bit moments
+constexpr int kChunk = kThreads * 8;  // elements per CTA of the step: a warp has one block
+
+// ---------------------------------------------------------------- norm of many gradients
+constexpr int kNormChunk = kThreads * 32;
+constexpr int kNormCtas = 152 * 4;
+
+struct GradEntry {
+  const void* g;
+  unsigned long long n;
+  unsigned first;   // its first chunk
+  bool bf16, vec;
+};
+template <int N>
+struct GradTable {
+  int count;
+  unsigned chunks;
+  GradEntry e[N];
+};
+constexpr int kGradTable = 1200;   // 24 bytes each
+
+// The entry that holds chunk i: the last whose first chunk is at or before it.
+template <typename T>
+__device__ __forceinline__ int find_entry(const T& table, unsigned i) {
+  int lo = 0, hi = table.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (table.e[mid].first <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Sum of squares of one thread's 32 elements of a chunk: groups of 8, kThreads groups apart.
+template <typename E>
+__device__ __forceinline__ double squares(const GradEntry& e, size_t at) {
+  const E* g = static_cast<const E*>(e.g);
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const size_t a = at + (size_t)(i * kThreads + threadIdx.x) * 8;
+    if (e.vec && a + 8 <= e.n) {
+      load8(g + a, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = a + j < e.n ? load(g + a + j) : 0.f;
+    }
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
+  if (s > 1e-30f && s < 1e38f) return (double)s;   // what underflowed is below the sum's last bit
+  double d = 0.;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v[i][j] != 0.f) d += (double)v[i][j] * (double)v[i][j];
+  return d;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  __shared__ double s[32];
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = 0.;
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) t += s[i];
+  return t;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+    grad_squares_kernel(const __grid_constant__ GradTable<N> table, double* part, bool add) {
+  double d = 0.;
+  for (unsigned i = blockIdx.x; i < table.chunks; i += gridDim.x) {
+    const GradEntry& e = table.e[find_entry(table, i)];
+    const size_t at = (size_t)(i - e.first) * kNormChunk;
+    d += e.bf16 ? squares<__nv_bfloat16>(e, at) : squares<float>(e, at);
+  }
+  d = block_sum(d);
+  if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + d : d;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const double* part, int parts, float max_norm, float scale, float* norm,
+                     float* coef) {
+  double d = 0.;
+  for (int i = threadIdx.x; i < parts; i += kThreads) d += part[i];
+  d = sqrt(block_sum(d)) * (double)scale;
+  if (threadIdx.x) return;
+  const float n = (float)d;
+  *norm = n;
+  *coef = !isfinite(n) ? NAN : d > (double)max_norm ? (float)(scale * (max_norm / d)) : scale;
+}
+
+// -------------------------------------------------------------------------- AdamW
+struct StepEntry {
+  void* p;
+  const void* g;
+  unsigned long long n;
+  unsigned long long base;   // its first element in the state
+  unsigned first;            // its first chunk
+  float decay;
+  bool p_bf16, g_bf16, p_vec, g_vec;
+};
+template <int N>
+struct StepTable {
+  int count;
+  StepEntry e[N];
+};
+constexpr int kStepTable = 640;   // 48 bytes each
+
+struct Step {
+  float beta1, beta2, rest1, rest2, eps;   // rest: 1 - beta
+  float lr, inv_c1, inv_sqrt_c2;           // c: 1 - beta^t
+  float log_beta1, log_beta2;              // for a step number on the device
+  int t;
+  const float* lr_dev;
+  const int32_t* t_dev;
+  const float* coef;
+  uint64_t seed;
+  float* master;
+  void *m, *v;
+  uint8_t* scales;
+};
+
+// 8-bit moments of the eight elements of a lane; the warp holds one block.
+__device__ __forceinline__ void decode8(const uint2 mc, const uint2 vc, int a, int b, float* m,
+                                        float* v) {
+  const float up = __int_as_float((a - 7) << 23);   // 2^(a - 134)
+  const uint32_t mw[2] = {mc.x, mc.y}, vw[2] = {vc.x, vc.y};
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint16_t two = (uint16_t)(mw[j / 4] >> (8 * (j & 3)));
+    uint32_t h2;   // two fp16
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+    float lo, hi;
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h2));
+    m[j] = lo * up;
+    m[j + 1] = hi * up;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t c = (vw[j / 4] >> (8 * (j & 3))) & 255u;
+    v[j] = c ? __int_as_float((int)(c << 20) + ((b - 30) << 23)) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void encode8(const float* m, const float* v, const uint4 noise,
+                                        uint2* mc, uint2* vc, int* a, int* b) {
+  uint32_t top_m = 0, top_v = 0;   // fp32 bits: their order is the values'
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = __float_as_uint(m[j]) & 0x7fffffffu, y = __float_as_uint(v[j]);
+    if (x >= 0x7f800000u || y >= 0x7f800000u) {
+      bad = true;
+    } else {
+      top_m = max(top_m, x);
+      top_v = max(top_v, y);
+    }
+  }
+  *a = max((int)(__reduce_max_sync(kAll, top_m) >> 23), 8);
+  *b = max((int)(__reduce_max_sync(kAll, top_v) >> 23), 31);
+  const float down = __int_as_float((261 - *a) << 23);   // 2^(134 - a)
+  const uint32_t r[4] = {noise.x, noise.y, noise.z, noise.w};
+  uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(m[j + 1] * down), "f"(m[j] * down));
+    mw[j / 4] |= (uint32_t)two << (8 * (j & 3));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int u = (j & 1) ? (int)(r[j / 2] >> 16) : (int)(r[j / 2] & 0xffffu);
+    int c = (__float_as_int(v[j]) - ((*b - 30) << 23) + (u << 4)) >> 20;
+    c = v[j] > 0.f ? min(max(c, 1), 255) : 0;
+    vw[j / 4] |= (uint32_t)c << (8 * (j & 3));
+  }
+  if (bad) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t x = __float_as_uint(m[j]) & 0x7fffffffu, y = __float_as_uint(v[j]);
+      if (x >= 0x7f800000u || y >= 0x7f800000u) {
+        mw[j / 4] |= 0x7fu << (8 * (j & 3));
+        vw[j / 4] |= 255u << (8 * (j & 3));
+      }
+    }
+  }
+  *mc = make_uint2(mw[0], mw[1]);
+  *vc = make_uint2(vw[0], vw[1]);
+}
+
+template <typename E>
+__device__ __forceinline__ void load_some(const E* p, bool vec, int cnt, float* v) {
+  if (vec && cnt == 8) {
+    load8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < cnt ? load(p + j) : 0.f;
+  }
+}
+template <typename E>
+__device__ __forceinline__ void store_some(E* p, bool vec, int cnt, const float* v) {
+  if (vec && cnt == 8) {
+    store8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < cnt) store(p + j, v[j]);
+  }
+}
+
+template <int N, bool SMALL>
+__global__ void __launch_bounds__(kThreads)
+    adamw_kernel(const __grid_constant__ StepTable<N> table, const __grid_constant__ Step q) {
+  const float coef = q.coef ? *q.coef : 1.f;
+  if (!isfinite(coef)) return;
+  const StepEntry& e = table.e[find_entry(table, blockIdx.x)];
+  // this lane's eight elements: i of the tensor, s of the state
+  const size_t i = (size_t)(blockIdx.x - e.first) * kChunk + threadIdx.x * 8;
+  const size_t s = e.base + i;
+  const int lane = threadIdx.x & 31;
+  if (i - lane * 8 >= e.n) return;   // the warp's block lies behind the tensor
+  const int cnt = i >= e.n ? 0 : e.n - i < 8 ? (int)(e.n - i) : 8;
+
+  float p[8], g[8], m[8], v[8];
+  if (e.g_bf16) load_some(static_cast<const __nv_bfloat16*>(e.g) + i, e.g_vec, cnt, g);
+  else load_some(static_cast<const float*>(e.g) + i, e.g_vec, cnt, g);
+  if (e.p_bf16) load8(q.master + s, p);
+  else load_some(static_cast<const float*>(e.p) + i, e.p_vec, cnt, p);
+  if constexpr (SMALL) {
+    const uchar2 ab = reinterpret_cast<const uchar2*>(q.scales)[s / kBlock];
+    decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(q.m) + s),
+            *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(q.v) + s), ab.x, ab.y, m, v);
+  } else {
+    load8(static_cast<const float*>(q.m) + s, m);
+    load8(static_cast<const float*>(q.v) + s, v);
+  }
+  float lr = q.lr, inv_c1 = q.inv_c1, inv_sqrt_c2 = q.inv_sqrt_c2;
+  int t = q.t;
+  if (q.lr_dev) lr = *q.lr_dev;
+  if (q.t_dev) {
+    t = max(*q.t_dev, 1);
+    inv_c1 = -1.f / expm1f((float)t * q.log_beta1);
+    inv_sqrt_c2 = 1.f / sqrtf(-expm1f((float)t * q.log_beta2));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // Every step of the moments is rounded by itself (no fused products): 8-bit moments are a
+    // function of these bits.
+    const float x = __fmul_rn(g[j], coef);
+    m[j] = __fadd_rn(__fmul_rn(m[j], q.beta1), __fmul_rn(x, q.rest1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], q.beta2), __fmul_rn(__fmul_rn(x, x), q.rest2));
+    const float step = m[j] * inv_c1 / (sqrtf(v[j]) * inv_sqrt_c2 + q.eps);
+    p[j] = fmaf(-lr, fmaf(e.decay, p[j], step), p[j]);
+  }
+  if (e.p_bf16) {
+    store_some(q.master + s, true, cnt, p);
+    store_some(static_cast<__nv_bfloat16*>(e.p) + i, e.p_vec, cnt, p);
+  } else {
+    store_some(static_cast<float*>(e.p) + i, e.p_vec, cnt, p);
+  }
+  if constexpr (SMALL) {
+    uint2 mc, vc;
+    int a, b;
+    encode8(m, v, philox<7>(s / 8, (uint32_t)t, q.seed), &mc, &vc, &a, &b);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q.m) + s) = mc;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q.v) + s) = vc;
+    if (lane == 0) reinterpret_cast<uchar2*>(q.scales)[s / kBlock] = make_uchar2(a, b);
+  } else {
+    store8(static_cast<float*>(q.m) + s, m);
+    store8(static_cast<float*>(q.v) + s, v);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+    moments_kernel(size_t elements, const uint8_t* mc, const uint8_t* vc, const uint8_t* scales,
+                   __nv_bfloat16* m_out, __nv_bfloat16* v_out) {
+  const size_t s = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+  if (s >= elements) return;
+  const uchar2 ab = reinterpret_cast<const uchar2*>(scales)[s / kBlock];
+  float m[8], v[8];
+  decode8(*reinterpret_cast<const uint2*>(mc + s), *reinterpret_cast<const uint2*>(vc + s), ab.x,
+          ab.y, m, v);
+  store8(m_out + s, m);
+  store8(v_out + s, v);
+}
+
+constexpr size_t kMaxElements = (size_t)1 << 40;
+
+// Bytes that a call reads or writes.
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+// Whether nothing that is written overlaps anything else.
+bool disjoint(Range* r, size_t n) {
+  std::sort(r, r + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, written = 0;   // the ends so far
+  for (size_t i = 0; i < n; ++i) {
+    if (r[i].begin < (r[i].written ? any : written)) return false;
+    any = std::max(any, r[i].end);
+    if (r[i].written) written = std::max(written, r[i].end);
+  }
+  return true;
+}
+
+}  // namespace
+}  // namespace mok
+
+extern "C" mok_status mok_grad_norm_get_sizes(size_t* workspace_bytes) {
+  using namespace mok;
+  if (!workspace_bytes) return MOK_ERR_INVALID_ARG;
+  *workspace_bytes = align_up(kNormCtas * sizeof(double), 256);
+  return MOK_OK;
+}
+
+extern "C" mok_status mok_grad_norm(int count, const mok_grad* grads, float max_norm, float scale,
+                                    float* norm, float* coef, void* workspace, void* stream) {
+  using namespace mok;
+  if (count < 0 || (count && !grads) || !(max_norm > 0.f) || !(scale > 0.f) ||
+      !std::isfinite(scale) || !norm || !coef || !aligned_to(norm, 4) || !aligned_to(coef, 4))
+    return MOK_ERR_INVALID_ARG;
+  if (!workspace || !aligned_to(workspace, 256)) return MOK_ERR_WORKSPACE;
+  for (int i = 0; i < count; ++i) {
+    const mok_grad& g = grads[i];
+    if (!is_type(g.type) || !aligned_to(g.g, g.type == MOK_OUT_BF16 ? 2 : 4) || g.n > kMaxElements)
+      return MOK_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(workspace);
+  int parts = 0;
+  GradTable<kGradTable> table;
+  table.count = 0;
+  table.chunks = 0;
+  auto flush = [&] {
+    if (!table.count) return;
+    const int ctas = parts ? parts : (int)std::min<size_t>(kNormCtas, table.chunks);
+    if (table.count <= 64) {
+      GradTable<64> small;
+      small.count = table.count;
+      small.chunks = table.chunks;
+      std::copy(table.e, table.e + table.count, small.e);
+      grad_squares_kernel<<<ctas, kThreads, 0, s>>>(small, part, parts > 0);
+    } else {
+      grad_squares_kernel<<<ctas, kThreads, 0, s>>>(table, part, parts > 0);
+    }
+    parts = ctas;
+    table.count = 0;
+    table.chunks = 0;
+  };
+  for (int i = 0; i < count; ++i) {
+    const mok_grad& g = grads[i];
+    if (!g.g || !g.n) continue;
+    const size_t chunks = (g.n + kNormChunk - 1) / kNormChunk;
+    if (table.count == kGradTable || table.chunks + chunks > 0x7fffffffu) flush();
+    table.e[table.count++] = {g.g, g.n, table.chunks, g.type == MOK_OUT_BF16, aligned_to(g.g, 16)};
+    table.chunks += (unsigned)chunks;
+  }
+  flush();
+  grad_norm_kernel<<<1, kThreads, 0, s>>>(part, parts, max_norm, scale, norm, coef);
+  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+extern "C" mok_status mok_adamw_get_sizes(int count, const size_t* n, size_t* elements) {
+  using namespace mok;
+  if (count < 0 || (count && !n) || !elements) return MOK_ERR_INVALID_ARG;
+  size_t sum = 0;
+  for (int i = 0; i < count; ++i) {
+    if (n[i] > kMaxElements) return MOK_ERR_INVALID_ARG;
+    sum += align_up(n[i], kBlock);
+    if (sum > kMaxElements) return MOK_ERR_INVALID_ARG;
+  }
+  *elements = sum;
+  return MOK_OK;
+}
+
+extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_adamw_tensor* tensors,
+                                const mok_adamw_state* st, double lr, const float* lr_dev, int t,
+                                const int32_t* t_dev, const float* coef, uint64_t seed,
+                                void* stream) {
+  using namespace mok;
+  if (!r || !st || count < 0 || (count && !tensors)) return MOK_ERR_INVALID_ARG;
+  if (!(r->beta1 >= 0. && r->beta1 < 1.) || !(r->beta2 >= 0. && r->beta2 < 1.) ||
+      !(r->eps >= FLT_MIN && r->eps <= FLT_MAX) || (r->bits != 8 && r->bits != 32))
+    return MOK_ERR_INVALID_ARG;
+  if ((!lr_dev && !std::isfinite(lr)) || (!t_dev && t < 1) || !aligned_to(lr_dev, 4) ||
+      !aligned_to(t_dev, 4) || !aligned_to(coef, 4))
+    return MOK_ERR_INVALID_ARG;
+  const bool small = r->bits == 8;
+  size_t total = 0;
+  bool any = false, masters = false;
+  for (int i = 0; i < count; ++i) {
+    const mok_adamw_tensor& x = tensors[i];
+    if (!is_type(x.p_type) || !is_type(x.g_type) || x.n > kMaxElements || !std::isfinite(x.decay) ||
+        (x.n && !x.p) || !aligned_to(x.p, x.p_type == MOK_OUT_BF16 ? 2 : 4) ||
+        !aligned_to(x.g, x.g_type == MOK_OUT_BF16 ? 2 : 4))
+      return MOK_ERR_INVALID_ARG;
+    total += align_up(x.n, kBlock);
+    if (total > kMaxElements) return MOK_ERR_INVALID_ARG;
+    any |= x.n > 0;
+    masters |= x.n > 0 && x.p_type == MOK_OUT_BF16;
+  }
+  if (!any) return MOK_OK;
+  if (!st->m || !st->v || (small && !st->scales) || (masters && !st->master) ||
+      !aligned_to(st->m, 16) || !aligned_to(st->v, 16) || !aligned_to(st->scales, 16) ||
+      !aligned_to(st->master, 16))
+    return MOK_ERR_INVALID_ARG;
+  {
+    std::unique_ptr<Range[]> ranges(new (std::nothrow) Range[2 * (size_t)count + 4]);
+    if (!ranges) return MOK_ERR_UNSUPPORTED;
+    size_t n = 0;
+    auto add = [&](const void* p, size_t bytes, bool written) {
+      if (p && bytes) ranges[n++] = {(uintptr_t)p, (uintptr_t)p + bytes, written};
+    };
+    for (int i = 0; i < count; ++i) {
+      const mok_adamw_tensor& x = tensors[i];
+      add(x.p, x.n * (x.p_type == MOK_OUT_BF16 ? 2 : 4), true);
+      add(x.g, x.n * (x.g_type == MOK_OUT_BF16 ? 2 : 4), false);
+    }
+    add(st->m, total * (small ? 1 : 4), true);
+    add(st->v, total * (small ? 1 : 4), true);
+    if (small) add(st->scales, total / kBlock * 2, true);
+    if (masters) add(st->master, total * 4, true);
+    if (!disjoint(ranges.get(), n)) return MOK_ERR_INVALID_ARG;
+  }
+  Step q{};
+  q.beta1 = (float)r->beta1; q.beta2 = (float)r->beta2;
+  q.rest1 = (float)(1. - r->beta1); q.rest2 = (float)(1. - r->beta2);
+  q.eps = (float)r->eps;
+  q.lr = (float)lr;
+  q.t = t_dev ? 1 : t;
+  q.inv_c1 = (float)(1. / (1. - std::pow(r->beta1, (double)q.t)));
+  q.inv_sqrt_c2 = (float)(1. / std::sqrt(1. - std::pow(r->beta2, (double)q.t)));
+  q.log_beta1 = (float)std::log(r->beta1); q.log_beta2 = (float)std::log(r->beta2);
+  q.lr_dev = lr_dev; q.t_dev = t_dev; q.coef = coef; q.seed = seed;
+  q.master = st->master; q.m = st->m; q.v = st->v; q.scales = st->scales;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  StepTable<kStepTable> table;
+  table.count = 0;
+  unsigned chunks = 0;
+  auto launch = [&](const auto& tab) {
+    if (small) adamw_kernel<std::extent<decltype(tab.e)>::value, true><<<chunks, kThreads, 0, s>>>(tab, q);
+    else adamw_kernel<std::extent<decltype(tab.e)>::value, false><<<chunks, kThreads, 0, s>>>(tab, q);
+  };
+  auto flush = [&] {
+    if (!table.count) return;
+    if (table.count <= 64) {
+      StepTable<64> few;
+      few.count = table.count;
+      std::copy(table.e, table.e + table.count, few.e);
+      launch(few);
+    } else {
+      launch(table);
+    }
+    table.count = 0;
+    chunks = 0;
+  };
+  size_t base = 0;
+  for (int i = 0; i < count; ++i) {
+    const mok_adamw_tensor& x = tensors[i];
+    const size_t own = (x.n + kChunk - 1) / kChunk;
+    if (x.g && x.n) {
+      if (table.count == kStepTable || chunks + own > 0x7fffffffu) flush();
+      table.e[table.count++] = {x.p, x.g, x.n, base, chunks, (float)x.decay,
+                                x.p_type == MOK_OUT_BF16, x.g_type == MOK_OUT_BF16,
+                                aligned_to(x.p, 16), aligned_to(x.g, 16)};
+      chunks += (unsigned)own;
+    }
+    base += align_up(x.n, kBlock);
+  }
+  flush();
+  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+extern "C" mok_status mok_adamw_moments(size_t elements, const mok_adamw_state* st, void* m,
+                                        void* v, void* stream) {
+  using namespace mok;
+  if (!st || elements % kBlock || elements > kMaxElements) return MOK_ERR_INVALID_ARG;
+  if (elements == 0) return MOK_OK;
+  if (!st->m || !st->v || !st->scales || !m || !v || !aligned_to(st->m, 16) ||
+      !aligned_to(st->v, 16) || !aligned_to(st->scales, 16) || !aligned_to(m, 16) ||
+      !aligned_to(v, 16))
+    return MOK_ERR_INVALID_ARG;
+  const size_t blocks = (elements / 8 + kThreads - 1) / kThreads;
+  moments_kernel<<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      elements, static_cast<const uint8_t*>(st->m), static_cast<const uint8_t*>(st->v), st->scales,
+      static_cast<__nv_bfloat16*>(m), static_cast<__nv_bfloat16*>(v));
+  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}

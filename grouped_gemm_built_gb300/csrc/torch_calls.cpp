@@ -1,6 +1,6 @@
-// The torch-facing calls of routing.py, dropout.py and lora.py in one step each: check the
-// tensors, allocate the results on the current stream, call the C ABI. A Python body of the
-// same steps takes 10 to 35 us, several times a small call's kernels.
+// The torch-facing calls of routing.py, dropout.py, lora.py, norm.py, balance.py and optim.py in
+// one step each: check the tensors, allocate the results on the current stream, call the C ABI. A
+// Python body of the same steps takes 10 to 35 us, several times a small call's kernels.
 //
 // Every function returns its results, None when an argument is not what the call takes (the
 // Python caller then finds out which, and says so), or the library's status when it refused.
@@ -18,6 +18,7 @@
 
 #include <climits>
 #include <cstring>
+#include <vector>
 
 #include "mok_ops.h"
 
@@ -30,6 +31,16 @@ struct Api {
   decltype(&mok_lora_get_sizes) lora_get_sizes;
   decltype(&mok_lora_fwd) lora_fwd;
   decltype(&mok_lora_bwd) lora_bwd;
+  decltype(&mok_norm_get_sizes) norm_get_sizes;
+  decltype(&mok_norm_fwd) norm_fwd;
+  decltype(&mok_norm_bwd) norm_bwd;
+  decltype(&mok_balance_get_sizes) balance_get_sizes;
+  decltype(&mok_balance_fwd) balance_fwd;
+  decltype(&mok_balance_bwd) balance_bwd;
+  decltype(&mok_grad_norm_get_sizes) grad_norm_get_sizes;
+  decltype(&mok_grad_norm) grad_norm;
+  decltype(&mok_adamw) adamw;
+  decltype(&mok_adamw_moments) adamw_moments;
 } api;
 
 // A dense CUDA tensor behind a Python object, or null.
@@ -82,15 +93,17 @@ bool read_struct(PyObject* o, S* out) {
   return ok;
 }
 
-// bind(route, route_bwd, dropout, lora_get_sizes, lora_fwd, lora_bwd): addresses in libmok
+// bind(the addresses in libmok of the functions of Api, in its order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 6)) return nullptr;
-  api.route = reinterpret_cast<decltype(api.route)>(PyLong_AsVoidPtr(a[0]));
-  api.route_bwd = reinterpret_cast<decltype(api.route_bwd)>(PyLong_AsVoidPtr(a[1]));
-  api.dropout = reinterpret_cast<decltype(api.dropout)>(PyLong_AsVoidPtr(a[2]));
-  api.lora_get_sizes = reinterpret_cast<decltype(api.lora_get_sizes)>(PyLong_AsVoidPtr(a[3]));
-  api.lora_fwd = reinterpret_cast<decltype(api.lora_fwd)>(PyLong_AsVoidPtr(a[4]));
-  api.lora_bwd = reinterpret_cast<decltype(api.lora_bwd)>(PyLong_AsVoidPtr(a[5]));
+  if (!count(n, 16)) return nullptr;
+  Py_ssize_t i = 0;
+  auto take = [&](auto& f) {
+    f = reinterpret_cast<std::decay_t<decltype(f)>>(PyLong_AsVoidPtr(a[i++]));
+  };
+  take(api.route), take(api.route_bwd), take(api.dropout), take(api.lora_get_sizes);
+  take(api.lora_fwd), take(api.lora_bwd), take(api.norm_get_sizes), take(api.norm_fwd);
+  take(api.norm_bwd), take(api.balance_get_sizes), take(api.balance_fwd), take(api.balance_bwd);
+  take(api.grad_norm_get_sizes), take(api.grad_norm), take(api.adamw), take(api.adamw_moments);
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -267,9 +280,315 @@ PyObject* lora_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A norm's parameters and rows: w [H] and b [H] or None of one type, x [T][H].
+struct Normed {
+  mok_norm_dims dims;
+  const at::Tensor *w, *b, *x;
+  bool read(PyObject* kind, PyObject* eps, PyObject* pw, PyObject* pb, PyObject* px) {
+    x = dense(px);
+    if (!x || x->dim() != 2 || x->size(0) > INT_MAX || x->size(1) > INT_MAX) return false;
+    const int64_t H = x->size(1);
+    w = dense(pw);
+    if (!w || w->dim() != 1 || !dense(pw, w->scalar_type(), H, *x)) return false;
+    b = pb == Py_None ? nullptr : dense(pb, w->scalar_type(), H, *x);
+    if (!b && pb != Py_None) return false;
+    const int xt = code_of(x->scalar_type()), wt = code_of(w->scalar_type());
+    const long k = PyLong_AsLong(kind);
+    const double e = PyFloat_AsDouble(eps);
+    if (xt < 0 || wt < 0 || PyErr_Occurred()) return false;
+    dims = {(int)x->size(0), (int)H, (int)k, (float)e, (mok_out_dtype)xt, MOK_OUT_F32,
+            (mok_out_dtype)wt};
+    return true;
+  }
+};
+
+// norm_fwd(kind, eps, w, b | None, x, add | None, code of y) -> (y, h, stats)
+PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 7)) return nullptr;
+  Normed r;
+  if (!r.read(a[0], a[1], a[2], a[3], a[4])) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  const at::Tensor& x = *r.x;
+  const at::Tensor* add = a[5] == Py_None ? nullptr : dense(a[5], x.scalar_type(), x.numel(), x);
+  if (!add && a[5] != Py_None) Py_RETURN_NONE;
+  const long code = PyLong_AsLong(a[6]);
+  if (PyErr_Occurred()) return nullptr;
+  r.dims.y_type = (mok_out_dtype)code;
+  mok_norm_sizes sizes;
+  mok_status st = api.norm_get_sizes(&r.dims, &sizes);
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  c10::cuda::OptionalCUDAGuard guard(x.device());
+  at::Tensor y = make(x.sizes(), type_of(code), x);
+  at::Tensor h = add ? make(x.sizes(), x.scalar_type(), x) : x;
+  at::Tensor stats = make({x.size(0), 2}, at::kFloat, x);
+  st = api.norm_fwd(&r.dims, x.data_ptr(), add ? add->data_ptr() : nullptr, r.w->data_ptr(),
+                    r.b ? r.b->data_ptr() : nullptr, add ? h.data_ptr() : nullptr, y.data_ptr(),
+                    stats.data_ptr<float>(), stream_of(x));
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  return results(std::move(y), std::move(h), std::move(stats));
+  END_HANDLE_TH_ERRORS
+}
+
+// norm_bwd(kind, eps, w, b | None, h, dY, stats, add | None) -> (dX, dW[, dB])
+PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 8)) return nullptr;
+  Normed r;
+  if (!r.read(a[0], a[1], a[2], a[3], a[4])) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  const at::Tensor& h = *r.x;
+  const at::Tensor* dY = dense(a[5]);
+  const int yt = dY ? code_of(dY->scalar_type()) : -1;
+  if (yt < 0 || !dense(a[5], dY->scalar_type(), h.numel(), h)) Py_RETURN_NONE;
+  const at::Tensor* stats = dense(a[6], at::kFloat, 2 * h.size(0), h);
+  const at::Tensor* add = a[7] == Py_None ? nullptr : dense(a[7], h.scalar_type(), h.numel(), h);
+  if (!stats || (!add && a[7] != Py_None)) Py_RETURN_NONE;
+  r.dims.y_type = (mok_out_dtype)yt;
+  mok_norm_sizes sizes;
+  mok_status st = api.norm_get_sizes(&r.dims, &sizes);
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  c10::cuda::OptionalCUDAGuard guard(h.device());
+  at::Tensor dX = make(h.sizes(), h.scalar_type(), h), dW = make({h.size(1)}, r.w->scalar_type(), h),
+             dB;
+  if (r.b) dB = make({h.size(1)}, r.w->scalar_type(), h);
+  const at::Tensor ws = make({(int64_t)sizes.workspace_bytes}, at::kByte, h);
+  st = api.norm_bwd(&r.dims, dY->data_ptr(), h.data_ptr(), r.w->data_ptr(), stats->data_ptr<float>(),
+                    add ? add->data_ptr() : nullptr, dX.data_ptr(), dW.data_ptr(),
+                    r.b ? dB.data_ptr() : nullptr, ws.data_ptr(), stream_of(h));
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  if (r.b) return results(std::move(dX), std::move(dW), std::move(dB));
+  return results(std::move(dX), std::move(dW));
+  END_HANDLE_TH_ERRORS
+}
+
+// A router's logits [T][E] and the sequences of their rows.
+struct Balanced {
+  mok_balance rule;
+  const at::Tensor *l, *seqs;
+  int code, T, S;
+  bool read(PyObject* pr, PyObject* pl, PyObject* ps) {
+    if (!read_struct(pr, &rule)) return false;
+    l = dense(pl);
+    if (!l || l->dim() != 2 || l->size(1) != rule.E || l->size(0) > INT_MAX) return false;
+    code = code_of(l->scalar_type());
+    if (code < 0) return false;
+    T = (int)l->size(0);
+    seqs = nullptr;
+    S = 1;
+    if (ps != Py_None) {
+      seqs = dense(ps);
+      if (!seqs || seqs->dim() != 1 || seqs->size(0) < 2 || seqs->size(0) > INT_MAX ||
+          !dense(ps, at::kInt, seqs->numel(), *l))
+        return false;
+      S = (int)seqs->size(0) - 1;
+    }
+    return true;
+  }
+  const int32_t* offsets() const { return seqs ? seqs->data_ptr<int32_t>() : nullptr; }
+};
+
+// balance_fwd(rule, logits, topk_idx, seqs | None) -> (losses, counts, saved)
+PyObject* balance_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 4)) return nullptr;
+  Balanced r;
+  if (!r.read(a[0], a[1], a[3])) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  const at::Tensor* idx = dense(a[2], at::kInt, (int64_t)r.T * r.rule.k, *r.l);
+  if (!idx) Py_RETURN_NONE;
+  size_t bytes = 0;
+  mok_status st = api.balance_get_sizes(&r.rule, r.T, r.S, &bytes);
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  c10::cuda::OptionalCUDAGuard guard(r.l->device());
+  at::Tensor losses = make({2}, at::kFloat, *r.l), counts = make({r.rule.E}, at::kInt, *r.l),
+             saved = make({(int64_t)bytes}, at::kByte, *r.l);
+  st = api.balance_fwd(&r.rule, r.T, r.l->data_ptr(), (mok_out_dtype)r.code,
+                       idx->data_ptr<int32_t>(), r.offsets(), r.S, losses.data_ptr<float>(),
+                       counts.data_ptr<int32_t>(), saved.data_ptr(), stream_of(*r.l));
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  return results(std::move(losses), std::move(counts), std::move(saved));
+  END_HANDLE_TH_ERRORS
+}
+
+// balance_bwd(rule, logits, seqs | None, saved, dlosses | None, add | None, code) -> (dlogits,)
+PyObject* balance_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 7)) return nullptr;
+  Balanced r;
+  if (!r.read(a[0], a[1], a[2])) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  size_t bytes = 0;
+  mok_status st = api.balance_get_sizes(&r.rule, r.T, r.S, &bytes);
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  const long code = PyLong_AsLong(a[6]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::ScalarType type = type_of(code);
+  const at::Tensor* saved = dense(a[3], at::kByte, (int64_t)bytes, *r.l);
+  const at::Tensor* dl = a[4] == Py_None ? nullptr : dense(a[4], at::kFloat, 2, *r.l);
+  const at::Tensor* add = a[5] == Py_None ? nullptr : dense(a[5], type, r.l->numel(), *r.l);
+  if (!saved || (!dl && a[4] != Py_None) || (!add && a[5] != Py_None)) Py_RETURN_NONE;
+  c10::cuda::OptionalCUDAGuard guard(r.l->device());
+  at::Tensor out = make(r.l->sizes(), type, *r.l);
+  st = api.balance_bwd(&r.rule, r.T, r.l->data_ptr(), (mok_out_dtype)r.code, r.offsets(), r.S,
+                       saved->data_ptr(), dl ? dl->data_ptr<float>() : nullptr,
+                       add ? add->data_ptr() : nullptr, out.data_ptr(), (mok_out_dtype)code,
+                       stream_of(*r.l));
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  return results(std::move(out));
+  END_HANDLE_TH_ERRORS
+}
+
+// The items of a list or tuple, without a reference of their own.
+bool items(PyObject* o, PyObject*** at, Py_ssize_t* n) {
+  if (!PyList_Check(o) && !PyTuple_Check(o)) return false;
+  *at = PySequence_Fast_ITEMS(o);
+  *n = PySequence_Fast_GET_SIZE(o);
+  return *n <= INT_MAX;
+}
+
+// grad_norm([tensor | None, ...], max_norm, scale) -> (norm, coef)
+PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 3)) return nullptr;
+  PyObject** g;
+  Py_ssize_t tensors;
+  if (!items(a[0], &g, &tensors)) Py_RETURN_NONE;
+  const double max_norm = PyFloat_AsDouble(a[1]), scale = PyFloat_AsDouble(a[2]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor* like = nullptr;
+  std::vector<mok_grad> grads((size_t)tensors);
+  for (Py_ssize_t i = 0; i < tensors; ++i) {
+    if (g[i] == Py_None) continue;
+    const at::Tensor* t = dense(g[i]);
+    const int code = t ? code_of(t->scalar_type()) : -1;
+    if (code < 0 || (like && t->device() != like->device())) Py_RETURN_NONE;
+    like = t;
+    grads[i] = {t->data_ptr(), (size_t)t->numel(), (mok_out_dtype)code};
+  }
+  if (!like) Py_RETURN_NONE;
+  size_t bytes = 0;
+  mok_status st = api.grad_norm_get_sizes(&bytes);
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  c10::cuda::OptionalCUDAGuard guard(like->device());
+  at::Tensor norm = make({1}, at::kFloat, *like), coef = make({1}, at::kFloat, *like);
+  const at::Tensor ws = make({(int64_t)bytes}, at::kByte, *like);
+  st = api.grad_norm((int)tensors, grads.data(), (float)max_norm, (float)scale,
+                     norm.data_ptr<float>(), coef.data_ptr<float>(), ws.data_ptr(),
+                     stream_of(*like));
+  if (st != MOK_OK) return PyLong_FromLong(st);
+  return results(std::move(norm), std::move(coef));
+  END_HANDLE_TH_ERRORS
+}
+
+// adamw(rule, params, sizes and decays, (master | None, m, v, scales | None), elements,
+//       grads, lr, t, coef | None, seed) -> ()
+// params: a tuple of tensors; sizes and decays: a tuple of (numel, type code, decay), what they
+// were when the state was made; grads: a list or tuple of a tensor or None for each; lr and t:
+// numbers, or tensors of one fp32 and one int32 value.
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 10)) return nullptr;
+  mok_adamw_rule rule;
+  if (!read_struct(a[0], &rule)) return nullptr;
+  PyObject **p, **d, **st, **g;
+  Py_ssize_t np, nd, ns, ng;
+  if (!items(a[1], &p, &np) || !items(a[2], &d, &nd) || !items(a[3], &st, &ns) ||
+      !items(a[5], &g, &ng) || np != nd || np != ng || ns != 4)
+    Py_RETURN_NONE;
+  const at::Tensor* m = dense(st[1]);
+  if (!m) Py_RETURN_NONE;
+  const int64_t elements = PyLong_AsLongLong(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  const bool small = rule.bits == 8;
+  const at::ScalarType kind = small ? at::kByte : at::kFloat;
+  const at::Tensor* master = st[0] == Py_None ? nullptr : dense(st[0], at::kFloat, elements, *m);
+  const at::Tensor* v = dense(st[2], kind, elements, *m);
+  const at::Tensor* scales = small ? dense(st[3], at::kByte, elements / 128, *m) : nullptr;
+  if (!dense(st[1], kind, elements, *m) || !v || (!master && st[0] != Py_None) || (small && !scales))
+    Py_RETURN_NONE;
+  std::vector<mok_adamw_tensor> tensors((size_t)np);
+  for (Py_ssize_t i = 0; i < np; ++i) {
+    if (!PyTuple_Check(d[i]) || PyTuple_GET_SIZE(d[i]) != 3) Py_RETURN_NONE;
+    const int64_t numel = PyLong_AsLongLong(PyTuple_GET_ITEM(d[i], 0));
+    const long code = PyLong_AsLong(PyTuple_GET_ITEM(d[i], 1));
+    const double decay = PyFloat_AsDouble(PyTuple_GET_ITEM(d[i], 2));
+    if (PyErr_Occurred()) return nullptr;
+    const at::Tensor* t = dense(p[i], type_of(code), numel, *m);
+    if (!t) Py_RETURN_NONE;
+    tensors[i] = {t->data_ptr(), nullptr, (size_t)numel, decay, (mok_out_dtype)code, MOK_OUT_F32};
+    if (g[i] == Py_None) continue;
+    const at::Tensor* x = dense(g[i]);
+    const int gc = x ? code_of(x->scalar_type()) : -1;
+    if (gc < 0 || x->numel() != numel || x->device() != m->device()) Py_RETURN_NONE;
+    tensors[i].g = x->data_ptr();
+    tensors[i].g_type = (mok_out_dtype)gc;
+  }
+  double lr = 0.;
+  long t = 1;
+  const at::Tensor *lr_dev = nullptr, *t_dev = nullptr;
+  if (THPVariable_Check(a[6])) {
+    if (!(lr_dev = dense(a[6], at::kFloat, 1, *m))) Py_RETURN_NONE;
+  } else {
+    lr = PyFloat_AsDouble(a[6]);
+  }
+  if (THPVariable_Check(a[7])) {
+    if (!(t_dev = dense(a[7], at::kInt, 1, *m))) Py_RETURN_NONE;
+  } else {
+    t = PyLong_AsLong(a[7]);
+  }
+  if (PyErr_Occurred()) return nullptr;
+  if (t > INT_MAX || t < 1) return PyLong_FromLong(MOK_ERR_INVALID_ARG);
+  const at::Tensor* coef = a[8] == Py_None ? nullptr : dense(a[8], at::kFloat, 1, *m);
+  if (!coef && a[8] != Py_None) Py_RETURN_NONE;
+  const uint64_t seed = PyLong_AsUnsignedLongLongMask(a[9]);
+  if (PyErr_Occurred()) return nullptr;
+  c10::cuda::OptionalCUDAGuard guard(m->device());
+  const mok_adamw_state state = {master ? master->data_ptr<float>() : nullptr, m->data_ptr(),
+                                 v->data_ptr(),
+                                 scales ? scales->data_ptr<uint8_t>() : nullptr};
+  const mok_status s = api.adamw(&rule, (int)np, tensors.data(), &state, lr,
+                                 lr_dev ? lr_dev->data_ptr<float>() : nullptr, (int)t,
+                                 t_dev ? t_dev->data_ptr<int32_t>() : nullptr,
+                                 coef ? coef->data_ptr<float>() : nullptr, seed, stream_of(*m));
+  if (s != MOK_OK) return PyLong_FromLong(s);
+  return PyTuple_New(0);
+  END_HANDLE_TH_ERRORS
+}
+
+// adamw_moments(m, v, scales) -> (m, v) in bf16
+PyObject* adamw_moments(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 3)) return nullptr;
+  const at::Tensor* m = dense(a[0]);
+  if (!m || m->scalar_type() != at::kByte) Py_RETURN_NONE;
+  const at::Tensor* v = dense(a[1], at::kByte, m->numel(), *m);
+  const at::Tensor* scales = dense(a[2], at::kByte, m->numel() / 128, *m);
+  if (!v || !scales) Py_RETURN_NONE;
+  c10::cuda::OptionalCUDAGuard guard(m->device());
+  at::Tensor mo = make({m->numel()}, at::kBFloat16, *m), vo = make({m->numel()}, at::kBFloat16, *m);
+  const mok_adamw_state state = {nullptr, m->data_ptr(), v->data_ptr(), scales->data_ptr<uint8_t>()};
+  const mok_status s = api.adamw_moments((size_t)m->numel(), &state, mo.data_ptr(), vo.data_ptr(),
+                                         stream_of(*m));
+  if (s != MOK_OK) return PyLong_FromLong(s);
+  return results(std::move(mo), std::move(vo));
+  END_HANDLE_TH_ERRORS
+}
+
 #define MOK_CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MOK_CALL(bind),     MOK_CALL(route),    MOK_CALL(route_bwd),
                          MOK_CALL(dropout),  MOK_CALL(lora_fwd), MOK_CALL(lora_bwd),
+                         MOK_CALL(norm_fwd), MOK_CALL(norm_bwd), MOK_CALL(balance_fwd),
+                         MOK_CALL(balance_bwd), MOK_CALL(grad_norm), MOK_CALL(adamw),
+                         MOK_CALL(adamw_moments),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mok_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -45,6 +45,8 @@ MOK_SCORE_SOFTMAX = 0
 MOK_SCORE_SIGMOID = 1
 MOK_GROUP_MAX = 0
 MOK_GROUP_TOP2 = 1
+MOK_NORM_LAYER = 0
+MOK_NORM_RMS = 1
 
 
 class MokDims(ctypes.Structure):
@@ -102,6 +104,38 @@ class MokLoraForms(ctypes.Structure):
         (n, c_int) for n in ("u_ranks", "u_split", "u_chunks", "grad_columns", "grad_split")]
 
 
+class MokNormDims(ctypes.Structure):
+    _fields_ = [("T", c_int), ("H", c_int), ("kind", c_int), ("eps", ctypes.c_float),
+                ("x_type", c_int), ("y_type", c_int), ("w_type", c_int)]
+
+
+class MokNormSizes(ctypes.Structure):
+    _fields_ = [("stats_bytes", c_size_t), ("workspace_bytes", c_size_t)]
+
+
+class MokBalance(ctypes.Structure):
+    _fields_ = [("E", c_int), ("k", c_int), ("score", c_int), ("coef", ctypes.c_float),
+                ("z_coef", ctypes.c_float)]
+
+
+class MokGrad(ctypes.Structure):
+    _fields_ = [("g", c_void_p), ("n", c_size_t), ("type", c_int)]
+
+
+class MokAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("g", c_void_p), ("n", c_size_t), ("decay", ctypes.c_double),
+                ("p_type", c_int), ("g_type", c_int)]
+
+
+class MokAdamwRule(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("bits", c_int)]
+
+
+class MokAdamwState(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("master", "m", "v", "scales")]
+
+
 class MokError(RuntimeError):
     def __init__(self, what, status):
         super().__init__(f"{what}: {mok_status_string(status)} ({status})")
@@ -152,6 +186,22 @@ def _declare(L):
                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
         "mok_lora_get_status": (c_int, [c_void_p, c_void_p]),
+        "mok_norm_get_sizes": (c_int, [_P(MokNormDims), _P(MokNormSizes)]),
+        "mok_norm_fwd": (c_int, [_P(MokNormDims)] + [c_void_p] * 8),
+        "mok_norm_bwd": (c_int, [_P(MokNormDims)] + [c_void_p] * 10),
+        "mok_balance_get_sizes": (c_int, [_P(MokBalance), c_int, c_int, _P(c_size_t)]),
+        "mok_balance_fwd": (c_int, [_P(MokBalance), c_int, c_void_p, c_int, c_void_p, c_void_p,
+                                    c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "mok_balance_bwd": (c_int, [_P(MokBalance), c_int, c_void_p, c_int, c_void_p, c_int,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
+        "mok_grad_norm_get_sizes": (c_int, [_P(c_size_t)]),
+        "mok_grad_norm": (c_int, [c_int, _P(MokGrad), ctypes.c_float, ctypes.c_float, c_void_p,
+                                  c_void_p, c_void_p, c_void_p]),
+        "mok_adamw_get_sizes": (c_int, [c_int, _P(c_size_t), _P(c_size_t)]),
+        "mok_adamw": (c_int, [_P(MokAdamwRule), c_int, _P(MokAdamwTensor), _P(MokAdamwState),
+                              ctypes.c_double, c_void_p, c_int, c_void_p, c_void_p,
+                              ctypes.c_uint64, c_void_p]),
+        "mok_adamw_moments": (c_int, [c_size_t, _P(MokAdamwState), c_void_p, c_void_p, c_void_p]),
         "mok_profile_enable": (c_int, [c_void_p, c_int]),
         "mok_lora_get_forms": (c_int, [_P(MokLoraDims), c_int, c_int, _P(MokLoraForms)]),
         "mok_profile_report": (c_int, [c_void_p, c_char_p, c_size_t, _P(c_int)]),
@@ -195,7 +245,9 @@ def torch_calls():
         loader.exec_module(m)
         m.bind(*(ctypes.cast(getattr(L, "mok_" + f), c_void_p).value
                  for f in ("route", "route_bwd", "dropout", "lora_get_sizes", "lora_fwd",
-                           "lora_bwd")))
+                           "lora_bwd", "norm_get_sizes", "norm_fwd", "norm_bwd",
+                           "balance_get_sizes", "balance_fwd", "balance_bwd",
+                           "grad_norm_get_sizes", "grad_norm", "adamw", "adamw_moments")))
         _TORCH_CALLS = m
     return _TORCH_CALLS
 
@@ -363,6 +415,74 @@ def mok_lora_get_forms(dims: MokLoraDims, backward=False, own_input=False) -> Mo
     _check(lib().mok_lora_get_forms(ctypes.byref(dims), int(backward), int(own_input),
                                     ctypes.byref(f)), "mok_lora_get_forms")
     return f
+
+
+def mok_norm_get_sizes(dims: MokNormDims) -> MokNormSizes:
+    s = MokNormSizes()
+    _check(lib().mok_norm_get_sizes(ctypes.byref(dims), ctypes.byref(s)), "mok_norm_get_sizes")
+    return s
+
+
+def mok_norm_fwd(dims: MokNormDims, x, add, w, b, h, y, stats, stream) -> None:
+    _check(lib().mok_norm_fwd(ctypes.byref(dims), x, add, w, b, h, y, stats, stream),
+           "mok_norm_fwd")
+
+
+def mok_norm_bwd(dims: MokNormDims, dY, h, w, stats, add, dX, dW, dB, workspace, stream) -> None:
+    _check(lib().mok_norm_bwd(ctypes.byref(dims), dY, h, w, stats, add, dX, dW, dB, workspace,
+                              stream), "mok_norm_bwd")
+
+
+def mok_balance_get_sizes(rule: MokBalance, T, S=1) -> int:
+    n = c_size_t()
+    _check(lib().mok_balance_get_sizes(ctypes.byref(rule), T, S, ctypes.byref(n)),
+           "mok_balance_get_sizes")
+    return n.value
+
+
+def mok_balance_fwd(rule: MokBalance, T, logits, logits_type, topk_idx, seqs, S, losses, counts,
+                    saved, stream) -> None:
+    _check(lib().mok_balance_fwd(ctypes.byref(rule), T, logits, logits_type, topk_idx, seqs, S,
+                                 losses, counts, saved, stream), "mok_balance_fwd")
+
+
+def mok_balance_bwd(rule: MokBalance, T, logits, logits_type, seqs, S, saved, dlosses, add,
+                    dlogits, dlogits_type, stream) -> None:
+    _check(lib().mok_balance_bwd(ctypes.byref(rule), T, logits, logits_type, seqs, S, saved,
+                                 dlosses, add, dlogits, dlogits_type, stream), "mok_balance_bwd")
+
+
+def mok_grad_norm_get_sizes() -> int:
+    n = c_size_t()
+    _check(lib().mok_grad_norm_get_sizes(ctypes.byref(n)), "mok_grad_norm_get_sizes")
+    return n.value
+
+
+def mok_grad_norm(grads, max_norm, scale, norm, coef, workspace, stream) -> None:
+    """``grads``: a sequence of MokGrad."""
+    _check(lib().mok_grad_norm(len(grads), (MokGrad * len(grads))(*grads), max_norm, scale, norm,
+                               coef, workspace, stream), "mok_grad_norm")
+
+
+def mok_adamw_get_sizes(sizes) -> int:
+    """State elements of tensors of these sizes."""
+    n = c_size_t()
+    _check(lib().mok_adamw_get_sizes(len(sizes), (c_size_t * len(sizes))(*sizes), ctypes.byref(n)),
+           "mok_adamw_get_sizes")
+    return n.value
+
+
+def mok_adamw(rule: MokAdamwRule, tensors, state: MokAdamwState, lr, lr_dev, t, t_dev, coef, seed,
+              stream) -> None:
+    """``tensors``: a sequence of MokAdamwTensor."""
+    _check(lib().mok_adamw(ctypes.byref(rule), len(tensors),
+                           (MokAdamwTensor * len(tensors))(*tensors), ctypes.byref(state), lr,
+                           lr_dev, t, t_dev, coef, seed & (2**64 - 1), stream), "mok_adamw")
+
+
+def mok_adamw_moments(elements, state: MokAdamwState, m, v, stream) -> None:
+    _check(lib().mok_adamw_moments(elements, ctypes.byref(state), m, v, stream),
+           "mok_adamw_moments")
 
 
 def mok_profile_enable(ctx, enable: bool) -> None:
