@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include "mok_internal.h"
+#include "mok_launch.cuh"
 #include "mok_ops.h"
 #include "mok_profile.h"
 #include "mok_ptx.cuh"
@@ -132,14 +133,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
-}
-// Programmatic dependent launch: let the next kernel of the stream start its own set-up, and
-// wait until the kernels before this one have finished and their writes are visible.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_prerequisites() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 // 16 consecutive TMEM columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
@@ -1573,25 +1566,6 @@ const Device* current_device() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::call_once(once[dev], [&] { init_device(devices[dev], dev); });
   return devices[dev].sms > 0 ? &devices[dev] : nullptr;
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), int grid, int threads, size_t smem, int cluster,
-                   bool early, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // early: may start before
-  attr[1].val.programmaticStreamSerializationAllowed = 1;            // the last kernel ends
-  cfg.attrs = attr;
-  cfg.numAttrs = early ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Rows of X (or u) that a tile loads: all 128, or the batch's own rounded up to 8 (the rows of
