@@ -69,10 +69,56 @@ __device__ __forceinline__ void put(E* p, const float* v) {
     store(p, v[0]);
   }
 }
-template <int V>
+// ... of a parameter, of type W, or (void) of the type that the call names
+template <int V, typename W>
 __device__ __forceinline__ void get_w(const NormArgs& q, const void* p, int c, float* v) {
-  if (q.w_bf16) get<V>(static_cast<const __nv_bfloat16*>(p) + c, v);
+  if constexpr (!std::is_void_v<W>) get<V>(static_cast<const W*>(p) + c, v);
+  else if (q.w_bf16) get<V>(static_cast<const __nv_bfloat16*>(p) + c, v);
   else get<V>(static_cast<const float*>(p) + c, v);
+}
+
+// V elements at a time, in pairs: one instruction does two fp32 operations, each rounded as usual.
+template <int V>
+struct Vec {
+  float v[V];
+  static __device__ __forceinline__ Vec all(float x) {
+    Vec o;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o.v[j] = x;
+    return o;
+  }
+  __device__ __forceinline__ float2 pair(int j) const { return make_float2(v[j], v[j + 1]); }
+  __device__ __forceinline__ void set(int j, float2 p) { v[j] = p.x; v[j + 1] = p.y; }
+  __device__ __forceinline__ float sum() const {
+    float t = v[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) t += v[j];
+    return t;
+  }
+};
+template <int V>
+__device__ __forceinline__ Vec<V> operator+(const Vec<V>& a, const Vec<V>& b) {
+  Vec<V> o;
+  if constexpr (V == 1) o.v[0] = a.v[0] + b.v[0];
+#pragma unroll
+  for (int j = 0; j + 1 < V; j += 2) o.set(j, __fadd2_rn(a.pair(j), b.pair(j)));
+  return o;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> operator*(const Vec<V>& a, const Vec<V>& b) {
+  Vec<V> o;
+  if constexpr (V == 1) o.v[0] = a.v[0] * b.v[0];
+#pragma unroll
+  for (int j = 0; j + 1 < V; j += 2) o.set(j, __fmul2_rn(a.pair(j), b.pair(j)));
+  return o;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> fma(const Vec<V>& a, const Vec<V>& b, const Vec<V>& c) {
+  Vec<V> o;
+  if constexpr (V == 1) o.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
+#pragma unroll
+  for (int j = 0; j + 1 < V; j += 2) o.set(j, __ffma2_rn(a.pair(j), b.pair(j), c.pair(j)));
+  return o;
 }
 
 template <int BYTES>
@@ -90,52 +136,95 @@ __device__ __forceinline__ void copies_wait(int n) {
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Sums of a and b over the threads of a team. `turn` alternates between two places, so that one
-// barrier a sum is enough.
-__device__ __forceinline__ float2 row_sum(float a, float b, int& turn) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (blockDim.x == 32) return make_float2(a, b);
+template <int ID>
+__device__ __forceinline__ void named_bar_sync(int count) {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(count) : "memory");
+}
+// Sums over the threads of a team of a, and of b where `both`. `turn` alternates between two places,
+// so that one barrier a sum is enough.
+__device__ __forceinline__ float2 row_sum(float a, float b, bool both, int& turn) {
+  const int lane = threadIdx.x & 31;
+  if (both) {   // the lower half warp goes on with a, the upper with b
+    const float other = __shfl_xor_sync(kAll, lane < 16 ? b : a, 16);
+    a = (lane < 16 ? a : b) + other;
+  } else {
+    a += __shfl_xor_sync(kAll, a, 16);
+  }
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) a += __shfl_xor_sync(kAll, a, off);
+  if (blockDim.x == 32)
+    return make_float2(__shfl_sync(kAll, a, 0), __shfl_sync(kAll, a, 16));
   __shared__ float2 s[2][32];
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, first = threadIdx.y * warps;
+  const int warps = blockDim.x >> 5, first = threadIdx.y * warps;
   turn ^= 1;
-  if (lane == 0) s[turn][first + (threadIdx.x >> 5)] = make_float2(a, b);
+  if ((lane & 15) == 0)
+    reinterpret_cast<float*>(&s[turn][first + (threadIdx.x >> 5)])[lane >> 4] = a;
+  // teams differ in their rows; constant numbers, as a number in a register takes all 16 barriers
   if (blockDim.y == 1) __syncthreads();
-  else named_bar_sync(1 + threadIdx.y, blockDim.x);   // teams differ in their rows
-  const float2 t = lane < warps ? s[turn][first + lane] : make_float2(0.f, 0.f);
+  else if (threadIdx.y == 0) named_bar_sync<1>(blockDim.x);
+  else if (threadIdx.y == 1) named_bar_sync<2>(blockDim.x);
+  else if (threadIdx.y == 2) named_bar_sync<3>(blockDim.x);
+  else named_bar_sync<4>(blockDim.x);
+  float2 t = make_float2(0.f, 0.f);
+  if (warps <= 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = s[turn][first + min(i, warps - 1)];
+      t.x += i < warps ? v.x : 0.f;
+      t.y += i < warps ? v.y : 0.f;
+    }
+    return t;
+  }
+  if (lane < warps) t = s[turn][first + lane];
   return make_float2(warp_sum(t.x), warp_sum(t.y));
 }
 
-// A thread's places in shared memory: `stages` rows of K tensors, N accesses of 16 bytes.
-extern __shared__ __align__(16) char ring[];
-template <int N>
-__device__ __forceinline__ char* slot(int stage, int K, int tensor, int i) {
-  const int threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x;
-  return ring + (size_t)(((stage * K + tensor) * N + i) * threads + me) * 16;
-}
-// Starts the copies of this thread's part of a row.
-template <int N, int V, typename E>
-__device__ __forceinline__ void fetch(const void* p, size_t row, int H, int stage, int K, int tensor) {
-  const E* from = static_cast<const E*>(p) + row * H;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-    if (c < H) copy_async<V * (int)sizeof(E)>(smem_u32(slot<N>(stage, K, tensor, i)), from + c);
+// A thread's part of a row: N accesses, 32 V elements apart, from element c0 on; those below `live`
+// lie in the row.
+template <int N, int V>
+struct Part {
+  int c0, live;
+  __device__ __forceinline__ explicit Part(int H) {
+    c0 = (int)(threadIdx.x >> 5) * (32 * N * V) + (int)(threadIdx.x & 31) * V;
+    live = c0 < H ? min(N, (H - c0 + 32 * V - 1) / (32 * V)) : 0;
   }
+};
+// A thread's places in shared memory, for two rows of K tensors: an access of its warp is 512 bytes
+// in one piece (asynchronous copies to places further apart took 1.4 times as long).
+extern __shared__ __align__(16) char ring[];
+constexpr int kPlace = 512;
+template <int N, int K>
+constexpr int kPlaces = 2 * K * N;
+template <int N, int K>
+__device__ __forceinline__ char* places() {
+  const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
+  return ring + (size_t)warp * (kPlaces<N, K> * kPlace) + (threadIdx.x & 31) * 16;
+}
+// Starts the copies of this thread's part of a row (`from`: its first element) to `to` on.
+template <int N, int V, typename E>
+__device__ __forceinline__ void fetch(uint32_t to, const E* from, int live) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < live) copy_async<V * (int)sizeof(E)>(to + i * kPlace, from + i * (32 * V));
 }
 
 // RING: V elements a copy, 16 bytes at most; else V = 1, any alignment.
-template <int N, int V, typename X, typename Y, bool RING, int THREADS, int CTAS>
+template <int N, int V, typename X, typename Y, typename W, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs q) {
+  constexpr bool RING = V > 1;
+  constexpr int K = 2;
+  const Part<N, V> part(q.H);
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int K = q.add ? 2 : 1;
   const float inv_h = 1.f / (float)q.H;
+  char* const mine = RING ? places<N, K>() : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
-        fetch<N, V, X>(q.x, r, q.H, stage, K, 0);
-        if (q.add) fetch<N, V, X>(q.add, r, q.H, stage, K, 1);
+        const uint32_t to = smem_u32(mine) + stage * (K * N * kPlace);
+        const size_t at = r * q.H + part.c0;
+        fetch<N, V>(to, static_cast<const X*>(q.x) + at, part.live);
+        if (q.add) fetch<N, V>(to + N * kPlace, static_cast<const X*>(q.add) + at, part.live);
       }
       copies_commit();
     }
@@ -143,41 +232,39 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
   int stage = 0, turn = 0;
   for (int s = 0; s < q.stages; ++s) start(row + s * step, s);
   for (; row < (size_t)q.T; row += step) {
-    const size_t at = row * q.H;
-    float v[N][V];
-    float sum = 0.f;
+    const size_t at = row * q.H + part.c0;
+    const char* here = mine + stage * (K * N * kPlace);
+    Vec<V> v[N];
     if constexpr (RING) copies_wait(q.stages - 1);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-      if (c < q.H)
-        get<V>(RING ? reinterpret_cast<const X*>(slot<N>(stage, K, 0, i))
-                    : static_cast<const X*>(q.x) + at + c, v[i]);
+      v[i] = Vec<V>::all(0.f);
+      if (i < part.live)
+        get<V>(RING ? reinterpret_cast<const X*>(here + i * kPlace)
+                    : static_cast<const X*>(q.x) + at + i * (32 * V), v[i].v);
     }
     if (q.add) {
-      float kept[RING ? 1 : N][V];   // without a ring: all loads before the first store
+      Vec<V> kept[RING ? 1 : N];   // without a ring: all loads before the first store
       if constexpr (!RING) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-          if (c < q.H) get<V>(static_cast<const X*>(q.add) + at + c, kept[i]);
-        }
+        for (int i = 0; i < N; ++i)
+          if (i < part.live) get<V>(static_cast<const X*>(q.add) + at + i * (32 * V), kept[i].v);
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-        if (c < q.H) {
-          float a[V];
-          if constexpr (RING) get<V>(reinterpret_cast<const X*>(slot<N>(stage, K, 1, i)), a);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            v[i][j] += RING ? a[j] : kept[RING ? 0 : i][j];
-            // the norm is that of the stored h
-            if constexpr (sizeof(X) == 2) v[i][j] = __bfloat162float(__float2bfloat16_rn(v[i][j]));
+        if (i < part.live) {
+          if constexpr (RING) {
+            Vec<V> a;
+            get<V>(reinterpret_cast<const X*>(here + (N + i) * kPlace), a.v);
+            v[i] = v[i] + a;
+          } else {
+            v[i] = v[i] + kept[i];
           }
-          put<V>(static_cast<X*>(q.h) + at + c, v[i]);
+          if constexpr (sizeof(X) == 2) {   // the norm is that of the stored h
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i].v[j] = __bfloat162float(__float2bfloat16_rn(v[i].v[j]));
+          }
+          put<V>(static_cast<X*>(q.h) + at + i * (32 * V), v[i].v);
         }
       }
     }
@@ -185,140 +272,126 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
     if (++stage >= q.stages) stage = 0;
     float mean = 0.f;
     if (!q.rms) {
+      Vec<V> sum = Vec<V>::all(0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum = sum + v[i];
+      mean = row_sum(sum.sum(), 0.f, false, turn).x * inv_h;
+      const Vec<V> minus = Vec<V>::all(-mean);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum += v[i][j];
-      mean = row_sum(sum, 0.f, turn).x * inv_h;
+        if (i < part.live) v[i] = v[i] + minus;
     }
-    float sq = 0.f;
+    Vec<V> sq = Vec<V>::all(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-      if (c < q.H) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          v[i][j] -= mean;
-          sq += v[i][j] * v[i][j];
-        }
-      }
-    }
-    const float r = 1.f / sqrtf(row_sum(sq, 0.f, turn).x * inv_h + q.eps);
+    for (int i = 0; i < N; ++i) sq = fma(v[i], v[i], sq);
+    const float r = 1.f / sqrtf(row_sum(sq.sum(), 0.f, false, turn).x * inv_h + q.eps);
     if (q.stats && threadIdx.x == 0) q.stats[row] = make_float2(mean, r);
+    const Vec<V> rv = Vec<V>::all(r);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-      if (c < q.H) {
-        float w[V], b[V];
-        get_w<V>(q, q.w, c, w);
-        if (q.b) get_w<V>(q, q.b, c, b);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * r * w[j] + (q.b ? b[j] : 0.f);
-        put<V>(static_cast<Y*>(q.y) + at + c, v[i]);
+      if (i < part.live) {
+        const int c = part.c0 + i * (32 * V);
+        Vec<V> w, b = Vec<V>::all(0.f);
+        get_w<V, W>(q, q.w, c, w.v);
+        if (q.b) get_w<V, W>(q, q.b, c, b.v);
+        const Vec<V> y = fma(v[i] * rv, w, b);
+        put<V>(static_cast<Y*>(q.y) + at + i * (32 * V), y.v);
       }
     }
   }
 }
 
-template <int N, int V, typename X, typename Y, bool RING, bool DB, int THREADS, int CTAS>
+template <int N, int V, typename X, typename Y, typename W, bool DB, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs q) {
   launch_dependents();
+  constexpr bool RING = V > 1;
+  constexpr int K = 3;
+  const Part<N, V> part(q.H);
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int K = q.add ? 3 : 2;
   const float inv_h = 1.f / (float)q.H;
+  char* const mine = RING ? places<N, K>() : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
-        fetch<N, V, Y>(q.dy, r, q.H, stage, K, 0);
-        fetch<N, V, X>(q.x, r, q.H, stage, K, 1);
-        if (q.add) fetch<N, V, X>(q.add, r, q.H, stage, K, 2);
+        const uint32_t to = smem_u32(mine) + stage * (K * N * kPlace);
+        const size_t at = r * q.H + part.c0;
+        fetch<N, V>(to, static_cast<const Y*>(q.dy) + at, part.live);
+        fetch<N, V>(to + N * kPlace, static_cast<const X*>(q.x) + at, part.live);
+        if (q.add) fetch<N, V>(to + 2 * N * kPlace, static_cast<const X*>(q.add) + at, part.live);
       }
       copies_commit();
     }
   };
-  float acc_w[N][V], acc_b[DB ? N : 1][V];
+  Vec<V> acc_w[N], acc_b[DB ? N : 1];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      acc_w[i][j] = 0.f;
-      if (DB) acc_b[i][j] = 0.f;
-    }
+  for (int i = 0; i < N; ++i) {
+    acc_w[i] = Vec<V>::all(0.f);
+    if constexpr (DB) acc_b[i] = acc_w[i];
+  }
   int stage = 0, turn = 0;
   for (int s = 0; s < q.stages; ++s) start(row + s * step, s);
   float2 st = row < (size_t)q.T ? q.stats[row] : make_float2(0.f, 0.f);
   for (; row < (size_t)q.T; row += step) {
-    const size_t at = row * q.H;
+    const size_t at = row * q.H + part.c0;
+    const char* here = mine + stage * (K * N * kPlace);
     const float mean = st.x, r = st.y;
     if (row + step < (size_t)q.T) st = q.stats[row + step];
-    if constexpr (RING) copies_wait(q.stages - 1);
-    float s1 = 0.f, s2 = 0.f;
+    Vec<V> s1 = Vec<V>::all(0.f), s2 = s1;
+    const Vec<V> minus_mean = Vec<V>::all(-mean), rv = Vec<V>::all(r);
     // what the second pass needs again: kept in registers without a ring
-    float kept_t[RING ? 1 : N][V], kept_x[RING ? 1 : N][V];
-    if constexpr (!RING) {
+    Vec<V> kept_y[RING ? 1 : N], kept_x[RING ? 1 : N];
+    if constexpr (RING) {
+      copies_wait(q.stages - 1);
+    } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-        if (c < q.H) {
-          get<V>(static_cast<const Y*>(q.dy) + at + c, kept_t[i]);
-          get<V>(static_cast<const X*>(q.x) + at + c, kept_x[i]);
+        if (i < part.live) {
+          get<V>(static_cast<const Y*>(q.dy) + at + i * (32 * V), kept_y[i].v);
+          get<V>(static_cast<const X*>(q.x) + at + i * (32 * V), kept_x[i].v);
         }
       }
     }
+    auto read = [&](int i, Vec<V>& dy, Vec<V>& x) {
+      if constexpr (RING) {
+        get<V>(reinterpret_cast<const Y*>(here + i * kPlace), dy.v);
+        get<V>(reinterpret_cast<const X*>(here + (N + i) * kPlace), x.v);
+      } else {
+        dy = kept_y[i];
+        x = kept_x[i];
+      }
+    };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-      if (c < q.H) {
-        float dy[V], x[V], w[V];
-        if constexpr (RING) {
-          get<V>(reinterpret_cast<const Y*>(slot<N>(stage, K, 0, i)), dy);
-          get<V>(reinterpret_cast<const X*>(slot<N>(stage, K, 1, i)), x);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            dy[j] = kept_t[i][j];
-            x[j] = kept_x[i][j];
-          }
-        }
-        get_w<V>(q, q.w, c, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float xh = (x[j] - mean) * r, t = dy[j] * w[j];
-          acc_w[i][j] += dy[j] * xh;
-          if (DB) acc_b[i][j] += dy[j];
-          s1 += t;
-          s2 += t * xh;
-        }
+      if (i < part.live) {
+        Vec<V> dy, x, w;
+        read(i, dy, x);
+        get_w<V, W>(q, q.w, part.c0 + i * (32 * V), w.v);
+        const Vec<V> xh = (x + minus_mean) * rv, t = dy * w;
+        acc_w[i] = fma(dy, xh, acc_w[i]);
+        if constexpr (DB) acc_b[i] = acc_b[i] + dy;
+        s1 = s1 + t;
+        s2 = fma(t, xh, s2);
       }
     }
-    float2 s = row_sum(q.rms ? 0.f : s1, s2, turn);
-    s.x *= inv_h;
-    s.y *= inv_h;
+    const float2 s = row_sum(s2.sum(), s1.sum(), !q.rms, turn);
+    // dX = r t - xh r mean(t xh) - r mean t + add
+    const Vec<V> slope = Vec<V>::all(-r * (s.x * inv_h)),
+                 shift = Vec<V>::all(q.rms ? 0.f : -r * (s.y * inv_h));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-      if (c < q.H) {
-        float dy[V], x[V], a[V], w[V];
-        if constexpr (RING) {
-          get<V>(reinterpret_cast<const Y*>(slot<N>(stage, K, 0, i)), dy);
-          get<V>(reinterpret_cast<const X*>(slot<N>(stage, K, 1, i)), x);
-          if (q.add) get<V>(reinterpret_cast<const X*>(slot<N>(stage, K, 2, i)), a);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            dy[j] = kept_t[i][j];
-            x[j] = kept_x[i][j];
-          }
-          if (q.add) get<V>(static_cast<const X*>(q.add) + at + c, a);
+      if (i < part.live) {
+        Vec<V> dy, x, w;
+        read(i, dy, x);
+        get_w<V, W>(q, q.w, part.c0 + i * (32 * V), w.v);
+        Vec<V> d = fma(dy * w, rv, fma((x + minus_mean) * rv, slope, shift));
+        if (q.add) {
+          Vec<V> a;
+          if constexpr (RING) get<V>(reinterpret_cast<const X*>(here + (2 * N + i) * kPlace), a.v);
+          else get<V>(static_cast<const X*>(q.add) + at + i * (32 * V), a.v);
+          d = d + a;
         }
-        get_w<V>(q, q.w, c, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float xh = (x[j] - mean) * r;
-          x[j] = r * (dy[j] * w[j] - s.x - xh * s.y) + (q.add ? a[j] : 0.f);
-        }
-        put<V>(static_cast<X*>(q.y) + at + c, x);
+        put<V>(static_cast<X*>(q.y) + at + i * (32 * V), d.v);
       }
     }
     start(row + q.stages * step, stage);
@@ -338,12 +411,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
       float* to_b = last ? q.part_b + (size_t)blockIdx.x * q.H : sum_b;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-        if (c < q.H) {
+        if (i < part.live) {
+          const int c = part.c0 + i * (32 * V);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            to_w[c + j] = acc_w[i][j] + (team ? sum_w[c + j] : 0.f);
-            if (DB) to_b[c + j] = acc_b[i][j] + (team ? sum_b[c + j] : 0.f);
+            to_w[c + j] = acc_w[i].v[j] + (team ? sum_w[c + j] : 0.f);
+            if constexpr (DB) to_b[c + j] = acc_b[i].v[j] + (team ? sum_b[c + j] : 0.f);
           }
         }
       }
@@ -392,21 +465,20 @@ uintptr_t size_of(mok_out_dtype t) { return t == MOK_OUT_BF16 ? 2 : 4; }
 bool whole(const void* p) { return aligned_to(p, 16); }
 
 
-// How a call runs: teams of bx threads a row, by teams a CTA, `stages` rows of `tensors` tensors in
-// flight per team.
+// How a call runs: teams of bx threads a row, by teams a CTA, `stages` rows in flight per team.
 struct Form {
   unsigned bx, by, grid;
   int stages;
   size_t smem;
 };
-// n accesses of v elements a thread; `threads` a SM is what the registers allow.
-Form form(const mok_norm_dims* d, int n, int v, int tensors, int threads, int most_ctas) {
+// `threads` a SM is what the registers allow.
+template <int N, int V, int K>
+Form form(const mok_norm_dims* d, int threads, int most_ctas) {
   Form f{};
-  f.bx = ((d->H + n * v - 1) / (n * v) + 31) / 32 * 32;
+  f.bx = ((d->H + N * V - 1) / (N * V) + 31) / 32 * 32;
   f.by = std::max(1u, 256 / f.bx);
-  const size_t row = (size_t)f.bx * f.by * n * tensors * 16;
-  f.stages = v == 1 ? 0 : row * 2 <= kRingBytes ? 2 : 1;
-  f.smem = row * f.stages;
+  f.stages = V == 1 ? 0 : 2;
+  f.smem = V == 1 ? 0 : (size_t)f.bx * f.by * kPlaces<N, K> * 16;
   int ctas = std::max(1, threads / (int)(f.bx * f.by));
   if (f.smem) ctas = std::max(1, std::min(ctas, (int)(kRingBytes / f.smem)));
   f.grid = (unsigned)std::min<size_t>(((size_t)d->T + f.by - 1) / f.by,
@@ -426,6 +498,10 @@ cudaError_t run(K kernel, const Form& f, const NormArgs& q, cudaStream_t s) {
   return launch(kernel, dim3(f.grid), dim3(f.bx, f.by), f.smem, 1, false, s, q);
 }
 
+template <typename T>
+struct Tag {
+  using type = T;
+};
 template <int N, int V, int THREADS, typename F>
 cudaError_t by_types(const mok_norm_dims* d, F f) {
   using B = __nv_bfloat16;
@@ -433,24 +509,29 @@ cudaError_t by_types(const mok_norm_dims* d, F f) {
   constexpr std::integral_constant<int, V> v{};
   constexpr std::integral_constant<int, THREADS> t{};
   const bool xb = d->x_type == MOK_OUT_BF16, yb = d->y_type == MOK_OUT_BF16;
+  auto with = [&](auto x, auto y) {
+    if constexpr (V == 1) return f(n, v, t, x, y, Tag<void>{});
+    else if (d->w_type == MOK_OUT_BF16) return f(n, v, t, x, y, Tag<B>{});
+    else return f(n, v, t, x, y, Tag<float>{});
+  };
   if constexpr (V != 4)
-    if (xb && yb) return f(n, v, t, B{}, B{});
+    if (xb && yb) return with(Tag<B>{}, Tag<B>{});
   if constexpr (V != 8) {
-    if (xb && !yb) return f(n, v, t, B{}, 0.f);
-    if (yb && !xb) return f(n, v, t, 0.f, B{});
-    return f(n, v, t, 0.f, 0.f);
+    if (xb && !yb) return with(Tag<B>{}, Tag<float>{});
+    if (yb && !xb) return with(Tag<float>{}, Tag<B>{});
+    return with(Tag<float>{}, Tag<float>{});
   }
   return cudaErrorInvalidValue;
 }
-// f(accesses a thread, elements an access, most threads of a CTA, X, Y) for the call's types, width
-// and alignment. `vec`: 32 elements a thread (8 for narrow rows) in accesses of 16 bytes of the
-// widest type, through the ring; element by element where rows are not aligned, or too wide for
-// it.
-template <typename F>
-cudaError_t by_form(const mok_norm_dims* d, bool vec, int tensors, F f) {
+// f(accesses a thread, elements an access, most threads of a CTA, X, Y, W) for the call's types,
+// width and alignment. `vec`: 32 elements a thread (8 for narrow rows) in accesses of 16 bytes of
+// the widest type, through a ring for K tensors; element by element where rows are not aligned, or
+// too wide for the ring.
+template <int K, typename F>
+cudaError_t by_form(const mok_norm_dims* d, bool vec, F f) {
   const bool wide = d->x_type != MOK_OUT_BF16 || d->y_type != MOK_OUT_BF16;
   const int bx = ((d->H + 31) / 32 + 31) / 32 * 32;
-  if ((size_t)bx * (wide ? 8 : 4) * tensors * 16 > kRingBytes) vec = false;
+  if ((size_t)bx * (wide ? kPlaces<8, K> : kPlaces<4, K>) * 16 > kRingBytes) vec = false;
   if (!vec) {
     if (d->H <= 2048) return by_types<8, 1, 256>(d, f);
     if (d->H <= 8192) return by_types<8, 1, 1024>(d, f);
@@ -495,14 +576,14 @@ extern "C" mok_status mok_norm_fwd(const mok_norm_dims* d, const void* x, const 
   q.stats = reinterpret_cast<float2*>(stats);
   const bool vec = d->H % 8 == 0 && whole(x) && whole(add) && whole(w) && whole(b) && whole(h) &&
                    whole(y);
-  const int tensors = add ? 2 : 1;
-  const cudaError_t e = by_form(d, vec, tensors, [&](auto n, auto v, auto threads, auto xt, auto yt) {
+  const cudaError_t e = by_form<2>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
     constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
     constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 6 : 3;
-    const Form f = form(d, N, V, tensors, THREADS * CTAS, INT_MAX);
+    const Form f = form<N, V, 2>(d, THREADS * CTAS, INT_MAX);
     q.stages = f.stages;
-    return run(norm_fwd_kernel<N, V, decltype(xt), decltype(yt), (V > 1), THREADS, CTAS>, f, q,
-               static_cast<cudaStream_t>(stream));
+    return run(norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type,
+                               typename decltype(wt)::type, THREADS, CTAS>,
+               f, q, static_cast<cudaStream_t>(stream));
   });
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
@@ -531,17 +612,18 @@ extern "C" mok_status mok_norm_bwd(const mok_norm_dims* d, const void* dY, const
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->T) {
     const bool vec = d->H % 8 == 0 && whole(dY) && whole(h) && whole(w) && whole(add) && whole(dX);
-    const int tensors = add ? 3 : 2;
-    const cudaError_t e = by_form(d, vec, tensors, [&](auto n, auto v, auto threads, auto xt, auto yt) {
+    const cudaError_t e = by_form<3>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
       constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
       constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 3 : 2;
-      Form f = form(d, N, V, tensors, THREADS * CTAS, most_parts(d));
+      using X = typename decltype(xt)::type;
+      using Y = typename decltype(yt)::type;
+      using W = typename decltype(wt)::type;
+      Form f = form<N, V, 3>(d, THREADS * CTAS, most_parts(d));
       if (f.by > 1) f.smem = std::max(f.smem, (size_t)d->H * sizeof(float2));   // joins the teams
       q.stages = f.stages;
       q.parts = (int)f.grid;
-      if (dB)
-        return run(norm_bwd_kernel<N, V, decltype(xt), decltype(yt), (V > 1), true, THREADS, CTAS>, f, q, s);
-      return run(norm_bwd_kernel<N, V, decltype(xt), decltype(yt), (V > 1), false, THREADS, CTAS>, f, q, s);
+      if (dB) return run(norm_bwd_kernel<N, V, X, Y, W, true, THREADS, CTAS>, f, q, s);
+      return run(norm_bwd_kernel<N, V, X, Y, W, false, THREADS, CTAS>, f, q, s);
     });
     if (e != cudaSuccess) return MOK_ERR_CUDA;
   }
