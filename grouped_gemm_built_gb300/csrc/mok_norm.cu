@@ -413,10 +413,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
       for (int i = 0; i < N; ++i) {
         if (i < part.live) {
           const int c = part.c0 + i * (32 * V);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            to_w[c + j] = acc_w[i].v[j] + (team ? sum_w[c + j] : 0.f);
-            if constexpr (DB) to_b[c + j] = acc_b[i].v[j] + (team ? sum_b[c + j] : 0.f);
+          Vec<V> b;
+          if (team) {
+            get<V>(sum_w + c, b.v);
+            acc_w[i] = acc_w[i] + b;
+          }
+          put<V>(to_w + c, acc_w[i].v);
+          if constexpr (DB) {
+            if (team) {
+              get<V>(sum_b + c, b.v);
+              acc_b[i] = acc_b[i] + b;
+            }
+            put<V>(to_b + c, acc_b[i].v);
           }
         }
       }
