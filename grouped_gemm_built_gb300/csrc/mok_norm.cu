@@ -23,7 +23,7 @@ namespace {
 constexpr int kMaxH = 32768;
 constexpr int kSms = 152;
 constexpr int kMaxParts = kSms * 4;    // partial rows of dW and dB
-constexpr int kRingBytes = 220 * 1024; // shared memory of an SM for rows in flight
+constexpr int kRingBytes = 224 * 1024; // shared memory of an SM for rows in flight
 
 struct NormArgs {
   int T, H;
@@ -75,6 +75,45 @@ __device__ __forceinline__ void get_w(const NormArgs& q, const void* p, int c, f
   if constexpr (!std::is_void_v<W>) get<V>(static_cast<const W*>(p) + c, v);
   else if (q.w_bf16) get<V>(static_cast<const __nv_bfloat16*>(p) + c, v);
   else get<V>(static_cast<const float*>(p) + c, v);
+}
+
+// V elements as they lie in memory, unpacked when they are used; a thread's place in shared memory
+// holds 16 bytes of them, the rest follows in a second place.
+constexpr int kPlace = 512;   // one access of a warp
+template <int V, typename E>
+constexpr int kWPlaces = V * (int)sizeof(E) > 16 ? 2 : 1;
+template <int V, typename E>
+struct __align__(V * sizeof(E)) Raw {
+  E v[V];
+  static constexpr int kBytes = V * (int)sizeof(E), kPart = kBytes < 16 ? kBytes : 16;
+  using Word = std::conditional_t<kPart == 16, uint4, std::conditional_t<kPart == 8, uint2, uint32_t>>;
+  __device__ __forceinline__ void read(const E* p) {
+#pragma unroll
+    for (int i = 0; i < kBytes / kPart; ++i)
+      reinterpret_cast<Word*>(v)[i] = reinterpret_cast<const Word*>(p)[i];
+  }
+  __device__ __forceinline__ void keep(char* to) const {
+#pragma unroll
+    for (int i = 0; i < kBytes / kPart; ++i)
+      *reinterpret_cast<Word*>(to + i * kPlace) = reinterpret_cast<const Word*>(v)[i];
+  }
+  __device__ __forceinline__ void fetch(const char* from) {
+#pragma unroll
+    for (int i = 0; i < kBytes / kPart; ++i)
+      reinterpret_cast<Word*>(v)[i] = *reinterpret_cast<const Word*>(from + i * kPlace);
+  }
+};
+// What a backward call needs beyond dX and dW: nothing for an RMS norm, the rows' means, dB as well.
+enum { kRms, kMeans, kBias };
+// Whether a backward kernel holds w in registers; else the places that it takes.
+template <int V, typename W>
+constexpr bool keeps_w(int mode) {
+  return V == 8 && std::is_same_v<W, __nv_bfloat16> && mode != kBias;
+}
+template <int N, int V, typename W>
+constexpr int w_places(int mode) {
+  if constexpr (V == 1) return 0;
+  else return keeps_w<V, W>(mode) ? 0 : N * kWPlaces<V, W>;
 }
 
 // V elements at a time, in pairs: one instruction does two fp32 operations, each rounded as usual.
@@ -136,6 +175,9 @@ __device__ __forceinline__ void copies_wait(int n) {
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
 template <int ID>
 __device__ __forceinline__ void named_bar_sync(int count) {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(count) : "memory");
@@ -191,14 +233,12 @@ struct Part {
 };
 // A thread's places in shared memory, for two rows of K tensors: an access of its warp is 512 bytes
 // in one piece (asynchronous copies to places further apart took 1.4 times as long).
+// `more` places beyond those.
 extern __shared__ __align__(16) char ring[];
-constexpr int kPlace = 512;
 template <int N, int K>
-constexpr int kPlaces = 2 * K * N;
-template <int N, int K>
-__device__ __forceinline__ char* places() {
+__device__ __forceinline__ char* places(int more) {
   const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
-  return ring + (size_t)warp * (kPlaces<N, K> * kPlace) + (threadIdx.x & 31) * 16;
+  return ring + (size_t)warp * ((2 * K * N + more) * kPlace) + (threadIdx.x & 31) * 16;
 }
 // Starts the copies of this thread's part of a row (`from`: its first element) to `to` on.
 template <int N, int V, typename E>
@@ -217,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
   const float inv_h = 1.f / (float)q.H;
-  char* const mine = RING ? places<N, K>() : nullptr;
+  char* const mine = RING ? places<N, K>(0) : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
@@ -231,6 +271,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
   };
   int stage = 0, turn = 0;
   for (int s = 0; s < q.stages; ++s) start(row + s * step, s);
+  if constexpr (RING) {   // the first row's second trip to memory, made beside its first
+    const int size = q.w_bf16 ? 2 : 4;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i < part.live) {
+        const size_t c = (size_t)(part.c0 + i * (32 * V)) * size;
+        prefetch_l1(static_cast<const char*>(q.w) + c);
+        if (q.b) prefetch_l1(static_cast<const char*>(q.b) + c);
+      }
+    }
+  }
   for (; row < (size_t)q.T; row += step) {
     const size_t at = row * q.H + part.c0;
     const char* here = mine + stage * (K * N * kPlace);
@@ -301,16 +352,21 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
   }
 }
 
-template <int N, int V, typename X, typename Y, typename W, bool DB, int THREADS, int CTAS>
+// The parameters are read once: w stays in registers in the type it has, or, where dB's sums need
+// those, in the thread's own places of shared memory. (Read again for every row through L1, twice,
+// they made up a fifth of the kernel's time: 8192 x 7168 bf16 with add 95.6 us, now 78.3.)
+template <int N, int V, typename X, typename Y, typename W, int MODE, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs q) {
   launch_dependents();
-  constexpr bool RING = V > 1;
+  constexpr bool RING = V > 1, DB = MODE == kBias, WREG = keeps_w<V, W>(MODE);
+  const bool rms = MODE == kRms || (MODE == kBias && q.rms);
   constexpr int K = 3;
   const Part<N, V> part(q.H);
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
   const float inv_h = 1.f / (float)q.H;
-  char* const mine = RING ? places<N, K>() : nullptr;
+  constexpr int MORE = w_places<N, V, W>(MODE);
+  char* const mine = RING ? places<N, K>(MORE) : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
@@ -321,6 +377,29 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
         if (q.add) fetch<N, V>(to + 2 * N * kPlace, static_cast<const X*>(q.add) + at, part.live);
       }
       copies_commit();
+    }
+  };
+  using WT = std::conditional_t<RING, W, float>;
+  Raw<V, WT> w_raw[WREG ? N : 1];
+  char* const w_mine = mine + 2 * K * N * kPlace;
+  if constexpr (RING) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      Raw<V, WT> w;
+      if (i < part.live) w.read(static_cast<const WT*>(q.w) + part.c0 + i * (32 * V));
+      if constexpr (WREG) w_raw[i] = w;
+      else w.keep(w_mine + i * (kWPlaces<V, WT> * kPlace));
+    }
+  }
+  auto read_w = [&](int i, Vec<V>& w) {
+    if constexpr (!RING) {
+      get_w<V, W>(q, q.w, part.c0 + i * (32 * V), w.v);
+    } else if constexpr (WREG) {
+      get<V>(w_raw[i].v, w.v);
+    } else {
+      Raw<V, WT> r;
+      r.fetch(w_mine + i * (kWPlaces<V, WT> * kPlace));
+      get<V>(r.v, w.v);
     }
   };
   Vec<V> acc_w[N], acc_b[DB ? N : 1];
@@ -352,6 +431,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
         }
       }
     }
+    auto normal = [&](const Vec<V>& x) { return MODE == kRms ? x * rv : (x + minus_mean) * rv; };
     auto read = [&](int i, Vec<V>& dy, Vec<V>& x) {
       if constexpr (RING) {
         get<V>(reinterpret_cast<const Y*>(here + i * kPlace), dy.v);
@@ -366,25 +446,25 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
       if (i < part.live) {
         Vec<V> dy, x, w;
         read(i, dy, x);
-        get_w<V, W>(q, q.w, part.c0 + i * (32 * V), w.v);
-        const Vec<V> xh = (x + minus_mean) * rv, t = dy * w;
+        read_w(i, w);
+        const Vec<V> xh = normal(x), t = dy * w;
         acc_w[i] = fma(dy, xh, acc_w[i]);
         if constexpr (DB) acc_b[i] = acc_b[i] + dy;
-        s1 = s1 + t;
+        if (MODE != kRms) s1 = s1 + t;
         s2 = fma(t, xh, s2);
       }
     }
-    const float2 s = row_sum(s2.sum(), s1.sum(), !q.rms, turn);
+    const float2 s = row_sum(s2.sum(), s1.sum(), !rms, turn);
     // dX = r t - xh r mean(t xh) - r mean t + add
     const Vec<V> slope = Vec<V>::all(-r * (s.x * inv_h)),
-                 shift = Vec<V>::all(q.rms ? 0.f : -r * (s.y * inv_h));
+                 shift = Vec<V>::all(rms ? 0.f : -r * (s.y * inv_h));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (i < part.live) {
         Vec<V> dy, x, w;
         read(i, dy, x);
-        get_w<V, W>(q, q.w, part.c0 + i * (32 * V), w.v);
-        Vec<V> d = fma(dy * w, rv, fma((x + minus_mean) * rv, slope, shift));
+        read_w(i, w);
+        Vec<V> d = fma(dy * w, rv, fma(normal(x), slope, shift));
         if (q.add) {
           Vec<V> a;
           if constexpr (RING) get<V>(reinterpret_cast<const X*>(here + (2 * N + i) * kPlace), a.v);
@@ -433,34 +513,33 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
   }
 }
 
-// dW and dB from the partial rows: 32 columns a CTA, 16 rows at a time.
-__global__ void __launch_bounds__(512) norm_dw_kernel(const NormArgs q) {
+// dW and dB from the partial rows: 32 columns a CTA, 32 rows at a time, eight of a thread's loads
+// in flight (608 partial rows of 1031 columns: 4 of them 9.6 us).
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const NormArgs q) {
   wait_prerequisites();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float w = 0.f, b = 0.f;
   if (c < q.H) {
-#pragma unroll 4
-    for (int i = threadIdx.y; i < q.parts; i += 16) {
+#pragma unroll 8
+    for (int i = threadIdx.y; i < q.parts; i += 32) {
       w += q.part_w[(size_t)i * q.H + c];
       if (q.db) b += q.part_b[(size_t)i * q.H + c];
     }
   }
-  __shared__ float2 s[16][32];
+  __shared__ float2 s[32][33];
   s[threadIdx.y][threadIdx.x] = make_float2(w, b);
   __syncthreads();
-  if (threadIdx.y || c >= q.H) return;
-  w = b = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    w += s[i][threadIdx.x].x;
-    b += s[i][threadIdx.x].y;
-  }
+  const float2 t = s[threadIdx.x][threadIdx.y];   // the warp of a column
+  w = warp_sum(t.x);
+  b = warp_sum(t.y);
+  const int column = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x || column >= q.H) return;
   if (q.w_bf16) {
-    store(static_cast<__nv_bfloat16*>(q.dw) + c, w);
-    if (q.db) store(static_cast<__nv_bfloat16*>(q.db) + c, b);
+    store(static_cast<__nv_bfloat16*>(q.dw) + column, w);
+    if (q.db) store(static_cast<__nv_bfloat16*>(q.db) + column, b);
   } else {
-    store(static_cast<float*>(q.dw) + c, w);
-    if (q.db) store(static_cast<float*>(q.db) + c, b);
+    store(static_cast<float*>(q.dw) + column, w);
+    if (q.db) store(static_cast<float*>(q.db) + column, b);
   }
 }
 
@@ -479,14 +558,14 @@ struct Form {
   int stages;
   size_t smem;
 };
-// `threads` a SM is what the registers allow.
+// `more`: places of a thread beyond the ring; `threads` a SM is what the registers allow.
 template <int N, int V, int K>
-Form form(const mok_norm_dims* d, int threads, int most_ctas) {
+Form form(const mok_norm_dims* d, int more, int threads, int most_ctas) {
   Form f{};
   f.bx = ((d->H + N * V - 1) / (N * V) + 31) / 32 * 32;
   f.by = std::max(1u, 256 / f.bx);
   f.stages = V == 1 ? 0 : 2;
-  f.smem = V == 1 ? 0 : (size_t)f.bx * f.by * kPlaces<N, K> * 16;
+  f.smem = V == 1 ? 0 : (size_t)(f.bx * f.by / 32) * (2 * K * N + more) * kPlace;
   int ctas = std::max(1, threads / (int)(f.bx * f.by));
   if (f.smem) ctas = std::max(1, std::min(ctas, (int)(kRingBytes / f.smem)));
   f.grid = (unsigned)std::min<size_t>(((size_t)d->T + f.by - 1) / f.by,
@@ -532,14 +611,15 @@ cudaError_t by_types(const mok_norm_dims* d, F f) {
   return cudaErrorInvalidValue;
 }
 // f(accesses a thread, elements an access, most threads of a CTA, X, Y, W) for the call's types,
-// width and alignment. `vec`: 32 elements a thread (8 for narrow rows) in accesses of 16 bytes of
-// the widest type, through a ring for K tensors; element by element where rows are not aligned, or
-// too wide for the ring.
-template <int K, typename F>
+// width and alignment. `vec`: 32 elements a thread (8 for narrow rows; PER, where a type is fp32)
+// in accesses of 16 bytes of the widest type, through a ring for K tensors; element by element where
+// rows are not aligned, or too wide for the ring and w.
+template <int K, int PER, typename F>
 cudaError_t by_form(const mok_norm_dims* d, bool vec, F f) {
   const bool wide = d->x_type != MOK_OUT_BF16 || d->y_type != MOK_OUT_BF16;
-  const int bx = ((d->H + 31) / 32 + 31) / 32 * 32;
-  if ((size_t)bx * (wide ? kPlaces<8, K> : kPlaces<4, K>) * 16 > kRingBytes) vec = false;
+  // places of 32 elements of each: 4 or 8 accesses of K tensors twice, and of w
+  const int places = (wide ? 8 : 4) * (2 * K + (wide || d->w_type == MOK_OUT_BF16 ? 1 : 2));
+  if ((size_t)((d->H + 1023) / 1024) * places * kPlace > kRingBytes) vec = false;
   if (!vec) {
     if (d->H <= 2048) return by_types<8, 1, 256>(d, f);
     if (d->H <= 8192) return by_types<8, 1, 1024>(d, f);
@@ -547,7 +627,7 @@ cudaError_t by_form(const mok_norm_dims* d, bool vec, F f) {
   }
   if (wide) {
     if (d->H <= 256) return by_types<2, 4, 256>(d, f);
-    if (d->H <= 8192) return by_types<8, 4, 256>(d, f);
+    if (d->H <= 8192) return by_types<PER / 4, 4, 8192 / PER>(d, f);
     return by_types<8, 4, 1024>(d, f);
   }
   if (d->H <= 256) return by_types<1, 8, 256>(d, f);
@@ -584,10 +664,10 @@ extern "C" mok_status mok_norm_fwd(const mok_norm_dims* d, const void* x, const 
   q.stats = reinterpret_cast<float2*>(stats);
   const bool vec = d->H % 8 == 0 && whole(x) && whole(add) && whole(w) && whole(b) && whole(h) &&
                    whole(y);
-  const cudaError_t e = by_form<2>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
+  const cudaError_t e = by_form<2, 32>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
     constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
     constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 6 : 3;
-    const Form f = form<N, V, 2>(d, THREADS * CTAS, INT_MAX);
+    const Form f = form<N, V, 2>(d, 0, THREADS * CTAS, INT_MAX);
     q.stages = f.stages;
     return run(norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type,
                                typename decltype(wt)::type, THREADS, CTAS>,
@@ -620,21 +700,26 @@ extern "C" mok_status mok_norm_bwd(const mok_norm_dims* d, const void* dY, const
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->T) {
     const bool vec = d->H % 8 == 0 && whole(dY) && whole(h) && whole(w) && whole(add) && whole(dX);
-    const cudaError_t e = by_form<3>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
+    const cudaError_t e = by_form<3, 16>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
       constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
-      constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 3 : 2;
+      constexpr int CTAS = THREADS > 256 ? 1 : V == 1 ? 3 : 2;
       using X = typename decltype(xt)::type;
       using Y = typename decltype(yt)::type;
       using W = typename decltype(wt)::type;
-      Form f = form<N, V, 3>(d, THREADS * CTAS, most_parts(d));
-      if (f.by > 1) f.smem = std::max(f.smem, (size_t)d->H * sizeof(float2));   // joins the teams
-      q.stages = f.stages;
-      q.parts = (int)f.grid;
-      if (dB) return run(norm_bwd_kernel<N, V, X, Y, W, true, THREADS, CTAS>, f, q, s);
-      return run(norm_bwd_kernel<N, V, X, Y, W, false, THREADS, CTAS>, f, q, s);
+      auto go = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
+        Form f = form<N, V, 3>(d, w_places<N, V, W>(MODE), THREADS * CTAS, most_parts(d));
+        if (f.by > 1) f.smem = std::max(f.smem, (size_t)d->H * sizeof(float2));   // joins the teams
+        q.stages = f.stages;
+        q.parts = (int)f.grid;
+        return run(norm_bwd_kernel<N, V, X, Y, W, MODE, THREADS, CTAS>, f, q, s);
+      };
+      if (dB) return go(std::integral_constant<int, kBias>{});
+      if (q.rms) return go(std::integral_constant<int, kRms>{});
+      return go(std::integral_constant<int, kMeans>{});
     });
     if (e != cudaSuccess) return MOK_ERR_CUDA;
   }
-  const cudaError_t e = launch(norm_dw_kernel, dim3((d->H + 31) / 32), dim3(32, 16), 0, 1, d->T > 0, s, q);
+  const cudaError_t e = launch(norm_dw_kernel, dim3((d->H + 31) / 32), dim3(32, 32), 0, 1, d->T > 0, s, q);
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
