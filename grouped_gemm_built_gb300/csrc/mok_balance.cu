@@ -4,20 +4,31 @@
 //   losses[1] = z_coef / Tv sum_t lse_t^2
 // With the choices c_s counted first, the loss is a sum over rows: one pass over the logits and
 // no sums over columns, however many sequences there are.
+//
+// Two launches: the choices are counted by a cluster of CTAs per sequence, which joins its counts
+// through distributed shared memory and so needs no zeroed memory and no atomics on it; then a warp
+// per row takes the scores and the product with its sequence's counts. The rows' kernel starts
+// while the choices are still counted and has its first logits by then; its last CTA adds the CTAs'
+// sums in their order.
+#include <climits>
+
 #include "mok_internal.h"
+#include "mok_launch.cuh"
 #include "mok_ops.h"
+#include "mok_ptx.cuh"
 #include "mok_rows.cuh"
 
 namespace mok {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kCountRows = 256;   // rows per CTA that counts
+constexpr int kCountThreads = 1024;
 constexpr int kMaxS = 1 << 20;
+constexpr int kParts = 152 * 8;   // CTAs of the rows' kernels at most
 
 struct Args {
   int T, E, k, S;
-  bool sigmoid, vec, vec_out;
+  bool vec, vec_out;
   float coef, z;             // coef E / k, z_coef
   const int32_t* idx;
   const int32_t* seqs;
@@ -25,103 +36,133 @@ struct Args {
   int32_t* counts;           // [E]
   float* losses;
   double2* part;             // one per CTA of the forward
+  unsigned* ticket;          // CTAs of the forward that are done
   const float* dlosses;
   int rows;                  // rows per CTA
 };
 
-// The last sequence that begins at or before row t (-1: none, S: behind the last).
+// The last sequence that begins at or before row t (-1: none, S: behind the last), by a whole warp:
+// 32 offsets at a time.
 __device__ __forceinline__ int find_sequence(const Args& q, int t) {
   if (!q.seqs) return 0;
-  int lo = -1, hi = q.S + 1;
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (q.seqs[mid] <= t) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = q.S + 1;   // the first offset above t lies in [lo, hi]
+  while (true) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const int below = __popc(__ballot_sync(kAll, i < hi && q.seqs[min(i, q.S)] <= t));
+    if (below == 0) return lo - 1;
+    lo += (below - 1) * step + 1;
+    hi = min(hi, lo + step - 1);
+    if (lo >= hi) return lo - 1;
   }
-  return lo;
 }
 
-__global__ void count_kernel(const Args q) {
+// Counts of the choices of one sequence by a cluster. Rank r takes the r-th share of the ids.
+__global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int ctas) {
+  launch_dependents();
   __shared__ int32_t hist[512];
-  for (int e = threadIdx.x; e < q.E; e += blockDim.x) hist[e] = 0;
-  const long long first = (long long)blockIdx.x * kCountRows;
-  const int end = (int)min(first + kCountRows, (long long)q.T);
-  __syncthreads();
-  for (int a = (int)first; a < end;) {
-    const int s = find_sequence(q, a);
-    int b = end;
-    if (q.seqs && s < q.S) b = max(a + 1, min(end, q.seqs[s + 1]));
-    if (s >= 0 && s < q.S) {
-      for (int i = threadIdx.x; i < (b - a) * q.k; i += blockDim.x) {
-        const int e = q.idx[(size_t)a * q.k + i];
-        if (e >= 0 && e < q.E) atomicAdd(&hist[e], 1);
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < q.E; e += blockDim.x) {
-        const int c = hist[e];
-        if (c) {
-          atomicAdd(&q.seq_counts[(size_t)s * q.E + e], c);   // integers: any order, one result
-          atomicAdd(&q.counts[e], c);
-        }
-        hist[e] = 0;
-      }
-      __syncthreads();
-    }
-    a = b;
+  const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  for (int e = threadIdx.x; e < 512; e += kCountThreads) hist[e] = 0;
+  int begin = 0, end = q.T;
+  if (q.seqs) {   // offsets outside the batch are cut off
+    begin = max(q.seqs[s], 0);
+    end = min(q.seqs[s + 1], q.T);
   }
+  __syncthreads();
+  if (end > begin) {
+    const size_t first = (size_t)begin * q.k, n = (size_t)(end - begin) * q.k;
+    const size_t lo = first + n * rank / ctas, hi = first + n * (rank + 1) / ctas;
+    auto count = [&](int e) {
+      if (e >= 0 && e < q.E) atomicAdd(&hist[e], 1);
+    };
+    // whole groups of four, and the ids before and behind them
+    const size_t a = min((lo + 3) & ~(size_t)3, hi), b = max(hi & ~(size_t)3, a);
+    if ((reinterpret_cast<uintptr_t>(q.idx) & 15) == 0) {
+      if (lo + threadIdx.x < a) count(q.idx[lo + threadIdx.x]);
+      if (b + threadIdx.x < hi) count(q.idx[b + threadIdx.x]);
+      const int4* v = reinterpret_cast<const int4*>(q.idx);
+#pragma unroll 8
+      for (size_t i = a / 4 + threadIdx.x; i < b / 4; i += kCountThreads) {
+        const int4 x = v[i];
+        count(x.x), count(x.y), count(x.z), count(x.w);
+      }
+    } else {
+#pragma unroll 8
+      for (size_t i = lo + threadIdx.x; i < hi; i += kCountThreads) count(q.idx[i]);
+    }
+  }
+  if (ctas > 1) cluster_sync_all();
+  else __syncthreads();
+  // the ranks' counts of a share of the experts each
+  for (int e = rank + threadIdx.x * ctas; e < q.E; e += kCountThreads * ctas) {
+    int c = 0;
+    for (int r = 0; r < ctas; ++r) {
+      int x = hist[e];
+      if (ctas > 1)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(mapa_rank(&hist[e], r)) : "memory");
+      c += x;
+    }
+    q.seq_counts[(size_t)s * q.E + e] = c;
+    if (s == 0) q.counts[e] = q.S == 1 ? c : 0;   // several: the rows' kernel adds them up
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *q.ticket = 0;
+    if (q.T == 0) q.losses[0] = q.losses[1] = 0.f;
+  }
+  if (ctas > 1) cluster_sync_all();   // nobody leaves while its counts are read
 }
 
-// A row's scores. In: cleaned logits (-inf past E). Out: p, and soft, lse where `z` is needed.
+constexpr float kLog2e = 1.44269504f;
+
+__device__ __forceinline__ float exp2_fast(float t) {   // 2^t to 2 ulp, 0 below 2^-126
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return e;
+}
+__device__ __forceinline__ float inverse(float x) {     // to 1 ulp; 0 above 2^126
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// e^x of NV values, x clamped to +-200 (NaN: the lower limit). One product x log2 e would leave
+// an error of |x| / 2 ulp; what its rounding cut off comes back as a factor.
 template <int NV>
-struct RowScores {
-  float p[NV], slope[NV], soft[NV], lse;
-  __device__ __forceinline__ void make(const float* l, bool is_sigmoid, bool z, bool gradient) {
-    float m = l[0];
+__device__ __forceinline__ Vec<NV> exp_vec(Vec<NV> x) {
 #pragma unroll
-    for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
-    lse = 0.f;
-    if (m == -INFINITY) {
+  for (int i = 0; i < NV; ++i) x.v[i] = fminf(fmaxf(x.v[i], -200.f), 200.f);
+  const Vec<NV> k = Vec<NV>::all(kLog2e), t = x * k;
+  const Vec<NV> cut = fma(x, k, t * Vec<NV>::all(-1.f)) * Vec<NV>::all(0.693147182f);
+  Vec<NV> e;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) p[i] = slope[i] = soft[i] = 0.f;
-      return;
-    }
-    if (!is_sigmoid || z) {
-      float sum = 0.f;
+  for (int i = 0; i < NV; ++i) e.v[i] = exp2_fast(t.v[i]);
+  return fma(e, cut, e);
+}
+
+// a and b summed over the warp: the lower half goes on with a, the upper with b.
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+  const bool low = (threadIdx.x & 16) == 0;
+  const float other = __shfl_xor_sync(kAll, low ? b : a, 16);
+  a = (low ? a : b) + other;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        soft[i] = expf(l[i] - m);
-        sum += soft[i];
-      }
-      sum = warp_sum(sum);
-      lse = m + logf(sum);
-      const float inv = 1.f / sum;
+  for (int off = 8; off > 0; off >>= 1) a += __shfl_xor_sync(kAll, a, off);
+  return make_float2(__shfl_sync(kAll, a, 0), __shfl_sync(kAll, a, 16));
+}
+
+// The largest logit of the warp's row, as the rule reads it: NaN is none, +inf becomes the largest
+// finite value, also in l.
+template <int NV>
+__device__ __forceinline__ float row_max(Vec<NV>& l) {
+  float m = l.v[0];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) soft[i] *= inv;
-    }
-    if (!is_sigmoid) {
+  for (int i = 1; i < NV; ++i) m = fmaxf(m, l.v[i]);
+  m = warp_max(m == m ? m : -INFINITY);
+  if (m == INFINITY) {
+    m = FLT_MAX;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) p[i] = slope[i] = soft[i];
-      return;
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      // below -17, 1 + e^l is 1 in fp32 and sigmoid(l) is e^l: relative to the largest, as
-      // their sum would underflow
-      p[i] = m > -17.f ? sigmoid(l[i]) : expf(l[i] - m);
-      if (l[i] == -INFINITY) p[i] = 0.f;
-      sum += p[i];
-    }
-    sum = warp_sum(sum);
-    const float inv = 1.f / sum;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      p[i] *= inv;
-      slope[i] = gradient && p[i] > 0.f ? p[i] * sigmoid(-l[i]) : 0.f;
-    }
+    for (int i = 0; i < NV; ++i) l.v[i] = fminf(l.v[i], FLT_MAX);
   }
-};
+  return m;
+}
 
 // What the rows of one sequence share, held by a warp while it stays in the sequence.
 template <int NV>
@@ -129,52 +170,98 @@ struct Sequence {
   int s = -2, end = 0;        // rows up to `end` belong to it
   bool live = false;
   float factor = 0.f;
-  int32_t c[NV];
-  __device__ __forceinline__ void move_to(const Args& q, int t, int e0, int tv) {
-    if (s != -2 && t < end) return;
+  // Whether row t begins another sequence; its counts are then the caller's to load.
+  __device__ __forceinline__ bool move_to(const Args& q, int t, int tv) {
+    if (s != -2 && t < end) return false;
     s = find_sequence(q, t);
     const int begin = !q.seqs ? 0 : s >= 0 ? q.seqs[s] : 0;
     end = !q.seqs || s >= q.S ? q.T : q.seqs[s + 1];
     live = s >= 0 && s < q.S && end > begin && tv > 0;
-    if (!live) return;
-    factor = q.coef / ((float)(end - begin) * (float)tv);
-    load_counts(q, e0);
-  }
-  __device__ __forceinline__ void load_counts(const Args& q, int e0) {
-    const int32_t* row = q.seq_counts + (size_t)s * q.E;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) c[i] = e0 + i < q.E ? row[e0 + i] : 0;
+    factor = live ? q.coef / ((float)(end - begin) * (float)tv) : 0.f;
+    return live;
   }
 };
-
+template <int NV>
+__device__ __forceinline__ void load_counts(const Args& q, int s, int e0, int32_t* c) {
+  const int32_t* row = q.seq_counts + (size_t)s * q.E;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) c[i] = e0 + i < q.E ? row[e0 + i] : 0;
+}
 __device__ __forceinline__ int valid_rows(const Args& q) {
   return q.seqs ? q.seqs[q.S] - q.seqs[0] : q.T;
 }
-
 template <int NV, typename LT>
+__device__ __forceinline__ void load_logits(const Args& q, const LT* logits, long long t, int e0, float* l) {
+  load_row<NV>(logits + (size_t)t * q.E, e0, q.E, q.vec, -INFINITY, l);
+}
+
+// Sigmoid scores whose sum is below this are taken relative to the largest logit: there each is e^l
+// to 32 bits, and the smallest would underflow.
+constexpr float kTiny = 1e-20f;
+
+// One product with log2 e: an exponential is off by up to |x| / 2 ulp, which the loss, a sum in which
+// the largest scores weigh most, does not show.
+template <int NV, bool SIGMOID, typename LT>
 __global__ void __launch_bounds__(32 * kWarps) loss_kernel(const Args q, const LT* logits) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * NV;
   const long long first = (long long)blockIdx.x * q.rows;
   const int end = (int)min(first + q.rows, (long long)q.T);
+  Vec<NV> next;
+  if (first + warp < end) load_logits<NV>(q, logits, first + warp, e0, next.v);
   const int tv = valid_rows(q);
   Sequence<NV> seq;
-  double sum = 0., sum_z = 0.;
-  for (long long t = first + warp; t < end; t += kWarps) {
-    seq.move_to(q, (int)t, e0, tv);
+  if (first + warp < end) seq.move_to(q, (int)first + warp, tv);
+  bool fresh = seq.live;
+  wait_prerequisites();
+  // with several sequences, this CTA's share of them into the counts of all
+  if (q.S > 1) {
+    for (int s = blockIdx.x; s < q.S; s += gridDim.x) {
+      for (int e = threadIdx.x; e < q.E; e += 32 * kWarps) {
+        const int c = q.seq_counts[(size_t)s * q.E + e];
+        if (c) atomicAdd(&q.counts[e], c);   // integers: any order, one result
+      }
+    }
+  }
+  float sum = 0.f, sum_z = 0.f;
+  Vec<NV> c;
+  for (int t = (int)first + warp; t < end; t += kWarps) {
+    Vec<NV> l = next;
+    if (end - t > kWarps) load_logits<NV>(q, logits, t + kWarps, e0, next.v);
+    fresh |= seq.move_to(q, t, tv);
     if (!seq.live) continue;
-    float l[NV];
-    load_row<NV>(logits + (size_t)t * q.E, e0, q.E, q.vec, -INFINITY, l);
+    if (fresh) {
+      int32_t n[NV];
+      load_counts<NV>(q, seq.s, e0, n);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = clean(l[i]);
-    RowScores<NV> r;
-    r.make(l, q.sigmoid, q.z > 0.f, false);
-    float dot = 0.f;
+      for (int i = 0; i < NV; ++i) c.v[i] = (float)n[i];
+      fresh = false;
+    }
+    float2 w;        // sum of the scores, their product with the counts
+    bool tiny = false;
+    if constexpr (SIGMOID) {
+      const Vec<NV> x = l * Vec<NV>::all(-kLog2e);
+      Vec<NV> p;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) dot += r.p[i] * (float)seq.c[i];
-    sum += (double)(seq.factor * warp_sum(dot));
-    sum_z += (double)(r.lse * r.lse);
+      for (int i = 0; i < NV; ++i) p.v[i] = inverse(1.f + exp2_fast(fminf(x.v[i], 200.f)));
+      w = warp_sum2(p.sum(), dot(p, c));
+      tiny = w.x < kTiny;
+    }
+    if (!SIGMOID || tiny || q.z > 0.f) {
+      const float m = row_max<NV>(l);
+      if (m == -INFINITY) continue;
+      const Vec<NV> x = (l + Vec<NV>::all(-m)) * Vec<NV>::all(kLog2e);
+      Vec<NV> p;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) p.v[i] = exp2_fast(fmaxf(x.v[i], -200.f));
+      const float2 v = warp_sum2(p.sum(), dot(p, c));
+      if (!SIGMOID || tiny) w = v;
+      const float lse = m + __logf(v.x);
+      sum_z = fmaf(lse, lse, sum_z);
+    }
+    sum += seq.factor * __fdividef(w.y, w.x);
   }
   __shared__ double2 s[kWarps];
+  __shared__ bool last;
   if (lane == 0) s[warp] = make_double2(sum, sum_z);
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -184,84 +271,100 @@ __global__ void __launch_bounds__(32 * kWarps) loss_kernel(const Args q, const L
       t.y += s[i].y;
     }
     q.part[blockIdx.x] = t;
+    __threadfence();
+    last = atomicAdd(q.ticket, 1u) + 1 == gridDim.x;
   }
-}
-
-__global__ void loss_sum_kernel(const Args q, int parts) {
-  __shared__ double2 s[256];
-  double2 t = make_double2(0., 0.);
-  for (int i = threadIdx.x; i < parts; i += 256) {
-    t.x += q.part[i].x;
-    t.y += q.part[i].y;
-  }
-  s[threadIdx.x] = t;
   __syncthreads();
-  for (int n = 128; n > 0; n >>= 1) {
-    if (threadIdx.x < n) {
-      s[threadIdx.x].x += s[threadIdx.x + n].x;
-      s[threadIdx.x].y += s[threadIdx.x + n].y;
-    }
-    __syncthreads();
+  if (!last) return;
+  // the last CTA: everyone's sums, in their order
+  __threadfence();
+  double2 t = make_double2(0., 0.);
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += 32 * kWarps) {
+    t.x += __ldcg(&q.part[i].x);
+    t.y += __ldcg(&q.part[i].y);
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    t.x += __shfl_xor_sync(kAll, t.x, off);
+    t.y += __shfl_xor_sync(kAll, t.y, off);
+  }
+  if (lane == 0) s[warp] = t;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    const int tv = valid_rows(q);
-    q.losses[0] = (float)s[0].x;
-    q.losses[1] = tv > 0 && q.z > 0.f ? (float)(s[0].y * q.z / tv) : 0.f;
+    t = make_double2(0., 0.);
+    for (int i = 0; i < kWarps; ++i) {
+      t.x += s[i].x;
+      t.y += s[i].y;
+    }
+    q.losses[0] = (float)t.x;
+    q.losses[1] = tv > 0 && q.z > 0.f ? (float)(t.y * q.z / tv) : 0.f;
   }
 }
 
-template <int NV, typename LT, typename DT>
+// softmax  p_e (u_e - p.u + 2 z / Tv lse);  sigmoid  p_e (1 - s_e) (u_e - p.u), the penalty apart
+template <int NV, bool SIGMOID, typename LT, typename DT>
 __global__ void __launch_bounds__(32 * kWarps)
     balance_bwd_kernel(const Args q, const LT* logits, const DT* add, DT* dlogits) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * NV;
   const long long first = (long long)blockIdx.x * q.rows;
   const int end = (int)min(first + q.rows, (long long)q.T);
+  Vec<NV> next, next_add = Vec<NV>::all(0.f);
+  auto load_next = [&](long long t) {
+    load_logits<NV>(q, logits, t, e0, next.v);
+    if (add) load_row<NV>(add + (size_t)t * q.E, e0, q.E, q.vec_out, 0.f, next_add.v);
+  };
+  if (first + warp < end) load_next(first + warp);
   const int tv = valid_rows(q);
   const float d0 = q.dlosses ? q.dlosses[0] : 1.f, d1 = q.dlosses ? q.dlosses[1] : 1.f;
   const float fz = q.z > 0.f && tv > 0 ? 2.f * q.z / (float)tv * d1 : 0.f;
   Sequence<NV> seq;
-  float u[NV];
-  int of = -2;
-  for (long long t = first + warp; t < end; t += kWarps) {
-    seq.move_to(q, (int)t, e0, tv);
-    float d[NV];
+  Vec<NV> u;
+  for (int t = (int)first + warp; t < end; t += kWarps) {
+    Vec<NV> l = next, d = next_add;
+    if (end - t > kWarps) load_next(t + kWarps);
+    if (seq.move_to(q, t, tv)) {
+      // counts relative to their mean, an integer: sum_e p_e = 1, so the gradient is the same,
+      // without the cancellation of nearly even counts
+      int32_t c[NV];
+      load_counts<NV>(q, seq.s, e0, c);
+      int total = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) d[i] = 0.f;
-    if (add) load_row<NV>(add + (size_t)t * q.E, e0, q.E, q.vec_out, 0.f, d);
-    if (seq.live) {
-      if (of != seq.s) {
-        // counts relative to their mean, an integer: sum_e p_e = 1, so the gradient is the same,
-        // without the cancellation of nearly even counts
-        int total = 0;
+      for (int i = 0; i < NV; ++i) total += c[i];
+      const int mean = __reduce_add_sync(kAll, total) / q.E;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) total += seq.c[i];
-        total = __reduce_add_sync(kAll, total);
-        const int mean = total / q.E;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) u[i] = (float)(seq.c[i] - mean) * (seq.factor * d0);
-        of = seq.s;
-      }
-      float l[NV];
-      load_row<NV>(logits + (size_t)t * q.E, e0, q.E, q.vec, -INFINITY, l);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) l[i] = clean(l[i]);
-      RowScores<NV> r;
-      r.make(l, q.sigmoid, fz != 0.f, true);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) dot += r.p[i] * u[i];
-      dot = warp_sum(dot);
+      for (int i = 0; i < NV; ++i) u.v[i] = (float)(c[i] - mean) * (seq.factor * d0);
+    }
+    bool tiny = false;
+    if (SIGMOID && seq.live) {
+      Vec<NV> e = exp_vec<NV>(l * Vec<NV>::all(-1.f)), p;   // e^-l, at most e^88
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        d[i] += r.slope[i] * (u[i] - dot);
-        if (fz != 0.f) d[i] += fz * r.lse * r.soft[i];
+        e.v[i] = l.v[i] > -88.f ? e.v[i] : FLT_MAX;   // and masked: a score of 0
+        p.v[i] = inverse(1.f + e.v[i]);
+      }
+      const float2 w = warp_sum2(p.sum(), dot(p, u));
+      tiny = w.x < kTiny;
+      if (!tiny) {
+        const float inv = 1.f / w.x;
+        // sigmoid (1 - sigmoid) = (e^-l sigmoid) sigmoid
+        d = fma((e * p) * (p * Vec<NV>::all(inv)), u + Vec<NV>::all(-w.y * inv), d);
       }
     }
-    store_row<NV>(dlogits + (size_t)t * q.E, e0, q.E, q.vec_out, d);
+    if (seq.live && (!SIGMOID || tiny || fz != 0.f)) {
+      const float m = row_max<NV>(l);
+      if (m > -INFINITY) {
+        const Vec<NV> p = exp_vec<NV>(l + Vec<NV>::all(-m));
+        const float2 w = warp_sum2(p.sum(), dot(p, u));
+        const float inv = 1.f / w.x;
+        const float shift = fz != 0.f ? fz * (m + logf(w.x)) : 0.f;
+        const Vec<NV> scores = p * Vec<NV>::all(inv);
+        if (!SIGMOID || tiny) d = fma(scores, u + Vec<NV>::all(shift - w.y * inv), d);
+        else d = fma(scores, Vec<NV>::all(shift), d);
+      }
+    }
+    store_row<NV>(dlogits + (size_t)t * q.E, e0, q.E, q.vec_out, d.v);
   }
 }
-
-constexpr int kParts = 152 * 8;
 
 bool make_args(const mok_balance* r, int T, int S, Args* q) {
   if (!r || T < 0 || S < 1 || S > kMaxS) return false;
@@ -271,7 +374,6 @@ bool make_args(const mok_balance* r, int T, int S, Args* q) {
     return false;
   *q = Args{};
   q->T = T; q->E = r->E; q->k = r->k; q->S = S;
-  q->sigmoid = r->score == MOK_SCORE_SIGMOID;
   q->coef = (float)((double)r->coef * r->E / r->k);
   q->z = r->z_coef;
   // rows per CTA: whole rounds of its warps, at most kParts CTAs
@@ -290,7 +392,7 @@ extern "C" mok_status mok_balance_get_sizes(const mok_balance* rule, int T, int 
   using namespace mok;
   Args q;
   if (!make_args(rule, T, S, &q) || !saved_bytes) return MOK_ERR_INVALID_ARG;
-  *saved_bytes = counts_bytes(rule, S) + kParts * sizeof(double2);
+  *saved_bytes = counts_bytes(rule, S) + kParts * sizeof(double2) + 256;
   return MOK_OK;
 }
 
@@ -310,24 +412,31 @@ extern "C" mok_status mok_balance_fwd(const mok_balance* rule, int T, const void
   q.idx = topk_idx; q.seqs = seqs; q.counts = counts; q.losses = losses;
   q.seq_counts = static_cast<int32_t*>(saved);
   q.part = reinterpret_cast<double2*>(static_cast<char*>(saved) + counts_bytes(rule, S));
+  q.ticket = reinterpret_cast<unsigned*>(q.part + kParts);
   q.vec = rows_vectorize(q.E, logits, logits_type);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(saved, 0, (size_t)S * q.E * 4, s) != cudaSuccess) return MOK_ERR_CUDA;
-  if (cudaMemsetAsync(counts, 0, (size_t)q.E * 4, s) != cudaSuccess) return MOK_ERR_CUDA;
-  unsigned parts = 0;
+  // a sequence's CTAs: eight, but one where sequences are short or many
+  const int ctas = (long long)T / S * q.k >= 4096 && S <= 4096 ? 8 : 1;
+  cudaError_t e = launch(count_kernel, dim3((unsigned)S * ctas), dim3(kCountThreads), 0, ctas, false, s,
+                         q, ctas);
+  if (e != cudaSuccess) return MOK_ERR_CUDA;
   if (T > 0) {
-    count_kernel<<<((unsigned)T + kCountRows - 1) / kCountRows, 256, 0, s>>>(q);
-    parts = ((unsigned)T + q.rows - 1) / q.rows;
+    const unsigned parts = ((unsigned)T + q.rows - 1) / q.rows;
     by_width(q.E, [&](auto nv) {
       constexpr int NV = decltype(nv)::value;
-      if (logits_type == MOK_OUT_BF16)
-        loss_kernel<NV><<<parts, 32 * kWarps, 0, s>>>(q, static_cast<const __nv_bfloat16*>(logits));
-      else
-        loss_kernel<NV><<<parts, 32 * kWarps, 0, s>>>(q, static_cast<const float*>(logits));
+      auto go = [&](auto kernel, auto* l) {
+        e = launch(kernel, dim3(parts), dim3(32 * kWarps), 0, 1, true, s, q, l);
+      };
+      const auto* lb = static_cast<const __nv_bfloat16*>(logits);
+      const auto* lf = static_cast<const float*>(logits);
+      const bool sg = rule->score == MOK_SCORE_SIGMOID, b = logits_type == MOK_OUT_BF16;
+      if (sg && b) go(loss_kernel<NV, true, __nv_bfloat16>, lb);
+      else if (sg) go(loss_kernel<NV, true, float>, lf);
+      else if (b) go(loss_kernel<NV, false, __nv_bfloat16>, lb);
+      else go(loss_kernel<NV, false, float>, lf);
     });
   }
-  loss_sum_kernel<<<1, 256, 0, s>>>(q, (int)parts);
-  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
 
 extern "C" mok_status mok_balance_bwd(const mok_balance* rule, int T, const void* logits,
@@ -358,8 +467,10 @@ extern "C" mok_status mok_balance_bwd(const mok_balance* rule, int T, const void
     auto go = [&](auto lt, auto dt) {
       using LT = decltype(lt);
       using DT = decltype(dt);
-      balance_bwd_kernel<NV><<<ctas, 32 * kWarps, 0, s>>>(
-          q, static_cast<const LT*>(logits), static_cast<const DT*>(add), static_cast<DT*>(dlogits));
+      auto* kernel = rule->score == MOK_SCORE_SIGMOID ? balance_bwd_kernel<NV, true, LT, DT>
+                                                      : balance_bwd_kernel<NV, false, LT, DT>;
+      kernel<<<ctas, 32 * kWarps, 0, s>>>(q, static_cast<const LT*>(logits),
+                                          static_cast<const DT*>(add), static_cast<DT*>(dlogits));
     };
     const bool lb = logits_type == MOK_OUT_BF16, db = dlogits_type == MOK_OUT_BF16;
     if (lb && db) go(__nv_bfloat16{}, __nv_bfloat16{});

@@ -116,50 +116,6 @@ constexpr int w_places(int mode) {
   else return keeps_w<V, W>(mode) ? 0 : N * kWPlaces<V, W>;
 }
 
-// V elements at a time, in pairs: one instruction does two fp32 operations, each rounded as usual.
-template <int V>
-struct Vec {
-  float v[V];
-  static __device__ __forceinline__ Vec all(float x) {
-    Vec o;
-#pragma unroll
-    for (int j = 0; j < V; ++j) o.v[j] = x;
-    return o;
-  }
-  __device__ __forceinline__ float2 pair(int j) const { return make_float2(v[j], v[j + 1]); }
-  __device__ __forceinline__ void set(int j, float2 p) { v[j] = p.x; v[j + 1] = p.y; }
-  __device__ __forceinline__ float sum() const {
-    float t = v[0];
-#pragma unroll
-    for (int j = 1; j < V; ++j) t += v[j];
-    return t;
-  }
-};
-template <int V>
-__device__ __forceinline__ Vec<V> operator+(const Vec<V>& a, const Vec<V>& b) {
-  Vec<V> o;
-  if constexpr (V == 1) o.v[0] = a.v[0] + b.v[0];
-#pragma unroll
-  for (int j = 0; j + 1 < V; j += 2) o.set(j, __fadd2_rn(a.pair(j), b.pair(j)));
-  return o;
-}
-template <int V>
-__device__ __forceinline__ Vec<V> operator*(const Vec<V>& a, const Vec<V>& b) {
-  Vec<V> o;
-  if constexpr (V == 1) o.v[0] = a.v[0] * b.v[0];
-#pragma unroll
-  for (int j = 0; j + 1 < V; j += 2) o.set(j, __fmul2_rn(a.pair(j), b.pair(j)));
-  return o;
-}
-template <int V>
-__device__ __forceinline__ Vec<V> fma(const Vec<V>& a, const Vec<V>& b, const Vec<V>& c) {
-  Vec<V> o;
-  if constexpr (V == 1) o.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
-#pragma unroll
-  for (int j = 0; j + 1 < V; j += 2) o.set(j, __ffma2_rn(a.pair(j), b.pair(j), c.pair(j)));
-  return o;
-}
-
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
   if constexpr (BYTES == 16)

@@ -51,6 +51,59 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// V elements at a time, in pairs: one instruction does two fp32 operations, each rounded as usual.
+template <int V>
+struct Vec {
+  float v[V];
+  static __device__ __forceinline__ Vec all(float x) {
+    Vec o;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o.v[j] = x;
+    return o;
+  }
+  __device__ __forceinline__ float2 pair(int j) const { return make_float2(v[j], v[(j + 1) % V]); }
+  __device__ __forceinline__ void set(int j, float2 p) { v[j] = p.x; v[(j + 1) % V] = p.y; }
+  __device__ __forceinline__ float sum() const {
+    if constexpr (V == 1) return v[0];
+    float2 t = pair(0);
+#pragma unroll
+    for (int j = 2; j + 1 < V; j += 2) t = __fadd2_rn(t, pair(j));
+    return t.x + t.y;
+  }
+};
+template <int V>
+__device__ __forceinline__ Vec<V> operator+(const Vec<V>& a, const Vec<V>& b) {
+  Vec<V> o;
+  if constexpr (V == 1) o.v[0] = a.v[0] + b.v[0];
+#pragma unroll
+  for (int j = 0; j + 1 < V; j += 2) o.set(j, __fadd2_rn(a.pair(j), b.pair(j)));
+  return o;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> operator*(const Vec<V>& a, const Vec<V>& b) {
+  Vec<V> o;
+  if constexpr (V == 1) o.v[0] = a.v[0] * b.v[0];
+#pragma unroll
+  for (int j = 0; j + 1 < V; j += 2) o.set(j, __fmul2_rn(a.pair(j), b.pair(j)));
+  return o;
+}
+template <int V>
+__device__ __forceinline__ float dot(const Vec<V>& a, const Vec<V>& b) {
+  if constexpr (V == 1) return a.v[0] * b.v[0];
+  float2 t = __fmul2_rn(a.pair(0), b.pair(0));
+#pragma unroll
+  for (int j = 2; j + 1 < V; j += 2) t = __ffma2_rn(a.pair(j), b.pair(j), t);
+  return t.x + t.y;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> fma(const Vec<V>& a, const Vec<V>& b, const Vec<V>& c) {
+  Vec<V> o;
+  if constexpr (V == 1) o.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
+#pragma unroll
+  for (int j = 0; j + 1 < V; j += 2) o.set(j, __ffma2_rn(a.pair(j), b.pair(j), c.pair(j)));
+  return o;
+}
+
 // A logit as the rule reads it: NaN masks like -inf, +inf is the largest finite value.
 __device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
