@@ -24,7 +24,13 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kCountThreads = 1024;
 constexpr int kMaxS = 1 << 20;
-constexpr int kParts = 152 * 8;   // CTAs of the rows' kernels at most
+constexpr int kSmallCtas = 8, kSmallWarps = 16, kSmallIds = 8192;
+constexpr int kGroups = 16;        // clusters that count one sequence at most
+constexpr int kSms = 152;
+constexpr int kLossCtas = 4;       // CTAs a SM
+constexpr int kParts = kSms * kLossCtas;
+template <int NV, bool SIGMOID>       // ... and of the backward: what the registers allow
+constexpr int kBwdCtas = NV <= 8 ? (SIGMOID ? 3 : 4) : NV <= 12 && !SIGMOID ? 3 : 2;
 
 struct Args {
   int T, E, k, S;
@@ -35,33 +41,21 @@ struct Args {
   int32_t* seq_counts;       // [S][E]
   int32_t* counts;           // [E]
   float* losses;
-  double2* part;             // one per CTA of the forward
+  int32_t* group_counts;     // [groups][E]: one sequence's counts, by several clusters
+  int groups;
+  float2* part;              // one per CTA of the forward
   unsigned* ticket;          // CTAs of the forward that are done
   const float* dlosses;
   int rows;                  // rows per CTA
 };
 
-// The last sequence that begins at or before row t (-1: none, S: behind the last), by a whole warp:
-// 32 offsets at a time.
-__device__ __forceinline__ int find_sequence(const Args& q, int t) {
-  if (!q.seqs) return 0;
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = q.S + 1;   // the first offset above t lies in [lo, hi]
-  while (true) {
-    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const int below = __popc(__ballot_sync(kAll, i < hi && q.seqs[min(i, q.S)] <= t));
-    if (below == 0) return lo - 1;
-    lo += (below - 1) * step + 1;
-    hi = min(hi, lo + step - 1);
-    if (lo >= hi) return lo - 1;
-  }
-}
-
-// Counts of the choices of one sequence by a cluster. Rank r takes the r-th share of the ids.
+// Counts of the choices of one sequence by a cluster, whose CTAs take a share of the ids each; a long
+// batch that is one sequence is shared by `groups` clusters, whose counts the rows' kernel adds up.
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int ctas) {
   launch_dependents();
   __shared__ int32_t hist[512];
-  const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int s = q.groups > 1 ? 0 : blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int share = q.groups > 1 ? blockIdx.x : rank, shares = q.groups * ctas;
   for (int e = threadIdx.x; e < 512; e += kCountThreads) hist[e] = 0;
   int begin = 0, end = q.T;
   if (q.seqs) {   // offsets outside the batch are cut off
@@ -71,7 +65,7 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int 
   __syncthreads();
   if (end > begin) {
     const size_t first = (size_t)begin * q.k, n = (size_t)(end - begin) * q.k;
-    const size_t lo = first + n * rank / ctas, hi = first + n * (rank + 1) / ctas;
+    const size_t lo = first + n * share / shares, hi = first + n * (share + 1) / shares;
     auto count = [&](int e) {
       if (e >= 0 && e < q.E) atomicAdd(&hist[e], 1);
     };
@@ -102,8 +96,12 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int 
         asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(mapa_rank(&hist[e], r)) : "memory");
       c += x;
     }
-    q.seq_counts[(size_t)s * q.E + e] = c;
-    if (s == 0) q.counts[e] = q.S == 1 ? c : 0;   // several: the rows' kernel adds them up
+    if (q.groups > 1) {
+      q.group_counts[blockIdx.x / ctas * q.E + e] = c;
+    } else {
+      q.seq_counts[(size_t)s * q.E + e] = c;
+      if (s == 0) q.counts[e] = q.S == 1 ? c : 0;   // several: the rows' kernel adds them up
+    }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *q.ticket = 0;
@@ -124,17 +122,15 @@ __device__ __forceinline__ float inverse(float x) {     // to 1 ulp; 0 above 2^1
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// e^x of NV values, x clamped to +-200 (NaN: the lower limit). One product x log2 e would leave
-// an error of |x| / 2 ulp; what its rounding cut off comes back as a factor.
+// e^x of NV values. One product x log2 e would leave an error of |x| / 2 ulp; what its rounding cut
+// off comes back as a factor. NaN for infinite x.
 template <int NV>
-__device__ __forceinline__ Vec<NV> exp_vec(Vec<NV> x) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) x.v[i] = fminf(fmaxf(x.v[i], -200.f), 200.f);
-  const Vec<NV> k = Vec<NV>::all(kLog2e), t = x * k;
-  const Vec<NV> cut = fma(x, k, t * Vec<NV>::all(-1.f)) * Vec<NV>::all(0.693147182f);
+__device__ __forceinline__ Vec<NV> exp_vec(const Vec<NV>& x) {
+  const Vec<NV> minus = x * Vec<NV>::all(-kLog2e);
+  const Vec<NV> cut = fma(x, Vec<NV>::all(kLog2e), minus) * Vec<NV>::all(0.693147182f);
   Vec<NV> e;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) e.v[i] = exp2_fast(t.v[i]);
+  for (int i = 0; i < NV; ++i) e.v[i] = exp2_fast(-minus.v[i]);
   return fma(e, cut, e);
 }
 
@@ -148,36 +144,69 @@ __device__ __forceinline__ float2 warp_sum2(float a, float b) {
   return make_float2(__shfl_sync(kAll, a, 0), __shfl_sync(kAll, a, 16));
 }
 
-// The largest logit of the warp's row, as the rule reads it: NaN is none, +inf becomes the largest
-// finite value, also in l.
+// The largest of the warp's cleaned logits; and e^(l - m), at least e^-200, which is 0.
 template <int NV>
-__device__ __forceinline__ float row_max(Vec<NV>& l) {
+__device__ __forceinline__ float row_max(const Vec<NV>& l) {
   float m = l.v[0];
 #pragma unroll
   for (int i = 1; i < NV; ++i) m = fmaxf(m, l.v[i]);
-  m = warp_max(m == m ? m : -INFINITY);
-  if (m == INFINITY) {
-    m = FLT_MAX;
+  return warp_max(m);
+}
+template <int NV>
+__device__ __forceinline__ Vec<NV> exp_below(Vec<NV> l, float m) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) l.v[i] = fminf(l.v[i], FLT_MAX);
-  }
-  return m;
+  for (int i = 0; i < NV; ++i) l.v[i] = fmaxf(l.v[i] - m, -200.f);
+  return exp_vec(l);
 }
 
-// What the rows of one sequence share, held by a warp while it stays in the sequence.
-template <int NV>
+// Where the warp's row lies, and what the rows of its sequence share. Up to 32 offsets stay in the
+// lanes, read once; more are searched 32 at a time.
 struct Sequence {
-  int s = -2, end = 0;        // rows up to `end` belong to it
+  int off;                    // lane i: offset i
+  int s = -2, end = 0;        // rows up to `end` belong to sequence s (-1: before the first, S: behind)
+  int valid;                  // rows of all sequences
   bool live = false;
   float factor = 0.f;
+  __device__ __forceinline__ explicit Sequence(const Args& q) {
+    const int lane = threadIdx.x & 31;
+    off = q.seqs ? q.seqs[min(lane, q.S)] : 0;
+    const int last = !q.seqs ? q.T : q.S < 32 ? __shfl_sync(kAll, off, q.S & 31) : q.seqs[q.S];
+    valid = last - __shfl_sync(kAll, off, 0);
+  }
+  // The number of offsets at or before t, less one.
+  __device__ __forceinline__ int find(const Args& q, int t) const {
+    const int lane = threadIdx.x & 31;
+    if (q.S < 32) return __popc(__ballot_sync(kAll, lane <= q.S && off <= t)) - 1;
+    int lo = 0, hi = q.S + 1;   // the first offset above t lies in [lo, hi]
+    while (true) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const int below = __popc(__ballot_sync(kAll, i < hi && q.seqs[min(i, q.S)] <= t));
+      if (below == 0) return lo - 1;
+      lo += (below - 1) * step + 1;
+      hi = min(hi, lo + step - 1);
+      if (lo >= hi) return lo - 1;
+    }
+  }
   // Whether row t begins another sequence; its counts are then the caller's to load.
-  __device__ __forceinline__ bool move_to(const Args& q, int t, int tv) {
+  __device__ __forceinline__ bool move_to(const Args& q, int t) {
     if (s != -2 && t < end) return false;
-    s = find_sequence(q, t);
-    const int begin = !q.seqs ? 0 : s >= 0 ? q.seqs[s] : 0;
-    end = !q.seqs || s >= q.S ? q.T : q.seqs[s + 1];
-    live = s >= 0 && s < q.S && end > begin && tv > 0;
-    factor = live ? q.coef / ((float)(end - begin) * (float)tv) : 0.f;
+    int begin = 0;
+    if (!q.seqs) {
+      s = 0;
+      end = q.T;
+    } else {
+      s = find(q, t);
+      if (q.S < 32) {
+        begin = __shfl_sync(kAll, off, s & 31);
+        end = __shfl_sync(kAll, off, (s + 1) & 31);
+      } else {
+        begin = q.seqs[max(s, 0)];
+        end = q.seqs[min(s + 1, q.S)];
+      }
+      if (s >= q.S) end = q.T;
+    }
+    live = s >= 0 && s < q.S && end > begin && valid > 0;
+    factor = live ? q.coef / ((float)(end - begin) * (float)valid) : 0.f;
     return live;
   }
 };
@@ -187,30 +216,180 @@ __device__ __forceinline__ void load_counts(const Args& q, int s, int e0, int32_
 #pragma unroll
   for (int i = 0; i < NV; ++i) c[i] = e0 + i < q.E ? row[e0 + i] : 0;
 }
-__device__ __forceinline__ int valid_rows(const Args& q) {
-  return q.seqs ? q.seqs[q.S] - q.seqs[0] : q.T;
-}
-template <int NV, typename LT>
-__device__ __forceinline__ void load_logits(const Args& q, const LT* logits, long long t, int e0, float* l) {
-  load_row<NV>(logits + (size_t)t * q.E, e0, q.E, q.vec, -INFINITY, l);
-}
+// A lane's NV elements of a row as they lie in memory (past the row's end: `fill`'s bits), loaded a
+// row ahead of their use.
+template <int NV, typename T>
+struct RawRow {
+  static constexpr int kBytes = NV * (int)sizeof(T), kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* row, int e0, int E, bool vec, uint32_t fill) {
+    const uint32_t twice = sizeof(T) == 4 ? fill : fill | fill << 16;
+    if constexpr (kBytes % 4 == 0) {
+      if (vec) {
+        if (e0 < E) {
+          constexpr int kWide = kBytes % 16 == 0 ? 4 : kBytes % 8 == 0 ? 2 : 1;
+          using Word = std::conditional_t<kWide == 4, uint4, std::conditional_t<kWide == 2, uint2, uint32_t>>;
+          const Word* from = reinterpret_cast<const Word*>(row + e0);
+#pragma unroll
+          for (int i = 0; i < kWords / kWide; ++i) {
+            const Word x = from[i];
+            if constexpr (kWide == 4) {
+              w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+            } else if constexpr (kWide == 2) {
+              w[2 * i] = x.x; w[2 * i + 1] = x.y;
+            } else {
+              w[i] = x;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) w[i] = twice;
+        }
+        return;
+      }
+    }
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(row);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) w[i] = e0 + i < E ? from[e0 + i] : fill;
+    } else {
+      const uint16_t* from = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t lo = e0 + 2 * i < E ? from[e0 + 2 * i] : fill;
+        const uint32_t hi = 2 * i + 1 < NV && e0 + 2 * i + 1 < E ? from[e0 + 2 * i + 1] : fill;
+        w[i] = lo | hi << 16;
+      }
+    }
+  }
+  __device__ __forceinline__ Vec<NV> values() const {
+    Vec<NV> v;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (sizeof(T) == 4) v.v[i] = __uint_as_float(w[i]);
+      else v.v[i] = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+    return v;
+  }
+};
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t minus_infinity() { return sizeof(T) == 4 ? 0xff800000u : 0xff80u; }
 
-// Sigmoid scores whose sum is below this are taken relative to the largest logit: there each is e^l
-// to 32 bits, and the smallest would underflow.
+// The scores of a row first come straight from its logits, without their maximum: e^l, or sigmoid(l).
+// A sum of them in these bounds says that none overflowed, that what underflowed is below 1e-32 of
+// it, and that no logit was NaN or (in exp_vec's two parts) infinite. Any other row is read again
+// as the rule says: NaN masks, +inf is the largest finite value, softmax scores relative to the
+// largest logit; and sigmoid scores too where all are tiny: there each is e^l to 32 bits.
+__device__ __forceinline__ bool plain_sum(float z) { return z > 1e-6f && z < 1e30f; }
 constexpr float kTiny = 1e-20f;
 
-// One product with log2 e: an exponential is off by up to |x| / 2 ulp, which the loss, a sum in which
-// the largest scores weigh most, does not show.
+template <int NV>
+__device__ __forceinline__ void clean_row(Vec<NV>& l) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) l.v[i] = clean(l.v[i]);
+}
+
+// (sum of the scores, their product with c, log sum e^l) of any row; sum 0 where all is masked.
+template <int NV, bool SIGMOID>
+__device__ __noinline__ float3 careful_sums(Vec<NV> l, Vec<NV> c) {
+  clean_row(l);
+  const float m = row_max(l);
+  if (m == -INFINITY) return make_float3(0.f, 0.f, 0.f);
+  Vec<NV> p = exp_below(l, m);
+  float2 w = warp_sum2(p.sum(), dot(p, c));
+  const float lse = m + logf(w.x);
+  if (SIGMOID && m > -17.f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) p.v[i] = sigmoid(l.v[i]);
+    w = warp_sum2(p.sum(), dot(p, c));
+  }
+  return make_float3(w.x, w.y, lse);
+}
+
+// A row's part of both sums. One product with log2 e here: an exponential is off by up to |l| / 2 ulp,
+// which the loss, a sum in which the largest scores weigh most, does not show.
+template <int NV, bool SIGMOID>
+__device__ __forceinline__ void add_row(const Args& q, const Vec<NV>& l, const Vec<NV>& c, float factor,
+                                        float& sum, float& sum_z) {
+  Vec<NV> p = l * Vec<NV>::all(SIGMOID ? -kLog2e : kLog2e);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) p.v[i] = SIGMOID ? inverse(1.f + exp2_fast(p.v[i])) : exp2_fast(p.v[i]);
+  float2 w = warp_sum2(p.sum(), dot(p, c));   // sum of the scores, their product with the counts
+  float lse = SIGMOID ? 0.f : __logf(w.x);
+  const bool plain = SIGMOID ? w.x > kTiny && w.x < 1e30f : plain_sum(w.x);
+  if (!plain || (SIGMOID && q.z > 0.f)) {
+    const float3 r = careful_sums<NV, SIGMOID>(l, c);
+    if (!(r.x > 0.f)) return;   // nothing unmasked in this row
+    if (!plain) w = make_float2(r.x, r.y);
+    lse = r.z;
+  }
+  sum_z = fmaf(lse, lse, sum_z);
+  sum += factor * __fdividef(w.y, w.x);
+}
+
+// Few rows in one sequence: one launch of one cluster. Every CTA counts all choices by itself and takes
+// its share of the rows; the cluster's sums meet in distributed shared memory.
 template <int NV, bool SIGMOID, typename LT>
-__global__ void __launch_bounds__(32 * kWarps) loss_kernel(const Args q, const LT* logits) {
+__global__ void __launch_bounds__(32 * kSmallWarps) small_loss_kernel(const Args q, const LT* logits) {
+  __shared__ int32_t hist[512];
+  __shared__ float2 s[kSmallWarps], mine;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * NV;
+  const int rank = (int)blockIdx.x, first = rank * kSmallWarps + warp;
+  RawRow<NV, LT> next;
+  auto load = [&](int t) { next.load(logits + (size_t)t * q.E, e0, q.E, q.vec, minus_infinity<LT>()); };
+  if (first < q.T) load(first);
+  for (int e = threadIdx.x; e < 512; e += 32 * kSmallWarps) hist[e] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < q.T * q.k; i += 32 * kSmallWarps) {
+    const int e = q.idx[i];
+    if (e >= 0 && e < q.E) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  for (int e = rank + kSmallCtas * threadIdx.x; e < q.E; e += kSmallCtas * 32 * kSmallWarps)
+    q.counts[e] = q.seq_counts[e] = hist[e];
+  const float factor = q.coef / ((float)q.T * (float)q.T);
+  float sum = 0.f, sum_z = 0.f;
+  Vec<NV> c;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) c.v[i] = e0 + i < q.E ? (float)hist[e0 + i] : 0.f;
+  for (int t = first; t < q.T; t += kSmallCtas * kSmallWarps) {
+    const Vec<NV> l = next.values();
+    if (t + kSmallCtas * kSmallWarps < q.T) load(t + kSmallCtas * kSmallWarps);
+    add_row<NV, SIGMOID>(q, l, c, factor, sum, sum_z);
+  }
+  if (lane == 0) s[warp] = make_float2(sum, sum_z);
+  __syncthreads();
+  if (warp == 0) {
+    const float2 v = lane < kSmallWarps ? s[lane] : make_float2(0.f, 0.f), t = warp_sum2(v.x, v.y);
+    if (lane == 0) mine = t;
+  }
+  cluster_sync_all();
+  if (rank == 0 && warp == 0) {
+    float2 v = make_float2(0.f, 0.f);
+    if (lane < kSmallCtas) {
+      const uint32_t at = mapa_rank(&mine, lane);
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    }
+    v = warp_sum2(v.x, v.y);
+    if (lane == 0) {
+      q.losses[0] = v.x;
+      q.losses[1] = q.z > 0.f ? v.y / (float)q.T * q.z : 0.f;
+    }
+  }
+  cluster_sync_all();   // nobody leaves while its sums are read
+}
+template <int NV, bool SIGMOID, typename LT>
+__global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args q, const LT* logits) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * NV;
   const long long first = (long long)blockIdx.x * q.rows;
   const int end = (int)min(first + q.rows, (long long)q.T);
-  Vec<NV> next;
-  if (first + warp < end) load_logits<NV>(q, logits, first + warp, e0, next.v);
-  const int tv = valid_rows(q);
-  Sequence<NV> seq;
-  if (first + warp < end) seq.move_to(q, (int)first + warp, tv);
+  RawRow<NV, LT> next;
+  const LT* row = logits + (size_t)(first + warp) * q.E;
+  auto load_next = [&] { next.load(row, e0, q.E, q.vec, minus_infinity<LT>()); };
+  if (first + warp < end) load_next();
+  Sequence seq(q);
+  if (first + warp < end) seq.move_to(q, (int)first + warp);
   bool fresh = seq.live;
   wait_prerequisites();
   // with several sequences, this CTA's share of them into the counts of all
@@ -222,107 +401,136 @@ __global__ void __launch_bounds__(32 * kWarps) loss_kernel(const Args q, const L
       }
     }
   }
+  __shared__ int32_t all[512];
+  if (q.groups > 1) {
+    for (int e = threadIdx.x; e < q.E; e += 32 * kWarps) {
+      int n = 0;
+#pragma unroll 4
+      for (int g = 0; g < q.groups; ++g) n += q.group_counts[g * q.E + e];
+      all[e] = n;
+      if (blockIdx.x == 0) q.seq_counts[e] = q.counts[e] = n;
+    }
+    __syncthreads();
+  }
   float sum = 0.f, sum_z = 0.f;
   Vec<NV> c;
   for (int t = (int)first + warp; t < end; t += kWarps) {
-    Vec<NV> l = next;
-    if (end - t > kWarps) load_logits<NV>(q, logits, t + kWarps, e0, next.v);
-    fresh |= seq.move_to(q, t, tv);
+    Vec<NV> l = next.values();
+    row += (size_t)kWarps * q.E;
+    if (end - t > kWarps) load_next();
+    fresh |= seq.move_to(q, t);
     if (!seq.live) continue;
     if (fresh) {
-      int32_t n[NV];
-      load_counts<NV>(q, seq.s, e0, n);
+      const int32_t* n = q.groups > 1 ? all : q.seq_counts + (size_t)seq.s * q.E;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) c.v[i] = (float)n[i];
+      for (int i = 0; i < NV; ++i) c.v[i] = e0 + i < q.E ? (float)n[e0 + i] : 0.f;
       fresh = false;
     }
-    float2 w;        // sum of the scores, their product with the counts
-    bool tiny = false;
-    if constexpr (SIGMOID) {
-      const Vec<NV> x = l * Vec<NV>::all(-kLog2e);
-      Vec<NV> p;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) p.v[i] = inverse(1.f + exp2_fast(fminf(x.v[i], 200.f)));
-      w = warp_sum2(p.sum(), dot(p, c));
-      tiny = w.x < kTiny;
-    }
-    if (!SIGMOID || tiny || q.z > 0.f) {
-      const float m = row_max<NV>(l);
-      if (m == -INFINITY) continue;
-      const Vec<NV> x = (l + Vec<NV>::all(-m)) * Vec<NV>::all(kLog2e);
-      Vec<NV> p;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) p.v[i] = exp2_fast(fmaxf(x.v[i], -200.f));
-      const float2 v = warp_sum2(p.sum(), dot(p, c));
-      if (!SIGMOID || tiny) w = v;
-      const float lse = m + __logf(v.x);
-      sum_z = fmaf(lse, lse, sum_z);
-    }
-    sum += seq.factor * __fdividef(w.y, w.x);
+    add_row<NV, SIGMOID>(q, l, c, seq.factor, sum, sum_z);
   }
-  __shared__ double2 s[kWarps];
+  // The sums of a CTA, then of all by the last CTA to arrive, in a fixed order. Positive terms, a few
+  // after one another: fp32 keeps them to some ulp.
+  __shared__ float2 s[kWarps];
   __shared__ bool last;
-  if (lane == 0) s[warp] = make_double2(sum, sum_z);
-  __syncthreads();
+  auto cta_sum = [&](float2 v) {
+    if (lane == 0) s[warp] = v;
+    __syncthreads();
+    const float2 t = lane < kWarps ? s[lane] : make_float2(0.f, 0.f);
+    return warp_sum2(t.x, t.y);
+  };
+  float2 t = cta_sum(make_float2(sum, sum_z));
   if (threadIdx.x == 0) {
-    double2 t = make_double2(0., 0.);
-    for (int i = 0; i < kWarps; ++i) {
-      t.x += s[i].x;
-      t.y += s[i].y;
-    }
     q.part[blockIdx.x] = t;
     __threadfence();
     last = atomicAdd(q.ticket, 1u) + 1 == gridDim.x;
   }
   __syncthreads();
   if (!last) return;
-  // the last CTA: everyone's sums, in their order
   __threadfence();
-  double2 t = make_double2(0., 0.);
+  t = make_float2(0.f, 0.f);
   for (int i = threadIdx.x; i < (int)gridDim.x; i += 32 * kWarps) {
-    t.x += __ldcg(&q.part[i].x);
-    t.y += __ldcg(&q.part[i].y);
+    const float2 v = __ldcg(&q.part[i]);
+    t.x += v.x;
+    t.y += v.y;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    t.x += __shfl_xor_sync(kAll, t.x, off);
-    t.y += __shfl_xor_sync(kAll, t.y, off);
-  }
-  if (lane == 0) s[warp] = t;
-  __syncthreads();
+  t = cta_sum(warp_sum2(t.x, t.y));
   if (threadIdx.x == 0) {
-    t = make_double2(0., 0.);
-    for (int i = 0; i < kWarps; ++i) {
-      t.x += s[i].x;
-      t.y += s[i].y;
-    }
-    q.losses[0] = (float)t.x;
-    q.losses[1] = tv > 0 && q.z > 0.f ? (float)(t.y * q.z / tv) : 0.f;
+    q.losses[0] = t.x;
+    q.losses[1] = seq.valid > 0 && q.z > 0.f ? t.y / (float)seq.valid * q.z : 0.f;
   }
+}
+
+// e = e^-l; p = 1 / (1 + e), 0 where e is at its limit; the sums of p and p u.
+template <int NV>
+__device__ __forceinline__ float2 sigmoids(const Vec<NV>& l, const Vec<NV>& u, Vec<NV>& e, Vec<NV>& p) {
+  e = exp_vec(l * Vec<NV>::all(-1.f));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    e.v[i] = l.v[i] < -88.f ? FLT_MAX : e.v[i];
+    p.v[i] = inverse(1.f + e.v[i]);
+  }
+  return warp_sum2(p.sum(), dot(p, u));
+}
+// d + sigmoid (1 - sigmoid) / sum (u - p.u) = d + (e^-l p) (p / sum) (u - p.u)
+template <int NV>
+__device__ __forceinline__ Vec<NV> sigmoid_gradient(const Vec<NV>& d, const Vec<NV>& u, const Vec<NV>& e,
+                                                    const Vec<NV>& p, float2 w) {
+  const float inv = 1.f / w.x;
+  return fma((e * p) * (p * Vec<NV>::all(inv)), u + Vec<NV>::all(-w.y * inv), d);
+}
+
+// d plus a row's gradient, for any row: that of the loss where `loss`, and fz lse softmax.
+template <int NV, bool SIGMOID>
+__device__ __noinline__ Vec<NV> careful_gradient(Vec<NV> l, Vec<NV> u, Vec<NV> d, float fz, bool loss) {
+  clean_row(l);
+  const float m = row_max(l);
+  if (m == -INFINITY) return d;
+  bool relative = loss;
+  if (SIGMOID && loss && m > -17.f) {
+    Vec<NV> below, e, p;   // finite, or masked
+#pragma unroll
+    for (int i = 0; i < NV; ++i) below.v[i] = fminf(l.v[i], 200.f);
+    const float2 w = sigmoids(below, u, e, p);
+    d = sigmoid_gradient(d, u, e, p, w);
+    relative = false;
+  }
+  if (relative || fz != 0.f) {
+    const Vec<NV> p = exp_below(l, m);
+    const float2 w = warp_sum2(p.sum(), dot(p, u));
+    const float inv = 1.f / w.x, shift = fz != 0.f ? fz * (m + logf(w.x)) : 0.f;
+    const Vec<NV> scores = p * Vec<NV>::all(inv);
+    d = relative ? fma(scores, u + Vec<NV>::all(shift - w.y * inv), d)
+                 : fma(scores, Vec<NV>::all(shift), d);
+  }
+  return d;
 }
 
 // softmax  p_e (u_e - p.u + 2 z / Tv lse);  sigmoid  p_e (1 - s_e) (u_e - p.u), the penalty apart
 template <int NV, bool SIGMOID, typename LT, typename DT>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, kBwdCtas<NV, SIGMOID>)
     balance_bwd_kernel(const Args q, const LT* logits, const DT* add, DT* dlogits) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * NV;
   const long long first = (long long)blockIdx.x * q.rows;
   const int end = (int)min(first + q.rows, (long long)q.T);
-  Vec<NV> next, next_add = Vec<NV>::all(0.f);
-  auto load_next = [&](long long t) {
-    load_logits<NV>(q, logits, t, e0, next.v);
-    if (add) load_row<NV>(add + (size_t)t * q.E, e0, q.E, q.vec_out, 0.f, next_add.v);
+  RawRow<NV, LT> next;
+  RawRow<NV, DT> next_add;
+  size_t at = (size_t)(first + warp) * q.E;
+  auto load_next = [&] {
+    next.load(logits + at, e0, q.E, q.vec, minus_infinity<LT>());
+    if (add) next_add.load(add + at, e0, q.E, q.vec_out, 0u);
   };
-  if (first + warp < end) load_next(first + warp);
-  const int tv = valid_rows(q);
+  if (first + warp < end) load_next();
   const float d0 = q.dlosses ? q.dlosses[0] : 1.f, d1 = q.dlosses ? q.dlosses[1] : 1.f;
-  const float fz = q.z > 0.f && tv > 0 ? 2.f * q.z / (float)tv * d1 : 0.f;
-  Sequence<NV> seq;
+  Sequence seq(q);
+  const float fz = q.z > 0.f && seq.valid > 0 ? 2.f * q.z / (float)seq.valid * d1 : 0.f;
   Vec<NV> u;
   for (int t = (int)first + warp; t < end; t += kWarps) {
-    Vec<NV> l = next, d = next_add;
-    if (end - t > kWarps) load_next(t + kWarps);
-    if (seq.move_to(q, t, tv)) {
+    const Vec<NV> l = next.values();
+    Vec<NV> d = add ? next_add.values() : Vec<NV>::all(0.f);
+    DT* to = dlogits + at;
+    at += (size_t)kWarps * q.E;
+    if (end - t > kWarps) load_next();
+    if (seq.move_to(q, t)) {
       // counts relative to their mean, an integer: sum_e p_e = 1, so the gradient is the same,
       // without the cancellation of nearly even counts
       int32_t c[NV];
@@ -334,35 +542,25 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
       for (int i = 0; i < NV; ++i) u.v[i] = (float)(c[i] - mean) * (seq.factor * d0);
     }
-    bool tiny = false;
-    if (SIGMOID && seq.live) {
-      Vec<NV> e = exp_vec<NV>(l * Vec<NV>::all(-1.f)), p;   // e^-l, at most e^88
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        e.v[i] = l.v[i] > -88.f ? e.v[i] : FLT_MAX;   // and masked: a score of 0
-        p.v[i] = inverse(1.f + e.v[i]);
-      }
-      const float2 w = warp_sum2(p.sum(), dot(p, u));
-      tiny = w.x < kTiny;
-      if (!tiny) {
-        const float inv = 1.f / w.x;
-        // sigmoid (1 - sigmoid) = (e^-l sigmoid) sigmoid
-        d = fma((e * p) * (p * Vec<NV>::all(inv)), u + Vec<NV>::all(-w.y * inv), d);
-      }
-    }
-    if (seq.live && (!SIGMOID || tiny || fz != 0.f)) {
-      const float m = row_max<NV>(l);
-      if (m > -INFINITY) {
-        const Vec<NV> p = exp_vec<NV>(l + Vec<NV>::all(-m));
+    if (seq.live) {
+      bool plain;
+      if constexpr (SIGMOID) {
+        Vec<NV> e, p;
+        const float2 w = sigmoids(l, u, e, p);
+        plain = w.x > kTiny && w.x < 1e30f;
+        if (plain) d = sigmoid_gradient(d, u, e, p, w);
+      } else {
+        const Vec<NV> p = exp_vec(l);
         const float2 w = warp_sum2(p.sum(), dot(p, u));
-        const float inv = 1.f / w.x;
-        const float shift = fz != 0.f ? fz * (m + logf(w.x)) : 0.f;
-        const Vec<NV> scores = p * Vec<NV>::all(inv);
-        if (!SIGMOID || tiny) d = fma(scores, u + Vec<NV>::all(shift - w.y * inv), d);
-        else d = fma(scores, Vec<NV>::all(shift), d);
+        plain = plain_sum(w.x);
+        if (plain) {
+          const float inv = 1.f / w.x, shift = fz != 0.f ? fz * logf(w.x) : 0.f;
+          d = fma(p * Vec<NV>::all(inv), u + Vec<NV>::all(shift - w.y * inv), d);
+        }
       }
+      if (!plain || (SIGMOID && fz != 0.f)) d = careful_gradient<NV, SIGMOID>(l, u, d, fz, !plain);
     }
-    store_row<NV>(dlogits + (size_t)t * q.E, e0, q.E, q.vec_out, d.v);
+    store_row<NV>(to, e0, q.E, q.vec_out, d.v);
   }
 }
 
@@ -376,11 +574,12 @@ bool make_args(const mok_balance* r, int T, int S, Args* q) {
   q->T = T; q->E = r->E; q->k = r->k; q->S = S;
   q->coef = (float)((double)r->coef * r->E / r->k);
   q->z = r->z_coef;
-  // rows per CTA: whole rounds of its warps, at most kParts CTAs
-  const long long per = ((long long)T + kParts - 1) / kParts;
-  q->rows = (int)((per + kWarps - 1) / kWarps * kWarps);
-  if (q->rows < kWarps) q->rows = kWarps;
   return true;
+}
+// Rows per CTA: whole rounds of its warps, one wave of `ctas` CTAs a SM at most.
+int cta_rows(int T, int ctas) {
+  const long long per = ((long long)T + kSms * ctas - 1) / (kSms * ctas);
+  return (int)std::max<long long>((per + kWarps - 1) / kWarps * kWarps, kWarps);
 }
 size_t counts_bytes(const mok_balance* r, int S) { return align_up((size_t)S * r->E * 4, 256); }
 
@@ -392,7 +591,7 @@ extern "C" mok_status mok_balance_get_sizes(const mok_balance* rule, int T, int 
   using namespace mok;
   Args q;
   if (!make_args(rule, T, S, &q) || !saved_bytes) return MOK_ERR_INVALID_ARG;
-  *saved_bytes = counts_bytes(rule, S) + kParts * sizeof(double2) + 256;
+  *saved_bytes = counts_bytes(rule, S) + kParts * sizeof(float2) + 256 + (size_t)kGroups * rule->E * 4;
   return MOK_OK;
 }
 
@@ -411,29 +610,48 @@ extern "C" mok_status mok_balance_fwd(const mok_balance* rule, int T, const void
   if (!saved || !aligned_to(saved, 256)) return MOK_ERR_WORKSPACE;
   q.idx = topk_idx; q.seqs = seqs; q.counts = counts; q.losses = losses;
   q.seq_counts = static_cast<int32_t*>(saved);
-  q.part = reinterpret_cast<double2*>(static_cast<char*>(saved) + counts_bytes(rule, S));
+  q.part = reinterpret_cast<float2*>(static_cast<char*>(saved) + counts_bytes(rule, S));
   q.ticket = reinterpret_cast<unsigned*>(q.part + kParts);
+  q.group_counts = reinterpret_cast<int32_t*>(q.ticket + 64);
   q.vec = rows_vectorize(q.E, logits, logits_type);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // a sequence's CTAs: eight, but one where sequences are short or many
-  const int ctas = (long long)T / S * q.k >= 4096 && S <= 4096 ? 8 : 1;
-  cudaError_t e = launch(count_kernel, dim3((unsigned)S * ctas), dim3(kCountThreads), 0, ctas, false, s,
-                         q, ctas);
+  auto by_score = [&](auto f) {   // f(score is a sigmoid, the logits)
+    const auto* lb = static_cast<const __nv_bfloat16*>(logits);
+    const auto* lf = static_cast<const float*>(logits);
+    const bool sg = rule->score == MOK_SCORE_SIGMOID, b = logits_type == MOK_OUT_BF16;
+    if (sg && b) f(std::true_type{}, lb);
+    else if (sg) f(std::true_type{}, lf);
+    else if (b) f(std::false_type{}, lb);
+    else f(std::false_type{}, lf);
+  };
+  cudaError_t e = cudaSuccess;
+  if (!seqs && T > 0 && (long long)T * q.k <= kSmallIds) {
+    by_width(q.E, [&](auto nv) {
+      by_score([&](auto sg, const auto* l) {
+        using LT = std::remove_const_t<std::remove_pointer_t<decltype(l)>>;
+        e = launch(small_loss_kernel<decltype(nv)::value, decltype(sg)::value, LT>, dim3(kSmallCtas),
+                   dim3(32 * kSmallWarps), 0, kSmallCtas, false, s, q, l);
+      });
+    });
+    return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  }
+  // A sequence's CTAs: eight, but one where sequences are short or many; and several clusters for one
+  // long sequence, 32 K ids each (65536 rows of 8: .. us by one cluster, .. by 16).
+  const long long ids = (long long)T / S * q.k;
+  const int ctas = ids >= 4096 && S <= 4096 ? 8 : 1;
+  q.groups = S > 1 ? 1 : (int)std::max(1ll, std::min<long long>(kGroups, ids >> 15));
+  e = launch(count_kernel, dim3((unsigned)(S * q.groups) * ctas), dim3(kCountThreads), 0, ctas,
+                         false, s, q, ctas);
   if (e != cudaSuccess) return MOK_ERR_CUDA;
   if (T > 0) {
+    q.rows = cta_rows(T, kLossCtas);
     const unsigned parts = ((unsigned)T + q.rows - 1) / q.rows;
     by_width(q.E, [&](auto nv) {
-      constexpr int NV = decltype(nv)::value;
-      auto go = [&](auto kernel, auto* l) {
-        e = launch(kernel, dim3(parts), dim3(32 * kWarps), 0, 1, true, s, q, l);
-      };
-      const auto* lb = static_cast<const __nv_bfloat16*>(logits);
-      const auto* lf = static_cast<const float*>(logits);
-      const bool sg = rule->score == MOK_SCORE_SIGMOID, b = logits_type == MOK_OUT_BF16;
-      if (sg && b) go(loss_kernel<NV, true, __nv_bfloat16>, lb);
-      else if (sg) go(loss_kernel<NV, true, float>, lf);
-      else if (b) go(loss_kernel<NV, false, __nv_bfloat16>, lb);
-      else go(loss_kernel<NV, false, float>, lf);
+      by_score([&](auto sg, const auto* l) {
+        using LT = std::remove_const_t<std::remove_pointer_t<decltype(l)>>;
+        e = launch(loss_kernel<decltype(nv)::value, decltype(sg)::value, LT>, dim3(parts), dim3(32 * kWarps),
+                   0, 1, true, s, q, l);
+      });
     });
   }
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
@@ -461,13 +679,15 @@ extern "C" mok_status mok_balance_bwd(const mok_balance* rule, int T, const void
   q.vec_out = rows_vectorize(q.E, dlogits, dlogits_type) &&
               (!add || rows_vectorize(q.E, add, dlogits_type));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned ctas = ((unsigned)T + q.rows - 1) / q.rows;
   by_width(q.E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
+    const bool sg = rule->score == MOK_SCORE_SIGMOID;
+    q.rows = cta_rows(T, sg ? kBwdCtas<NV, true> : kBwdCtas<NV, false>);
+    const unsigned ctas = ((unsigned)T + q.rows - 1) / q.rows;
     auto go = [&](auto lt, auto dt) {
       using LT = decltype(lt);
       using DT = decltype(dt);
-      auto* kernel = rule->score == MOK_SCORE_SIGMOID ? balance_bwd_kernel<NV, true, LT, DT>
+      auto* kernel = sg ? balance_bwd_kernel<NV, true, LT, DT>
                                                       : balance_bwd_kernel<NV, false, LT, DT>;
       kernel<<<ctas, 32 * kWarps, 0, s>>>(q, static_cast<const LT*>(logits),
                                           static_cast<const DT*>(add), static_cast<DT*>(dlogits));
