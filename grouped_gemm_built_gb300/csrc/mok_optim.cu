@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;           // state elements that share the scales of 8-bit moments
-constexpr int kChunk = kThreads * 8;  // elements per CTA of the step: a warp has one block
+constexpr int kRound = kThreads * 8;  // elements of a CTA at a time: a warp has one block
 
 // ---------------------------------------------------------------- norm of many gradients
 constexpr int kNormChunk = kThreads * 32;
@@ -124,7 +124,7 @@ struct StepEntry {
 };
 template <int N>
 struct StepTable {
-  int count;
+  int count, rounds;   // a chunk: `rounds` times kRound elements
   StepEntry e[N];
 };
 constexpr int kStepTable = 640;   // 48 bytes each
@@ -133,6 +133,7 @@ struct Step {
   float beta1, beta2, rest1, rest2, eps;   // rest: 1 - beta
   float lr, inv_c1, inv_sqrt_c2;           // c: 1 - beta^t
   float log_beta1, log_beta2;              // for a step number on the device
+  float minus_zero;
   int t;
   const float* lr_dev;
   const int32_t* t_dev;
@@ -143,74 +144,101 @@ struct Step {
   uint8_t* scales;
 };
 
+using Eight = Vec<8>;
+
+// Products that are rounded by themselves, as a b + (-0) with a -0 that the compiler does not know:
+// it fuses a paired product with the sum that follows, also where both are written as rounded.
+__device__ __forceinline__ Eight mul_rn(const Eight& a, const Eight& b, const Eight& minus_zero) {
+  return fma(a, b, minus_zero);
+}
+
 // 8-bit moments of the eight elements of a lane; the warp holds one block.
-__device__ __forceinline__ void decode8(const uint2 mc, const uint2 vc, int a, int b, float* m,
-                                        float* v) {
-  const float up = __int_as_float((a - 7) << 23);   // 2^(a - 134)
+__device__ __forceinline__ void decode8(const uint2 mc, const uint2 vc, int a, int b, Eight& m, Eight& v) {
   const uint32_t mw[2] = {mc.x, mc.y}, vw[2] = {vc.x, vc.y};
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const uint16_t two = (uint16_t)(mw[j / 4] >> (8 * (j & 3)));
     uint32_t h2;   // two fp16
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-    float lo, hi;
     asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
-        : "=f"(lo), "=f"(hi)
+        : "=f"(m.v[j]), "=f"(m.v[j + 1])
         : "r"(h2));
-    m[j] = lo * up;
-    m[j + 1] = hi * up;
   }
+  m = m * Eight::all(__int_as_float((a - 7) << 23));   // 2^(a - 134)
+  const int base = (b - 30) << 23;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t c = (vw[j / 4] >> (8 * (j & 3))) & 255u;
-    v[j] = c ? __int_as_float((int)(c << 20) + ((b - 30) << 23)) : 0.f;
+    const int up = 20 - 8 * (j & 3);   // the code's byte goes to bits 20 .. 27
+    const uint32_t c = (up >= 0 ? vw[j / 4] << up : vw[j / 4] >> -up) & 0x0ff00000u;
+    v.v[j] = c ? __int_as_float((int)c + base) : 0.f;
   }
 }
 
-__device__ __forceinline__ void encode8(const float* m, const float* v, const uint4 noise,
-                                        uint2* mc, uint2* vc, int* a, int* b) {
-  uint32_t top_m = 0, top_v = 0;   // fp32 bits: their order is the values'
-  bool bad = false;
+// Codes of finite moments, or (CHECK) of any: those that are not finite count for no scale.
+template <bool CHECK>
+__device__ __forceinline__ bool encode8(const Eight& m, const Eight& v, const uint4 noise, uint2* mc,
+                                        uint2* vc, int* a, int* b) {
+  // the largest |m| and v by their fp32 bits, whose order is the values'
+  uint32_t top_m = 0, top_v = 0;
+  auto bad = [&](int j) {
+    return (__float_as_uint(m.v[j]) & 0x7fffffffu) >= 0x7f800000u || __float_as_uint(v.v[j]) >= 0x7f800000u;
+  };
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t x = __float_as_uint(m[j]) & 0x7fffffffu, y = __float_as_uint(v[j]);
-    if (x >= 0x7f800000u || y >= 0x7f800000u) {
-      bad = true;
-    } else {
-      top_m = max(top_m, x);
-      top_v = max(top_v, y);
-    }
+    if (CHECK && bad(j)) continue;
+    top_m = max(top_m, __float_as_uint(m.v[j]) & 0x7fffffffu);
+    top_v = max(top_v, __float_as_uint(v.v[j]));
   }
-  *a = max((int)(__reduce_max_sync(kAll, top_m) >> 23), 8);
-  *b = max((int)(__reduce_max_sync(kAll, top_v) >> 23), 31);
-  const float down = __int_as_float((261 - *a) << 23);   // 2^(134 - a)
+  top_m = __reduce_max_sync(kAll, top_m);
+  top_v = __reduce_max_sync(kAll, top_v);
+  if (!CHECK && max(top_m, top_v) >= 0x7f800000u) return false;
+  *a = max((int)(top_m >> 23), 8);
+  *b = max((int)(top_v >> 23), 31);
+  const Eight x = m * Eight::all(__int_as_float((261 - *a) << 23));   // 2^(134 - a)
+  uint32_t mw[2], vw[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.v[4 * i + 1]), "f"(x.v[4 * i]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x.v[4 * i + 3]), "f"(x.v[4 * i + 2]));
+    mw[i] = (uint32_t)lo | (uint32_t)hi << 16;
+  }
+  // v: the bits below the code's last, plus noise of 16 bits, carry into the code. Up to 248, as the
+  // largest exponent leaves room; at least 1 above 0.
   const uint32_t r[4] = {noise.x, noise.y, noise.z, noise.w};
-  uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    uint16_t two;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(m[j + 1] * down), "f"(m[j] * down));
-    mw[j / 4] |= (uint32_t)two << (8 * (j & 3));
-  }
+  const int base = (*b - 30) << 23;
+  int c[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int u = (j & 1) ? (int)(r[j / 2] >> 16) : (int)(r[j / 2] & 0xffffu);
-    int c = (__float_as_int(v[j]) - ((*b - 30) << 23) + (u << 4)) >> 20;
-    c = v[j] > 0.f ? min(max(c, 1), 255) : 0;
-    vw[j / 4] |= (uint32_t)c << (8 * (j & 3));
+    const int u = (int)((j & 1) ? r[j / 2] >> 12 : r[j / 2] << 4) & 0xffff0;
+    const int bits = __float_as_int(v.v[j]);
+    c[j] = max((bits + u - base) >> 20, min(bits, 1));
   }
-  if (bad) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t x = __float_as_uint(m[j]) & 0x7fffffffu, y = __float_as_uint(v[j]);
-      if (x >= 0x7f800000u || y >= 0x7f800000u) {
-        mw[j / 4] |= 0x7fu << (8 * (j & 3));
-        vw[j / 4] |= 255u << (8 * (j & 3));
+  for (int i = 0; i < 2; ++i)
+    vw[i] = (uint32_t)(c[4 * i] + (c[4 * i + 1] << 8) + (c[4 * i + 2] << 16)) + ((uint32_t)c[4 * i + 3] << 24);
+  if (CHECK) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t byte = 255u << (8 * j);
+        if (bad(4 * i + j)) {
+          mw[i] = (mw[i] & ~byte) | (0x7fu << (8 * j));
+          c[4 * i + j] = 255;
+        }
       }
+      vw[i] = (uint32_t)c[4 * i] | (uint32_t)c[4 * i + 1] << 8 | (uint32_t)c[4 * i + 2] << 16 |
+              (uint32_t)c[4 * i + 3] << 24;
     }
   }
   *mc = make_uint2(mw[0], mw[1]);
   *vc = make_uint2(vw[0], vw[1]);
+  return true;
+}
+__device__ __noinline__ void encode8_any(const Eight m, const Eight v, const uint4 noise, uint2* mc, uint2* vc,
+                                         int* a, int* b) {
+  encode8<true>(m, v, noise, mc, vc, a, b);
 }
 
 template <typename E>
@@ -233,32 +261,24 @@ __device__ __forceinline__ void store_some(E* p, bool vec, int cnt, const float*
   }
 }
 
-template <int N, bool SMALL>
-__global__ void __launch_bounds__(kThreads)
-    adamw_kernel(const __grid_constant__ StepTable<N> table, const __grid_constant__ Step q) {
-  const float coef = q.coef ? *q.coef : 1.f;
-  if (!isfinite(coef)) return;
-  const StepEntry& e = table.e[find_entry(table, blockIdx.x)];
-  // this lane's eight elements: i of the tensor, s of the state
-  const size_t i = (size_t)(blockIdx.x - e.first) * kChunk + threadIdx.x * 8;
-  const size_t s = e.base + i;
-  const int lane = threadIdx.x & 31;
-  if (i - lane * 8 >= e.n) return;   // the warp's block lies behind the tensor
-  const int cnt = i >= e.n ? 0 : e.n - i < 8 ? (int)(e.n - i) : 8;
+__device__ __forceinline__ float root(float x) {      // to 2 ulp, of subnormal numbers too
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float inverse(float x) {   // to 1 ulp, of normal numbers
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
-  float p[8], g[8], m[8], v[8];
-  if (e.g_bf16) load_some(static_cast<const __nv_bfloat16*>(e.g) + i, e.g_vec, cnt, g);
-  else load_some(static_cast<const float*>(e.g) + i, e.g_vec, cnt, g);
-  if (e.p_bf16) load8(q.master + s, p);
-  else load_some(static_cast<const float*>(e.p) + i, e.p_vec, cnt, p);
-  if constexpr (SMALL) {
-    const uchar2 ab = reinterpret_cast<const uchar2*>(q.scales)[s / kBlock];
-    decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(q.m) + s),
-            *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(q.v) + s), ab.x, ab.y, m, v);
-  } else {
-    load8(static_cast<const float*>(q.m) + s, m);
-    load8(static_cast<const float*>(q.v) + s, v);
-  }
+template <int N, bool SMALL>
+__global__ void __launch_bounds__(kThreads, 4)
+    adamw_kernel(const __grid_constant__ StepTable<N> table, const __grid_constant__ Step q) {
+  const StepEntry& e = table.e[find_entry(table, blockIdx.x)];
+  const int lane = threadIdx.x & 31;
+  size_t i = ((size_t)(blockIdx.x - e.first) * table.rounds) * kRound + threadIdx.x * 8;
+  const float coef = q.coef ? *q.coef : 1.f;
   float lr = q.lr, inv_c1 = q.inv_c1, inv_sqrt_c2 = q.inv_sqrt_c2;
   int t = q.t;
   if (q.lr_dev) lr = *q.lr_dev;
@@ -267,32 +287,53 @@ __global__ void __launch_bounds__(kThreads)
     inv_c1 = -1.f / expm1f((float)t * q.log_beta1);
     inv_sqrt_c2 = 1.f / sqrtf(-expm1f((float)t * q.log_beta2));
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int round = 0; round < table.rounds; ++round, i += kRound) {
+    // this lane's eight elements: i of the tensor, s of the state
+    if (i - lane * 8 >= e.n) return;   // the warp's block lies behind the tensor
+    const size_t s = e.base + i;
+    const int cnt = i >= e.n ? 0 : e.n - i < 8 ? (int)(e.n - i) : 8;
+    Eight p, g, m, v;
+    if (e.g_bf16) load_some(static_cast<const __nv_bfloat16*>(e.g) + i, e.g_vec, cnt, g.v);
+    else load_some(static_cast<const float*>(e.g) + i, e.g_vec, cnt, g.v);
+    if (e.p_bf16) load8(q.master + s, p.v);
+    else load_some(static_cast<const float*>(e.p) + i, e.p_vec, cnt, p.v);
+    if constexpr (SMALL) {
+      const uchar2 ab = reinterpret_cast<const uchar2*>(q.scales)[s / kBlock];
+      decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(q.m) + s),
+              *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(q.v) + s), ab.x, ab.y, m, v);
+    } else {
+      load8(static_cast<const float*>(q.m) + s, m.v);
+      load8(static_cast<const float*>(q.v) + s, v.v);
+    }
+    if (!isfinite(coef)) return;
     // Every step of the moments is rounded by itself (no fused products): 8-bit moments are a
     // function of these bits.
-    const float x = __fmul_rn(g[j], coef);
-    m[j] = __fadd_rn(__fmul_rn(m[j], q.beta1), __fmul_rn(x, q.rest1));
-    v[j] = __fadd_rn(__fmul_rn(v[j], q.beta2), __fmul_rn(__fmul_rn(x, x), q.rest2));
-    const float step = m[j] * inv_c1 / (sqrtf(v[j]) * inv_sqrt_c2 + q.eps);
-    p[j] = fmaf(-lr, fmaf(e.decay, p[j], step), p[j]);
-  }
-  if (e.p_bf16) {
-    store_some(q.master + s, true, cnt, p);
-    store_some(static_cast<__nv_bfloat16*>(e.p) + i, e.p_vec, cnt, p);
-  } else {
-    store_some(static_cast<float*>(e.p) + i, e.p_vec, cnt, p);
-  }
-  if constexpr (SMALL) {
-    uint2 mc, vc;
-    int a, b;
-    encode8(m, v, philox<7>(s / 8, (uint32_t)t, q.seed), &mc, &vc, &a, &b);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q.m) + s) = mc;
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q.v) + s) = vc;
-    if (lane == 0) reinterpret_cast<uchar2*>(q.scales)[s / kBlock] = make_uchar2(a, b);
-  } else {
-    store8(static_cast<float*>(q.m) + s, m);
-    store8(static_cast<float*>(q.v) + s, v);
+    const Eight z = Eight::all(q.minus_zero);
+    g = mul_rn(g, Eight::all(coef), z);
+    m = mul_rn(m, Eight::all(q.beta1), z) + mul_rn(g, Eight::all(q.rest1), z);
+    v = mul_rn(v, Eight::all(q.beta2), z) + mul_rn(mul_rn(g, g, z), Eight::all(q.rest2), z);
+    Eight d;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d.v[j] = inverse(fmaf(root(v.v[j]), inv_sqrt_c2, q.eps));
+    p = fma(fma(p, Eight::all(e.decay), (m * Eight::all(inv_c1)) * d), Eight::all(-lr), p);
+    if (e.p_bf16) {
+      store_some(q.master + s, true, cnt, p.v);
+      store_some(static_cast<__nv_bfloat16*>(e.p) + i, e.p_vec, cnt, p.v);
+    } else {
+      store_some(static_cast<float*>(e.p) + i, e.p_vec, cnt, p.v);
+    }
+    if constexpr (SMALL) {
+      uint2 mc, vc;
+      int a, b;
+      const uint4 noise = philox<7>(s / 8, (uint32_t)t, q.seed);
+      if (!encode8<false>(m, v, noise, &mc, &vc, &a, &b)) encode8_any(m, v, noise, &mc, &vc, &a, &b);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q.m) + s) = mc;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q.v) + s) = vc;
+      if (lane == 0) reinterpret_cast<uchar2*>(q.scales)[s / kBlock] = make_uchar2(a, b);
+    } else {
+      store8(static_cast<float*>(q.m) + s, m.v);
+      store8(static_cast<float*>(q.v) + s, v.v);
+    }
   }
 }
 
@@ -302,11 +343,11 @@ __global__ void __launch_bounds__(kThreads)
   const size_t s = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 8;
   if (s >= elements) return;
   const uchar2 ab = reinterpret_cast<const uchar2*>(scales)[s / kBlock];
-  float m[8], v[8];
+  Eight m, v;
   decode8(*reinterpret_cast<const uint2*>(mc + s), *reinterpret_cast<const uint2*>(vc + s), ab.x,
           ab.y, m, v);
-  store8(m_out + s, m);
-  store8(v_out + s, v);
+  store8(m_out + s, m.v);
+  store8(v_out + s, v.v);
 }
 
 constexpr size_t kMaxElements = (size_t)1 << 40;
@@ -456,12 +497,16 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
   q.inv_c1 = (float)(1. / (1. - std::pow(r->beta1, (double)q.t)));
   q.inv_sqrt_c2 = (float)(1. / std::sqrt(1. - std::pow(r->beta2, (double)q.t)));
   q.log_beta1 = (float)std::log(r->beta1); q.log_beta2 = (float)std::log(r->beta2);
+  q.minus_zero = -0.f;
   q.lr_dev = lr_dev; q.t_dev = t_dev; q.coef = coef; q.seed = seed;
   q.master = st->master; q.m = st->m; q.v = st->v; q.scales = st->scales;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
+  // chunks of up to four rounds, fewer where that would leave SMs idle
   StepTable<kStepTable> table;
   table.count = 0;
+  table.rounds = total / kRound < 152 * 32 ? 1 : total / kRound < 152 * 64 ? 2 : 4;
+  const size_t chunk = (size_t)table.rounds * kRound;
   unsigned chunks = 0;
   auto launch = [&](const auto& tab) {
     if (small) adamw_kernel<std::extent<decltype(tab.e)>::value, true><<<chunks, kThreads, 0, s>>>(tab, q);
@@ -472,6 +517,7 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
     if (table.count <= 64) {
       StepTable<64> few;
       few.count = table.count;
+      few.rounds = table.rounds;
       std::copy(table.e, table.e + table.count, few.e);
       launch(few);
     } else {
@@ -483,7 +529,7 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
   size_t base = 0;
   for (int i = 0; i < count; ++i) {
     const mok_adamw_tensor& x = tensors[i];
-    const size_t own = (x.n + kChunk - 1) / kChunk;
+    const size_t own = (x.n + chunk - 1) / chunk;
     if (x.g && x.n) {
       if (table.count == kStepTable || chunks + own > 0x7fffffffu) flush();
       table.e[table.count++] = {x.p, x.g, x.n, base, chunks, (float)x.decay,
