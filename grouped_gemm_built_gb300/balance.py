@@ -59,8 +59,10 @@ class Balance:
         bf16 or fp32 whose router chose topk_idx [T,k] int32. ``seqs`` [S + 1] int32 on the
         device: row offsets of sequences that are balanced one by one; rows outside take no
         part. ``saved`` is what ``backward`` takes."""
-        return _results(mok.torch_calls().balance_fwd(self.rule, logits, topk_idx, seqs),
-                        "mok_balance_fwd", lambda: self._check_forward(logits, topk_idx, seqs))
+        got = mok.torch_calls().balance_fwd(self.rule, logits, topk_idx, seqs)
+        if type(got) is tuple:
+            return got
+        return _results(got, "mok_balance_fwd", lambda: self._check_forward(logits, topk_idx, seqs))
 
     def backward(self, logits: torch.Tensor, saved: torch.Tensor,
                  seqs: Optional[torch.Tensor] = None, dlosses: Optional[torch.Tensor] = None,
@@ -71,5 +73,7 @@ class Balance:
         dtype = dtype or getattr(logits if add is None else add, "dtype", None)
         got = mok.torch_calls().balance_bwd(self.rule, logits, seqs, saved, dlosses, add,
                                             _result_code(dtype, "dlogits"))
+        if type(got) is tuple:
+            return got[0]
         return _results(got, "mok_balance_bwd", lambda: self._check_backward(
             logits, saved, seqs, dlosses, add, dtype))[0]

@@ -9,6 +9,7 @@
 // and leave as one partial row per CTA, which a second, overlapped kernel sums up. Each thread
 // copies its own part of the next row to shared memory (cp.async: asynchronous, and nobody else
 // reads it, so there is no barrier and no wait on another thread) while the team reduces this one.
+#include <atomic>
 #include <climits>
 
 #include "mok_internal.h"
@@ -187,14 +188,14 @@ struct Part {
     live = c0 < H ? min(N, (H - c0 + 32 * V - 1) / (32 * V)) : 0;
   }
 };
-// A thread's places in shared memory, for two rows of K tensors: an access of its warp is 512 bytes
+// A thread's places in shared memory, for `stages` rows of K tensors: an access of its warp is 512 bytes
 // in one piece (asynchronous copies to places further apart took 1.4 times as long).
 // `more` places beyond those.
 extern __shared__ __align__(16) char ring[];
 template <int N, int K>
-__device__ __forceinline__ char* places(int more) {
+__device__ __forceinline__ char* places(int stages, int more) {
   const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
-  return ring + (size_t)warp * ((2 * K * N + more) * kPlace) + (threadIdx.x & 31) * 16;
+  return ring + (size_t)warp * ((stages * K * N + more) * kPlace) + (threadIdx.x & 31) * 16;
 }
 // Starts the copies of this thread's part of a row (`from`: its first element) to `to` on.
 template <int N, int V, typename E>
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
   const float inv_h = 1.f / (float)q.H;
-  char* const mine = RING ? places<N, K>(0) : nullptr;
+  char* const mine = RING ? places<N, K>(q.stages, 0) : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
   const float inv_h = 1.f / (float)q.H;
   constexpr int MORE = w_places<N, V, W>(MODE);
-  char* const mine = RING ? places<N, K>(MORE) : nullptr;
+  char* const mine = RING ? places<N, K>(q.stages, MORE) : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
   };
   using WT = std::conditional_t<RING, W, float>;
   Raw<V, WT> w_raw[WREG ? N : 1];
-  char* const w_mine = mine + 2 * K * N * kPlace;
+  char* const w_mine = mine + q.stages * (K * N * kPlace);
   if constexpr (RING) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -520,8 +521,8 @@ Form form(const mok_norm_dims* d, int more, int threads, int most_ctas) {
   Form f{};
   f.bx = ((d->H + N * V - 1) / (N * V) + 31) / 32 * 32;
   f.by = std::max(1u, 256 / f.bx);
-  f.stages = V == 1 ? 0 : 2;
-  f.smem = V == 1 ? 0 : (size_t)(f.bx * f.by / 32) * (2 * K * N + more) * kPlace;
+  f.stages = V == 1 ? 0 : d->T <= kSms * (int)f.by ? 1 : 2;   // one, where no team has a second row
+  f.smem = V == 1 ? 0 : (size_t)(f.bx * f.by / 32) * (f.stages * K * N + more) * kPlace;
   int ctas = std::max(1, threads / (int)(f.bx * f.by));
   if (f.smem) ctas = std::max(1, std::min(ctas, (int)(kRingBytes / f.smem)));
   f.grid = (unsigned)std::min<size_t>(((size_t)d->T + f.by - 1) / f.by,
@@ -531,14 +532,29 @@ Form form(const mok_norm_dims* d, int more, int threads, int most_ctas) {
 // Partial rows of dW and dB at most.
 int most_parts(const mok_norm_dims* d) { return std::min(d->T, d->H <= 2048 ? kMaxParts : kMaxParts / 2); }
 
-template <typename K>
-cudaError_t run(K kernel, const Form& f, const NormArgs& q, cudaStream_t s) {
+// Lets a kernel have more than 48 KB of shared memory, once on each device.
+template <auto KERNEL>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit)) return e;
+  cudaFuncAttributes a;
+  e = cudaFuncGetAttributes(&a, KERNEL);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(227 * 1024 - a.sharedSizeBytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+template <auto KERNEL>
+cudaError_t run(const Form& f, const NormArgs& q, cudaStream_t s) {
   if (f.smem > 40 * 1024) {   // 48 KB with the static part
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)f.smem);
+    const cudaError_t e = allow_smem<KERNEL>();
     if (e != cudaSuccess) return e;
   }
-  return launch(kernel, dim3(f.grid), dim3(f.bx, f.by), f.smem, 1, false, s, q);
+  return launch(KERNEL, dim3(f.grid), dim3(f.bx, f.by), f.smem, 1, false, s, q);
 }
 
 template <typename T>
@@ -625,9 +641,9 @@ extern "C" mok_status mok_norm_fwd(const mok_norm_dims* d, const void* x, const 
     constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 6 : 3;
     const Form f = form<N, V, 2>(d, 0, THREADS * CTAS, INT_MAX);
     q.stages = f.stages;
-    return run(norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type,
-                               typename decltype(wt)::type, THREADS, CTAS>,
-               f, q, static_cast<cudaStream_t>(stream));
+    return run<norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type,
+                               typename decltype(wt)::type, THREADS, CTAS>>(
+        f, q, static_cast<cudaStream_t>(stream));
   });
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
@@ -668,7 +684,7 @@ extern "C" mok_status mok_norm_bwd(const mok_norm_dims* d, const void* dY, const
         if (f.by > 1) f.smem = std::max(f.smem, (size_t)d->H * sizeof(float2));   // joins the teams
         q.stages = f.stages;
         q.parts = (int)f.grid;
-        return run(norm_bwd_kernel<N, V, X, Y, W, MODE, THREADS, CTAS>, f, q, s);
+        return run<norm_bwd_kernel<N, V, X, Y, W, MODE, THREADS, CTAS>>(f, q, s);
       };
       if (dB) return go(std::integral_constant<int, kBias>{});
       if (q.rms) return go(std::integral_constant<int, kRms>{});

@@ -6,6 +6,7 @@
 #include <new>
 
 #include "mok_internal.h"
+#include "mok_launch.cuh"
 #include "mok_ops.h"
 #include "mok_rows.cuh"
 
@@ -17,22 +18,23 @@ constexpr int kBlock = 256;           // state elements that share the scales of
 constexpr int kRound = kThreads * 8;  // elements of a CTA at a time: a warp has one block
 
 // ---------------------------------------------------------------- norm of many gradients
-constexpr int kNormChunk = kThreads * 32;
-constexpr int kNormCtas = 152 * 4;
+// A CTA takes 16 KB of a tensor at a time, four 16-byte loads a thread.
+constexpr int kNormBytes = kThreads * 64;
+constexpr int kNormCtas = 152 * 6;
 
 struct GradEntry {
   const void* g;
   unsigned long long n;
-  unsigned first;   // its first chunk
   bool bf16, vec;
 };
 template <int N>
 struct GradTable {
   int count;
   unsigned chunks;
+  unsigned first[N];   // an entry's first chunk: by themselves, as a search reads only these
   GradEntry e[N];
 };
-constexpr int kGradTable = 1200;   // 24 bytes each
+constexpr int kGradTable = 1100;   // 28 bytes each
 
 // The entry that holds chunk i: the last whose first chunk is at or before it.
 template <typename T>
@@ -40,61 +42,99 @@ __device__ __forceinline__ int find_entry(const T& table, unsigned i) {
   int lo = 0, hi = table.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (table.e[mid].first <= i) lo = mid;
+    if (table.first[mid] <= i) lo = mid;
     else hi = mid;
   }
   return lo;
 }
 
-// Sum of squares of one thread's 32 elements of a chunk: groups of 8, kThreads groups apart.
+// Sum of the squares of four vectors' elements, in fp32.
 template <typename E>
-__device__ __forceinline__ double squares(const GradEntry& e, size_t at) {
-  const E* g = static_cast<const E*>(e.g);
-  float v[4][8];
+__device__ __forceinline__ float squares(const uint4 (&x)[4]) {
+  constexpr int V = 16 / (int)sizeof(E);
+  Vec<V> s = Vec<V>::all(0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const size_t a = at + (size_t)(i * kThreads + threadIdx.x) * 8;
-    if (e.vec && a + 8 <= e.n) {
-      load8(g + a, v[i]);
-    } else {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    Vec<V> v;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = a + j < e.n ? load(g + a + j) : 0.f;
+    for (int j = 0; j < V; ++j) {
+      if constexpr (sizeof(E) == 4) v.v[j] = __uint_as_float(w[j]);
+      else v.v[j] = __uint_as_float((j & 1) ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+    s = fma(v, v, s);
+  }
+  return s.sum();
+}
+// The same in fp64, for sums that fp32 cannot hold; zeros cost little.
+template <typename E>
+__device__ __noinline__ double wide_squares(uint4 a, uint4 b, uint4 c, uint4 d) {
+  const uint4 x[4] = {a, b, c, d};
+  double s = 0.;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int j = 0; j < 4; ++j) {
+      const float lo = __uint_as_float(sizeof(E) == 4 ? w[j] : w[j] << 16);
+      const float hi = sizeof(E) == 4 ? 0.f : __uint_as_float(w[j] & 0xffff0000u);
+      if (lo != 0.f) s += (double)lo * (double)lo;
+      if (hi != 0.f) s += (double)hi * (double)hi;
     }
   }
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
-  if (s > 1e-30f && s < 1e38f) return (double)s;   // what underflowed is below the sum's last bit
-  double d = 0.;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (v[i][j] != 0.f) d += (double)v[i][j] * (double)v[i][j];
-  return d;
+  return s;
 }
 
-__device__ __forceinline__ double block_sum(double v) {
+// The sum of one thread's share of a chunk that begins at element `at`.
+template <typename E>
+__device__ __forceinline__ double chunk_squares(const GradEntry& e, size_t at) {
+  constexpr int V = 16 / (int)sizeof(E);
+  const E* g = static_cast<const E*>(e.g);
+  uint4 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const size_t a = at + (size_t)(i * kThreads + threadIdx.x) * V;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (e.vec && a + V <= e.n) {
+      x[i] = *reinterpret_cast<const uint4*>(g + a);
+    } else if (a < e.n) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (a + j < e.n) {
+          if constexpr (sizeof(E) == 4) w[j] = __float_as_uint(g[a + j]);
+          else w[j / 2] |= (uint32_t)__bfloat16_as_ushort(g[a + j]) << (16 * (j & 1));
+        }
+      }
+      x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  const float s = squares<E>(x);
+  if (s > 1e-30f && s < 1e38f) return (double)s;   // what underflowed is below the sum's last bit
+  return wide_squares<E>(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ double block_sum(double v) {   // in thread 0
+  __shared__ double s[kThreads / 32];
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
-  __shared__ double s[32];
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  double t = 0.;
-  for (int i = 0; i < (int)blockDim.x / 32; ++i) t += s[i];
-  return t;
+  if (threadIdx.x >= 32) return 0.;
+  v = threadIdx.x < kThreads / 32 ? s[threadIdx.x] : 0.;
+#pragma unroll
+  for (int off = kThreads / 64; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  return v;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     grad_squares_kernel(const __grid_constant__ GradTable<N> table, double* part, bool add) {
+  launch_dependents();
   double d = 0.;
   for (unsigned i = blockIdx.x; i < table.chunks; i += gridDim.x) {
-    const GradEntry& e = table.e[find_entry(table, i)];
-    const size_t at = (size_t)(i - e.first) * kNormChunk;
-    d += e.bf16 ? squares<__nv_bfloat16>(e, at) : squares<float>(e, at);
+    const int at = find_entry(table, i);
+    const GradEntry& e = table.e[at];
+    const size_t c = i - table.first[at];
+    d += e.bf16 ? chunk_squares<__nv_bfloat16>(e, c * (kNormBytes / 2)) : chunk_squares<float>(e, c * (kNormBytes / 4));
   }
   d = block_sum(d);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + d : d;
@@ -103,10 +143,12 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const double* part, int parts, float max_norm, float scale, float* norm,
                      float* coef) {
+  wait_prerequisites();
   double d = 0.;
   for (int i = threadIdx.x; i < parts; i += kThreads) d += part[i];
-  d = sqrt(block_sum(d)) * (double)scale;
+  d = block_sum(d);
   if (threadIdx.x) return;
+  d = sqrt(d) * (double)scale;
   const float n = (float)d;
   *norm = n;
   *coef = !isfinite(n) ? NAN : d > (double)max_norm ? (float)(scale * (max_norm / d)) : scale;
@@ -118,16 +160,16 @@ struct StepEntry {
   const void* g;
   unsigned long long n;
   unsigned long long base;   // its first element in the state
-  unsigned first;            // its first chunk
   float decay;
   bool p_bf16, g_bf16, p_vec, g_vec;
 };
 template <int N>
 struct StepTable {
   int count, rounds;   // a chunk: `rounds` times kRound elements
+  unsigned first[N];   // an entry's first chunk
   StepEntry e[N];
 };
-constexpr int kStepTable = 640;   // 48 bytes each
+constexpr int kStepTable = 700;   // 44 bytes each
 
 struct Step {
   float beta1, beta2, rest1, rest2, eps;   // rest: 1 - beta
@@ -272,12 +314,15 @@ __device__ __forceinline__ float inverse(float x) {   // to 1 ulp, of normal num
   return r;
 }
 
+// CTAs a SM: 8-bit moments wait for their loads at four (742 us for 235M elements, 677 at six); 32-bit
+// ones keep the memory busy (971 us, 1011).
 template <int N, bool SMALL>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, SMALL ? 6 : 4)
     adamw_kernel(const __grid_constant__ StepTable<N> table, const __grid_constant__ Step q) {
-  const StepEntry& e = table.e[find_entry(table, blockIdx.x)];
+  const int at = find_entry(table, blockIdx.x);
+  const StepEntry& e = table.e[at];
   const int lane = threadIdx.x & 31;
-  size_t i = ((size_t)(blockIdx.x - e.first) * table.rounds) * kRound + threadIdx.x * 8;
+  size_t i = ((size_t)(blockIdx.x - table.first[at]) * table.rounds) * kRound + threadIdx.x * 8;
   const float coef = q.coef ? *q.coef : 1.f;
   float lr = q.lr, inv_c1 = q.inv_c1, inv_sqrt_c2 = q.inv_sqrt_c2;
   int t = q.t;
@@ -397,18 +442,26 @@ extern "C" mok_status mok_grad_norm(int count, const mok_grad* grads, float max_
   GradTable<kGradTable> table;
   table.count = 0;
   table.chunks = 0;
+  cudaError_t status = cudaSuccess;
   auto flush = [&] {
-    if (!table.count) return;
+    if (!table.count || status != cudaSuccess) return;
+    // a later table of a longer list adds to the first's sums, in its places
     const int ctas = parts ? parts : (int)std::min<size_t>(kNormCtas, table.chunks);
-    if (table.count <= 64) {
-      GradTable<64> small;
+    auto go = [&](const auto& tab) {
+      constexpr int N = std::extent<decltype(tab.e)>::value;
+      status = launch(grad_squares_kernel<N>, dim3(ctas), dim3(kThreads), 0, 1, false, s, tab, part, parts > 0);
+    };
+    auto few = [&](auto size) {
+      GradTable<decltype(size)::value> small;
       small.count = table.count;
       small.chunks = table.chunks;
+      std::copy(table.first, table.first + table.count, small.first);
       std::copy(table.e, table.e + table.count, small.e);
-      grad_squares_kernel<<<ctas, kThreads, 0, s>>>(small, part, parts > 0);
-    } else {
-      grad_squares_kernel<<<ctas, kThreads, 0, s>>>(table, part, parts > 0);
-    }
+      go(small);
+    };
+    if (table.count <= 16) few(std::integral_constant<int, 16>{});
+    else if (table.count <= 128) few(std::integral_constant<int, 128>{});
+    else go(table);
     parts = ctas;
     table.count = 0;
     table.chunks = 0;
@@ -416,14 +469,17 @@ extern "C" mok_status mok_grad_norm(int count, const mok_grad* grads, float max_
   for (int i = 0; i < count; ++i) {
     const mok_grad& g = grads[i];
     if (!g.g || !g.n) continue;
-    const size_t chunks = (g.n + kNormChunk - 1) / kNormChunk;
+    const size_t per = kNormBytes / (g.type == MOK_OUT_BF16 ? 2 : 4), chunks = (g.n + per - 1) / per;
     if (table.count == kGradTable || table.chunks + chunks > 0x7fffffffu) flush();
-    table.e[table.count++] = {g.g, g.n, table.chunks, g.type == MOK_OUT_BF16, aligned_to(g.g, 16)};
+    table.first[table.count] = table.chunks;
+    table.e[table.count++] = {g.g, g.n, g.type == MOK_OUT_BF16, aligned_to(g.g, 16)};
     table.chunks += (unsigned)chunks;
   }
   flush();
-  grad_norm_kernel<<<1, kThreads, 0, s>>>(part, parts, max_norm, scale, norm, coef);
-  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  if (status != cudaSuccess) return MOK_ERR_CUDA;
+  status = launch(grad_norm_kernel, dim3(1), dim3(kThreads), 0, 1, parts > 0, s, (const double*)part, parts,
+                  max_norm, scale, norm, coef);
+  return status == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
 
 extern "C" mok_status mok_adamw_get_sizes(int count, const size_t* n, size_t* elements) {
@@ -508,21 +564,25 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
   table.rounds = total / kRound < 152 * 32 ? 1 : total / kRound < 152 * 64 ? 2 : 4;
   const size_t chunk = (size_t)table.rounds * kRound;
   unsigned chunks = 0;
-  auto launch = [&](const auto& tab) {
-    if (small) adamw_kernel<std::extent<decltype(tab.e)>::value, true><<<chunks, kThreads, 0, s>>>(tab, q);
-    else adamw_kernel<std::extent<decltype(tab.e)>::value, false><<<chunks, kThreads, 0, s>>>(tab, q);
-  };
   auto flush = [&] {
     if (!table.count) return;
-    if (table.count <= 64) {
-      StepTable<64> few;
-      few.count = table.count;
-      few.rounds = table.rounds;
-      std::copy(table.e, table.e + table.count, few.e);
-      launch(few);
-    } else {
-      launch(table);
-    }
+    auto go = [&](const auto& tab) {
+      constexpr int N = std::extent<decltype(tab.e)>::value;
+      if (small) adamw_kernel<N, true><<<chunks, kThreads, 0, s>>>(tab, q);
+      else adamw_kernel<N, false><<<chunks, kThreads, 0, s>>>(tab, q);
+    };
+    auto few = [&](auto size) {
+      StepTable<decltype(size)::value> part;
+      part.count = table.count;
+      part.rounds = table.rounds;
+      std::copy(table.first, table.first + table.count, part.first);
+      std::copy(table.e, table.e + table.count, part.e);
+      go(part);
+    };
+    if (table.count <= 16) few(std::integral_constant<int, 16>{});
+    else if (table.count <= 64) few(std::integral_constant<int, 64>{});
+    else if (table.count <= 256) few(std::integral_constant<int, 256>{});
+    else go(table);
     table.count = 0;
     chunks = 0;
   };
@@ -532,7 +592,8 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
     const size_t own = (x.n + chunk - 1) / chunk;
     if (x.g && x.n) {
       if (table.count == kStepTable || chunks + own > 0x7fffffffu) flush();
-      table.e[table.count++] = {x.p, x.g, x.n, base, chunks, (float)x.decay,
+      table.first[table.count] = chunks;
+      table.e[table.count++] = {x.p, x.g, x.n, base, (float)x.decay,
                                 x.p_type == MOK_OUT_BF16, x.g_type == MOK_OUT_BF16,
                                 aligned_to(x.p, 16), aligned_to(x.g, 16)};
       chunks += (unsigned)own;

@@ -70,9 +70,11 @@ class Norm:
         stream); y in the type ``out`` (x's by default). Without ``add``, h is x itself. ``h``
         and ``stats`` are what ``backward`` takes."""
         code = _result_code(out or getattr(x, "dtype", None), "y")
-        return _results(mok.torch_calls().norm_fwd(self.KINDS[self.kind], self.eps, self.weight,
-                                                   self.bias, x, add, code),
-                        "mok_norm_fwd", lambda: self._check_forward(x, add))
+        got = mok.torch_calls().norm_fwd(self.KINDS[self.kind], self.eps, self.weight, self.bias, x,
+                                         add, code)
+        if type(got) is tuple:
+            return got
+        return _results(got, "mok_norm_fwd", lambda: self._check_forward(x, add))
 
     def backward(self, dY: torch.Tensor, h: torch.Tensor, stats: torch.Tensor,
                  add: Optional[torch.Tensor] = None):
@@ -81,5 +83,6 @@ class Norm:
         along the residual stream. dX is the gradient of x and of forward's ``add``."""
         got = mok.torch_calls().norm_bwd(self.KINDS[self.kind], self.eps, self.weight, self.bias,
                                          h, dY, stats, add)
-        got = _results(got, "mok_norm_bwd", lambda: self._check_backward(dY, h, stats, add))
+        if type(got) is not tuple:
+            _results(got, "mok_norm_bwd", lambda: self._check_backward(dY, h, stats, add))
         return dict(zip(("dX", "dW", "dB"), got))

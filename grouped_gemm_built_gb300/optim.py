@@ -31,12 +31,16 @@ def grad_norm(grads: Sequence[Optional[torch.Tensor]], max_norm: float = float("
     """(norm, coef), fp32 tensors of one value: norm = scale * the 2-norm of all gradients (bf16
     or fp32 tensors on one device, None for none), coef = scale * min(1, max_norm / norm), NaN
     when the norm is not finite."""
+    got = mok.torch_calls().grad_norm(grads, max_norm, scale)
+    if type(got) is tuple:
+        return got
+
     def check():
         _check_grads(grads)
         if all(g is None for g in grads):
             raise ValueError("grads must hold at least one tensor")
 
-    return _results(mok.torch_calls().grad_norm(grads, max_norm, scale), "mok_grad_norm", check)
+    return _results(got, "mok_grad_norm", check)
 
 
 class AdamW:
@@ -126,7 +130,8 @@ class AdamW:
         got = mok.torch_calls().adamw(self.rule, self.params, self._what,
                                       (self.master, self.m, self.v, self.scales), self.elements,
                                       grads, lr, t, coef, self.seed)
-        _results(got, "mok_adamw", lambda: self._check(grads, lr, t, coef))
+        if type(got) is not tuple:
+            _results(got, "mok_adamw", lambda: self._check(grads, lr, t, coef))
         if step is None:
             self.steps += 1
 
