@@ -1,6 +1,9 @@
-// Launches that overlap (programmatic dependent launch) and clusters.
+// Launches that overlap (programmatic dependent launch), clusters, large shared memory, and copies to it
+// that a thread makes for itself (cp.async).
 #pragma once
+#include <atomic>
 #include <cstddef>
+#include <cstdint>
 #include <cuda_runtime.h>
 
 namespace mok {
@@ -15,6 +18,39 @@ __device__ __forceinline__ void wait_prerequisites() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// At most the newest `n` (0, 1 or 2) groups still in flight.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+
+// Lets a kernel have more than 48 KB of shared memory, once on each device.
+template <auto KERNEL>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit)) return e;
+  cudaFuncAttributes a;
+  e = cudaFuncGetAttributes(&a, KERNEL);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(227 * 1024 - a.sharedSizeBytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 // Clusters of `cluster` CTAs; `early`: may start before the last kernel of the stream ends.
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 threads, size_t smem, int cluster,

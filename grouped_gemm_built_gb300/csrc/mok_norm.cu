@@ -9,7 +9,6 @@
 // and leave as one partial row per CTA, which a second, overlapped kernel sums up. Each thread
 // copies its own part of the next row to shared memory (cp.async: asynchronous, and nobody else
 // reads it, so there is no barrier and no wait on another thread) while the team reduces this one.
-#include <atomic>
 #include <climits>
 
 #include "mok_internal.h"
@@ -115,21 +114,6 @@ template <int N, int V, typename W>
 constexpr int w_places(int mode) {
   if constexpr (V == 1) return 0;
   else return keeps_w<V, W>(mode) ? 0 : N * kWPlaces<V, W>;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// At most the newest `n` (0 or 1) groups still in flight.
-__device__ __forceinline__ void copies_wait(int n) {
-  if (n) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void prefetch_l1(const void* p) {
@@ -532,22 +516,6 @@ Form form(const mok_norm_dims* d, int more, int threads, int most_ctas) {
 // Partial rows of dW and dB at most.
 int most_parts(const mok_norm_dims* d) { return std::min(d->T, d->H <= 2048 ? kMaxParts : kMaxParts / 2); }
 
-// Lets a kernel have more than 48 KB of shared memory, once on each device.
-template <auto KERNEL>
-cudaError_t allow_smem() {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit)) return e;
-  cudaFuncAttributes a;
-  e = cudaFuncGetAttributes(&a, KERNEL);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(227 * 1024 - a.sharedSizeBytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
 template <auto KERNEL>
 cudaError_t run(const Form& f, const NormArgs& q, cudaStream_t s) {
   if (f.smem > 40 * 1024) {   // 48 KB with the static part
