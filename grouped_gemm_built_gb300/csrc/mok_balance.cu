@@ -2,14 +2,14 @@
 //
 //   losses[0] = sum_t f_s (p_t . c_s),  f_s = coef E / (k T_s Tv),  s: row t's sequence
 //   losses[1] = z_coef / Tv sum_t lse_t^2
-// With the choices c_s counted first, the loss is a sum over rows: one pass over the logits and
-// no sums over columns, however many sequences there are.
+// With the choices c_s counted, the loss is a sum over rows: one pass over the logits, however many
+// sequences there are. A warp adds up the scores of its rows per expert, and multiplies by the counts
+// when it leaves a sequence.
 //
 // Two launches: the choices are counted by a cluster of CTAs per sequence, which joins its counts
 // through distributed shared memory and so needs no zeroed memory and no atomics on it; then a warp
-// per row takes the scores and the product with its sequence's counts. The rows' kernel starts
-// while the choices are still counted and has its first logits by then; its last CTA adds the CTAs'
-// sums in their order.
+// per row takes the scores. The rows' kernel runs while the choices are still counted, and waits for
+// the counts when it has its scores; its last CTA adds the CTAs' sums in their order.
 #include <climits>
 
 #include "mok_internal.h"
@@ -187,9 +187,10 @@ struct Sequence {
       if (lo >= hi) return lo - 1;
     }
   }
+  __device__ __forceinline__ bool ends_before(int t) const { return s == -2 || t >= end; }
   // Whether row t begins another sequence; its counts are then the caller's to load.
   __device__ __forceinline__ bool move_to(const Args& q, int t) {
-    if (s != -2 && t < end) return false;
+    if (!ends_before(t)) return false;
     int begin = 0;
     if (!q.seqs) {
       s = 0;
@@ -311,42 +312,57 @@ __device__ __forceinline__ void clean_row(Vec<NV>& l) {
   for (int i = 0; i < NV; ++i) l.v[i] = clean(l.v[i]);
 }
 
-// (sum of the scores, their product with c, log sum e^l) of any row; sum 0 where all is masked.
+// The scores of any row over their sum (0 where all is masked) added to p; log sum e^l squared.
 template <int NV, bool SIGMOID>
-__device__ __noinline__ float3 careful_sums(Vec<NV> l, Vec<NV> c) {
+__device__ __noinline__ Vec<NV> careful_scores(Vec<NV> l, Vec<NV> p, bool scores, float* lse_squared) {
   clean_row(l);
   const float m = row_max(l);
-  if (m == -INFINITY) return make_float3(0.f, 0.f, 0.f);
-  Vec<NV> p = exp_below(l, m);
-  float2 w = warp_sum2(p.sum(), dot(p, c));
-  const float lse = m + logf(w.x);
+  if (m == -INFINITY) return p;
+  Vec<NV> s = exp_below(l, m);
+  float z = warp_sum(s.sum());
+  const float lse = m + logf(z);
+  *lse_squared += lse * lse;
+  if (!scores) return p;
   if (SIGMOID && m > -17.f) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) p.v[i] = sigmoid(l.v[i]);
-    w = warp_sum2(p.sum(), dot(p, c));
+    for (int i = 0; i < NV; ++i) s.v[i] = sigmoid(l.v[i]);
+    z = warp_sum(s.sum());
   }
-  return make_float3(w.x, w.y, lse);
+  return fma(s, Vec<NV>::all(1.f / z), p);
 }
 
-// A row's part of both sums. One product with log2 e here: an exponential is off by up to |l| / 2 ulp,
-// which the loss, a sum in which the largest scores weigh most, does not show.
+// Adds a row's scores over their sum to p, and its log sum e^l squared to sum_z. One product with log2 e
+// here: an exponential is off by up to |l| / 2 ulp, which the loss, a sum in which the largest scores
+// weigh most, does not show.
 template <int NV, bool SIGMOID>
-__device__ __forceinline__ void add_row(const Args& q, const Vec<NV>& l, const Vec<NV>& c, float factor,
-                                        float& sum, float& sum_z) {
-  Vec<NV> p = l * Vec<NV>::all(SIGMOID ? -kLog2e : kLog2e);
+__device__ __forceinline__ void add_row(const Args& q, const Vec<NV>& l, Vec<NV>& p, float& sum_z) {
+  Vec<NV> s = l * Vec<NV>::all(SIGMOID ? -kLog2e : kLog2e);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) p.v[i] = SIGMOID ? inverse(1.f + exp2_fast(p.v[i])) : exp2_fast(p.v[i]);
-  float2 w = warp_sum2(p.sum(), dot(p, c));   // sum of the scores, their product with the counts
-  float lse = SIGMOID ? 0.f : __logf(w.x);
-  const bool plain = SIGMOID ? w.x > kTiny && w.x < 1e30f : plain_sum(w.x);
-  if (!plain || (SIGMOID && q.z > 0.f)) {
-    const float3 r = careful_sums<NV, SIGMOID>(l, c);
-    if (!(r.x > 0.f)) return;   // nothing unmasked in this row
-    if (!plain) w = make_float2(r.x, r.y);
-    lse = r.z;
+  for (int i = 0; i < NV; ++i) s.v[i] = SIGMOID ? inverse(1.f + exp2_fast(s.v[i])) : exp2_fast(s.v[i]);
+  const float z = warp_sum(s.sum());
+  const bool plain = SIGMOID ? z > kTiny && z < 1e30f : plain_sum(z);
+  if (plain) {
+    p = fma(s, Vec<NV>::all(inverse(z)), p);
+    const float lse = SIGMOID ? 0.f : __logf(z);
+    sum_z = fmaf(lse, lse, sum_z);
   }
-  sum_z = fmaf(lse, lse, sum_z);
-  sum += factor * __fdividef(w.y, w.x);
+  if (!plain || (SIGMOID && q.z > 0.f)) {
+    float more = 0.f;
+    p = careful_scores<NV, SIGMOID>(l, p, !plain, &more);
+    sum_z += more;
+  }
+}
+
+// Scores summed per expert times the experts' counts, over the warp.
+template <int NV>
+__device__ __forceinline__ float counted(const Args& q, const Vec<NV>& p, const int32_t* counts) {
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = element<NV>(q.vec, i);
+    if (e < q.E) t = fmaf(p.v[i], (float)counts[e], t);
+  }
+  return warp_sum(t);
 }
 
 // Few rows in one sequence: one launch of one cluster. Every CTA counts all choices by itself and takes
@@ -370,19 +386,14 @@ __global__ void __launch_bounds__(32 * kSmallWarps) small_loss_kernel(const Args
   __syncthreads();
   for (int e = rank + kSmallCtas * threadIdx.x; e < q.E; e += kSmallCtas * 32 * kSmallWarps)
     q.counts[e] = q.seq_counts[e] = hist[e];
-  const float factor = q.coef / ((float)q.T * (float)q.T);
-  float sum = 0.f, sum_z = 0.f;
-  Vec<NV> c;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = element<NV>(q.vec, i);
-    c.v[i] = e < q.E ? (float)hist[e] : 0.f;
-  }
+  float sum_z = 0.f;
+  Vec<NV> p = Vec<NV>::all(0.f);
   for (int t = first; t < q.T; t += kSmallCtas * kSmallWarps) {
     const Vec<NV> l = next.values();
     if (t + kSmallCtas * kSmallWarps < q.T) load(t + kSmallCtas * kSmallWarps);
-    add_row<NV, SIGMOID>(q, l, c, factor, sum, sum_z);
+    add_row<NV, SIGMOID>(q, l, p, sum_z);
   }
+  const float sum = q.coef / ((float)q.T * (float)q.T) * counted(q, p, hist);
   if (lane == 0) s[warp] = make_float2(sum, sum_z);
   __syncthreads();
   if (warp == 0) {
@@ -414,20 +425,25 @@ __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args
   auto load_next = [&] { next.load(row, q.E, q.vec, minus_infinity<LT>()); };
   if (first + warp < end) load_next();
   Sequence seq(q);
-  if (first + warp < end) seq.move_to(q, (int)first + warp);
-  bool fresh = seq.live;
-  wait_prerequisites();
-  // with several sequences, this CTA's share of them into the counts of all
-  if (q.S > 1) {
-    for (int s = blockIdx.x; s < q.S; s += gridDim.x) {
-      for (int e = threadIdx.x; e < q.E; e += 32 * kWarps) {
-        const int c = q.seq_counts[(size_t)s * q.E + e];
-        if (c) atomicAdd(&q.counts[e], c);   // integers: any order, one result
+  float sum = 0.f, sum_z = 0.f;
+  Vec<NV> p = Vec<NV>::all(0.f);
+  for (int t = (int)first + warp; t < end; t += kWarps) {
+    const Vec<NV> l = next.values();
+    row += (size_t)kWarps * q.E;
+    if (end - t > kWarps) load_next();
+    if (seq.ends_before(t)) {
+      if (seq.live) {
+        wait_prerequisites();
+        sum = fmaf(seq.factor, counted(q, p, q.seq_counts + (size_t)seq.s * q.E), sum);
       }
+      p = Vec<NV>::all(0.f);
+      seq.move_to(q, t);
     }
+    if (seq.live) add_row<NV, SIGMOID>(q, l, p, sum_z);
   }
-  __shared__ int32_t all[512];
-  if (q.groups > 1) {
+  wait_prerequisites();
+  if (q.groups > 1) {   // one sequence, counted in parts
+    __shared__ int32_t all[512];
     for (int e = threadIdx.x; e < q.E; e += 32 * kWarps) {
       int n = 0;
 #pragma unroll
@@ -436,25 +452,16 @@ __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args
       if (blockIdx.x == 0) q.seq_counts[e] = q.counts[e] = n;
     }
     __syncthreads();
-  }
-  float sum = 0.f, sum_z = 0.f;
-  Vec<NV> c;
-  for (int t = (int)first + warp; t < end; t += kWarps) {
-    Vec<NV> l = next.values();
-    row += (size_t)kWarps * q.E;
-    if (end - t > kWarps) load_next();
-    fresh |= seq.move_to(q, t);
-    if (!seq.live) continue;
-    if (fresh) {
-      const int32_t* n = q.groups > 1 ? all : q.seq_counts + (size_t)seq.s * q.E;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = element<NV>(q.vec, i);
-        c.v[i] = e < q.E ? (float)n[e] : 0.f;
+    sum = seq.factor * counted(q, p, all);
+  } else {
+    if (seq.live) sum = fmaf(seq.factor, counted(q, p, q.seq_counts + (size_t)seq.s * q.E), sum);
+    // with several sequences, this CTA's share of them into the counts of all
+    for (int s = blockIdx.x; q.S > 1 && s < q.S; s += gridDim.x) {
+      for (int e = threadIdx.x; e < q.E; e += 32 * kWarps) {
+        const int c = q.seq_counts[(size_t)s * q.E + e];
+        if (c) atomicAdd(&q.counts[e], c);   // integers: any order, one result
       }
-      fresh = false;
     }
-    add_row<NV, SIGMOID>(q, l, c, seq.factor, sum, sum_z);
   }
   // The sums of a CTA, then of all by the last CTA to arrive, in a fixed order. Positive terms, a few
   // after one another: fp32 keeps them to some ulp.
