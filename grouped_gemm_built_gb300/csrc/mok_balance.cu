@@ -24,7 +24,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kCountThreads = 1024;
 constexpr int kMaxS = 1 << 20;
-constexpr int kSmallCtas = 8, kSmallWarps = 16, kSmallIds = 8192;
+constexpr int kSmallCtas = 8, kSmallWarps = 16;
+constexpr int kSmallIds = 8192, kSmallRows = 1024, kSmallScores = 1 << 18;
 constexpr int kGroups = 16;        // clusters that count one sequence at most
 constexpr int kSms = 152;
 constexpr int kLossCtas = 4;       // CTAs a SM
@@ -50,7 +51,7 @@ struct Args {
 };
 
 // Counts of the choices of one sequence by a cluster, whose CTAs take a share of the ids each; a long
-// batch that is one sequence is shared by `groups` clusters, whose counts the rows' kernel adds up.
+// batch without offsets is shared by `groups` clusters, whose counts the rows' kernel adds up.
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int ctas) {
   launch_dependents();
   __shared__ int32_t hist[512];
@@ -427,10 +428,11 @@ __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args
   Sequence seq(q);
   float sum = 0.f, sum_z = 0.f;
   Vec<NV> p = Vec<NV>::all(0.f);
-  for (int t = (int)first + warp; t < end; t += kWarps) {
+  for (int left = end - (int)first - warp; left > 0; left -= kWarps) {
+    const int t = end - left;
     const Vec<NV> l = next.values();
     row += (size_t)kWarps * q.E;
-    if (end - t > kWarps) load_next();
+    if (left > kWarps) load_next();
     if (seq.ends_before(t)) {
       if (seq.live) {
         wait_prerequisites();
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args
     if (seq.live) add_row<NV, SIGMOID>(q, l, p, sum_z);
   }
   wait_prerequisites();
-  if (q.groups > 1) {   // one sequence, counted in parts
+  if (q.groups > 1) {   // all rows are one sequence, counted in parts
     __shared__ int32_t all[512];
     for (int e = threadIdx.x; e < q.E; e += 32 * kWarps) {
       int n = 0;
@@ -559,21 +561,24 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas<NV, SIGMOID>)
   Sequence seq(q);
   const float fz = q.z > 0.f && seq.valid > 0 ? 2.f * q.z / (float)seq.valid * d1 : 0.f;
   Vec<NV> u;
-  for (int t = (int)first + warp; t < end; t += kWarps) {
+  for (int left = end - (int)first - warp; left > 0; left -= kWarps) {
+    const int t = end - left;
     const Vec<NV> l = next.values();
     Vec<NV> d = add ? next_add.values() : Vec<NV>::all(0.f);
     DT* to = dlogits + at;
     at += (size_t)kWarps * q.E;
-    if (end - t > kWarps) load_next();
+    if (left > kWarps) load_next();
     if (seq.move_to(q, t)) {
       // counts relative to their mean, an integer: sum_e p_e = 1, so the gradient is the same,
       // without the cancellation of nearly even counts
       int32_t c[NV];
       load_counts<NV>(q.seq_counts + (size_t)seq.s * q.E, q.E, q.vec, c);
-      int total = 0;
+      long long total = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) total += c[i];
-      const int mean = __reduce_add_sync(kAll, total) / q.E;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kAll, total, off);
+      const int mean = (int)(total / q.E);
 #pragma unroll
       for (int i = 0; i < NV; ++i) u.v[i] = (float)(c[i] - mean) * (seq.factor * d0);
     }
@@ -660,7 +665,9 @@ extern "C" mok_status mok_balance_fwd(const mok_balance* rule, int T, const void
     else f(std::false_type{}, lf);
   };
   cudaError_t e = cudaSuccess;
-  if (!seqs && T > 0 && (long long)T * q.k <= kSmallIds) {
+  // One launch against two, top-8 fp32, us: 128 x 256 6.3 and 8.4, 1024 x 256 9.0 and 9.6, 2048 x 256
+  // 12.6 and 10.5, 1024 x 512 12.7 and 10.6.
+  if (!seqs && T > 0 && T <= kSmallRows && T * q.k <= kSmallIds && T * q.E <= kSmallScores) {
     by_width(q.E, [&](auto nv) {
       by_score([&](auto sg, const auto* l) {
         using LT = std::remove_const_t<std::remove_pointer_t<decltype(l)>>;
@@ -670,11 +677,11 @@ extern "C" mok_status mok_balance_fwd(const mok_balance* rule, int T, const void
     });
     return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
   }
-  // A sequence's CTAs: eight, but one where sequences are short or many; and several clusters for one
-  // long sequence, 32 K ids each (65536 rows of 8: .. us by one cluster, .. by 16).
+  // A sequence's CTAs: eight, but one where sequences are short or many; and several clusters for a
+  // long batch without offsets, 32 K ids each (65536 rows of 8: 10.6 us by one cluster, 6.8 by 16).
   const long long ids = (long long)T / S * q.k;
   const int ctas = ids >= 4096 && S <= 4096 ? 8 : 1;
-  q.groups = S > 1 ? 1 : (int)std::max(1ll, std::min<long long>(kGroups, ids >> 15));
+  q.groups = seqs ? 1 : (int)std::max(1ll, std::min<long long>(kGroups, ids >> 15));
   e = launch(count_kernel, dim3((unsigned)(S * q.groups) * ctas), dim3(kCountThreads), 0, ctas,
                          false, s, q, ctas);
   if (e != cudaSuccess) return MOK_ERR_CUDA;

@@ -171,7 +171,7 @@ mok_status mok_norm_fwd(const mok_norm_dims* dims, const void* x, const void* ad
  *   dW = sum over rows of dY xh;  dB = sum over rows of dY      (dB may be NULL)
  * add [T][H] (x_type) or NULL: the gradient that reaches h along the residual stream; dX is
  * the gradient of x and of mok_norm_fwd's add alike, and may be add. Row sums are fp32, in an
- * order that depends on T, H and the device only; T = 0 writes zeros. `workspace`:
+ * order that depends on the dims and the alignment only; T = 0 writes zeros. `workspace`:
  * mok_norm_sizes.workspace_bytes, 256-byte aligned. */
 mok_status mok_norm_bwd(const mok_norm_dims* dims, const void* dY, const void* h, const void* w,
                         const float* stats, const void* add, void* dX, void* dW, void* dB,
@@ -203,7 +203,7 @@ mok_status mok_balance_get_sizes(const mok_balance* rule, int T, int S, size_t* 
  * sequences' rows. As in mok_route a logit of -inf or NaN masks its expert (p = 0) and +inf
  * is the largest finite value; a row without an unmasked expert has p = 0 and no part in
  * losses[1]. losses 4-, saved 256-byte aligned. Offsets that do not ascend, or lie outside
- * [0, T], give unspecified losses. */
+ * [0, T], give unspecified results, and no access outside the tensors. */
 mok_status mok_balance_fwd(const mok_balance* rule, int T, const void* logits,
                            mok_out_dtype logits_type, const int32_t* topk_idx,
                            const int32_t* seqs, int S, float* losses, int32_t* counts,

@@ -61,6 +61,9 @@ def check(l, idx, score, coef=0.5, z=0.25, seqs=None, add=None, dlosses=None, dt
             _, live, s = scores(ld[t], score)
             if not live.any():
                 continue
+            if s.sum() < 1e-30:                 # as in the reference: relative to the largest logit
+                top = ld[t][live].max()
+                s = np.where(live, np.exp(np.where(live, ld[t], top) - top), 0.0)
             p = s / s.sum()
             dot = p @ np.abs(f)
             # p bounds the slope; lse, whose gradient is 2 z / Tv lse softmax, is off by q
@@ -149,6 +152,53 @@ def test_nearly_even_counts_keep_their_gradient():
     idx[:3] = 0
     check(l, idx.cuda(), "softmax", z=0.0)
     check(l, idx.cuda(), "sigmoid", z=0.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,seqs", [
+    (513, 16, 16, None), (1025, 16, 1, None), (1024, 257, 2, None), (1000, 24, 9, None),   # around one launch
+    (9000, 16, 8, None), (9001, 9, 7, None),                            # counted by several clusters
+    (9000, 16, 8, [0, 9000]), (9000, 16, 8, [5, 8990]), (9000, 12, 8, [0, 4, 8999])])
+def test_forms_of_the_forward(score, T, E, k, seqs):
+    """One launch for few rows, two otherwise; a long batch counted in parts, or as sequences with
+    padding before and behind."""
+    l, idx = make(T, E, k, BF, seed=T, std=1.0)
+    check(l, idx, score, seqs=seqs)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_choices_and_logits_off_16_byte_boundaries(shift):
+    l, idx = make(3000, 64, 5, F32, seed=4)
+    ids = torch.cat([idx.flatten()[:shift], idx.flatten()])[shift:].reshape(3000, 5)
+    lg = torch.cat([l.flatten()[:shift], l.flatten()])[shift:].reshape(3000, 64)
+    assert ids.data_ptr() % 16 and lg.data_ptr() % 16
+    a, _, _ = check(lg, ids, "sigmoid", seqs=[7, 500, 2999])
+    b, _, _ = check(l, idx, "sigmoid", seqs=[7, 500, 2999])
+    torch.testing.assert_close(a, b, rtol=2 * 26 * U, atol=0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_of_any_size(score):
+    """Rows whose scores overflow, vanish or spread over the whole range beside ordinary ones."""
+    l, idx = make(600, 40, 3, F32, seed=12)
+    for t, (a, b) in enumerate([(90, 1), (-90, 1), (300, 5), (-300, 5), (0, 60), (1e4, 1e3), (-1e4, 1e3), (40, 10)]):
+        l[t::17] = l[t::17] * b + a
+    check(l, idx, score, z=0.0)
+    check(l, idx, score, z=1e-6, seqs=[0, 100, 590])
+
+
+def test_every_row_count_that_an_int_holds():
+    T = 2 ** 31 - 1
+    l = torch.zeros((T, 1), dtype=BF, device="cuda")
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    B = Balance(1, 1, coef=0.5, z_coef=0.1)
+    losses, counts, saved = B.forward(l, idx)
+    assert int(counts) == T
+    # up to 2^31 / (608 CTAs 8 warps) = 441506 rows of one expert after one another, 0.5 / T each: a bit
+    # of the sum an addition at worst, 441506 u
+    assert abs(float(losses[0]) - 0.5) <= 441506 * U * 0.5 + 60 * U and float(losses[1]) == 0.0
+    dl = B.backward(l, saved)
+    assert not dl[:1000].any() and not dl[-1000:].any()
 
 
 def test_repeats_bit_for_bit_and_in_place():

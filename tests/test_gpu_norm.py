@@ -101,6 +101,22 @@ def test_types(kind, x_t, y_t, w_t, H):
     run(37, H, kind, x_t, y_t, w_t)
 
 
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("T,H", [(3, 8), (400, 136), (20, 260), (700, 1024), (9, 4096), (400, 7168), (3, 8192), (3, 8200),
+                                 (2, 16384), (2, 20001)])
+def test_sizes_in_fp32(kind, T, H):
+    run(T, H, kind, F32, F32, F32)
+    run(T, H, kind, F32, BF, F32, bias=False)
+
+
+@pytest.mark.parametrize("T,H", [(500, 7168), (900, 1536), (3000, 256)])
+def test_long_batches(T, H):
+    """Several rows a team, and weights of either type beside the ring."""
+    run(T, H, "layer", w_t=F32)
+    run(T, H, "rms", bias=False)
+    run(T, H, "layer", bias=False, add=False)
+
+
 @pytest.mark.parametrize("add,bias", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("H", [2048, 2047])
 def test_without_residual_or_bias(add, bias, H):
