@@ -561,7 +561,7 @@ cudaError_t by_form(const mok_norm_dims* d, bool vec, F f) {
   const int places = (wide ? 8 : 4) * (2 * K + (wide || d->w_type == MOK_OUT_BF16 ? 1 : 2));
   if ((size_t)((d->H + 1023) / 1024) * places * kPlace > kRingBytes) vec = false;
   if (!vec) {
-    if (d->H <= 2048) return by_types<8, 1, 256>(d, f);
+    if (d->H <= 1536) return by_types<6, 1, 256>(d, f);   // 2371 x 1031 fp32, bias: 29 us of eight, 25
     if (d->H <= 8192) return by_types<8, 1, 1024>(d, f);
     return by_types<32, 1, 1024>(d, f);
   }
@@ -606,7 +606,7 @@ extern "C" mok_status mok_norm_fwd(const mok_norm_dims* d, const void* x, const 
                    whole(y);
   const cudaError_t e = by_form<2, 32>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
     constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
-    constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 6 : 3;
+    constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 5 : 3;
     const Form f = form<N, V, 2>(d, 0, THREADS * CTAS, INT_MAX);
     q.stages = f.stages;
     return run<norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type,

@@ -400,16 +400,20 @@ constexpr size_t kMaxElements = (size_t)1 << 40;
 // Bytes that a call reads or writes.
 struct Range {
   uintptr_t begin, end;
-  bool written;
 };
-// Whether nothing that is written overlaps anything else.
-bool disjoint(Range* r, size_t n) {
-  std::sort(r, r + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
-  uintptr_t any = 0, written = 0;   // the ends so far
-  for (size_t i = 0; i < n; ++i) {
-    if (r[i].begin < (r[i].written ? any : written)) return false;
-    any = std::max(any, r[i].end);
-    if (r[i].written) written = std::max(written, r[i].end);
+void ascend(Range* r, size_t n) {
+  const auto less = [](const Range& a, const Range& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(r, r + n, less)) std::sort(r, r + n, less);   // one buffer's parts come sorted
+}
+// Whether what is written overlaps nothing else. Both lists are sorted here.
+bool disjoint(Range* written, size_t n, Range* read, size_t m) {
+  ascend(written, n);
+  ascend(read, m);
+  for (size_t i = 1; i < n; ++i)
+    if (written[i].begin < written[i - 1].end) return false;
+  for (size_t i = 0, w = 0; i < m; ++i) {
+    while (w < n && written[w].end <= read[i].begin) ++w;
+    if (w < n && written[w].begin < read[i].end) return false;
   }
   return true;
 }
@@ -529,20 +533,23 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
   {
     std::unique_ptr<Range[]> ranges(new (std::nothrow) Range[2 * (size_t)count + 4]);
     if (!ranges) return MOK_ERR_UNSUPPORTED;
-    size_t n = 0;
-    auto add = [&](const void* p, size_t bytes, bool written) {
-      if (p && bytes) ranges[n++] = {(uintptr_t)p, (uintptr_t)p + bytes, written};
+    Range *written = ranges.get(), *read = written + count + 4;
+    size_t n = 0, m = 0;
+    auto bytes = [](const void* p, size_t n, mok_out_dtype type) {
+      return Range{(uintptr_t)p, (uintptr_t)p + n * (type == MOK_OUT_BF16 ? 2 : 4)};
     };
     for (int i = 0; i < count; ++i) {
       const mok_adamw_tensor& x = tensors[i];
-      add(x.p, x.n * (x.p_type == MOK_OUT_BF16 ? 2 : 4), true);
-      add(x.g, x.n * (x.g_type == MOK_OUT_BF16 ? 2 : 4), false);
+      if (!x.n) continue;
+      written[n++] = bytes(x.p, x.n, x.p_type);
+      if (x.g) read[m++] = bytes(x.g, x.n, x.g_type);
     }
-    add(st->m, total * (small ? 1 : 4), true);
-    add(st->v, total * (small ? 1 : 4), true);
-    if (small) add(st->scales, total / kBlock * 2, true);
-    if (masters) add(st->master, total * 4, true);
-    if (!disjoint(ranges.get(), n)) return MOK_ERR_INVALID_ARG;
+    const uintptr_t kind = small ? 1 : 4;
+    written[n++] = {(uintptr_t)st->m, (uintptr_t)st->m + total * kind};
+    written[n++] = {(uintptr_t)st->v, (uintptr_t)st->v + total * kind};
+    if (small) written[n++] = {(uintptr_t)st->scales, (uintptr_t)st->scales + total / kBlock * 2};
+    if (masters) written[n++] = {(uintptr_t)st->master, (uintptr_t)st->master + total * 4};
+    if (!disjoint(written, n, read, m)) return MOK_ERR_INVALID_ARG;
   }
   Step q{};
   q.beta1 = (float)r->beta1; q.beta2 = (float)r->beta2;

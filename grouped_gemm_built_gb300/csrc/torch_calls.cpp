@@ -489,21 +489,27 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// adamw(rule, params, sizes and decays, (master | None, m, v, scales | None), elements,
-//       grads, lr, t, coef | None, seed) -> ()
-// params: a tuple of tensors; sizes and decays: a tuple of (numel, type code, decay), what they
-// were when the state was made; grads: a list or tuple of a tensor or None for each; lr and t:
+// adamw(rule, params, what, (master | None, m, v, scales | None), elements, grads, lr, t, coef | None,
+//       seed) -> ()
+// params: a tuple of tensors; what: an array of mok_adamw_tensor with their sizes, types and decays,
+// which the state was made for; grads: a list or tuple of a tensor or None for each; lr and t:
 // numbers, or tensors of one fp32 and one int32 value.
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 10)) return nullptr;
   mok_adamw_rule rule;
   if (!read_struct(a[0], &rule)) return nullptr;
-  PyObject **p, **d, **st, **g;
-  Py_ssize_t np, nd, ns, ng;
-  if (!items(a[1], &p, &np) || !items(a[2], &d, &nd) || !items(a[3], &st, &ns) ||
-      !items(a[5], &g, &ng) || np != nd || np != ng || ns != 4)
+  PyObject **p, **st, **g;
+  Py_ssize_t np, ns, ng;
+  if (!items(a[1], &p, &np) || !items(a[3], &st, &ns) || !items(a[5], &g, &ng) || np != ng || ns != 4)
     Py_RETURN_NONE;
+  std::vector<mok_adamw_tensor> tensors((size_t)np);
+  Py_buffer b;
+  if (PyObject_GetBuffer(a[2], &b, PyBUF_SIMPLE) != 0) return nullptr;
+  const bool fits = b.len == np * (Py_ssize_t)sizeof(mok_adamw_tensor);
+  if (fits) std::memcpy(tensors.data(), b.buf, (size_t)b.len);
+  PyBuffer_Release(&b);
+  if (!fits) Py_RETURN_NONE;
   const at::Tensor* m = dense(st[1]);
   if (!m) Py_RETURN_NONE;
   const int64_t elements = PyLong_AsLongLong(a[4]);
@@ -515,22 +521,19 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* scales = small ? dense(st[3], at::kByte, elements / 128, *m) : nullptr;
   if (!dense(st[1], kind, elements, *m) || !v || (!master && st[0] != Py_None) || (small && !scales))
     Py_RETURN_NONE;
-  std::vector<mok_adamw_tensor> tensors((size_t)np);
   for (Py_ssize_t i = 0; i < np; ++i) {
-    if (!PyTuple_Check(d[i]) || PyTuple_GET_SIZE(d[i]) != 3) Py_RETURN_NONE;
-    const int64_t numel = PyLong_AsLongLong(PyTuple_GET_ITEM(d[i], 0));
-    const long code = PyLong_AsLong(PyTuple_GET_ITEM(d[i], 1));
-    const double decay = PyFloat_AsDouble(PyTuple_GET_ITEM(d[i], 2));
-    if (PyErr_Occurred()) return nullptr;
-    const at::Tensor* t = dense(p[i], type_of(code), numel, *m);
+    mok_adamw_tensor& x = tensors[i];
+    const at::Tensor* t = dense(p[i], type_of(x.p_type), (int64_t)x.n, *m);
     if (!t) Py_RETURN_NONE;
-    tensors[i] = {t->data_ptr(), nullptr, (size_t)numel, decay, (mok_out_dtype)code, MOK_OUT_F32};
+    x.p = t->data_ptr();
+    x.g = nullptr;
+    x.g_type = MOK_OUT_F32;
     if (g[i] == Py_None) continue;
-    const at::Tensor* x = dense(g[i]);
-    const int gc = x ? code_of(x->scalar_type()) : -1;
-    if (gc < 0 || x->numel() != numel || x->device() != m->device()) Py_RETURN_NONE;
-    tensors[i].g = x->data_ptr();
-    tensors[i].g_type = (mok_out_dtype)gc;
+    const at::Tensor* d = dense(g[i]);
+    const int code = d ? code_of(d->scalar_type()) : -1;
+    if (code < 0 || d->numel() != (int64_t)x.n || d->device() != m->device()) Py_RETURN_NONE;
+    x.g = d->data_ptr();
+    x.g_type = (mok_out_dtype)code;
   }
   double lr = 0.;
   long t = 1;

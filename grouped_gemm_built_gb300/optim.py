@@ -76,8 +76,9 @@ class AdamW:
         mok.mok_adamw(self.rule, [], mok.MokAdamwState(), 0.0, None, 1, None, None, 0, None)
         self.bits, self.seed, self.steps = bits, int(seed), 0
         sizes = [p.numel() for p in self.params]
-        self._what = tuple((n, _result_code(p.dtype, "p"), d)
-                           for n, p, d in zip(sizes, self.params, weight_decay))
+        self._what = (mok.MokAdamwTensor * len(sizes))(
+            *(mok.MokAdamwTensor(n=n, decay=d, p_type=_result_code(p.dtype, "p"))
+              for n, p, d in zip(sizes, self.params, weight_decay)))
         self.elements = mok.mok_adamw_get_sizes(sizes)
         self.device = self.params[0].device
         kind = torch.uint8 if bits == 8 else torch.float32
@@ -103,11 +104,11 @@ class AdamW:
         _check_grads(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"grads must hold {len(self.params)} tensors, got {len(grads)}")
-        for i, (p, g, (n, code, _)) in enumerate(zip(self.params, grads, self._what)):
-            kind = torch.float32 if code == mok.MOK_OUT_F32 else torch.bfloat16
-            _dev(p, f"params[{i}]", kind, n)
+        for i, (p, g, what) in enumerate(zip(self.params, grads, self._what)):
+            kind = torch.float32 if what.p_type == mok.MOK_OUT_F32 else torch.bfloat16
+            _dev(p, f"params[{i}]", kind, what.n)
             if g is not None:
-                _dev(g, f"grads[{i}]", g.dtype, n)
+                _dev(g, f"grads[{i}]", g.dtype, what.n)
         if isinstance(lr, torch.Tensor):
             _dev(lr, "lr", torch.float32, 1)
         if isinstance(t, torch.Tensor):
