@@ -107,6 +107,10 @@ __device__ __forceinline__ double chunk_squares(const GradEntry& e, size_t at) {
       x[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= x[i].x | x[i].y | x[i].z | x[i].w;
+  if (!any) return 0.;   // zeros, or behind the tensor's end
   const float s = squares<E>(x);
   if (s > 1e-30f && s < 1e38f) return (double)s;   // what underflowed is below the sum's last bit
   return wide_squares<E>(x[0], x[1], x[2], x[3]);
