@@ -26,6 +26,15 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES)
                  : "memory");
 }
+// ... of which the first `some` bytes are read, and zeros take the others' place.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int some) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(some)
+                 : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // At most the newest `n` (0, 1 or 2) groups still in flight.
 __device__ __forceinline__ void copies_wait(int n) {

@@ -37,6 +37,8 @@ struct NormArgs {
   float *part_w, *part_b;        // [parts][H]
   void *dw, *db;
   int parts;
+  int part_row;                  // elements of a partial row
+  int part_shift;                // a partial row i lies (i H) % part_shift elements behind its place; 0: none
 };
 
 // V consecutive elements of a tensor or of shared memory
@@ -110,6 +112,11 @@ template <int V, typename W>
 constexpr bool keeps_w(int mode) {
   return V == 8 && std::is_same_v<W, __nv_bfloat16> && mode != kBias;
 }
+template <int N, int V, typename W, bool SHIFT>
+constexpr int fwd_places() {   // of a forward kernel: for w and b, where rows are shifted
+  if constexpr (SHIFT) return 2 * N * kWPlaces<V, W>;
+  else return 0;
+}
 template <int N, int V, typename W>
 constexpr int w_places(int mode) {
   if constexpr (V == 1) return 0;
@@ -163,13 +170,63 @@ __device__ __forceinline__ float2 row_sum(float a, float b, bool both, int& turn
 }
 
 // A thread's part of a row: N accesses, 32 V elements apart, from element c0 on; those below `live`
-// lie in the row.
-template <int N, int V>
+// lie in the row. SHIFT: rows of any length, in accesses of a tensor that begins at a 16-byte boundary. A
+// row then begins `shift` elements behind one, and its first and last access hold other rows'
+// elements too (edge), which count as 0 and are not written. The rows of a team are a multiple of V
+// apart and so have one shift.
+template <int N, int V, bool SHIFT>
 struct Part {
-  int c0, live;
-  __device__ __forceinline__ explicit Part(int H) {
+  int c0, live, shift, end;
+  __device__ __forceinline__ Part(int H, size_t first_row) {
+    shift = SHIFT ? (int)(first_row * H % V) : 0;
+    end = H + shift;
     c0 = (int)(threadIdx.x >> 5) * (32 * N * V) + (int)(threadIdx.x & 31) * V;
-    live = c0 < H ? min(N, (H - c0 + 32 * V - 1) / (32 * V)) : 0;
+    live = c0 < end ? min(N, (end - c0 + 32 * V - 1) / (32 * V)) : 0;
+  }
+  __device__ __forceinline__ int at(int i) const { return c0 + i * (32 * V); }
+  __device__ __forceinline__ bool edge(int i) const {
+    return SHIFT && (at(i) < shift || at(i) + V > end);
+  }
+  __device__ __forceinline__ bool holds(int i, int j) const {
+    return !SHIFT || (at(i) + j >= shift && at(i) + j < end);
+  }
+  __device__ __forceinline__ void clear(int i, Vec<V>& v) const {
+    if (!edge(i)) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (!holds(i, j)) v.v[j] = 0.f;
+  }
+  // p: the row's tensor at c0
+  template <typename E>
+  __device__ __forceinline__ void write(int i, E* p, const Vec<V>& v) const {
+    if (!edge(i)) {
+      put<V>(p + i * (32 * V), v.v);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (holds(i, j)) store(p + i * (32 * V) + j, v.v[j]);
+  }
+  // Starts the copies of a row (p: its tensor at c0) to `to` on; nothing behind its end is read.
+  template <typename E>
+  __device__ __forceinline__ void fetch(uint32_t to, const E* p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i >= live) continue;
+      constexpr int bytes = V * (int)sizeof(E);
+      if constexpr (SHIFT) copy_async<bytes>(to + i * kPlace, p + i * (32 * V), min(V, end - at(i)) * (int)sizeof(E));
+      else copy_async<bytes>(to + i * kPlace, p + i * (32 * V));
+    }
+  }
+  // The parameter's elements of access i.
+  template <typename W>
+  __device__ __forceinline__ void parameter(int i, const W* w, Raw<V, W>& r) const {
+    if constexpr (!SHIFT) {
+      r.read(w + at(i));
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) r.v[j] = holds(i, j) ? w[at(i) + j - shift] : W(0.f);
+    }
   }
 };
 // A thread's places in shared memory, for `stages` rows of K tensors: an access of its warp is 512 bytes
@@ -181,59 +238,68 @@ __device__ __forceinline__ char* places(int stages, int more) {
   const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
   return ring + (size_t)warp * ((stages * K * N + more) * kPlace) + (threadIdx.x & 31) * 16;
 }
-// Starts the copies of this thread's part of a row (`from`: its first element) to `to` on.
-template <int N, int V, typename E>
-__device__ __forceinline__ void fetch(uint32_t to, const E* from, int live) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i < live) copy_async<V * (int)sizeof(E)>(to + i * kPlace, from + i * (32 * V));
-}
-
 // RING: V elements a copy, 16 bytes at most; else V = 1, any alignment.
-template <int N, int V, typename X, typename Y, typename W, int THREADS, int CTAS>
+template <int N, int V, typename X, typename Y, typename W, bool SHIFT, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs q) {
   constexpr bool RING = V > 1;
   constexpr int K = 2;
-  const Part<N, V> part(q.H);
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const Part<N, V, SHIFT> part(q.H, row);
   const float inv_h = 1.f / (float)q.H;
-  char* const mine = RING ? places<N, K>(q.stages, 0) : nullptr;
+  char* const mine = RING ? places<N, K>(q.stages, fwd_places<N, V, W, SHIFT>()) : nullptr;
   auto start = [&](size_t r, int stage) {
     if constexpr (RING) {
       if (r < (size_t)q.T) {
         const uint32_t to = smem_u32(mine) + stage * (K * N * kPlace);
-        const size_t at = r * q.H + part.c0;
-        fetch<N, V>(to, static_cast<const X*>(q.x) + at, part.live);
-        if (q.add) fetch<N, V>(to + N * kPlace, static_cast<const X*>(q.add) + at, part.live);
+        const size_t at = r * q.H + part.c0 - part.shift;
+        part.fetch(to, static_cast<const X*>(q.x) + at);
+        if (q.add) part.fetch(to + N * kPlace, static_cast<const X*>(q.add) + at);
       }
       copies_commit();
     }
   };
   int stage = 0, turn = 0;
   for (int s = 0; s < q.stages; ++s) start(row + s * step, s);
-  if constexpr (RING) {   // the first row's second trip to memory, made beside its first
+  using WT = std::conditional_t<RING, W, float>;
+  char* const w_mine = mine + q.stages * (K * N * kPlace);
+  constexpr int W_STEP = kWPlaces<V, WT> * kPlace;
+  if constexpr (SHIFT) {   // parameters in no row's alignment: taken apart once, kept
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i >= part.live) continue;
+      Raw<V, WT> r;
+      part.parameter(i, static_cast<const WT*>(q.w), r);
+      r.keep(w_mine + i * W_STEP);
+      if (q.b) {
+        part.parameter(i, static_cast<const WT*>(q.b), r);
+        r.keep(w_mine + (N + i) * W_STEP);
+      }
+    }
+  } else if constexpr (RING) {   // the first row's second trip to memory, made beside its first
     const int size = q.w_bf16 ? 2 : 4;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (i < part.live) {
-        const size_t c = (size_t)(part.c0 + i * (32 * V)) * size;
+        const size_t c = (size_t)part.at(i) * size;
         prefetch_l1(static_cast<const char*>(q.w) + c);
         if (q.b) prefetch_l1(static_cast<const char*>(q.b) + c);
       }
     }
   }
   for (; row < (size_t)q.T; row += step) {
-    const size_t at = row * q.H + part.c0;
+    const size_t at = row * q.H + part.c0 - part.shift;
     const char* here = mine + stage * (K * N * kPlace);
     Vec<V> v[N];
     if constexpr (RING) copies_wait(q.stages - 1);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = Vec<V>::all(0.f);
-      if (i < part.live)
+      if (i < part.live) {
         get<V>(RING ? reinterpret_cast<const X*>(here + i * kPlace)
                     : static_cast<const X*>(q.x) + at + i * (32 * V), v[i].v);
+        part.clear(i, v[i]);
+      }
     }
     if (q.add) {
       Vec<V> kept[RING ? 1 : N];   // without a ring: all loads before the first store
@@ -248,6 +314,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
           if constexpr (RING) {
             Vec<V> a;
             get<V>(reinterpret_cast<const X*>(here + (N + i) * kPlace), a.v);
+            part.clear(i, a);
             v[i] = v[i] + a;
           } else {
             v[i] = v[i] + kept[i];
@@ -256,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i].v[j] = __bfloat162float(__float2bfloat16_rn(v[i].v[j]));
           }
-          put<V>(static_cast<X*>(q.h) + at + i * (32 * V), v[i].v);
+          part.write(i, static_cast<X*>(q.h) + at, v[i]);
         }
       }
     }
@@ -270,8 +337,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
       mean = row_sum(sum.sum(), 0.f, false, turn).x * inv_h;
       const Vec<V> minus = Vec<V>::all(-mean);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < part.live) v[i] = v[i] + minus;
+      for (int i = 0; i < N; ++i) {
+        if (i < part.live) {
+          v[i] = v[i] + minus;
+          part.clear(i, v[i]);
+        }
+      }
     }
     Vec<V> sq = Vec<V>::all(0.f);
 #pragma unroll
@@ -282,29 +353,40 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_fwd_kernel(const NormArgs 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (i < part.live) {
-        const int c = part.c0 + i * (32 * V);
         Vec<V> w, b = Vec<V>::all(0.f);
-        get_w<V, W>(q, q.w, c, w.v);
-        if (q.b) get_w<V, W>(q, q.b, c, b.v);
-        const Vec<V> y = fma(v[i] * rv, w, b);
-        put<V>(static_cast<Y*>(q.y) + at + i * (32 * V), y.v);
+        if constexpr (SHIFT) {
+          Raw<V, WT> r;
+          r.fetch(w_mine + i * W_STEP);
+          get<V>(r.v, w.v);
+          if (q.b) {
+            r.fetch(w_mine + (N + i) * W_STEP);
+            get<V>(r.v, b.v);
+          }
+        } else {
+          get_w<V, W>(q, q.w, part.at(i), w.v);
+          if (q.b) get_w<V, W>(q, q.b, part.at(i), b.v);
+        }
+        part.write(i, static_cast<Y*>(q.y) + at, fma(v[i] * rv, w, b));
       }
     }
   }
 }
 
+// Words that the sums of a row take in shared memory.
+__host__ __device__ constexpr int join_row(int H) { return H + H / 32 + 1; }
+
 // The parameters are read once: w stays in registers in the type it has, or, where dB's sums need
 // those, in the thread's own places of shared memory. (Read again for every row through L1, twice,
 // they made up a fifth of the kernel's time: 8192 x 7168 bf16 with add 95.6 us, now 78.3.)
-template <int N, int V, typename X, typename Y, typename W, int MODE, int THREADS, int CTAS>
+template <int N, int V, typename X, typename Y, typename W, bool SHIFT, int MODE, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs q) {
   launch_dependents();
   constexpr bool RING = V > 1, DB = MODE == kBias, WREG = keeps_w<V, W>(MODE);
   const bool rms = MODE == kRms || (MODE == kBias && q.rms);
   constexpr int K = 3;
-  const Part<N, V> part(q.H);
   const size_t step = (size_t)gridDim.x * blockDim.y;
   size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const Part<N, V, SHIFT> part(q.H, row);
   const float inv_h = 1.f / (float)q.H;
   constexpr int MORE = w_places<N, V, W>(MODE);
   char* const mine = RING ? places<N, K>(q.stages, MORE) : nullptr;
@@ -312,10 +394,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
     if constexpr (RING) {
       if (r < (size_t)q.T) {
         const uint32_t to = smem_u32(mine) + stage * (K * N * kPlace);
-        const size_t at = r * q.H + part.c0;
-        fetch<N, V>(to, static_cast<const Y*>(q.dy) + at, part.live);
-        fetch<N, V>(to + N * kPlace, static_cast<const X*>(q.x) + at, part.live);
-        if (q.add) fetch<N, V>(to + 2 * N * kPlace, static_cast<const X*>(q.add) + at, part.live);
+        const size_t at = r * q.H + part.c0 - part.shift;
+        part.fetch(to, static_cast<const Y*>(q.dy) + at);
+        part.fetch(to + N * kPlace, static_cast<const X*>(q.x) + at);
+        if (q.add) part.fetch(to + 2 * N * kPlace, static_cast<const X*>(q.add) + at);
       }
       copies_commit();
     }
@@ -327,14 +409,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       Raw<V, WT> w;
-      if (i < part.live) w.read(static_cast<const WT*>(q.w) + part.c0 + i * (32 * V));
+      if (i < part.live) part.parameter(i, static_cast<const WT*>(q.w), w);
       if constexpr (WREG) w_raw[i] = w;
       else w.keep(w_mine + i * (kWPlaces<V, WT> * kPlace));
     }
   }
   auto read_w = [&](int i, Vec<V>& w) {
     if constexpr (!RING) {
-      get_w<V, W>(q, q.w, part.c0 + i * (32 * V), w.v);
+      get_w<V, W>(q, q.w, part.at(i), w.v);
     } else if constexpr (WREG) {
       get<V>(w_raw[i].v, w.v);
     } else {
@@ -353,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
   for (int s = 0; s < q.stages; ++s) start(row + s * step, s);
   float2 st = row < (size_t)q.T ? q.stats[row] : make_float2(0.f, 0.f);
   for (; row < (size_t)q.T; row += step) {
-    const size_t at = row * q.H + part.c0;
+    const size_t at = row * q.H + part.c0 - part.shift;
     const char* here = mine + stage * (K * N * kPlace);
     const float mean = st.x, r = st.y;
     if (row + step < (size_t)q.T) st = q.stats[row + step];
@@ -377,6 +459,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
       if constexpr (RING) {
         get<V>(reinterpret_cast<const Y*>(here + i * kPlace), dy.v);
         get<V>(reinterpret_cast<const X*>(here + (N + i) * kPlace), x.v);
+        part.clear(i, dy);
+        part.clear(i, x);
       } else {
         dy = kept_y[i];
         x = kept_x[i];
@@ -412,45 +496,48 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
           else get<V>(static_cast<const X*>(q.add) + at + i * (32 * V), a.v);
           d = d + a;
         }
-        put<V>(static_cast<X*>(q.y) + at + i * (32 * V), d.v);
+        part.write(i, static_cast<X*>(q.y) + at, d);
       }
     }
     start(row + q.stages * step, stage);
     if (++stage >= q.stages) stage = 0;
   }
-  // this CTA's partial rows: its teams' sums one after another through shared memory
-  float* sum_w = reinterpret_cast<float*>(ring);
-  float* sum_b = sum_w + q.H;
-  if (blockDim.y > 1) {
-    if constexpr (RING) copies_wait(0);
-    __syncthreads();
-  }
-  for (int team = 0; team < (int)blockDim.y; ++team) {
-    if ((int)threadIdx.y == team) {
-      const bool last = team + 1 == (int)blockDim.y;
-      float* to_w = last ? q.part_w + (size_t)blockIdx.x * q.H : sum_w;
-      float* to_b = last ? q.part_b + (size_t)blockIdx.x * q.H : sum_b;
+  // This CTA's partial rows: a single team's as it holds them, several teams' summed up in shared
+  // memory, where 33 words hold 32 columns, so that a warp's places lie in different banks.
+  if (blockDim.y == 1) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (i < part.live) {
-          const int c = part.c0 + i * (32 * V);
-          Vec<V> b;
-          if (team) {
-            get<V>(sum_w + c, b.v);
-            acc_w[i] = acc_w[i] + b;
-          }
-          put<V>(to_w + c, acc_w[i].v);
-          if constexpr (DB) {
-            if (team) {
-              get<V>(sum_b + c, b.v);
-              acc_b[i] = acc_b[i] + b;
-            }
-            put<V>(to_b + c, acc_b[i].v);
-          }
-        }
-      }
+    for (int i = 0; i < N; ++i) {
+      if (i >= part.live) continue;
+      const size_t to = (size_t)blockIdx.x * q.part_row + part.at(i);
+      put<V>(q.part_w + to, acc_w[i].v);
+      if constexpr (DB) put<V>(q.part_b + to, acc_b[i].v);
     }
-    if (blockDim.y > 1) __syncthreads();
+    return;
+  }
+  const int teams = blockDim.y, threads = blockDim.x * teams, pitch = join_row(q.H);
+  float* sum_w = reinterpret_cast<float*>(ring);
+  float* sum_b = sum_w + teams * pitch;
+  if constexpr (RING) copies_wait(0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = part.at(i) + j - part.shift, to = threadIdx.y * pitch + c + (c >> 5);
+      if (i >= part.live || !part.holds(i, j)) continue;
+      sum_w[to] = acc_w[i].v[j];
+      if constexpr (DB) sum_b[to] = acc_b[i].v[j];
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < q.H; c += threads) {
+    float w = 0.f, b = 0.f;
+    for (int t = 0; t < teams; ++t) {
+      w += sum_w[t * pitch + c + (c >> 5)];
+      if constexpr (DB) b += sum_b[t * pitch + c + (c >> 5)];
+    }
+    q.part_w[(size_t)blockIdx.x * q.part_row + c] = w;
+    if constexpr (DB) q.part_b[(size_t)blockIdx.x * q.part_row + c] = b;
   }
 }
 
@@ -463,8 +550,10 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const NormArgs q) {
   if (c < q.H) {
 #pragma unroll 8
     for (int i = threadIdx.y; i < q.parts; i += 32) {
-      w += q.part_w[(size_t)i * q.H + c];
-      if (q.db) b += q.part_b[(size_t)i * q.H + c];
+      const int shift = q.part_shift ? (int)((unsigned)i * (unsigned)q.H % (unsigned)q.part_shift) : 0;
+      const size_t at = (size_t)i * q.part_row + c + shift;
+      w += q.part_w[at];
+      if (q.db) b += q.part_b[at];
     }
   }
   __shared__ float2 s[32][33];
@@ -492,7 +581,6 @@ bool check(const mok_norm_dims* d) {
 uintptr_t size_of(mok_out_dtype t) { return t == MOK_OUT_BF16 ? 2 : 4; }
 bool whole(const void* p) { return aligned_to(p, 16); }
 
-
 // How a call runs: teams of bx threads a row, by teams a CTA, `stages` rows in flight per team.
 struct Form {
   unsigned bx, by, grid;
@@ -503,7 +591,7 @@ struct Form {
 template <int N, int V, int K>
 Form form(const mok_norm_dims* d, int more, int threads, int most_ctas) {
   Form f{};
-  f.bx = ((d->H + N * V - 1) / (N * V) + 31) / 32 * 32;
+  f.bx = ((d->H + (d->H % 8 ? V - 1 : 0) + N * V - 1) / (N * V) + 31) / 32 * 32;   // room for a shift
   f.by = std::max(1u, 256 / f.bx);
   f.stages = V == 1 ? 0 : d->T <= kSms * (int)f.by ? 1 : 2;   // one, where no team has a second row
   f.smem = V == 1 ? 0 : (size_t)(f.bx * f.by / 32) * (f.stages * K * N + more) * kPlace;
@@ -525,21 +613,25 @@ cudaError_t run(const Form& f, const NormArgs& q, cudaStream_t s) {
   return launch(KERNEL, dim3(f.grid), dim3(f.bx, f.by), f.smem, 1, false, s, q);
 }
 
+// Elements of a partial row, with room for a shift.
+int part_row(const mok_norm_dims* d) { return (d->H + 15) / 8 * 8; }
+
 template <typename T>
 struct Tag {
   using type = T;
 };
-template <int N, int V, int THREADS, typename F>
+template <int N, int V, bool SHIFT, int THREADS, typename F>
 cudaError_t by_types(const mok_norm_dims* d, F f) {
   using B = __nv_bfloat16;
   constexpr std::integral_constant<int, N> n{};
   constexpr std::integral_constant<int, V> v{};
   constexpr std::integral_constant<int, THREADS> t{};
+  constexpr std::bool_constant<SHIFT> shift{};
   const bool xb = d->x_type == MOK_OUT_BF16, yb = d->y_type == MOK_OUT_BF16;
   auto with = [&](auto x, auto y) {
-    if constexpr (V == 1) return f(n, v, t, x, y, Tag<void>{});
-    else if (d->w_type == MOK_OUT_BF16) return f(n, v, t, x, y, Tag<B>{});
-    else return f(n, v, t, x, y, Tag<float>{});
+    if constexpr (V == 1) return f(n, v, shift, t, x, y, Tag<void>{});
+    else if (d->w_type == MOK_OUT_BF16) return f(n, v, shift, t, x, y, Tag<B>{});
+    else return f(n, v, shift, t, x, y, Tag<float>{});
   };
   if constexpr (V != 4)
     if (xb && yb) return with(Tag<B>{}, Tag<B>{});
@@ -550,29 +642,44 @@ cudaError_t by_types(const mok_norm_dims* d, F f) {
   }
   return cudaErrorInvalidValue;
 }
-// f(accesses a thread, elements an access, most threads of a CTA, X, Y, W) for the call's types,
-// width and alignment. `vec`: 32 elements a thread (8 for narrow rows; PER, where a type is fp32)
-// in accesses of 16 bytes of the widest type, through a ring for K tensors; element by element where
-// rows are not aligned, or too wide for the ring and w.
+// f(accesses a thread, elements an access, shift, most threads of a CTA, X, Y, W) for the call's types,
+// width and alignment. `whole_rows`: tensors of rows begin at 16-byte boundaries; then accesses of 16
+// bytes of the widest type through a ring for K tensors, PER (where a type is fp32) or 32 elements a
+// thread, fewer of narrow rows; shifted where rows begin between boundaries, or the parameters do
+// (not `whole_w`). Element by element where tensors begin between boundaries, or rows are too wide for
+// the ring. Forward and backward, bf16 with add, us: 8192 x 7167 shifted 78 and 92, element by element
+// 159 and 289. Shifted rows forward, 16 and 32 elements a thread: 8192 x 2047 bf16 29 and 34, fp32 38
+// and 73, 8192 x 7167 bf16 83 and 78, fp32 174 and 157; backward: 32768 x 511 with dB 50 and 72 (spills).
 template <int K, int PER, typename F>
-cudaError_t by_form(const mok_norm_dims* d, bool vec, F f) {
+cudaError_t by_form(const mok_norm_dims* d, bool whole_rows, bool whole_w, F f) {
   const bool wide = d->x_type != MOK_OUT_BF16 || d->y_type != MOK_OUT_BF16;
-  // places of 32 elements of each: 4 or 8 accesses of K tensors twice, and of w
-  const int places = (wide ? 8 : 4) * (2 * K + (wide || d->w_type == MOK_OUT_BF16 ? 1 : 2));
-  if ((size_t)((d->H + 1023) / 1024) * places * kPlace > kRingBytes) vec = false;
+  const bool shift = d->H % 8 != 0 || !whole_w;
+  // a warp's places for 1024 elements of K tensors twice, and of what a kernel may keep of w and b
+  const int kept = K == 3 ? 1 : shift ? 2 : 0;
+  const int places = (wide ? 8 : 4) * (2 * K + kept * (wide || d->w_type == MOK_OUT_BF16 ? 1 : 2));
+  const int warps = (d->H + (shift ? 7 : 0) + 1023) / 1024;
+  const bool vec = whole_rows && (size_t)warps * places * kPlace <= kRingBytes;
   if (!vec) {
-    if (d->H <= 1536) return by_types<6, 1, 256>(d, f);   // 2371 x 1031 fp32, bias: 29 us of eight, 25
-    if (d->H <= 8192) return by_types<8, 1, 1024>(d, f);
-    return by_types<32, 1, 1024>(d, f);
+    if (d->H <= 2048) return by_types<8, 1, false, 256>(d, f);
+    return by_types<32, 1, false, 1024>(d, f);
   }
+  const bool broad = warps > 8;
   if (wide) {
-    if (d->H <= 256) return by_types<2, 4, 256>(d, f);
-    if (d->H <= 8192) return by_types<PER / 4, 4, 8192 / PER>(d, f);
-    return by_types<8, 4, 1024>(d, f);
+    if (shift && d->H <= 2040) return by_types<2, 4, true, 256>(d, f);
+    if (shift && (d->H <= 4088 || K == 3) && !broad) return by_types<4, 4, true, 512>(d, f);
+    if (shift && !broad) return by_types<8, 4, true, 256>(d, f);
+    if (shift) return by_types<32, 1, false, 1024>(d, f);
+    if (d->H <= 256) return by_types<2, 4, false, 256>(d, f);
+    if (!broad) return by_types<PER / 4, 4, false, 8192 / PER>(d, f);
+    return by_types<8, 4, false, 512>(d, f);   // 14 warps at most
   }
-  if (d->H <= 256) return by_types<1, 8, 256>(d, f);
-  if (d->H <= 8192) return by_types<4, 8, 256>(d, f);
-  return by_types<4, 8, 1024>(d, f);
+  if (shift && K == 2 && !broad && d->H > 4088) return by_types<4, 8, true, 256>(d, f);
+  if (shift && !broad) return by_types<2, 8, true, 512>(d, f);
+  if (shift) return by_types<32, 1, false, 1024>(d, f);
+  if (d->H <= 256) return by_types<1, 8, false, 256>(d, f);
+  if (d->H <= 512) return by_types<2, 8, false, 256>(d, f);
+  if (!broad) return by_types<4, 8, false, 256>(d, f);
+  return by_types<4, 8, false, K == 2 ? 1024 : 512>(d, f);   // the backward's w takes it to 16 warps at most
 }
 
 }  // namespace
@@ -582,7 +689,7 @@ extern "C" mok_status mok_norm_get_sizes(const mok_norm_dims* d, mok_norm_sizes*
   using namespace mok;
   if (!check(d) || !out) return MOK_ERR_INVALID_ARG;
   out->stats_bytes = (size_t)d->T * sizeof(float2);
-  out->workspace_bytes = align_up((size_t)most_parts(d) * d->H * sizeof(float2), 256) + 256;
+  out->workspace_bytes = align_up((size_t)most_parts(d) * part_row(d) * sizeof(float2), 256) + 256;
   return MOK_OK;
 }
 
@@ -602,16 +709,18 @@ extern "C" mok_status mok_norm_fwd(const mok_norm_dims* d, const void* x, const 
   q.rms = d->kind == MOK_NORM_RMS; q.w_bf16 = d->w_type == MOK_OUT_BF16;
   q.x = x; q.add = add; q.w = w; q.b = b; q.h = h; q.y = y;
   q.stats = reinterpret_cast<float2*>(stats);
-  const bool vec = d->H % 8 == 0 && whole(x) && whole(add) && whole(w) && whole(b) && whole(h) &&
-                   whole(y);
-  const cudaError_t e = by_form<2, 32>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
+  const bool whole_rows = whole(x) && whole(add) && whole(h) && whole(y), whole_w = whole(w) && whole(b);
+  const cudaError_t e = by_form<2, 32>(d, whole_rows, whole_w, [&](auto n, auto v, auto sh, auto threads, auto xt, auto yt,
+                                                                auto wt) {
     constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
-    constexpr int CTAS = THREADS == 1024 ? 1 : V == 1 ? 5 : 3;
-    const Form f = form<N, V, 2>(d, 0, THREADS * CTAS, INT_MAX);
+    constexpr bool SHIFT = decltype(sh)::value;
+    using W = typename decltype(wt)::type;
+    constexpr int CTAS = THREADS > 512 ? 1 : SHIFT ? (N * V == 32 ? 2 : 1024 / THREADS)
+                         : THREADS > 256 ? 1 : V == 1 ? 5 : N < 4 ? 4 : 3;
+    const Form f = form<N, V, 2>(d, fwd_places<N, V, W, SHIFT>(), THREADS * CTAS, INT_MAX);
     q.stages = f.stages;
-    return run<norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type,
-                               typename decltype(wt)::type, THREADS, CTAS>>(
-        f, q, static_cast<cudaStream_t>(stream));
+    return run<norm_fwd_kernel<N, V, typename decltype(xt)::type, typename decltype(yt)::type, W, SHIFT,
+                               THREADS, CTAS>>(f, q, static_cast<cudaStream_t>(stream));
   });
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
@@ -636,23 +745,28 @@ extern "C" mok_status mok_norm_bwd(const mok_norm_dims* d, const void* dY, const
   q.dy = dY; q.x = h; q.w = w; q.add = add; q.y = dX; q.dw = dW; q.db = dB;
   q.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
   q.part_w = static_cast<float*>(workspace);
-  q.part_b = q.part_w + (size_t)most_parts(d) * d->H;
+  q.part_row = part_row(d);
+  q.part_b = q.part_w + (size_t)most_parts(d) * q.part_row;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->T) {
-    const bool vec = d->H % 8 == 0 && whole(dY) && whole(h) && whole(w) && whole(add) && whole(dX);
-    const cudaError_t e = by_form<3, 16>(d, vec, [&](auto n, auto v, auto threads, auto xt, auto yt, auto wt) {
+    const bool whole_rows = whole(dY) && whole(h) && whole(add) && whole(dX);
+    const cudaError_t e = by_form<3, 16>(d, whole_rows, whole(w), [&](auto n, auto v, auto sh, auto threads, auto xt,
+                                                                  auto yt, auto wt) {
       constexpr int N = decltype(n)::value, V = decltype(v)::value, THREADS = decltype(threads)::value;
-      constexpr int CTAS = THREADS > 256 ? 1 : V == 1 ? 3 : 2;
+      constexpr bool SHIFT = decltype(sh)::value;
+      constexpr int CTAS = THREADS > 256 ? 1 : V == 1 || N * V == 8 ? 3 : 2;
       using X = typename decltype(xt)::type;
       using Y = typename decltype(yt)::type;
       using W = typename decltype(wt)::type;
       auto go = [&](auto mode) {
         constexpr int MODE = decltype(mode)::value;
         Form f = form<N, V, 3>(d, w_places<N, V, W>(MODE), THREADS * CTAS, most_parts(d));
-        if (f.by > 1) f.smem = std::max(f.smem, (size_t)d->H * sizeof(float2));   // joins the teams
+        if (f.by > 1)   // joins the teams
+          f.smem = std::max(f.smem, f.by * join_row(d->H) * (MODE == kBias ? sizeof(float2) : sizeof(float)));
         q.stages = f.stages;
         q.parts = (int)f.grid;
-        return run<norm_bwd_kernel<N, V, X, Y, W, MODE, THREADS, CTAS>>(f, q, s);
+        q.part_shift = SHIFT && f.by == 1 ? V : 0;   // several teams are joined at their places
+        return run<norm_bwd_kernel<N, V, X, Y, W, SHIFT, MODE, THREADS, CTAS>>(f, q, s);
       };
       if (dB) return go(std::integral_constant<int, kBias>{});
       if (q.rms) return go(std::integral_constant<int, kRms>{});

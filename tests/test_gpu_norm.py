@@ -45,7 +45,7 @@ def check(got, want, bound, dtype, what):
     assert not bad.any(), (what, np.argwhere(bad)[:3], got[bad][:3], want[bad][:3], tol[bad][:3])
 
 
-def run(T, H, kind, x_t=BF, y_t=BF, w_t=BF, add=True, bias=True, eps=1e-5, mean=0.0, shift=0):
+def run(T, H, kind, x_t=BF, y_t=BF, w_t=BF, add=True, bias=True, eps=1e-5, mean=0.0, shift=0, w_shift=0):
     def rows(dtype, seed, std=1.0, m=0.0):
         if not shift:
             return draw((T, H), dtype, seed, std, m)
@@ -53,7 +53,7 @@ def run(T, H, kind, x_t=BF, y_t=BF, w_t=BF, add=True, bias=True, eps=1e-5, mean=
         return flat[shift:].reshape(T, H)
 
     x, a = rows(x_t, 1, 1.0, mean), rows(x_t, 2, 2.0) if add else None
-    w, b = draw((H,), w_t, 3, 0.3, 1.0), draw((H,), w_t, 4) if bias else None
+    w, b = draw((H + w_shift,), w_t, 3, 0.3, 1.0)[w_shift:], draw((H + w_shift,), w_t, 4)[w_shift:] if bias else None
     dY, da = rows(y_t, 5), rows(x_t, 6) if add else None
     n = Norm(w, b, kind=kind, eps=eps)
     y, h, stats = n.forward(x, add=a, out=y_t)
@@ -134,6 +134,63 @@ def test_row_counts(T):
 def test_rows_off_16_byte_boundaries(H, shift):
     run(20, H, "rms", shift=shift)
     run(20, H, "layer", F32, F32, F32, shift=shift)
+
+
+@pytest.mark.parametrize("T,H", [(1, 255), (700, 57), (3, 1025), (2500, 1031), (9, 2041), (700, 2047), (5, 4087),
+                                 (5, 4089), (330, 4099), (330, 7167), (3, 8177), (3, 8185), (3, 8193)])
+def test_rows_that_begin_between_boundaries(T, H):
+    run(T, H, "layer")
+    run(T, H, "rms", w_t=F32, bias=False)
+    run(T, H, "layer", bias=False, add=False)
+    run(T, H, "layer", F32, F32, F32)
+    run(T, H, "rms", F32, BF, BF, bias=False)
+
+
+@pytest.mark.parametrize("x_t", [BF, F32])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("H", [57, 1031, 4100, 7167])
+def test_a_row_without_numbers_leaves_its_neighbours_alone(x_t, kind, H):
+    """Rows share accesses with the rows beside them; so do the buffers' ends with what follows."""
+    from grouped_gemm_built_gb300 import mok
+    T = 310
+    x, a, dY, da = (draw((T, H), x_t, i) for i in range(4))
+    w, b = draw((H,), x_t, 5), draw((H,), x_t, 6)
+    bad = torch.arange(T, device="cuda") % 3 == 1
+    good = ~bad
+    n = Norm(w, b, kind=kind)
+    y, h, stats = n.forward(x, add=a)
+    g = n.backward(dY, h, stats, add=da)
+    for value in (float("nan"), float("inf")):
+        x2 = x.clone()
+        x2[bad] = value
+        flat = torch.full((3, T * H + 16), 7.0, dtype=x_t, device="cuda")
+        y2, h2, dX2 = (f[:T * H].view(T, H) for f in flat)
+        whole = all(t.data_ptr() % 16 == 0 for t in (y2, h2, dX2))
+        st, dW, dB = torch.empty_like(stats), torch.empty_like(w), torch.empty_like(w)
+        t = 0 if x_t == BF else 1
+        dims = mok.MokNormDims(T=T, H=H, kind=mok.MOK_NORM_RMS if kind == "rms" else mok.MOK_NORM_LAYER, eps=n.eps,
+                               x_type=t, y_type=t, w_type=t)
+        s = torch.cuda.current_stream().cuda_stream
+        mok.mok_norm_fwd(dims, x2.data_ptr(), a.data_ptr(), w.data_ptr(), b.data_ptr(), h2.data_ptr(), y2.data_ptr(),
+                         st.data_ptr(), s)
+        ws = torch.empty(mok.mok_norm_get_sizes(dims).workspace_bytes, dtype=torch.uint8, device="cuda")
+        mok.mok_norm_bwd(dims, dY.data_ptr(), h2.data_ptr(), w.data_ptr(), st.data_ptr(), da.data_ptr(), dX2.data_ptr(),
+                         dW.data_ptr(), dB.data_ptr(), ws.data_ptr(), s)
+        if whole:                                            # the same form of kernel
+            assert torch.equal(h2[good], h[good]) and torch.equal(y2[good], y[good])
+            assert torch.equal(st[good], stats[good]) and torch.equal(dX2[good], g["dX"][good])
+            assert torch.equal(dB, g["dB"])                  # a sum of dY alone
+        assert y2[good].isfinite().all() and dX2[good].isfinite().all() and dB.isfinite().all()
+        assert y2[bad].isnan().any(1).all()
+        assert (flat[:, T * H:] == 7.0).all()
+
+
+@pytest.mark.parametrize("H", [64, 1024, 7168])
+def test_parameters_off_16_byte_boundaries(H):
+    """Aligned rows with parameters that are slices of one tensor."""
+    run(40, H, "layer", w_shift=1)
+    run(40, H, "rms", w_t=F32, bias=False, w_shift=1)
+    run(40, H, "layer", F32, F32, F32, w_shift=1)
 
 
 @pytest.mark.parametrize("H", [1024, 5000])
