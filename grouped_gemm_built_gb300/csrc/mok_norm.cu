@@ -177,15 +177,25 @@ __device__ __forceinline__ float2 row_sum(float a, float b, bool both, int& turn
 template <int N, int V, bool SHIFT>
 struct Part {
   int c0, live, shift, end;
+  // Long parts: the accesses where a lane of the warp has an edge; the rest branches around what edges
+  // take (8192 x 7167 fp32 with add forward 144 us, 157 without). Short ones gain nothing.
+  static constexpr bool VOTE = SHIFT && N * V >= 32;
+  uint32_t edges = 0;
   __device__ __forceinline__ Part(int H, size_t first_row) {
     shift = SHIFT ? (int)(first_row * H % V) : 0;
     end = H + shift;
     c0 = (int)(threadIdx.x >> 5) * (32 * N * V) + (int)(threadIdx.x & 31) * V;
     live = c0 < end ? min(N, (end - c0 + 32 * V - 1) / (32 * V)) : 0;
+    if constexpr (VOTE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (__any_sync(kAll, outer(i))) edges |= 1u << i;
+    }
   }
   __device__ __forceinline__ int at(int i) const { return c0 + i * (32 * V); }
+  __device__ __forceinline__ bool outer(int i) const { return at(i) < shift || at(i) + V > end; }
   __device__ __forceinline__ bool edge(int i) const {
-    return SHIFT && (at(i) < shift || at(i) + V > end);
+    return VOTE ? edges >> i & 1u : SHIFT && outer(i);
   }
   __device__ __forceinline__ bool holds(int i, int j) const {
     return !SHIFT || (at(i) + j >= shift && at(i) + j < end);
@@ -199,7 +209,7 @@ struct Part {
   // p: the row's tensor at c0
   template <typename E>
   __device__ __forceinline__ void write(int i, E* p, const Vec<V>& v) const {
-    if (!edge(i)) {
+    if (!edge(i) || (VOTE && !outer(i))) {
       put<V>(p + i * (32 * V), v.v);
       return;
     }
@@ -214,7 +224,8 @@ struct Part {
     for (int i = 0; i < N; ++i) {
       if (i >= live) continue;
       constexpr int bytes = V * (int)sizeof(E);
-      if constexpr (SHIFT) copy_async<bytes>(to + i * kPlace, p + i * (32 * V), min(V, end - at(i)) * (int)sizeof(E));
+      if (VOTE ? edge(i) : SHIFT)
+        copy_async<bytes>(to + i * kPlace, p + i * (32 * V), min(V, end - at(i)) * (int)sizeof(E));
       else copy_async<bytes>(to + i * kPlace, p + i * (32 * V));
     }
   }
@@ -647,9 +658,9 @@ cudaError_t by_types(const mok_norm_dims* d, F f) {
 // bytes of the widest type through a ring for K tensors, PER (where a type is fp32) or 32 elements a
 // thread, fewer of narrow rows; shifted where rows begin between boundaries, or the parameters do
 // (not `whole_w`). Element by element where tensors begin between boundaries, or rows are too wide for
-// the ring. Forward and backward, bf16 with add, us: 8192 x 7167 shifted 78 and 92, element by element
+// the ring. Forward and backward, bf16 with add, us: 8192 x 7167 shifted 76 and 92, element by element
 // 159 and 289. Shifted rows forward, 16 and 32 elements a thread: 8192 x 2047 bf16 29 and 34, fp32 38
-// and 73, 8192 x 7167 bf16 83 and 78, fp32 174 and 157; backward: 32768 x 511 with dB 50 and 72 (spills).
+// and 73, 8192 x 7167 bf16 83 and 76, fp32 174 and 145; backward: 32768 x 511 with dB 50 and 72 (spills).
 template <int K, int PER, typename F>
 cudaError_t by_form(const mok_norm_dims* d, bool whole_rows, bool whole_w, F f) {
   const bool wide = d->x_type != MOK_OUT_BF16 || d->y_type != MOK_OUT_BF16;
