@@ -129,6 +129,8 @@ __device__ __forceinline__ double block_sum(double v) {   // in thread 0
   return v;
 }
 
+// Bound by memory: 352M elements 105 us in bf16 (6.7 TB/s), 198 in fp32 (7.1). The CTAs' sums go on in 64
+// bits, in a fixed order.
 template <int N>
 __global__ void __launch_bounds__(kThreads, 6)
     grad_squares_kernel(const __grid_constant__ GradTable<N> table, double* part, bool add) {
@@ -319,7 +321,10 @@ __device__ __forceinline__ float inverse(float x) {   // to 1 ulp, of normal num
 }
 
 // CTAs a SM: 8-bit moments wait for their loads at four (742 us for 235M elements, 677 at six); 32-bit
-// ones keep the memory busy (971 us, 1011).
+// ones keep the memory busy (971 us, 1011). With fp32 masters and bf16 gradients, 352M elements: 32 bits
+// 1451 us (6.8 TB/s), bound by memory; 8 bits 1018 us (5.5 TB/s), by the waits for its loads beside 64
+// instructions an element. (The next elements' loads started ahead, through shared memory: 750 against
+// 677 us; the noise drawn before the loads are waited for: 720.)
 template <int N, bool SMALL>
 __global__ void __launch_bounds__(kThreads, SMALL ? 6 : 4)
     adamw_kernel(const __grid_constant__ StepTable<N> table, const __grid_constant__ Step q) {
@@ -386,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 6 : 4)
   }
 }
 
+// Bound by memory: 352M elements 305 us (6.9 TB/s).
 __global__ void __launch_bounds__(kThreads)
     moments_kernel(size_t elements, const uint8_t* mc, const uint8_t* vc, const uint8_t* scales,
                    __nv_bfloat16* m_out, __nv_bfloat16* v_out) {
