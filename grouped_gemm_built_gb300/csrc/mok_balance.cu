@@ -688,8 +688,8 @@ extern "C" mok_status mok_balance_fwd(const mok_balance* rule, int T, const void
   const long long ids = (long long)T / S * q.k;
   const int ctas = ids >= 4096 && S <= 4096 ? 8 : 1;
   q.groups = seqs ? 1 : (int)std::max(1ll, std::min<long long>(kGroups, ids >> 15));
-  e = launch(count_kernel, dim3((unsigned)(S * q.groups) * ctas), dim3(kCountThreads), 0, ctas,
-                         false, s, q, ctas);
+  e = launch(count_kernel, dim3((unsigned)(S * q.groups) * ctas), dim3(kCountThreads), 0, ctas, false, s, q,
+             ctas);
   if (e != cudaSuccess) return MOK_ERR_CUDA;
   if (T > 0) {
     q.rows = cta_rows(T, kLossCtas);
@@ -728,6 +728,7 @@ extern "C" mok_status mok_balance_bwd(const mok_balance* rule, int T, const void
   q.vec = q.vec && rows_vectorize(q.E, dlogits, dlogits_type) &&
           (!add || rows_vectorize(q.E, add, dlogits_type));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   by_width(q.E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     const bool sg = rule->score == MOK_SCORE_SIGMOID;
@@ -736,10 +737,9 @@ extern "C" mok_status mok_balance_bwd(const mok_balance* rule, int T, const void
     auto go = [&](auto lt, auto dt) {
       using LT = decltype(lt);
       using DT = decltype(dt);
-      auto* kernel = sg ? balance_bwd_kernel<NV, true, LT, DT>
-                                                      : balance_bwd_kernel<NV, false, LT, DT>;
-      kernel<<<ctas, 32 * kWarps, 0, s>>>(q, static_cast<const LT*>(logits),
-                                          static_cast<const DT*>(add), static_cast<DT*>(dlogits));
+      e = launch(sg ? balance_bwd_kernel<NV, true, LT, DT> : balance_bwd_kernel<NV, false, LT, DT>, dim3(ctas),
+                 dim3(32 * kWarps), 0, 1, false, s, q, static_cast<const LT*>(logits),
+                 static_cast<const DT*>(add), static_cast<DT*>(dlogits));
     };
     const bool lb = logits_type == MOK_OUT_BF16, db = dlogits_type == MOK_OUT_BF16;
     if (lb && db) go(__nv_bfloat16{}, __nv_bfloat16{});
@@ -747,5 +747,5 @@ extern "C" mok_status mok_balance_bwd(const mok_balance* rule, int T, const void
     else if (db) go(0.f, __nv_bfloat16{});
     else go(0.f, 0.f);
   });
-  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }

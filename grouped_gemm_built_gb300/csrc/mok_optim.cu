@@ -581,12 +581,13 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
   table.rounds = total / kRound < 152 * 32 ? 1 : total / kRound < 152 * 64 ? 2 : 4;
   const size_t chunk = (size_t)table.rounds * kRound;
   unsigned chunks = 0;
+  cudaError_t status = cudaSuccess;
   auto flush = [&] {
-    if (!table.count) return;
+    if (!table.count || status != cudaSuccess) return;
     auto go = [&](const auto& tab) {
       constexpr int N = std::extent<decltype(tab.e)>::value;
-      if (small) adamw_kernel<N, true><<<chunks, kThreads, 0, s>>>(tab, q);
-      else adamw_kernel<N, false><<<chunks, kThreads, 0, s>>>(tab, q);
+      status = launch(small ? adamw_kernel<N, true> : adamw_kernel<N, false>, dim3(chunks), dim3(kThreads), 0, 1,
+                      false, s, tab, q);
     };
     auto few = [&](auto size) {
       StepTable<decltype(size)::value> part;
@@ -618,7 +619,7 @@ extern "C" mok_status mok_adamw(const mok_adamw_rule* r, int count, const mok_ad
     base += align_up(x.n, kBlock);
   }
   flush();
-  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  return status == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
 
 extern "C" mok_status mok_adamw_moments(size_t elements, const mok_adamw_state* st, void* m,
@@ -631,8 +632,9 @@ extern "C" mok_status mok_adamw_moments(size_t elements, const mok_adamw_state* 
       !aligned_to(v, 16))
     return MOK_ERR_INVALID_ARG;
   const size_t blocks = (elements / 8 + kThreads - 1) / kThreads;
-  moments_kernel<<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      elements, static_cast<const uint8_t*>(st->m), static_cast<const uint8_t*>(st->v), st->scales,
-      static_cast<__nv_bfloat16*>(m), static_cast<__nv_bfloat16*>(v));
-  return cudaGetLastError() == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  const cudaError_t e = launch(moments_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, 1, false,
+                               static_cast<cudaStream_t>(stream), elements, static_cast<const uint8_t*>(st->m),
+                               static_cast<const uint8_t*>(st->v), (const uint8_t*)st->scales,
+                               static_cast<__nv_bfloat16*>(m), static_cast<__nv_bfloat16*>(v));
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }

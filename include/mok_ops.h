@@ -142,8 +142,8 @@ typedef enum { MOK_NORM_LAYER = 0, MOK_NORM_RMS = 1 } mok_norm_kind;
 /* T rows of H elements, 0 <= T <= 2^31 - 1, 1 <= H <= 32768; eps >= 0, finite. Types
  * (MOK_OUT_BF16 or MOK_OUT_F32) of three groups of tensors: x_type of the stream (x, add, h,
  * dX), y_type of the normalised rows (y, dY), w_type of the parameters (w, b, dW, dB).
- * Addresses need their type's alignment only; rows of whole 16 bytes at 16-byte aligned
- * addresses are the fast case. */
+ * Addresses need their type's alignment only; tensors at 16-byte aligned addresses are the
+ * fast case, rows of whole 16 bytes the fastest. */
 typedef struct {
   int T, H;
   int kind; /* mok_norm_kind */
