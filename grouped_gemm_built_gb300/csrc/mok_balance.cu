@@ -22,7 +22,7 @@ namespace mok {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kCountThreads = 1024;
+constexpr int kCountThreads = 512;   // at most
 constexpr int kMaxS = 1 << 20;
 constexpr int kSmallCtas = 8, kSmallWarps = 16;
 constexpr int kSmallIds = 8192, kSmallRows = 1024, kSmallScores = 1 << 18;
@@ -54,10 +54,11 @@ struct Args {
 // batch without offsets is shared by `groups` clusters, whose counts the rows' kernel adds up.
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int ctas) {
   launch_dependents();
+  const int threads = blockDim.x;
   __shared__ int32_t hist[512];
   const int s = q.groups > 1 ? 0 : blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int share = q.groups > 1 ? blockIdx.x : rank, shares = q.groups * ctas;
-  for (int e = threadIdx.x; e < 512; e += kCountThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < 512; e += threads) hist[e] = 0;
   int begin = 0, end = q.T;
   if (q.seqs) {   // offsets outside the batch are cut off
     begin = max(q.seqs[s], 0);
@@ -77,19 +78,19 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const Args q, int 
       if (b + threadIdx.x < hi) count(q.idx[b + threadIdx.x]);
       const int4* v = reinterpret_cast<const int4*>(q.idx);
 #pragma unroll 8
-      for (size_t i = a / 4 + threadIdx.x; i < b / 4; i += kCountThreads) {
+      for (size_t i = a / 4 + threadIdx.x; i < b / 4; i += threads) {
         const int4 x = v[i];
         count(x.x), count(x.y), count(x.z), count(x.w);
       }
     } else {
 #pragma unroll 8
-      for (size_t i = lo + threadIdx.x; i < hi; i += kCountThreads) count(q.idx[i]);
+      for (size_t i = lo + threadIdx.x; i < hi; i += threads) count(q.idx[i]);
     }
   }
   if (ctas > 1) cluster_sync_all();
   else __syncthreads();
   // the ranks' counts of a share of the experts each
-  for (int e = rank + threadIdx.x * ctas; e < q.E; e += kCountThreads * ctas) {
+  for (int e = rank + threadIdx.x * ctas; e < q.E; e += threads * ctas) {
     int c = 0;
     for (int r = 0; r < ctas; ++r) {
       int x = hist[e];
@@ -418,8 +419,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps) small_loss_kernel(const Args
 }
 
 // A warp a row at a time, rows a CTA apart. Bound by instruction issue (144 a row of 384 bf16, 58% of
-// the slots). With the counts: 65536 rows of 384 bf16, softmax and z, 20.6 us (2.4 TB/s), 16384 of 256
-// fp32 sigmoid in one sequence 10.9 us.
+// the slots). With the counts: 65536 rows of 384 bf16, softmax and z, 20.0 us (2.5 TB/s), 16384 of 256
+// fp32 sigmoid in one sequence 10.2 us.
 template <int NV, bool SIGMOID, typename LT>
 __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args q, const LT* logits) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -688,8 +689,12 @@ extern "C" mok_status mok_balance_fwd(const mok_balance* rule, int T, const void
   const long long ids = (long long)T / S * q.k;
   const int ctas = ids >= 4096 && S <= 4096 ? 8 : 1;
   q.groups = seqs ? 1 : (int)std::max(1ll, std::min<long long>(kGroups, ids >> 15));
-  e = launch(count_kernel, dim3((unsigned)(S * q.groups) * ctas), dim3(kCountThreads), 0, ctas, false, s, q,
-             ctas);
+  // Few threads, so that the rows' kernel has room beside them. Forward with 1024 a CTA and now, us: 16384
+  // rows of 256 in one sequence 11.3 and 9.9, in 512 16.6 and 12.7. Clusters keep 512, as sequences
+  // differ (24 of 16384 rows, forward and backward: 22.3, with 256 22.4, 128 24.0, 1024 23.5).
+  const long long share = ids / ctas;
+  const unsigned threads = ctas > 1 || share >= 2048 ? kCountThreads : share >= 1024 ? 256 : 128;
+  e = launch(count_kernel, dim3((unsigned)(S * q.groups) * ctas), dim3(threads), 0, ctas, false, s, q, ctas);
   if (e != cudaSuccess) return MOK_ERR_CUDA;
   if (T > 0) {
     q.rows = cta_rows(T, kLossCtas);
