@@ -280,13 +280,16 @@ mok_status mok_adamw_get_sizes(int count, const size_t* n, size_t* elements);
  * with the step number t >= 1 and lr from host values, or from the device where t_dev (int32)
  * or lr_dev is given, so that a captured graph can advance them. coef: a device value, or
  * NULL for 1; a coef that is not finite skips the step, nothing is written. A bf16 p is the
- * rounded master. Moments in 8 bits are rounded after p has been computed: m to nearest; v up
- * or down at random so that its mean is kept (a nearest rounding would never move it), but
- * never from above 0 to 0, by 16-bit words of Philox4x32-7 keyed by `seed`: counter words
- * (position / 8 in the state, 64 bits; t; 0) give elements 8 (position / 8) .. + 7, words in
- * order, low half first. An m or v that is not finite becomes an m of NaN and counts for no
- * block's scale. `tensors`: a host array, read during the call; p's may not overlap one
- * another, gradients or the state. */
+ * rounded master. Moments in 8 bits are rounded after p has been computed. v goes up or down at
+ * random so that its mean is kept (a nearest rounding would never move it), but never from above
+ * 0 to 0, by 16-bit words of Philox4x32-7 keyed by `seed`: counter words (position / 8 in the
+ * state, 64 bits; t; 0) give elements 8 (position / 8) .. + 7, words in order, low half first. m
+ * goes to nearest (ties to even) where beta1 <= 0.9 and |m| >= 2^(a - 140), i.e. where a step's
+ * decay is more than half a code, so that m follows a gradient that fades; a gradient that stays
+ * leaves m at a code within 1 / 16 / (1 - beta1) of it, relative to m. Elsewhere m goes up or down
+ * at random too, with the same words' bits in reverse order, the highest inverted. An m or v that
+ * is not finite becomes an m of NaN and counts for no block's scale. `tensors`: a host array,
+ * read during the call; p's may not overlap one another, gradients or the state. */
 mok_status mok_adamw(const mok_adamw_rule* rule, int count, const mok_adamw_tensor* tensors,
                      const mok_adamw_state* state, double lr, const float* lr_dev, int t,
                      const int32_t* t_dev, const float* coef, uint64_t seed, void* stream);

@@ -109,7 +109,20 @@ def noise_words(first, n, seed, t):
     return np.array(out)
 
 
-def moment_codes(m, v, words):
+def random_code(x, word):
+    """The code of 0 <= x < 256 rounded up or down by a 16-bit word, whose bits count in reverse
+    order, the highest inverted. Codes are 2^20 apart: in the bits of an fp32 x from 2^-6 on, in
+    steps of 2^-29 (those of x + 2^-6) below."""
+    f, least = np.float32, np.float32(2.0 ** -6)
+    if x < least:
+        place = int((f(x) + least).view(np.uint32)) - (121 << 23)
+    else:
+        place = int(f(x).view(np.uint32)) - (120 << 23)
+    u = int(f"{int(word):016b}"[::-1], 2) ^ 0x8000
+    return (place + (u << 4)) >> 20
+
+
+def moment_codes(m, v, words, beta1=0.9):
     """(codes of m, codes of v, scales) of fp32 moments [n], n a multiple of 256."""
     m, v = np.asarray(m, np.float32), np.asarray(v, np.float32)
     mc, vc = np.zeros(len(m), np.uint8), np.zeros(len(v), np.uint8)
@@ -134,6 +147,8 @@ def moment_codes(m, v, words):
             if at > 0 and (at == 127 or x - finite[at - 1] < finite[at] - x or
                            (x - finite[at - 1] == finite[at] - x and (at - 1) % 2 == 0)):
                 at -= 1
+            if beta1 > 0.9 or x < 2.0 ** -6:
+                at = random_code(x, words[i])
             mc[i] = at + (128 if np.signbit(m[i]) else 0)
             if v[i] > 0:
                 # the position among the codes, in steps of 2^-20 of a code
