@@ -304,8 +304,10 @@ __device__ __forceinline__ constexpr uint32_t minus_infinity() { return sizeof(T
 // A sum of them in these bounds says that none overflowed, that what underflowed is below 1e-32 of
 // it, and that no logit was NaN or (in exp_vec's two parts) infinite. Any other row is read again
 // as the rule says: NaN masks, +inf is the largest finite value, softmax scores relative to the
-// largest logit; and sigmoid scores too where all are tiny: there each is e^l to 32 bits.
+// largest logit; and sigmoid scores too where all are tiny: there each is e^l to 32 bits. So is a row
+// whose log sum e^l is wanted and lies near 0, where its digits cancel.
 __device__ __forceinline__ bool plain_sum(float z) { return z > 1e-6f && z < 1e30f; }
+__device__ __forceinline__ bool near_one(float z) { return z > 0.5f && z < 2.f; }
 constexpr float kTiny = 1e-20f;
 
 template <int NV>
@@ -342,10 +344,10 @@ __device__ __forceinline__ void add_row(const Args& q, const Vec<NV>& l, Vec<NV>
 #pragma unroll
   for (int i = 0; i < NV; ++i) s.v[i] = SIGMOID ? inverse(1.f + exp2_fast(s.v[i])) : exp2_fast(s.v[i]);
   const float z = warp_sum(s.sum());
-  const bool plain = SIGMOID ? z > kTiny && z < 1e30f : plain_sum(z);
+  const bool plain = SIGMOID ? z > kTiny && z < 1e30f : plain_sum(z) && !(q.z > 0.f && near_one(z));
   if (plain) {
     p = fma(s, Vec<NV>::all(inverse(z)), p);
-    const float lse = SIGMOID ? 0.f : __logf(z);
+    const float lse = SIGMOID ? 0.f : __logf(z);   // to 3 ulp
     sum_z = fmaf(lse, lse, sum_z);
   }
   if (!plain || (SIGMOID && q.z > 0.f)) {
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas<NV, SIGMOID>)
       } else {
         const Vec<NV> p = exp_vec(l);
         const float2 w = warp_sum2(p.sum(), dot(p, u));
-        plain = plain_sum(w.x);
+        plain = plain_sum(w.x) && !(fz != 0.f && near_one(w.x));
         if (plain) {
           const float inv = inverse(w.x), shift = fz * __logf(w.x);   // fz 0: w.x is finite
           d = fma(p * Vec<NV>::all(inv), u + Vec<NV>::all(shift - w.y * inv), d);
