@@ -124,15 +124,21 @@ __device__ __forceinline__ float inverse(float x) {     // to 1 ulp; 0 above 2^1
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// e^x of NV values. One product x log2 e would leave an error of |x| / 2 ulp; what its rounding cut
-// off comes back as a factor. NaN for infinite x.
+// e^x of NV values to 5 u + |x| u / 20, u = 2^-24: 2^t with t = x log2 e rounded down, from a little below, and
+// what that cut off, x - t ln 2, as a factor. It lies in (0, 2^-16) for -88 <= x <= 88, so that a saturated
+// sum gives it; which is 0, not NaN, for x = -inf, and e^x is 0. NaN for NaN, inf or NaN for inf.
 template <int NV>
 __device__ __forceinline__ Vec<NV> exp_vec(const Vec<NV>& x) {
-  const Vec<NV> minus = x * Vec<NV>::all(-kLog2e);
-  const Vec<NV> cut = fma(x, Vec<NV>::all(kLog2e), minus) * Vec<NV>::all(0.693147182f);
-  Vec<NV> e;
+  Vec<NV> t, e, cut;
+  if constexpr (NV == 1) t.v[0] = __fmaf_rd(x.v[0], kLog2e, -0x1p-19f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) e.v[i] = exp2_fast(-minus.v[i]);
+  for (int i = 0; i + 1 < NV; i += 2)
+    t.set(i, __ffma2_rd(x.pair(i), make_float2(kLog2e, kLog2e), make_float2(-0x1p-19f, -0x1p-19f)));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    e.v[i] = exp2_fast(t.v[i]);
+    cut.v[i] = __saturatef(fmaf(-t.v[i], 0.693147182f, x.v[i]));
+  }
   return fma(e, cut, e);
 }
 
@@ -146,7 +152,7 @@ __device__ __forceinline__ float2 warp_sum2(float a, float b) {
   return make_float2(__shfl_sync(kAll, a, 0), __shfl_sync(kAll, a, 16));
 }
 
-// The largest of the warp's cleaned logits; and e^(l - m), at least e^-200, which is 0.
+// The largest of the warp's cleaned logits; and e^(l - m), at least e^-200, which is 0: 1 for the largest.
 template <int NV>
 __device__ __forceinline__ float row_max(const Vec<NV>& l) {
   float m = l.v[0];
@@ -158,7 +164,11 @@ template <int NV>
 __device__ __forceinline__ Vec<NV> exp_below(Vec<NV> l, float m) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) l.v[i] = fmaxf(l.v[i] - m, -200.f);
-  return exp_vec(l);
+  const Vec<NV> minus = l * Vec<NV>::all(-kLog2e), cut = fma(minus, Vec<NV>::all(0.693147182f), l);
+  Vec<NV> e;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) e.v[i] = exp2_fast(-minus.v[i]);
+  return fma(e, cut, e);
 }
 
 // Where the warp's row lies, and what the rows of its sequence share. Up to 32 offsets stay in the
@@ -300,12 +310,12 @@ __device__ __forceinline__ void store_values(T* row, int E, bool vec, const Vec<
 template <typename T>
 __device__ __forceinline__ constexpr uint32_t minus_infinity() { return sizeof(T) == 4 ? 0xff800000u : 0xff80u; }
 
-// The scores of a row first come straight from its logits, without their maximum: e^l, or sigmoid(l).
-// A sum of them in these bounds says that none overflowed, that what underflowed is below 1e-32 of
-// it, and that no logit was NaN or (in exp_vec's two parts) infinite. Any other row is read again
-// as the rule says: NaN masks, +inf is the largest finite value, softmax scores relative to the
-// largest logit; and sigmoid scores too where all are tiny: there each is e^l to 32 bits. So is a row
-// whose log sum e^l is wanted and lies near 0, where its digits cancel.
+// The scores of a row first come straight from its logits, without their maximum: e^l, or sigmoid(l);
+// masked ones, and what lies past the row's end, are 0. A sum of them in these bounds says that none
+// overflowed, that what underflowed is below 1e-32 of it, and that no softmax logit was NaN or +inf.
+// Any other row is read again as the rule says: NaN masks, +inf is the largest finite value, softmax
+// scores relative to the largest logit; and sigmoid scores too where all are tiny: there each is
+// e^l to 32 bits. So is a row whose log sum e^l is wanted and lies near 0, where its digits cancel.
 __device__ __forceinline__ bool plain_sum(float z) { return z > 1e-6f && z < 1e30f; }
 __device__ __forceinline__ bool near_one(float z) { return z > 0.5f && z < 2.f; }
 constexpr float kTiny = 1e-20f;
@@ -335,14 +345,26 @@ __device__ __noinline__ Vec<NV> careful_scores(Vec<NV> l, Vec<NV> p, bool scores
   return fma(s, Vec<NV>::all(1.f / z), p);
 }
 
-// Adds a row's scores over their sum to p, and its log sum e^l squared to sum_z. One product with log2 e
-// here: an exponential is off by up to |l| / 2 ulp, which the loss, a sum in which the largest scores
-// weigh most, does not show.
+// e^-l, at most e^88, whose sigmoid is 0: that of masked logits.
+template <int NV>
+__device__ __forceinline__ Vec<NV> exp_minus(const Vec<NV>& l) {
+  Vec<NV> x;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x.v[i] = fminf(-l.v[i], 88.f);
+  return exp_vec(x);
+}
+
+// Adds a row's scores over their sum to p, and its log sum e^l squared to sum_z.
 template <int NV, bool SIGMOID>
 __device__ __forceinline__ void add_row(const Args& q, const Vec<NV>& l, Vec<NV>& p, float& sum_z) {
-  Vec<NV> s = l * Vec<NV>::all(SIGMOID ? -kLog2e : kLog2e);
+  Vec<NV> s;
+  if constexpr (SIGMOID) {
+    s = exp_minus(l);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) s.v[i] = SIGMOID ? inverse(1.f + exp2_fast(s.v[i])) : exp2_fast(s.v[i]);
+    for (int i = 0; i < NV; ++i) s.v[i] = inverse(1.f + s.v[i]);
+  } else {
+    s = exp_vec(l);
+  }
   const float z = warp_sum(s.sum());
   const bool plain = SIGMOID ? z > kTiny && z < 1e30f : plain_sum(z) && !(q.z > 0.f && near_one(z));
   if (plain) {
@@ -504,15 +526,12 @@ __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args
   }
 }
 
-// e = e^-l; p = 1 / (1 + e), 0 where e is at its limit; the sums of p and p u.
+// e = e^-l; p = 1 / (1 + e); the sums of p and p u.
 template <int NV>
 __device__ __forceinline__ float2 sigmoids(const Vec<NV>& l, const Vec<NV>& u, Vec<NV>& e, Vec<NV>& p) {
-  e = exp_vec(l * Vec<NV>::all(-1.f));
+  e = exp_minus(l);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    e.v[i] = l.v[i] < -88.f ? FLT_MAX : e.v[i];
-    p.v[i] = inverse(1.f + e.v[i]);
-  }
+  for (int i = 0; i < NV; ++i) p.v[i] = inverse(1.f + e.v[i]);
   return warp_sum2(p.sum(), dot(p, u));
 }
 // d + sigmoid (1 - sigmoid) / sum (u - p.u) = d + (e^-l p) (p / sum) (u - p.u)
@@ -531,10 +550,8 @@ __device__ __noinline__ Vec<NV> careful_gradient(Vec<NV> l, Vec<NV> u, Vec<NV> d
   if (m == -INFINITY) return d;
   bool relative = loss;
   if (SIGMOID && loss && m > -17.f) {
-    Vec<NV> below, e, p;   // finite, or masked
-#pragma unroll
-    for (int i = 0; i < NV; ++i) below.v[i] = fminf(l.v[i], 200.f);
-    const float2 w = sigmoids(below, u, e, p);
+    Vec<NV> e, p;
+    const float2 w = sigmoids(l, u, e, p);
     d = sigmoid_gradient(d, u, e, p, w);
     relative = false;
   }
