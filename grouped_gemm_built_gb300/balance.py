@@ -43,15 +43,23 @@ class Balance:
             _dev(seqs, "seqs", torch.int32, seqs.numel())
         return logits.shape[0], 1 if seqs is None else seqs.numel() - 1
 
+    @staticmethod
+    def _shape(t, name, *shape):
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+
     def _check_forward(self, logits, topk_idx, seqs):
         T, _ = self._check(logits, seqs)
         _dev(topk_idx, "topk_idx", torch.int32, T * self.k)
+        self._shape(topk_idx, "topk_idx", T, self.k)
 
     def _check_backward(self, logits, saved, seqs, dlosses, add, dtype):
         T, S = self._check(logits, seqs)
         _dev(saved, "saved", torch.uint8, mok.mok_balance_get_sizes(self.rule, T, S))
         _dev(dlosses, "dlosses", torch.float32, 2, optional=True)
         _dev(add, "add", dtype, T * self.E, optional=True)
+        if add is not None:
+            self._shape(add, "add", T, self.E)
 
     def forward(self, logits: torch.Tensor, topk_idx: torch.Tensor,
                 seqs: Optional[torch.Tensor] = None):

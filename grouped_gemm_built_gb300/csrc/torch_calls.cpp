@@ -56,6 +56,11 @@ const at::Tensor* dense(PyObject* o, at::ScalarType type, int64_t numel, const a
              ? t
              : nullptr;
 }
+// ... of the shape of `like` too
+const at::Tensor* rows_like(PyObject* o, at::ScalarType type, const at::Tensor& like) {
+  const at::Tensor* t = dense(o, type, like.numel(), like);
+  return t && t->sizes() == like.sizes() ? t : nullptr;
+}
 // The ABI's code of a result type, -1 for others.
 int code_of(at::ScalarType t) {
   return t == at::kBFloat16 ? MOK_OUT_BF16 : t == at::kFloat ? MOK_OUT_F32 : -1;
@@ -312,7 +317,7 @@ PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   }
   const at::Tensor& x = *r.x;
-  const at::Tensor* add = a[5] == Py_None ? nullptr : dense(a[5], x.scalar_type(), x.numel(), x);
+  const at::Tensor* add = a[5] == Py_None ? nullptr : rows_like(a[5], x.scalar_type(), x);
   if (!add && a[5] != Py_None) Py_RETURN_NONE;
   const long code = PyLong_AsLong(a[6]);
   if (PyErr_Occurred()) return nullptr;
@@ -344,9 +349,9 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& h = *r.x;
   const at::Tensor* dY = dense(a[5]);
   const int yt = dY ? code_of(dY->scalar_type()) : -1;
-  if (yt < 0 || !dense(a[5], dY->scalar_type(), h.numel(), h)) Py_RETURN_NONE;
+  if (yt < 0 || !rows_like(a[5], dY->scalar_type(), h)) Py_RETURN_NONE;
   const at::Tensor* stats = dense(a[6], at::kFloat, 2 * h.size(0), h);
-  const at::Tensor* add = a[7] == Py_None ? nullptr : dense(a[7], h.scalar_type(), h.numel(), h);
+  const at::Tensor* add = a[7] == Py_None ? nullptr : rows_like(a[7], h.scalar_type(), h);
   if (!stats || (!add && a[7] != Py_None)) Py_RETURN_NONE;
   r.dims.y_type = (mok_out_dtype)yt;
   mok_norm_sizes sizes;
@@ -402,7 +407,7 @@ PyObject* balance_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   }
   const at::Tensor* idx = dense(a[2], at::kInt, (int64_t)r.T * r.rule.k, *r.l);
-  if (!idx) Py_RETURN_NONE;
+  if (!idx || idx->dim() != 2 || idx->size(0) != r.T) Py_RETURN_NONE;
   size_t bytes = 0;
   mok_status st = api.balance_get_sizes(&r.rule, r.T, r.S, &bytes);
   if (st != MOK_OK) return PyLong_FromLong(st);
@@ -434,7 +439,7 @@ PyObject* balance_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::ScalarType type = type_of(code);
   const at::Tensor* saved = dense(a[3], at::kByte, (int64_t)bytes, *r.l);
   const at::Tensor* dl = a[4] == Py_None ? nullptr : dense(a[4], at::kFloat, 2, *r.l);
-  const at::Tensor* add = a[5] == Py_None ? nullptr : dense(a[5], type, r.l->numel(), *r.l);
+  const at::Tensor* add = a[5] == Py_None ? nullptr : rows_like(a[5], type, *r.l);
   if (!saved || (!dl && a[4] != Py_None) || (!add && a[5] != Py_None)) Py_RETURN_NONE;
   c10::cuda::OptionalCUDAGuard guard(r.l->device());
   at::Tensor out = make(r.l->sizes(), type, *r.l);

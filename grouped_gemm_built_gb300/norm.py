@@ -43,25 +43,27 @@ class Norm:
         _dev(self.bias, "bias", w.dtype, H, optional=True)
         return H
 
-    def _rows(self, t, name: str) -> int:
+    def _rows(self, t, name: str, T=None, dtype=None) -> int:
+        """The rows of a tensor [T, H], of a given number or type where one is named."""
         dt = t.dtype if isinstance(t, torch.Tensor) else None
         _result_code(dt, name)
-        if t.dim() != 2 or t.shape[1] != self.H:
-            raise ValueError(f"{name} must be [T, {self.H}], got {tuple(t.shape)}")
-        _dev(t, name, dt, t.numel())
+        if t.dim() != 2 or t.shape[1] != self.H or T not in (None, t.shape[0]):
+            raise ValueError(f"{name} must be [{'T' if T is None else T}, {self.H}], got {tuple(t.shape)}")
+        _dev(t, name, dtype or dt, t.numel())
         return t.shape[0]
 
     def _check_forward(self, x, add):
-        self._rows(x, "x")
-        _dev(add, "add", x.dtype, x.numel(), optional=True)
+        T = self._rows(x, "x")
+        if add is not None:
+            self._rows(add, "add", T, x.dtype)
         self._check_weights()
 
     def _check_backward(self, dY, h, stats, add):
         T = self._rows(h, "h")
-        self._rows(dY, "dY")
-        _dev(dY, "dY", dY.dtype, T * self.H)
+        self._rows(dY, "dY", T)
         _dev(stats, "stats", torch.float32, 2 * T)
-        _dev(add, "add", h.dtype, T * self.H, optional=True)
+        if add is not None:
+            self._rows(add, "add", T, h.dtype)
         self._check_weights()
 
     def forward(self, x: torch.Tensor, add: Optional[torch.Tensor] = None,
