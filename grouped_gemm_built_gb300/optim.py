@@ -91,6 +91,7 @@ class AdamW:
             self.master = torch.zeros(self.elements, dtype=torch.float32, device=self.device)
             self.read_params()
 
+    @torch.no_grad()
     def read_params(self) -> None:
         """Sets ``master`` to the values of the bf16 parameters."""
         at = 0
