@@ -669,7 +669,8 @@ cudaError_t by_types(const mok_norm_dims* d, F f) {
 // bytes of the widest type through a ring for K tensors, PER (where a type is fp32) or 32 elements a
 // thread, fewer of narrow rows; shifted where rows begin between boundaries, or the parameters do
 // (not `whole_w`). Element by element where tensors begin between boundaries, or rows are too wide for
-// the ring. Forward and backward, bf16 with add, us: 8192 x 7167 shifted 76 and 92, element by element
+// the ring: above 2048 elements 32 a thread of 1024, whose 64 registers spill (200 bytes each way forward,
+// 440 to 700 out and 800 to 1200 back in backward). Forward and backward, bf16 with add, us: 8192 x 7167 shifted 76 and 92, element by element
 // 159 and 289. Shifted rows forward, 16 and 32 elements a thread: 8192 x 2047 bf16 29 and 34, fp32 38
 // and 73, 8192 x 7167 bf16 83 and 76, fp32 174 and 145; backward: 32768 x 511 with dB 50 and 72 (spills).
 template <int K, int PER, typename F>
@@ -689,13 +690,16 @@ cudaError_t by_form(const mok_norm_dims* d, bool whole_rows, bool whole_w, F f) 
   if (wide) {
     if (shift && d->H <= 2040) return by_types<2, 4, true, 256>(d, f);
     if (shift && (d->H <= 4088 || K == 3) && !broad) return by_types<4, 4, true, 512>(d, f);
-    if (shift && !broad) return by_types<8, 4, true, 256>(d, f);
+    if constexpr (K == 2)
+      if (shift && !broad) return by_types<8, 4, true, 256>(d, f);
     if (shift) return by_types<32, 1, false, 1024>(d, f);
     if (d->H <= 256) return by_types<2, 4, false, 256>(d, f);
-    if (!broad) return by_types<PER / 4, 4, false, 8192 / PER>(d, f);
-    return by_types<8, 4, false, 512>(d, f);   // 14 warps at most
+    if constexpr (K == 2)
+      if (broad) return by_types<8, 4, false, 512>(d, f);   // 14 warps at most; the backward's 8 are not broad
+    return by_types<PER / 4, 4, false, 8192 / PER>(d, f);
   }
-  if (shift && K == 2 && !broad && d->H > 4088) return by_types<4, 8, true, 256>(d, f);
+  if constexpr (K == 2)
+    if (shift && !broad && d->H > 4088) return by_types<4, 8, true, 256>(d, f);
   if (shift && !broad) return by_types<2, 8, true, 512>(d, f);
   if (shift) return by_types<32, 1, false, 1024>(d, f);
   if (d->H <= 256) return by_types<1, 8, false, 256>(d, f);
