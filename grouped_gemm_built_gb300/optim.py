@@ -139,7 +139,8 @@ class AdamW:
 
     def moments(self):
         """(m, v) of all tensors in the state's layout: the fp32 tensors themselves, or the
-        values of 8-bit moments in bf16, which holds them exactly."""
+        values of 8-bit moments in bf16, which holds them exactly (an m below 2^-117, the
+        largest of its block, to 2^-134)."""
         if self.bits == 32:
             return self.m, self.v
         return _results(mok.torch_calls().adamw_moments(self.m, self.v, self.scales),

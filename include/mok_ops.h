@@ -294,7 +294,8 @@ mok_status mok_adamw(const mok_adamw_rule* rule, int count, const mok_adamw_tens
                      const mok_adamw_state* state, double lr, const float* lr_dev, int t,
                      const int32_t* t_dev, const float* coef, uint64_t seed, void* stream);
 
-/* The values of 8-bit moments of `elements` state elements (a multiple of 256), bf16: exact. */
+/* The values of 8-bit moments of `elements` state elements (a multiple of 256) in bf16: exact, but
+ * for an m in a block with a < 10 (none above 2^-117), which is rounded to bf16's last step 2^-133. */
 mok_status mok_adamw_moments(size_t elements, const mok_adamw_state* state, void* m, void* v,
                              void* stream);
 

@@ -70,3 +70,22 @@ def test_codes_bit_for_bit(beta1):
         np.testing.assert_array_equal(opt.m.cpu().numpy(), mc)
         np.testing.assert_array_equal(opt.v.cpu().numpy(), vc)
         np.testing.assert_array_equal(opt.scales.cpu().numpy(), sc)
+
+
+def test_values_of_tiny_moments():
+    """Blocks whose largest |m| goes down to 2^-130: bf16 holds the codes' values exactly from a = 10
+    on (steps of 2^(a - 143), bf16's smallest is 2^-133), smaller ones to half of 2^-133."""
+    import numpy as np
+
+    n, f = 256 * 14, np.float32
+    g = torch.randn(n, generator=torch.Generator().manual_seed(4)).clamp(-1.9, 1.9)
+    g *= 2.0 ** -(116.0 + torch.arange(n) // 256)
+    opt = AdamW([torch.zeros(n, device="cuda")], betas=(0.0, 0.95), bits=8, seed=3)
+    opt.step([g.cuda()], lr=0.0)
+    mv, vv = ref.moment_values(opt.m.cpu().numpy(), opt.v.cpu().numpy(), opt.scales.cpu().numpy())
+    m, v = (x.double().cpu().numpy() for x in opt.moments())
+    a = np.repeat(opt.scales[:, 0].cpu().numpy(), 256)
+    assert a.min() == 8 and a.max() >= 11
+    np.testing.assert_array_equal(m[a >= 10], mv[a >= 10])
+    assert np.abs(m - mv).max() <= 2.0 ** -134 and (m != mv).any()
+    np.testing.assert_array_equal(v, vv)
