@@ -442,9 +442,9 @@ __global__ void __launch_bounds__(32 * kSmallWarps) small_loss_kernel(const Args
   cluster_sync_all();   // nobody leaves while its sums are read
 }
 
-// A warp a row at a time, rows a CTA apart. Bound by instruction issue (144 a row of 384 bf16, 58% of
-// the slots). With the counts: 65536 rows of 384 bf16, softmax and z, 20.0 us (2.5 TB/s), 16384 of 256
-// fp32 sigmoid in one sequence 10.2 us.
+// A warp a row at a time, rows a CTA apart. Bound by instruction issue (170 a row of 384 bf16, 63% of
+// the slots). With the counts: 65536 rows of 384 bf16, softmax and z, 21.4 us (2.4 TB/s), 16384 of 256
+// fp32 sigmoid in one sequence 10.5 us.
 template <int NV, bool SIGMOID, typename LT>
 __global__ void __launch_bounds__(32 * kWarps, kLossCtas) loss_kernel(const Args q, const LT* logits) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -567,8 +567,8 @@ __device__ __noinline__ Vec<NV> careful_gradient(Vec<NV> l, Vec<NV> u, Vec<NV> d
 }
 
 // softmax  p_e (u_e - p.u + 2 z / Tv lse);  sigmoid  p_e (1 - s_e) (u_e - p.u), the penalty apart
-// Bound by instruction issue (214 a row of 384 bf16 with z, 63% of the slots): 65536 of those 22.8 us
-// (4.4 TB/s), 16384 rows of 256 fp32, sigmoid, 7.9 us (4.2 TB/s).
+// Bound by instruction issue (219 a row of 384 bf16 with z, 63% of the slots): 65536 of those 20.9 us
+// (4.8 TB/s), 16384 rows of 256 fp32, sigmoid, 7.7 us (4.4 TB/s).
 template <int NV, bool SIGMOID, typename LT, typename DT>
 __global__ void __launch_bounds__(32 * kWarps, kBwdCtas<NV, SIGMOID>)
     balance_bwd_kernel(const Args q, const LT* logits, const DT* add, DT* dlogits) {

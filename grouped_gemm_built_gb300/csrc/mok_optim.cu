@@ -355,9 +355,9 @@ __device__ __forceinline__ float inverse(float x) {   // to 1 ulp, of normal num
   return r;
 }
 
-// CTAs a SM: 8-bit moments wait for their loads at four (742 us for 235M elements, 677 at six); 32-bit
-// ones keep the memory busy (971 us, 1011). With fp32 masters and bf16 gradients, 352M elements: 32 bits
-// 1451 us (6.8 TB/s), bound by memory; 8 bits 1018 us (5.5 TB/s), by the waits for its loads beside 64
+// CTAs a SM: 8-bit moments wait for their loads at four (742 us for 235M elements, 677 at six; m's small
+// codes, rounded at random, add 4); 32-bit ones keep the memory busy (971 us, 1011). With fp32 masters and bf16 gradients, 352M elements: 32 bits
+// 1451 us (6.8 TB/s), bound by memory; 8 bits 1016 us (5.5 TB/s), by the waits for its loads beside 67
 // instructions an element. (The next elements' loads started ahead, through shared memory: 750 against
 // 677 us; the noise drawn before the loads are waited for: 720.)
 template <int N, bool SMALL>
