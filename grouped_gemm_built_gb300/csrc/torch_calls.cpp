@@ -494,6 +494,11 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Whether two tensors of as many elements hold them in one order: one shape, or a flat view of it.
+bool same_order(const at::Tensor& a, const at::Tensor& b) {
+  return a.dim() <= 1 || b.dim() <= 1 || a.sizes() == b.sizes();
+}
+
 // adamw(rule, params, what, (master | None, m, v, scales | None), elements, grads, lr, t, coef | None,
 //       seed) -> ()
 // params: a tuple of tensors; what: an array of mok_adamw_tensor with their sizes, types and decays,
@@ -536,7 +541,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (g[i] == Py_None) continue;
     const at::Tensor* d = dense(g[i]);
     const int code = d ? code_of(d->scalar_type()) : -1;
-    if (code < 0 || d->numel() != (int64_t)x.n || d->device() != m->device()) Py_RETURN_NONE;
+    if (code < 0 || d->numel() != (int64_t)x.n || d->device() != m->device() || !same_order(*d, *t)) Py_RETURN_NONE;
     x.g = d->data_ptr();
     x.g_type = (mok_out_dtype)code;
   }

@@ -110,6 +110,8 @@ class AdamW:
             _dev(p, f"params[{i}]", kind, what.n)
             if g is not None:
                 _dev(g, f"grads[{i}]", g.dtype, what.n)
+                if g.shape != p.shape and min(g.dim(), p.dim()) > 1:
+                    raise ValueError(f"grads[{i}] must be {list(p.shape)} or flat, got {tuple(g.shape)}")
         if isinstance(lr, torch.Tensor):
             _dev(lr, "lr", torch.float32, 1)
         if isinstance(t, torch.Tensor):
@@ -123,7 +125,8 @@ class AdamW:
 
     def step(self, grads: Sequence[Optional[torch.Tensor]], lr: Union[float, torch.Tensor],
              coef: Optional[torch.Tensor] = None, step: Optional[torch.Tensor] = None) -> None:
-        """One step with a gradient (bf16 or fp32) per tensor, None to leave a tensor as it is.
+        """One step with a gradient (bf16 or fp32, of the tensor's shape or flat) per tensor, None
+        to leave a tensor as it is.
         ``coef``: factor of all gradients on the device (``grad_norm``'s); the step is skipped
         where it is not finite. A step captured in a graph takes its number from ``step``, an
         int32 tensor of one value that the graph advances, and a changing ``lr`` from an fp32

@@ -6,6 +6,7 @@ import torch
 from grouped_gemm_built_gb300 import build, mok
 from grouped_gemm_built_gb300.balance import Balance
 from grouped_gemm_built_gb300.norm import Norm
+from grouped_gemm_built_gb300.optim import AdamW
 from tests.test_layer_args import dev
 
 I32, F32 = torch.int32, torch.float32
@@ -61,3 +62,24 @@ def test_balance_gradient(make, shape):
         B.backward(make(3, 64), saved, add=make(*shape))
     with pytest.raises(ValueError, match="add"):
         B.backward(make(3, 64), saved, add=make(*shape, dtype=F32), dtype=F32)
+
+
+def test_adamw_gradients(make):
+    """A gradient has its tensor's shape, or is a flat view in its order."""
+    opt = AdamW([make(8, 32), make(64), make(2, 3, 4)])
+    good = [make(8, 32), make(64), make(2, 3, 4)]
+    for i, shape in ((0, (32, 8)), (0, (1, 256)), (2, (4, 3, 2)), (2, (6, 4)), (2, (2, 12))):
+        with pytest.raises(ValueError, match=rf"grads\[{i}\]"):
+            opt.step(good[:i] + [make(*shape)] + good[i + 1:], lr=0.1)
+    assert opt.steps == 0
+
+
+@pytest.mark.gpu
+def test_adamw_takes_flat_gradients():
+    g = torch.randn(8, 32, generator=torch.Generator().manual_seed(1)).cuda()
+    p, q, flat = (torch.ones(8, 32, device="cuda") for _ in range(3))
+    for t, d in ((p, g), (q, g.view(-1))):
+        AdamW([t]).step([d], lr=0.1)
+    flat = flat.view(-1)
+    AdamW([flat]).step([g], lr=0.1)
+    assert torch.equal(p, q) and torch.equal(p.view(-1), flat) and not torch.equal(p, torch.ones_like(p))
