@@ -245,12 +245,13 @@ __device__ __noinline__ uint2 round_at_random(const Eight x, const uint2 mc, con
   return make_uint2(w[0], w[1]);
 }
 
-// Codes of finite moments, or (CHECK) of any: those that are not finite count for no scale. m is
-// rounded to nearest while a step's decay takes it past half a code, which for beta1 <= 0.9 it does at
-// all but the codes below 2^-6 (a code is at most 1/8 of the next); where it does not, a nearest rounding
-// would keep m when the gradient fades while v, rounded at random, goes on falling: those are rounded
-// at random too. (60 steps of normal gradients, then 200 of zeros, beta1 = beta2 = 0.95: to nearest a
-// weight went 157 times as far as with fp32 moments, at random 1.06 times.)
+// Codes of finite moments, or (CHECK) of any: those that are not finite count for no scale. m goes to
+// nearest where a step's decay, (1 - beta1) of it, is more than half the distance to the next code: for
+// beta1 <= 0.9 everywhere but below 2^-6, as codes from there on are 1/16 to 1/8 of themselves apart.
+// Where it is less, a nearest rounding would keep m when the gradient fades while v, rounded at random,
+// goes on falling: there m is rounded at random too. (60 steps of normal gradients, then 200 of zeros,
+// beta1 = beta2 = 0.95: to nearest a weight went 157 times as far as with fp32 moments, at random 1.06
+// times.) All codes at random: 705 us for 235M elements, the small ones 681, none 677.
 template <bool CHECK>
 __device__ __forceinline__ bool encode8(const Eight& m, const Eight& v, const uint4 noise, bool all_random, uint2* mc,
                                         uint2* vc, int* a, int* b) {
